@@ -290,6 +290,70 @@ moe_status_t moe_dense_mlp(int64_t T, int32_t d, int32_t I, moe_dtype_t act_dtyp
                            const void* W13, const void* W2, void* out, void* ws, size_t ws_bytes,
                            void* stream);
 
+/* The whole layer for a few tokens in one kernel launch: moe_forward for decode steps of one to
+ * MOE_FEW_MAX_TOKENS sequences, where launches and intermediates of the staged path cost as much
+ * as the weights.  Arguments, layouts and shapes as moe_forward (K2 and latent form), with these
+ * differences:
+ *   - T <= MOE_FEW_MAX_TOKENS, else MOE_ERR_UNSUPPORTED.  Widths: d, I and d_latent multiples of
+ *     32 (bf16, int4), 128 (e4m3) or 16 (fp32) and at most 65536; d_latent with bf16 or fp32
+ *     weights.  cfg->flags must be 0.
+ *   - Arithmetic: every sum in fp32; SiLU(g) * u, the latent activations and the normed latent sum
+ *     keep at least 16 significant bits between the products (moe_forward rounds them to bf16),
+ *     the output is rounded once.  e4m3 experts take the bf16 activations as they are (moe_forward
+ *     quantises them), so both stay within that layer's tolerance of each other.
+ *   - ws: moe_few_workspace_size() bytes, laid out differently from moe_workspace_size()'s.  One
+ *     workspace serves one call at a time.
+ *   - The launch is cooperative (one thread block on each SM, which wait for one another between
+ *     the layer's steps); it can be captured into a CUDA graph.  Every wait is bounded: a wait that
+ *     expires raises MOE_ERR_TIMEOUT in the device status and the output is incomplete.
+ * The result depends on nothing but the arguments: equal calls give equal bits. */
+#define MOE_FEW_MAX_TOKENS 16
+size_t moe_few_workspace_size(const moe_config_t* cfg);
+moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, const float* W_r,
+                             const float* b, const void* W13, const void* W2,
+                             const float* W13_scale, const float* W2_scale, const void* Ws13,
+                             const void* Ws2, const float* Ws13_scale, const float* Ws2_scale,
+                             const void* W_down, const void* W_up, void* out, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* What stands between two blocks of a stack, in one pass over the rows: the branch's post-norm, its
+ * gate and scale, the residual sum, and the norm that the next block starts with.  Per row
+ *   v  = branch * post_w / sqrt(mean(branch^2) + rms_eps)        (v = branch without post_w)
+ *   r' = resid_scale * resid + branch_scale * g * v
+ *   normed = r' * pre_w / sqrt(mean(r'^2) + rms_eps)             (without normed: not computed)
+ * with g = 1, the gate's value, or its sigmoid.  All in fp32; r' is rounded once to resid_dtype and
+ * normed, computed from the unrounded r', once to act_dtype.
+ * Unlike the layer's buffers, rows may lie in wider buffers (the ld_* pitches, in elements) and
+ * pointers need only their element's alignment; 16-byte aligned pointers and pitches with
+ * d % 8 == 0 run wide loads. */
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_CHANNEL = 1, /* gate [d]                */
+  MOE_GATE_TOKEN = 2,   /* gate [T]                */
+  MOE_GATE_ELEMENT = 3  /* gate [T][d], ld_gate    */
+} moe_gate_t;
+#define MOE_JOIN_GATE_SIGMOID 0x1u /* g = 1 / (1 + exp(-gate)) */
+#define MOE_JOIN_MAX_D 32768
+typedef struct {
+  int64_t T;            /* rows, >= 0; T == 0 is a no-op                                      */
+  int32_t d;            /* row width, 1 .. MOE_JOIN_MAX_D                                     */
+  int32_t act_dtype;    /* MOE_F32 or MOE_BF16: branch, post_w, gate, pre_w, normed           */
+  int32_t resid_dtype;  /* act_dtype, or MOE_F32 with bf16 activations: resid, resid_out      */
+  int32_t gate;         /* MOE_GATE_*                                                         */
+  uint32_t flags;       /* MOE_JOIN_*                                                         */
+  float resid_scale;
+  float branch_scale;
+  float rms_eps;
+  int64_t ld_resid, ld_branch, ld_gate, ld_resid_out, ld_normed; /* row pitches; 0: d          */
+} moe_join_config_t;
+/*   resid [T][d], branch [T][d]; post_w [d] or NULL; gate as its kind says (NULL without);
+ *   pre_w [d] and normed [T][d], both or neither; resid_out [T][d].
+ * resid_out may be resid, and normed may be branch (same pointer, pitch and type); other overlaps
+ * are not allowed. */
+moe_status_t moe_block_join(const moe_join_config_t* cfg, const void* resid, const void* branch,
+                            const void* post_w, const void* gate, const void* pre_w,
+                            void* resid_out, void* normed, void* stream);
+
 /* Reset the device status word (first 256 bytes of ws) to "no error", enqueued on stream. */
 moe_status_t moe_reset_device_status(void* ws, size_t ws_bytes, void* stream);
 

@@ -30,13 +30,16 @@ MOE_FLAG_DECODE_FUSED = 0x200
 MOE_FLAG_GEMM_PAIR = 0x400
 MOE_FLAG_EXPERT_OUT_BF16 = 0x800
 MOE_FLAG_EXPERT_OUT_F32 = 0x1000
+MOE_FEW_MAX_TOKENS = 16
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_ELEMENT = 0, 1, 2, 3
+MOE_JOIN_GATE_SIGMOID = 0x1
 
 EXPORTED = ("moe_workspace_size", "moe_router", "moe_permute", "moe_experts", "moe_combine",
             "moe_forward", "moe_forward_host_io", "moe_reset_device_status", "moe_device_status",
             "moe_status_string", "moe_launch_count", "moe_reset_launch_count",
             "moe_profile_enable", "moe_profile_read", "moe_permute_noalloc",
             "moe_last_error_string", "moe_dense_mlp_workspace_size", "moe_dense_mlp",
-            "moe_forward_block")
+            "moe_forward_block", "moe_few_workspace_size", "moe_forward_few", "moe_block_join")
 
 
 class MoEError(RuntimeError):
@@ -56,6 +59,16 @@ class moe_config_t(ctypes.Structure):
                 ("w_dtype", ctypes.c_int32), ("quant_block", ctypes.c_int32),
                 ("flags", ctypes.c_uint32), ("gate_scale", ctypes.c_float),
                 ("rms_eps", ctypes.c_float), ("reserved_", ctypes.c_int32)]
+
+
+class moe_join_config_t(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("d", ctypes.c_int32), ("act_dtype", ctypes.c_int32),
+                ("resid_dtype", ctypes.c_int32), ("gate", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("resid_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float), ("rms_eps", ctypes.c_float),
+                ("ld_resid", ctypes.c_int64), ("ld_branch", ctypes.c_int64),
+                ("ld_gate", ctypes.c_int64), ("ld_resid_out", ctypes.c_int64),
+                ("ld_normed", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -90,6 +103,13 @@ def load_library():
             lib.moe_forward_block.restype = S
             lib.moe_forward_block.argtypes = [C, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P,
                                               ctypes.c_size_t, P]
+            lib.moe_few_workspace_size.restype = ctypes.c_size_t
+            lib.moe_few_workspace_size.argtypes = [C]
+            lib.moe_forward_few.restype = S
+            lib.moe_forward_few.argtypes = lib.moe_forward.argtypes
+            lib.moe_block_join.restype = S
+            lib.moe_block_join.argtypes = [ctypes.POINTER(moe_join_config_t), P, P, P, P, P, P, P,
+                                           P]
             lib.moe_forward_host_io.restype = S
             lib.moe_forward_host_io.argtypes = lib.moe_forward.argtypes
             lib.moe_reset_device_status.restype = S
@@ -252,6 +272,73 @@ def moe_forward_block(cfg, x_resid, norm_w, W_r, b, W13, W2, W13_scale, W2_scale
         _dev(W13_scale), _dev(W2_scale), _dev(Ws13), _dev(Ws2), _dev(Ws13_scale), _dev(Ws2_scale),
         _dev(W_down), _dev(W_up), _dev(out), _dev(ws), ws.numel(), _stream(stream)),
         "moe_forward_block")
+
+
+def moe_few_workspace_size(cfg: moe_config_t) -> int:
+    return int(load_library().moe_few_workspace_size(ctypes.byref(cfg)))
+
+
+def alloc_few_workspace(cfg: moe_config_t, device="cuda") -> torch.Tensor:
+    """The workspace of moe_forward_few (at most MOE_FEW_MAX_TOKENS tokens)."""
+    n = moe_few_workspace_size(cfg)
+    if n == 0:
+        raise MoEError(MOE_ERR_INVALID_ARG, "moe_few_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def moe_forward_few(cfg, x, W_r, b, W13, W2, W13_scale, W2_scale, Ws13, Ws2, Ws13_scale,
+                    Ws2_scale, W_down, W_up, out, ws, stream=None):
+    """moe_forward for T <= MOE_FEW_MAX_TOKENS tokens in one kernel launch; ws from
+    alloc_few_workspace."""
+    _check(load_library().moe_forward_few(
+        ctypes.byref(cfg), _dev(x), _dev(W_r), _dev(b), _dev(W13), _dev(W2), _dev(W13_scale),
+        _dev(W2_scale), _dev(Ws13), _dev(Ws2), _dev(Ws13_scale), _dev(Ws2_scale), _dev(W_down),
+        _dev(W_up), _dev(out), _dev(ws), ws.numel(), _stream(stream)), "moe_forward_few")
+
+
+_GATES = {"none": MOE_GATE_NONE, "channel": MOE_GATE_CHANNEL, "token": MOE_GATE_TOKEN,
+          "element": MOE_GATE_ELEMENT}
+
+
+def make_join_config(T: int, d: int, act_dtype: torch.dtype = torch.bfloat16,
+                     resid_dtype: Optional[torch.dtype] = None, gate: str = "none",
+                     gate_sigmoid: bool = False, resid_scale: float = 1.0,
+                     branch_scale: float = 1.0, rms_eps: float = 1e-6, ld_resid: int = 0,
+                     ld_branch: int = 0, ld_gate: int = 0, ld_resid_out: int = 0,
+                     ld_normed: int = 0) -> moe_join_config_t:
+    """gate: "none", "channel" ([d]), "token" ([T]) or "element" ([T][d]); ld_*: row pitches in
+    elements, 0 for d."""
+    return moe_join_config_t(int(T), int(d), _dt(act_dtype), _dt(resid_dtype or act_dtype),
+                             _GATES[gate], MOE_JOIN_GATE_SIGMOID if gate_sigmoid else 0,
+                             float(resid_scale), float(branch_scale), float(rms_eps),
+                             int(ld_resid), int(ld_branch), int(ld_gate), int(ld_resid_out),
+                             int(ld_normed))
+
+
+def _pitched(t, T: int, d: int, ld: int, name: str) -> Optional[int]:
+    """Address of a [T][d] tensor whose rows lie `ld` (0: d) elements apart."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if tuple(t.shape) != (T, d):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, the configuration says {(T, d)}")
+    if (d > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) != (ld or d)):
+        raise ValueError(f"{name}: strides {t.stride()} do not match the row pitch {ld or d}")
+    return t.data_ptr()
+
+
+def moe_block_join(cfg: moe_join_config_t, resid, branch, post_w, gate, pre_w, resid_out, normed,
+                   stream=None):
+    """r' = resid_scale resid + branch_scale g RMSNorm(branch) post_w; normed = RMSNorm(r') pre_w."""
+    T, d = cfg.T, cfg.d
+    g = (_pitched(gate, T, d, cfg.ld_gate, "gate") if cfg.gate == MOE_GATE_ELEMENT
+         else _dev(gate))
+    _check(load_library().moe_block_join(
+        ctypes.byref(cfg), _pitched(resid, T, d, cfg.ld_resid, "resid"),
+        _pitched(branch, T, d, cfg.ld_branch, "branch"), _dev(post_w), g, _dev(pre_w),
+        _pitched(resid_out, T, d, cfg.ld_resid_out, "resid_out"),
+        _pitched(normed, T, d, cfg.ld_normed, "normed"), _stream(stream)), "moe_block_join")
 
 
 def moe_forward_host_io(cfg, x_host, W_r, b, W13, W2, W13_scale, W2_scale, Ws13, Ws2,

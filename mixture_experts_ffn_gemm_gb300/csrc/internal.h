@@ -253,6 +253,9 @@ cudaError_t launch_latent_combine(const void* y_perm, const int32_t* perm_dst,
                                   int norm, float eps, void* u_hat, int num_sms,
                                   cudaStream_t st);
 
+// SMs of the current device (cached per device).
+int num_sms();
+
 // A failed CUDA call as a status: MOE_OK for cudaSuccess, else MOE_ERR_CUDA with the error's name
 // and text kept for moe_last_error_string() (per host thread).
 moe_status_t status_from_cuda(cudaError_t e);

@@ -64,7 +64,7 @@ LaunchScope::~LaunchScope() {
   }
 }
 
-static int num_sms() {
+int num_sms() {
   static int cache[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
