@@ -3,7 +3,8 @@
 //
 //   v = y w_post / sqrt(mean(y^2) + eps) ;  r' = a r + b g v ;  n = r' w_pre / sqrt(mean(r'^2) + eps)
 //
-// One CTA per row (grid-stride); the row's r' stays in shared memory between the two norms.
+// Bound by memory: resid, branch (and an element gate) are read once and resid_out and normed written
+// once, the row waiting in registers between the two norms.
 #include "common.cuh"
 #include "internal.h"
 
@@ -30,71 +31,276 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
-// Sum over the CTA, the same value on every thread; red holds one float per warp.
-__device__ __forceinline__ float block_sum(float v, float* red) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  __syncthreads();  // red of the previous sum has been read
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float s = 0.0f;
-  for (int i = 0; i < (int)(blockDim.x >> 5); ++i) s += red[i];
-  return s;
+// Streamed operands: read once, so they leave L1 to the per-channel vectors that every row reads.
+__device__ __forceinline__ uint4 ld_stream16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
 }
 
-template <typename TA, typename TR>
-__global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
-  extern __shared__ float row[];
-  __shared__ float red[32];
-  const TA* pw = static_cast<const TA*>(p.post_w);
-  const TA* qw = static_cast<const TA*>(p.pre_w);
-  const TA* gp = static_cast<const TA*>(p.g);
-  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-    const TA* y = static_cast<const TA*>(p.branch) + t * p.ld_y;
-    const TR* r = static_cast<const TR*>(p.resid) + t * p.ld_r;
-    float inv = 1.0f;
-    if (pw) {
-      float ss = 0.0f;
-      for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
-        const float v = to_f32<TA>(y[c]);
-        ss = fmaf(v, v, ss);
-      }
-      inv = 1.0f / sqrtf(block_sum(ss, red) / (float)p.d + p.eps);
+// V consecutive elements as they are stored: 16-byte words for V = 8, one element for V = 1.
+template <typename T, int V>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16, 8> {
+  uint4 q;
+  __device__ __forceinline__ void stream(const __nv_bfloat16* p) { q = ld_stream16(p); }
+  __device__ __forceinline__ void cached(const __nv_bfloat16* p) {
+    q = __ldg(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-    float ss = 0.0f;
-    for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
-      float v = to_f32<TA>(y[c]);
-      if (pw) v = v * inv * to_f32<TA>(pw[c]);
-      if (p.gate != MOE_GATE_NONE) {
-        float g = to_f32<TA>(gp[p.gate == MOE_GATE_CHANNEL ? c
-                                : p.gate == MOE_GATE_TOKEN ? t : t * p.ld_g + c]);
-        if (p.sigmoid) g = 1.0f / (1.0f + expf(-g));
-        v *= g;
-      }
-      const float s = p.a * to_f32<TR>(r[c]) + p.b * v;
-      row[c] = s;
-      ss = fmaf(s, s, ss);
+  }
+};
+template <>
+struct Raw<float, 8> {
+  uint4 q[2];
+  __device__ __forceinline__ void stream(const float* p) {
+    q[0] = ld_stream16(p);
+    q[1] = ld_stream16(p + 4);
+  }
+  __device__ __forceinline__ void cached(const float* p) {
+    q[0] = __ldg(reinterpret_cast<const uint4*>(p));
+    q[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[4 * i] = __uint_as_float(q[i].x);
+      v[4 * i + 1] = __uint_as_float(q[i].y);
+      v[4 * i + 2] = __uint_as_float(q[i].z);
+      v[4 * i + 3] = __uint_as_float(q[i].w);
     }
-    float ninv = 0.0f;
-    if (p.normed) ninv = 1.0f / sqrtf(block_sum(ss, red) / (float)p.d + p.eps);
-    for (int c = threadIdx.x; c < p.d; c += blockDim.x) {  // each thread reads back its own columns
-      const float s = row[c];
-      static_cast<TR*>(p.resid_out)[t * p.ld_ro + c] = from_f32<TR>(s);
-      if (p.normed)
-        static_cast<TA*>(p.normed)[t * p.ld_n + c] = from_f32<TA>(s * ninv * to_f32<TA>(qw[c]));
-    }
+  }
+};
+template <typename T>
+struct Raw<T, 1> {
+  T q;
+  __device__ __forceinline__ void stream(const T* p) { q = *p; }
+  __device__ __forceinline__ void cached(const T* p) { q = __ldg(p); }
+  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = to_f32<T>(q); }
+};
+template <typename T>
+__device__ __forceinline__ void put(T* p, const float (&v)[8]) { store8(p, v); }
+template <typename T>
+__device__ __forceinline__ void put(T* p, const float (&v)[1]) { *p = from_f32<T>(v[0]); }
+
+// Sum over the `lanes` threads of a row: a power of two of one warp's lanes, or the whole CTA
+// through red (one float per warp; the caller uses another array for its next sum, so one barrier
+// is enough).  The same order, hence the same bits, on every thread.
+template <bool BLOCK>
+__device__ __forceinline__ float row_sum(float v, int lanes, float* red) {
+  if constexpr (!BLOCK) {
+    for (int off = lanes >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+  } else {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    float s = lane < (int)(blockDim.x >> 5) ? red[lane] : 0.0f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    return s;
   }
 }
 
+// A row on `lanes` threads, NC chunks of V columns each, held in registers from the only read to
+// the only write: chunk i of thread j covers columns (j + i * lanes) * V ...  BLOCK: the row takes
+// the whole CTA; else lanes (a power of two <= 32) of a warp, several rows to a CTA.
+template <typename TA, typename TR, int V, int NC, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? 1024 : 256) join_kernel(const JoinParams p, int lanes) {
+  __shared__ float red[2][32];
+  const int j = BLOCK ? (int)threadIdx.x : (int)threadIdx.x & (lanes - 1);
+  const int64_t t = BLOCK ? (int64_t)blockIdx.x
+                          : blockIdx.x * (int64_t)(256 / lanes) + threadIdx.x / lanes;
+  const bool live = t < p.T;  // BLOCK: always; idle threads still take part in the shuffles
+  const TA* pw = static_cast<const TA*>(p.post_w);
+  const TA* qw = static_cast<const TA*>(p.pre_w);
+  const TA* gp = static_cast<const TA*>(p.g);
+  const TA* y = static_cast<const TA*>(p.branch) + t * p.ld_y;
+  const TR* r = static_cast<const TR*>(p.resid) + t * p.ld_r;
+  Raw<TA, V> yr[NC], gr[NC];
+  Raw<TR, V> rr[NC];
+  bool on[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = (j + i * lanes) * V;
+    on[i] = live && c < p.d;
+    if (on[i]) {
+      yr[i].stream(y + c);
+      rr[i].stream(r + c);
+      if (p.gate == MOE_GATE_ELEMENT) gr[i].stream(gp + t * p.ld_g + c);
+    }
+  }
+  float tg = 1.0f;
+  if (p.gate == MOE_GATE_TOKEN && live) {
+    tg = to_f32<TA>(gp[t]);
+    if (p.sigmoid) tg = 1.0f / (1.0f + expf(-tg));
+  }
+  float inv = 1.0f;
+  if (pw) {
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (on[i]) {
+        float v[V];
+        yr[i].get(v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) ss = fmaf(v[e], v[e], ss);
+      }
+    inv = 1.0f / sqrtf(row_sum<BLOCK>(ss, lanes, red[0]) / (float)p.d + p.eps);
+  }
+  float s[NC][V];
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    if (!on[i]) continue;
+    const int c = (j + i * lanes) * V;
+    float rv[V];
+    yr[i].get(s[i]);
+    rr[i].get(rv);
+    if (pw) {
+      Raw<TA, V> wr;
+      float w[V];
+      wr.cached(pw + c);
+      wr.get(w);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[i][e] = s[i][e] * inv * w[e];
+    }
+    if (p.gate == MOE_GATE_CHANNEL || p.gate == MOE_GATE_ELEMENT) {
+      float g[V];
+      if (p.gate == MOE_GATE_CHANNEL) gr[i].cached(gp + c);
+      gr[i].get(g);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (p.sigmoid) g[e] = 1.0f / (1.0f + expf(-g[e]));
+        s[i][e] *= g[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      s[i][e] = p.a * rv[e] + p.b * (s[i][e] * tg);
+      ss = fmaf(s[i][e], s[i][e], ss);
+    }
+    if (live) put(static_cast<TR*>(p.resid_out) + t * p.ld_ro + c, s[i]);
+  }
+  if (!p.normed) return;
+  const float ninv = 1.0f / sqrtf(row_sum<BLOCK>(ss, lanes, red[1]) / (float)p.d + p.eps);
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    if (!on[i]) continue;
+    const int c = (j + i * lanes) * V;
+    Raw<TA, V> wr;
+    float w[V];
+    wr.cached(qw + c);
+    wr.get(w);
+#pragma unroll
+    for (int e = 0; e < V; ++e) s[i][e] = s[i][e] * ninv * w[e];
+    put(static_cast<TA*>(p.normed) + t * p.ld_n + c, s[i]);
+  }
+}
+
+// Rows too wide for registers without wide loads: r' waits in shared memory between the norms, each
+// thread reading back its own columns.
 template <typename TA, typename TR>
-cudaError_t launch(const JoinParams& p, cudaStream_t st) {
+__global__ void __launch_bounds__(1024) join_wide_kernel(const JoinParams p) {
+  extern __shared__ float row[];
+  __shared__ float red[2][32];
+  const TA* pw = static_cast<const TA*>(p.post_w);
+  const TA* qw = static_cast<const TA*>(p.pre_w);
+  const TA* gp = static_cast<const TA*>(p.g);
+  const int64_t t = blockIdx.x;
+  const TA* y = static_cast<const TA*>(p.branch) + t * p.ld_y;
+  const TR* r = static_cast<const TR*>(p.resid) + t * p.ld_r;
+  float inv = 1.0f;
+  if (pw) {
+    float ss = 0.0f;
+    for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
+      const float v = to_f32<TA>(y[c]);
+      ss = fmaf(v, v, ss);
+    }
+    inv = 1.0f / sqrtf(row_sum<true>(ss, 0, red[0]) / (float)p.d + p.eps);
+  }
+  float ss = 0.0f;
+  for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
+    float v = to_f32<TA>(y[c]);
+    if (pw) v = v * inv * to_f32<TA>(pw[c]);
+    if (p.gate != MOE_GATE_NONE) {
+      float g = to_f32<TA>(gp[p.gate == MOE_GATE_CHANNEL ? c
+                              : p.gate == MOE_GATE_TOKEN ? t : t * p.ld_g + c]);
+      if (p.sigmoid) g = 1.0f / (1.0f + expf(-g));
+      v *= g;
+    }
+    const float s = p.a * to_f32<TR>(r[c]) + p.b * v;
+    row[c] = s;
+    ss = fmaf(s, s, ss);
+  }
+  float ninv = 0.0f;
+  if (p.normed) ninv = 1.0f / sqrtf(row_sum<true>(ss, 0, red[1]) / (float)p.d + p.eps);
+  for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
+    const float s = row[c];
+    static_cast<TR*>(p.resid_out)[t * p.ld_ro + c] = from_f32<TR>(s);
+    if (p.normed)
+      static_cast<TA*>(p.normed)[t * p.ld_n + c] = from_f32<TA>(s * ninv * to_f32<TA>(qw[c]));
+  }
+}
+
+template <typename TA, typename TR, int V, int NC>
+void start_rows(const JoinParams& p, bool block, int lanes, cudaStream_t st) {
+  if (block)
+    join_kernel<TA, TR, V, NC, true><<<(unsigned)p.T, lanes, 0, st>>>(p, lanes);
+  else
+    join_kernel<TA, TR, V, NC, false>
+        <<<(unsigned)((p.T + 256 / lanes - 1) / (256 / lanes)), 256, 0, st>>>(p, lanes);
+}
+
+template <typename TA, typename TR, int V>
+cudaError_t launch_rows(const JoinParams& p, int chunks, cudaStream_t st) {
+  // Chunks per thread: four keep 4 x 16 bytes of each operand in flight per thread, so few threads
+  // hold a row and several rows share an SM; with fewer rows than SMs that only lengthens the one
+  // row's chain, and the row takes as many threads as it has chunks.
+  const bool few = p.T <= num_sms();
+  int nc = few ? 1 : 4;
+  bool block;
+  int lanes;
+  if (chunks <= 32 * nc) {
+    block = false;
+    lanes = 1;
+    while (lanes * nc < chunks) lanes *= 2;
+  } else {
+    block = true;
+    if (chunks > 1024 * nc) nc = 4;
+    if (chunks > 1024 * nc) nc = 8;  // V = 1 only
+    lanes = ((chunks + nc - 1) / nc + 31) / 32 * 32;
+  }
+  if (nc == 1)
+    start_rows<TA, TR, V, 1>(p, block, lanes, st);
+  else if (V == 8 || nc == 4)
+    start_rows<TA, TR, V, 4>(p, block, lanes, st);
+  else
+    start_rows<TA, TR, 1, 8>(p, block, lanes, st);
+  return cudaGetLastError();
+}
+
+template <typename TA, typename TR>
+cudaError_t launch(const JoinParams& p, bool wide_loads, cudaStream_t st) {
+  LaunchScope ls("block_join", st);
+  if (wide_loads) return launch_rows<TA, TR, 8>(p, p.d / 8, st);  // d <= 32768: 4096 chunks
+  if (p.d <= 8192) return launch_rows<TA, TR, 1>(p, p.d, st);
   const size_t smem = (size_t)p.d * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(join_kernel<TA, TR>,
+  cudaError_t e = cudaFuncSetAttribute(join_wide_kernel<TA, TR>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int64_t cap = (int64_t)num_sms() * 8;
-  LaunchScope ls("block_join", st);
-  join_kernel<TA, TR><<<(unsigned)(p.T < cap ? p.T : cap), 256, smem, st>>>(p);
+  join_wide_kernel<TA, TR><<<(unsigned)p.T, 1024, smem, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -114,7 +320,7 @@ extern "C" moe_status_t moe_block_join(const moe_join_config_t* cfg, const void*
   if (cfg->resid_dtype != MOE_F32 && cfg->resid_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
   if (cfg->gate < MOE_GATE_NONE || cfg->gate > MOE_GATE_ELEMENT) return MOE_ERR_INVALID_ARG;
   if (cfg->flags & ~MOE_JOIN_GATE_SIGMOID) return MOE_ERR_INVALID_ARG;
-  if (cfg->d > MOE_JOIN_MAX_D || cfg->T > ((int64_t)1 << 40)) return MOE_ERR_UNSUPPORTED;
+  if (cfg->d > MOE_JOIN_MAX_D || cfg->T > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (cfg->act_dtype == MOE_F32 && cfg->resid_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
   const int64_t d = cfg->d, max_ld = (int64_t)1 << 20;
   const int64_t lds[] = {cfg->ld_resid, cfg->ld_branch, cfg->ld_gate, cfg->ld_resid_out,
@@ -151,14 +357,22 @@ extern "C" moe_status_t moe_block_join(const moe_join_config_t* cfg, const void*
   p.pre_w = pre_w;
   p.resid_out = resid_out;
   p.normed = normed;
+  // 8-column chunks: whole chunks only, every row and operand on 16 bytes (ld in elements of 2 or 4)
+  bool wide = d % 8 == 0;
+  for (const void* q : {resid, branch, post_w, cfg->gate == MOE_GATE_TOKEN ? nullptr : gate, pre_w,
+                        (const void*)resid_out, (const void*)normed})
+    wide = wide && aligned_to(q, 16);
+  const size_t ga = cfg->gate == MOE_GATE_ELEMENT ? (size_t)p.ld_g * ab : 0;
+  wide = wide && (p.ld_r * rb) % 16 == 0 && (p.ld_ro * rb) % 16 == 0 && (p.ld_y * ab) % 16 == 0 &&
+         (p.ld_n * ab) % 16 == 0 && ga % 16 == 0;
   (void)cudaGetLastError();  // start from a clean launch-error state
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (cfg->act_dtype == MOE_F32)
-    e = launch<float, float>(p, st);
+    e = launch<float, float>(p, wide, st);
   else if (cfg->resid_dtype == MOE_F32)
-    e = launch<__nv_bfloat16, float>(p, st);
+    e = launch<__nv_bfloat16, float>(p, wide, st);
   else
-    e = launch<__nv_bfloat16, __nv_bfloat16>(p, st);
+    e = launch<__nv_bfloat16, __nv_bfloat16>(p, wide, st);
   return status_from_cuda(e);
 }
