@@ -4,14 +4,15 @@
 //   E_i(x) = (SiLU(x W1_i) * (x W3_i)) W2_i ;  y = sum_sel G_i E_i(x) + E_shared(x)
 //   latent: experts on x W_down; y = RMSNorm(sum_sel G_i E_i) W_up + E_shared(x)
 //
-// Steps, with a grid barrier between them (each reads what every CTA of the step before wrote):
+// Bound by memory: with T tokens a weight is used at most T times, so the layer is one pass over
+// the selected experts' weights.  Two kernels, both one CTA per SM with equal calls giving equal
+// bits: few_stream_kernel (bf16 activations) keeps that pass going through all steps; few_kernel
+// (fp32, small models) is plain.  Steps, each needing what every CTA wrote in the one before:
 //   A  router logits; W_down rows; the shared expert's W1|W3 rows
 //   B  every CTA repeats the selection, then W1|W3 rows of the distinct selected experts, each
 //      read once for all of its tokens; h = G SiLU(g) u per (expert, token) row
 //   C  W2: each output feature's sum over every selected expert (and the shared one)
-//   D  (latent) the norm of the latent sum, W_up rows and the shared expert's W2 rows
-// One warp computes one feature: lanes stride over its weight row(s), fp32 sums, a shuffle at the
-// end, so equal calls give equal bits.
+//   D  (latent) W_up rows and the shared expert's W2 rows
 #include "common.cuh"
 #include "internal.h"
 
@@ -37,14 +38,20 @@ struct FewParams {
   void* out;
   uint32_t* err;
   uint32_t* bar;   // one arrival counter per barrier, zeroed before the launch
-  float* logits;   // [T][E]
+  float* logits;   // [parts][T][E]: sums over consecutive ranges of part_cols input channels
+  int parts, part_cols;
+  // fp32 kernel
   float* x_lat;    // [T][L]
   float* h;        // [T * k + T][I]: routed rows expert by expert, then the shared rows
   float* y_lat;    // [T][L]
+  // bf16 kernel: the same as two bf16 planes, value = plane 0 + plane 1 to 16 bits or more
+  __nv_bfloat16 *x_lat2, *h2, *y_lat2;
+  float* ssq;      // [CTAs][16] sums of squares of each CTA's latent features
 };
 
 struct Selection {
-  uint16_t mask[kMaxE + 1];      // tokens of each expert
+  uint32_t mask[kMaxE + 1];      // tokens of each expert
+  int16_t slot[kMaxE + 1];       // its place in active
   int16_t active[kMaxPairs];     // distinct selected experts, ascending
   int16_t row0[kMaxPairs + 1];   // first h row of each
   int16_t pair_e[kMaxPairs];
@@ -53,6 +60,26 @@ struct Selection {
   int n_active;
 };
 
+// Waits (bounded) until `counter` reaches `want`; one thread.
+__device__ __forceinline__ bool counter_reached(const uint32_t* counter, uint32_t want) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+  return v >= want;
+}
+__device__ bool counter_wait(const uint32_t* counter, uint32_t want, volatile int* abort,
+                             uint32_t* err) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!counter_reached(counter, want)) {
+    if (abort && *abort) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      if (abort) *abort = 1;
+      raise_flag(err, kErrTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
 // Arrive and wait until every CTA of the (cooperative) grid has; false once the wait expires.
 __device__ bool grid_barrier(uint32_t* counter, uint32_t* err) {
   __shared__ int ok;
@@ -60,18 +87,7 @@ __device__ bool grid_barrier(uint32_t* counter, uint32_t* err) {
   if (threadIdx.x == 0) {
     __threadfence();
     atomicAdd(counter, 1u);
-    const uint64_t t0 = globaltimer_ns();
-    ok = 1;
-    while (true) {
-      uint32_t v;
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
-      if (v >= gridDim.x) break;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
-        raise_flag(err, kErrTimeout);
-        ok = 0;
-        break;
-      }
-    }
+    ok = counter_wait(counter, gridDim.x, nullptr, err);
     __threadfence();
   }
   __syncthreads();
@@ -80,45 +96,60 @@ __device__ bool grid_barrier(uint32_t* counter, uint32_t* err) {
   return r;
 }
 
-// One warp selects the experts of token t: k rounds of the largest key, ties to the lower index;
-// NaN keys count as -infinity.
+// Order-preserving map of a key to an unsigned integer >= 1; NaN keys count as -infinity.
+__device__ __forceinline__ uint32_t key_bits(float v) {
+  if (isnan(v)) v = -INFINITY;
+  if (v == 0.0f) v = 0.0f;  // -0 ties with +0
+  const uint32_t u = __float_as_uint(v);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// One warp selects the experts of token t: k rounds of the largest key, ties to the lower index.
+// Lane l holds experts l, l + 32, ... in registers (N >= ceil(E / 32) of them).
+template <int N>
 __device__ void select_token(const FewParams& p, int t, Selection& sel) {
   const int lane = threadIdx.x & 31;
-  uint32_t taken = 0;
+  uint32_t key[N];
+  float z[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int e = lane + 32 * j;
+    z[j] = 0.0f;
+    if (e < p.E)
+      for (int q = 0; q < p.parts; ++q)
+        z[j] += __ldcg(p.logits + ((int64_t)q * p.T + t) * p.E + e);
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int e = lane + 32 * j;
+    z[j] = 1.0f / (1.0f + expf(-z[j]));
+    key[j] = e < p.E ? key_bits(z[j] + p.b[e]) : 0u;
+  }
   float my_s = 0.0f, den = 0.0f;
   int my_e = 0;
   for (int slot = 0; slot < p.k; ++slot) {
-    float bk = -INFINITY, bs = 0.0f;
-    int be = 0x7fffffff;
-    for (int j = 0; lane + 32 * j < p.E; ++j) {
-      const int e = lane + 32 * j;
-      if ((taken >> j) & 1u) continue;
-      const float s = 1.0f / (1.0f + expf(-__ldcg(p.logits + (int64_t)t * p.E + e)));
-      float key = s + p.b[e];
-      if (isnan(key)) key = -INFINITY;
-      if (key > bk || (key == bk && e < be)) {
-        bk = key;
-        be = e;
-        bs = s;
-      }
-    }
+    uint32_t best = 0;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const float ok = __shfl_xor_sync(0xffffffffu, bk, off);
-      const int oe = __shfl_xor_sync(0xffffffffu, be, off);
-      const float os = __shfl_xor_sync(0xffffffffu, bs, off);
-      if (ok > bk || (ok == bk && oe < be)) {
-        bk = ok;
-        be = oe;
-        bs = os;
+    for (int j = 0; j < N; ++j) best = max(best, key[j]);
+    best = __reduce_max_sync(0xffffffffu, best);
+    uint32_t e = 0xffffffffu;
+#pragma unroll
+    for (int j = N - 1; j >= 0; --j)
+      if (key[j] == best) e = lane + 32 * j;
+    e = __reduce_min_sync(0xffffffffu, e);  // best >= 1: always an expert not taken yet
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if ((int)e == lane + 32 * j) {
+        s = z[j];
+        key[j] = 0;
       }
-    }
+    s = __shfl_sync(0xffffffffu, s, e & 31);
     if (lane == slot) {
-      my_e = be;
-      my_s = bs;
+      my_e = (int)e;
+      my_s = s;
     }
-    den += bs;
-    if ((be & 31) == lane) taken |= 1u << (be >> 5);
+    den += s;
   }
   if (lane < p.k) {
     sel.pair_e[t * p.k + lane] = (int16_t)my_e;
@@ -126,86 +157,54 @@ __device__ void select_token(const FewParams& p, int t, Selection& sel) {
   }
 }
 
-// The CTA's copy of the selection: per-expert token masks, the distinct experts in index order,
-// the first h row of each and each row's gate.
-__device__ void build_selection(const FewParams& p, Selection& sel) {
-  const int warp = threadIdx.x >> 5;
-  for (int t = warp; t < p.T; t += kWarps) select_token(p, t, sel);
-  for (int e = threadIdx.x; e < p.E; e += kThreads) sel.mask[e] = 0;
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kThreads) {
-    uint32_t m = 0;
-    for (int i = 0; i < p.T * p.k; ++i)
-      if (sel.pair_e[i] == e) m |= 1u << (i / p.k);
-    sel.mask[e] = (uint16_t)m;
+// The CTA's copy of the selection, by n_warps warps of which this thread is number tid (barrier
+// `bar` is theirs): per-expert token masks, the distinct experts in index order, the first h row of
+// each and each row's gate.
+__device__ void build_selection(const FewParams& p, Selection& sel, int tid, int n_warps, int bar) {
+  const int n = n_warps * 32, lane = tid & 31;
+  for (int e = tid; e < p.E; e += n) sel.mask[e] = 0;
+  for (int t = tid >> 5; t < p.T; t += n_warps) {
+    if (p.E <= 64)
+      select_token<2>(p, t, sel);
+    else if (p.E <= 384)
+      select_token<12>(p, t, sel);
+    else
+      select_token<32>(p, t, sel);
   }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int n = 0, row = 0;
-    for (int e = 0; e < p.E; ++e) {
-      if (!sel.mask[e]) continue;
-      sel.active[n] = (int16_t)e;
-      sel.row0[n++] = (int16_t)row;
-      row += __popc(sel.mask[e]);
+  named_barrier(bar, n);
+  for (int i = tid; i < p.T * p.k; i += n) atomicOr(&sel.mask[sel.pair_e[i]], 1u << (i / p.k));
+  named_barrier(bar, n);
+  if (tid < 32) {  // compact: 32 experts at a time
+    int na = 0, row = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const uint32_t m = e0 + lane < p.E ? sel.mask[e0 + lane] : 0u;
+      const uint32_t act = __ballot_sync(0xffffffffu, m != 0);
+      int incl = __popc(m);  // rows up to and including this expert
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += v;
+      }
+      if (m) {
+        const int a = na + __popc(act & ((1u << lane) - 1u));
+        sel.active[a] = (int16_t)(e0 + lane);
+        sel.row0[a] = (int16_t)(row + incl - __popc(m));
+        sel.slot[e0 + lane] = (int16_t)a;
+      }
+      na += __popc(act);
+      row += __shfl_sync(0xffffffffu, incl, 31);
     }
-    sel.row0[n] = (int16_t)row;
-    sel.n_active = n;
+    if (lane == 0) {
+      sel.row0[na] = (int16_t)row;
+      sel.n_active = na;
+    }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.T * p.k; i += kThreads) {
+  named_barrier(bar, n);
+  for (int i = tid; i < p.T * p.k; i += n) {
     const int e = sel.pair_e[i], t = i / p.k;
-    int a = 0;
-    while (sel.active[a] != e) ++a;
-    sel.row_gate[sel.row0[a] + __popc(sel.mask[e] & ((1u << t) - 1u))] = sel.pair_g[i];
+    sel.row_gate[sel.row0[sel.slot[e]] + __popc(sel.mask[e] & ((1u << t) - 1u))] = sel.pair_g[i];
   }
-  __syncthreads();
-}
-
-__device__ __forceinline__ void decode_bf16x8(uint4 raw, float (&v)[8]) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
-// e4m3 to fp32: the bits moved to fp32's exponent and mantissa give value * 2^-120, subnormals
-// included (the product below is exact).
-__device__ __forceinline__ float e4m3_to_f32(uint32_t b) {
-  if ((b & 0x7fu) == 0x7fu) return __uint_as_float(0x7fffffffu);
-  return __uint_as_float(((b & 0x80u) << 24) | ((b & 0x7fu) << 20)) * 0x1p120f;
-}
-
-// 8 consecutive weights (row `row` of matrix `e`, columns c..c+7) of stacked [n][R][K] matrices.
-template <int WD>
-__device__ __forceinline__ void weights8(const void* w, const void* s, int64_t e, int R, int K,
-                                         int row, int c, float (&v)[8]) {
-  const int64_t at = (e * R + row) * K + c;
-  if constexpr (WD == MOE_F32) {
-    load8(static_cast<const float*>(w) + at, v);
-  } else if constexpr (WD == MOE_BF16) {
-    load8(static_cast<const __nv_bfloat16*>(w) + at, v);
-  } else if constexpr (WD == MOE_FP8_E4M3) {
-    const uint2 raw = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(w) + at));
-    const float sc = __ldg(static_cast<const float*>(s) +
-                           (e * (R / 128) + row / 128) * (K / 128) + c / 128);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = e4m3_to_f32(raw.x >> (8 * i) & 0xffu) * sc;
-      v[4 + i] = e4m3_to_f32(raw.y >> (8 * i) & 0xffu) * sc;
-    }
-  } else {
-    const uint32_t raw =
-        __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(w) + at / 2));
-    const float sc = __bfloat162float(
-        static_cast<const __nv_bfloat16*>(s)[(e * (K / 32) + c / 32) * (int64_t)R + row]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int code = (int)(raw >> (4 * (i / 2 + 4 * (i % 2))) & 15u) - 8;
-      v[i] = __bfloat162float(__float2bfloat16_rn((float)code * sc));
-    }
-  }
+  named_barrier(bar, n);
 }
 
 // 8 values that an earlier step of this kernel wrote (past L1).
@@ -223,12 +222,12 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // acc[n] += dot(weight row, activation row n) over this lane's columns; act(n, c, v) loads 8.
-template <int WD, typename Act>
-__device__ __forceinline__ void dot_rows(float (&acc)[kMaxT], int n, const void* w, const void* s,
-                                         int64_t e, int R, int K, int row, Act act) {
+template <typename Act>
+__device__ __forceinline__ void dot_rows(float (&acc)[kMaxT], int n, const float* w, int K,
+                                         Act act) {
   for (int c = (threadIdx.x & 31) * 8; c < K; c += 256) {
     float v[8];
-    weights8<WD>(w, s, e, R, K, row, c, v);
+    load8(w + c, v);
 #pragma unroll
     for (int i = 0; i < kMaxT; ++i) {
       if (i < n) {
@@ -246,30 +245,27 @@ __device__ __forceinline__ void zero(float (&acc)[kMaxT]) {
   for (int i = 0; i < kMaxT; ++i) acc[i] = 0.0f;
 }
 
-template <typename TA>
-__device__ __forceinline__ void store_act(void* out, int64_t i, float v);
-template <>
-__device__ __forceinline__ void store_act<float>(void* out, int64_t i, float v) {
-  static_cast<float*>(out)[i] = v;
-}
-template <>
-__device__ __forceinline__ void store_act<__nv_bfloat16>(void* out, int64_t i, float v) {
-  static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
-}
-
 // The n-th token of a mask.
-__device__ __forceinline__ int nth_token(uint32_t mask, int n) { return __fns(mask, 0, n + 1); }
+__device__ __forceinline__ int nth_token(uint32_t mask, int n) {
+  for (; n > 0; --n) mask &= mask - 1u;
+  return __ffs(mask) - 1;
+}
 
-template <typename TA, int WD>
+// The fp32 layer: a warp computes one feature, lanes stride over its weight row(s), a shuffle at the
+// end.  For small models, whose weights sit in L2: bound by the steps' latency.
 __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
   __shared__ Selection sel;
   __shared__ float inv_rms[kMaxT];
-  constexpr int AD = WD == MOE_F32 ? MOE_F32 : MOE_BF16;  // W_down, W_up: the activations' type
   const int lane = threadIdx.x & 31;
   const int gw = blockIdx.x * kWarps + (threadIdx.x >> 5), nw = gridDim.x * kWarps;
   const int de = p.L ? p.L : p.d;
   const int P = p.T * p.k;
-  const TA* x = static_cast<const TA*>(p.x);
+  const float* x = static_cast<const float*>(p.x);
+  const float *W13 = static_cast<const float*>(p.W13), *W2 = static_cast<const float*>(p.W2),
+              *Ws13 = static_cast<const float*>(p.Ws13), *Ws2 = static_cast<const float*>(p.Ws2),
+              *W_down = static_cast<const float*>(p.W_down),
+              *W_up = static_cast<const float*>(p.W_up);
+  float* out = static_cast<float*>(p.out);
   float acc[kMaxT], acu[kMaxT];
 
   // A
@@ -277,28 +273,25 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
   auto act_x = [&](int n, int c, float(&a)[8]) { load8(x + (int64_t)n * p.d + c, a); };
   for (int u = gw; u < nA; u += nw) {
     zero(acc);
-    if (u < p.E) {
-      dot_rows<MOE_F32>(acc, p.T, p.W_r, nullptr, 0, p.E, p.d, u, act_x);
+    if (u < p.E + p.L) {
+      const float* w = u < p.E ? p.W_r + (int64_t)u * p.d : W_down + (int64_t)(u - p.E) * p.d;
+      dot_rows(acc, p.T, w, p.d, act_x);
 #pragma unroll
       for (int n = 0; n < kMaxT; ++n)
         if (n < p.T) {
           const float z = warp_sum(acc[n]);
-          if (lane == 0) p.logits[(int64_t)n * p.E + u] = z;
-        }
-    } else if (u < p.E + p.L) {
-      const int f = u - p.E;
-      dot_rows<AD>(acc, p.T, p.W_down, nullptr, 0, p.L, p.d, f, act_x);
-#pragma unroll
-      for (int n = 0; n < kMaxT; ++n)
-        if (n < p.T) {
-          const float v = warp_sum(acc[n]);
-          if (lane == 0) p.x_lat[(int64_t)n * p.L + f] = v;
+          if (lane == 0) {
+            if (u < p.E)
+              p.logits[(int64_t)n * p.E + u] = z;
+            else
+              p.x_lat[(int64_t)n * p.L + u - p.E] = z;
+          }
         }
     } else {
       const int f = u - p.E - p.L;
       zero(acu);
-      dot_rows<WD>(acc, p.T, p.Ws13, p.ss13, 0, 2 * p.I, p.d, f, act_x);
-      dot_rows<WD>(acu, p.T, p.Ws13, p.ss13, 0, 2 * p.I, p.d, p.I + f, act_x);
+      dot_rows(acc, p.T, Ws13 + (int64_t)f * p.d, p.d, act_x);
+      dot_rows(acu, p.T, Ws13 + (int64_t)(p.I + f) * p.d, p.d, act_x);
 #pragma unroll
       for (int n = 0; n < kMaxT; ++n)
         if (n < p.T) {
@@ -310,10 +303,11 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
   if (!grid_barrier(p.bar, p.err)) return;
 
   // B
-  build_selection(p, sel);
+  build_selection(p, sel, threadIdx.x, kWarps, 1);
   for (int64_t u = gw; u < (int64_t)sel.n_active * p.I; u += nw) {
     const int a = (int)(u / p.I), f = (int)(u - (int64_t)a * p.I);
-    const int e = sel.active[a], row0 = sel.row0[a], n_e = sel.row0[a + 1] - row0;
+    const int64_t e = sel.active[a];
+    const int row0 = sel.row0[a], n_e = sel.row0[a + 1] - row0;
     const uint32_t mask = sel.mask[e];
     zero(acc);
     zero(acu);
@@ -324,8 +318,8 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
       else
         load8(x + (int64_t)t * p.d + c, v);
     };
-    dot_rows<WD>(acc, n_e, p.W13, p.s13, e, 2 * p.I, de, f, act);
-    dot_rows<WD>(acu, n_e, p.W13, p.s13, e, 2 * p.I, de, p.I + f, act);
+    dot_rows(acc, n_e, W13 + (e * 2 * p.I + f) * de, de, act);
+    dot_rows(acu, n_e, W13 + (e * 2 * p.I + p.I + f) * de, de, act);
 #pragma unroll
     for (int n = 0; n < kMaxT; ++n)
       if (n < n_e) {
@@ -343,14 +337,15 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
   for (int f = gw; f < de; f += nw) {
     zero(acc);
     for (int a = 0; a < sel.n_active; ++a) {
-      const int e = sel.active[a], row0 = sel.row0[a], n_e = sel.row0[a + 1] - row0;
+      const int64_t e = sel.active[a];
+      const int row0 = sel.row0[a], n_e = sel.row0[a + 1] - row0;
       const uint32_t mask = sel.mask[e];
       float part[kMaxT];
       zero(part);
       auto act = [&](int n, int c, float(&v)[8]) {
         load8_cg(p.h + (int64_t)(row0 + n) * p.I + c, v);
       };
-      dot_rows<WD>(part, n_e, p.W2, p.s2, e, de, p.I, f, act);
+      dot_rows(part, n_e, W2 + (e * de + f) * p.I, p.I, act);
 #pragma unroll
       for (int t = 0; t < kMaxT; ++t) {
         const int n = __popc(mask & ((1u << t) - 1u));
@@ -359,17 +354,12 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
           if ((mask >> t & 1u) && i == n) acc[t] += part[i];
       }
     }
-    if (!p.L && p.n_shared) dot_rows<WD>(acc, p.T, p.Ws2, p.ss2, 0, p.d, p.I, f, act_sh);
+    if (!p.L && p.n_shared) dot_rows(acc, p.T, Ws2 + (int64_t)f * p.I, p.I, act_sh);
 #pragma unroll
     for (int t = 0; t < kMaxT; ++t)
       if (t < p.T) {
         const float v = warp_sum(acc[t]);
-        if (lane == 0) {
-          if (p.L)
-            p.y_lat[(int64_t)t * p.L + f] = v;
-          else
-            store_act<TA>(p.out, (int64_t)t * p.d + f, v);
-        }
+        if (lane == 0) (p.L ? p.y_lat : out)[(int64_t)t * de + f] = v;
       }
   }
   if (!p.L) return;
@@ -393,20 +383,764 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
   };
   for (int f = gw; f < p.d; f += nw) {
     zero(acc);
-    dot_rows<AD>(acc, p.T, p.W_up, nullptr, 0, p.d, p.L, f, act_u);
-    if (p.n_shared) dot_rows<WD>(acc, p.T, p.Ws2, p.ss2, 0, p.d, p.I, f, act_sh);
+    dot_rows(acc, p.T, W_up + (int64_t)f * p.L, p.L, act_u);
+    if (p.n_shared) dot_rows(acc, p.T, Ws2 + (int64_t)f * p.I, p.I, act_sh);
 #pragma unroll
     for (int t = 0; t < kMaxT; ++t)
       if (t < p.T) {
         const float v = warp_sum(acc[t]);
-        if (lane == 0) store_act<TA>(p.out, (int64_t)t * p.d + f, v);
+        if (lane == 0) out[(int64_t)t * p.d + f] = v;
       }
   }
 }
 
-struct FewLayout {
-  size_t logits, x_lat, h, y_lat, total;
+// ---------------------------------------------------------------------------------------------
+// bf16 activations: one stream of weights through shared memory per SM.
+//
+// A producer warp walks the CTA's share of every step and copies it (bulk asynchronous copies, a row
+// piece each) into a ring of kSlots slots: 16 weight rows times up to a few thousand input channels,
+// and the same channels of the activations they meet.  Sixteen consumer warps split a slot's
+// channels, multiply 16 rows by 8 tokens with mma.sync m16n8k16 and, when a tile of rows is
+// complete, add their partial sums in a fixed order through shared memory.  The products' K index
+// may be permuted as long as both operands agree, so a lane takes 16 consecutive bytes of its row
+// (8 bf16, 16 e4m3 or 32 4-bit weights) and the same channels of its token: shared memory is read
+// in 16-byte words with no transposition.  (tcgen05 would need 16 token rows of shared memory and
+// tensor memory round trips for one or two tokens per expert; nothing here is bound by products.)
+//
+// The stream does not stop at the steps' barriers.  Weights are copied ahead of them and only the
+// activations' copies wait for the barrier (each slot's barrier counts two arrivals, weights and
+// activations); four more warps wait for the router logits and repeat the selection while the
+// shared expert's weights pass by.
+//
+// Values that one step leaves to the next (h, the latent activations) are kept as two bf16 planes,
+// hi = bf16(v) and lo = bf16(v - hi), and multiplied plane by plane into the same fp32 sum: 16 bits
+// or more of each, where one bf16 would add a rounding of 2^-9.
+// ---------------------------------------------------------------------------------------------
+constexpr int kCons = 16;      // consumer warps
+constexpr int kSelWarps = 3;
+constexpr int kFirstCons = 1 + kSelWarps;
+constexpr int kStreamThreads = 32 * (kFirstCons + kCons);
+constexpr int kSlots = 5;
+constexpr int kSlotBytes = 38912;
+
+// Counters of the launch (FewParams::bar): arrivals of CTAs at the end of each part.
+enum : int { kCntRouter = 0, kCntDown = 1, kCntH = 2, kCntLat = 3 };
+constexpr int kNoDep = -1;
+
+template <int WD>
+struct Wt {
+  static constexpr int kBits = WD == MOE_BF16 ? 16 : WD == MOE_FP8_E4M3 ? 8 : 4;
+  static constexpr int kChunk = 128 / kBits;     // channels of a lane's 16 bytes
+  static constexpr int kStep = 4 * kChunk;       // channels of a warp's 16-byte loads
+  static constexpr int kUnit = WD == MOE_BF16 ? 32 : 128;  // channels a warp takes at a time
+  static constexpr int kGran = WD == MOE_BF16 ? 64 : WD == MOE_FP8_E4M3 ? 128 : 256;
+  static __device__ __forceinline__ int bytes(int cols) { return cols * kBits / 8; }
 };
+
+// Row pitch in a slot: 64 bytes past a multiple of 128, so that the 16-byte loads of eight lanes
+// (two rows, four words each) meet different banks.
+__device__ __forceinline__ int slot_pitch(int bytes) { return ((bytes + 127) & ~127) + 64; }
+
+// 16 weight rows (pair: rows f0.. of W1 and of W3, eight each) times activation rows, over K.
+struct Seg {
+  const uint8_t* w;   // matrix [R][K]
+  const void* s;      // its scales
+  int R, K;
+  int f0, cnt, u_off; // features f0 .. f0+cnt; u_off > 0: pairs, W3 rows at + u_off
+  const __nv_bfloat16* act[2];  // planes; the second may be null
+  int row0;           // first activation row, or -1: the tokens of mask
+  uint32_t mask;      // tokens
+  int dep;            // counter that must be complete before the activations are read
+  bool scaled;        // multiply by the tokens' 1 / rms (latent up-projection)
+
+  __device__ __forceinline__ int planes() const { return act[1] ? 2 : 1; }
+  __device__ __forceinline__ int row(int i) const {  // feature row of slot row i (clamped)
+    if (u_off) return (i < 8 ? 0 : u_off) + f0 + min(i & 7, cnt - 1);
+    return f0 + min(i, cnt - 1);
+  }
+  __device__ __forceinline__ bool has(int i) const { return (u_off ? i & 7 : i) < cnt; }
+};
+
+// Geometry of a segment's slots.
+template <int WD>
+struct Geo {
+  int cols, wpitch, apitch, soff, aoff;
+  __device__ __forceinline__ explicit Geo(const Seg& g) {
+    const int nr = __popc(g.mask) * g.planes();
+    constexpr int per16 = 16 * Wt<WD>::kBits / 8 + (WD == MOE_INT4 ? 1 : 0);
+    int c = (kSlotBytes - (16 + nr) * 64) / (per16 + 2 * nr);
+    constexpr int half = 8 * Wt<WD>::kUnit;  // half a round of the consumer warps
+    c = c >= half ? c / half * half : c / Wt<WD>::kGran * Wt<WD>::kGran;
+    cols = c;
+    wpitch = slot_pitch(Wt<WD>::bytes(c));
+    apitch = slot_pitch(c * 2);
+    soff = 16 * wpitch;
+    aoff = soff + (WD == MOE_INT4 ? c : 0);  // c / 32 groups of 16 bf16 scales
+  }
+};
+
+struct Pending {  // activations of a slot whose step is not complete yet
+  Seg seg;
+  int c0, cols, slot, apitch, aoff;
+};
+
+struct StreamHead {
+  uint64_t full[kSlots], empty[kSlots], sel_bar, inv_bar;
+  Pending pend[kSlots];
+  float inv[kMaxT];
+  int abort;
+  Selection sel;
+};
+constexpr size_t head_bytes() { return (sizeof(StreamHead) + 127) & ~size_t(127); }
+constexpr size_t stream_smem(int nt) {
+  return 128 + head_bytes() + (size_t)kCons * nt * 512 + (size_t)kSlots * kSlotBytes;
+}
+
+static_assert(stream_smem(2) <= 227 * 1024, "one CTA's shared memory");
+
+enum Kind { kDown, kHid, kLat, kOut };
+
+// The parts of the layer in stream order, each split evenly over the CTAs by features.
+enum Part { kPartDown, kPartShared, kPartRouted, kPartW2, kPartUp, kParts };
+
+// The s-th segment of a tile of features f0 .. f0 + cnt of a part (a: the routed expert's place).
+template <int WD>
+__device__ __forceinline__ Seg segment(const FewParams& p, const Selection& sel, int part, int s,
+                                       int a, int f0, int cnt) {
+  const uint32_t all = (1u << p.T) - 1u;
+  const int P = p.T * p.k, de = p.L ? p.L : p.d;
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
+  const __nv_bfloat16* h_lo = p.h2 + (int64_t)(P + p.T) * p.I;
+  Seg g;
+  g.s = nullptr;
+  g.f0 = f0;
+  g.cnt = cnt;
+  g.u_off = 0;
+  g.act[0] = x;
+  g.act[1] = nullptr;
+  g.row0 = 0;
+  g.mask = all;
+  g.dep = kNoDep;
+  g.scaled = false;
+  g.R = p.L;
+  g.K = p.d;
+  int64_t e = -1;  // routed expert
+  const void* w;
+  if (part == kPartDown) {
+    w = p.W_down;
+  } else if (part == kPartShared || part == kPartRouted) {
+    g.R = 2 * p.I;
+    g.u_off = p.I;
+    if (part == kPartShared) {
+      w = p.Ws13;
+      g.s = p.ss13;
+    } else {
+      w = p.W13;
+      g.s = p.s13;
+      e = sel.active[a];
+      g.K = de;
+      g.row0 = -1;
+      if (p.L) {
+        g.act[0] = p.x_lat2;
+        g.act[1] = p.x_lat2 + (int64_t)p.T * p.L;
+        g.dep = kCntDown;
+      }
+    }
+  } else if (part == kPartW2 ? s < sel.n_active : s == 1) {
+    if (part == kPartW2) {
+      w = p.W2;
+      g.s = p.s2;
+      e = sel.active[s];
+      g.row0 = sel.row0[s];
+      g.R = de;
+      g.K = p.I;
+      g.act[0] = p.h2;
+      g.act[1] = h_lo;
+      g.dep = kCntH;
+    } else {
+      w = p.W_up;
+      g.R = p.d;
+      g.K = p.L;
+      g.act[0] = p.y_lat2;
+      g.act[1] = p.y_lat2 + (int64_t)p.T * p.L;
+      g.dep = kCntLat;
+      g.scaled = true;
+    }
+  } else {
+    w = p.Ws2;
+    g.s = p.ss2;
+    g.R = p.d;
+    g.K = p.I;
+    g.act[0] = p.h2;
+    g.act[1] = h_lo;
+    g.row0 = P;
+    g.dep = kCntH;
+  }
+  g.w = static_cast<const uint8_t*>(w);
+  if (e >= 0) {
+    g.mask = sel.mask[e];
+    g.w += e * g.R * g.K * Wt<WD>::kBits / 8;
+    if constexpr (WD == MOE_FP8_E4M3)
+      g.s = static_cast<const float*>(g.s) + e * (g.R / 128) * (g.K / 128);
+    if constexpr (WD == MOE_INT4)
+      g.s = static_cast<const __nv_bfloat16*>(g.s) + e * (g.K / 32) * g.R;
+  }
+  return g;
+}
+
+// The CTA's share of the layer; the producer and the consumers follow it alike.
+// V: begin(), seg(Seg), end(kind, f0, cnt, mask, first h row, gated), done(counter), selected().
+template <int WD, typename V>
+__device__ __forceinline__ void walk(const FewParams& p, const Selection& sel, V& v) {
+  constexpr int G = WD == MOE_INT4 ? 2 : 1;  // 4-byte copies of the bf16 scales of two rows
+  const uint32_t all = (1u << p.T) - 1u;
+  const int P = p.T * p.k;
+#pragma unroll 1
+  for (int part = 0; part < kParts; ++part) {
+    if ((part == kPartDown || part == kPartUp) && !p.L) continue;
+    if (part == kPartShared && !p.n_shared) continue;
+    if (part == kPartRouted && !v.selected()) return;
+    const bool pair = part == kPartShared || part == kPartRouted;
+    const int64_t total = part == kPartShared   ? p.I
+                          : part == kPartRouted ? (int64_t)sel.n_active * p.I
+                          : part == kPartUp     ? p.d
+                                                : p.L ? p.L : p.d;
+    const int64_t u1 = total / G * (blockIdx.x + 1) / gridDim.x * G;
+    int n_seg = 1;
+    if (part == kPartW2) n_seg = sel.n_active + (p.L ? 0 : p.n_shared);
+    if (part == kPartUp) n_seg = 2;
+#pragma unroll 1
+    for (int64_t u = total / G * blockIdx.x / gridDim.x * G; u < u1;) {
+      int a = 0, f = (int)u, len = (int)(u1 - u);
+      if (part == kPartRouted) {
+        a = (int)(u / p.I);
+        f = (int)(u - (int64_t)a * p.I);
+        len = (int)min(u1 - u, (int64_t)(p.I - f));
+      }
+      const int n = (len + (pair ? 7 : 15)) / (pair ? 8 : 16);  // tiles left, evenly
+      const int cnt = (len / G + n - 1) / n * G;
+      v.begin();
+#pragma unroll 1
+      for (int s = part == kPartUp && !p.n_shared ? 1 : 0; s < n_seg; ++s)
+        v.seg(segment<WD>(p, sel, part, s, a, f, cnt));
+      const bool routed = part == kPartRouted;
+      v.end(part == kPartDown              ? kDown
+            : pair                         ? kHid
+            : part == kPartW2 && p.L       ? kLat
+                                           : kOut,
+            f, cnt, routed ? sel.mask[sel.active[a]] : all, routed ? sel.row0[a] : P, routed);
+      u += cnt;
+    }
+    if (part == kPartDown) v.done(kCntDown);
+    if (part == kPartRouted) v.done(kCntH);
+    if (part == kPartW2 && p.L) v.done(kCntLat);
+  }
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The producer warp.
+template <int WD>
+struct Producer {
+  const FewParams& p;
+  StreamHead& hd;
+  uint8_t* slots;
+  int lane;
+  uint32_t issued = 0;   // slots filled so far
+  int n_pend = 0, pend0 = 0;
+  uint32_t complete = 0; // counters known to be complete
+  bool failed = false;
+
+  // lane 0 asks, every lane gets the answer; the copies after it see what the counter published
+  __device__ bool ready(int dep) {
+    if (dep == kNoDep || (complete >> dep & 1u)) return true;
+    int r = 0;
+    if (lane == 0) r = counter_reached(p.bar + dep, gridDim.x);
+    r = __shfl_sync(0xffffffffu, r, 0);
+    if (r) {
+      complete |= 1u << dep;
+      asm volatile("fence.proxy.async;" ::: "memory");
+      __syncwarp();
+    }
+    return r != 0;
+  }
+  __device__ void load_acts(const Seg& g, int c0, int cols, int slot, int apitch, int aoff) {
+    const int n = __popc(g.mask), rows = n * g.planes();
+    if (lane == 0) mbar_arrive_expect_tx(&hd.full[slot], rows * cols * 2);
+    __syncwarp();
+    for (int i = lane; i < rows; i += 32) {
+      const int pl = i >= n, j = i - pl * n;
+      const int64_t src = g.row0 < 0 ? nth_token(g.mask, j) : g.row0 + j;
+      bulk_load(slots + (size_t)slot * kSlotBytes + aoff + i * apitch,
+                g.act[pl] + src * g.K + c0, cols * 2, &hd.full[slot]);
+    }
+  }
+  // Copies the waiting activations whose counters are complete (force: all of them).
+  __device__ void flush(bool force) {
+    while (n_pend > 0) {
+      const Pending& q = hd.pend[pend0];
+      if (!force && !ready(q.seg.dep)) return;
+      load_acts(q.seg, q.c0, q.cols, q.slot, q.apitch, q.aoff);
+      __syncwarp();
+      pend0 = pend0 + 1 == kSlots ? 0 : pend0 + 1;
+      --n_pend;
+    }
+  }
+  // Waits until the next slot is free, copying waiting activations meanwhile.
+  __device__ bool slot_free(int slot, uint32_t parity) {
+    uint64_t t0 = 0;
+    while (true) {
+      int r = 0;
+      if (lane == 0) {
+        if (mbar_test(&hd.empty[slot], parity)) {
+          r = 1;
+        } else if (*(volatile int*)&hd.abort) {
+          r = 2;
+        } else {
+          const uint64_t t = globaltimer_ns();
+          if (t0 == 0) t0 = t;
+          if (t - t0 > kWaitLimitNs) {
+            hd.abort = 1;
+            raise_flag(p.err, kErrTimeout);
+            r = 2;
+          }
+        }
+      }
+      r = __shfl_sync(0xffffffffu, r, 0);
+      if (r) return r == 1;
+      flush(false);
+    }
+  }
+  __device__ void begin() {}
+  __device__ void end(Kind, int, int, uint32_t, int, bool) {}
+  __device__ void done(int) {}
+  __device__ bool selected() {
+    if (failed || !mbar_wait(&hd.sel_bar, 0, &hd.abort, p.err)) failed = true;
+    failed = __any_sync(0xffffffffu, failed);
+    return !failed;
+  }
+  __device__ void seg(const Seg& g) {
+    const Geo<WD> geo(g);
+    for (int c0 = 0; c0 < g.K && !failed; c0 += geo.cols) {
+      const int cols = min(geo.cols, g.K - c0);
+      const int slot = issued % kSlots;
+      if (!slot_free(slot, (issued / kSlots & 1u) ^ 1u)) {
+        failed = true;
+        return;
+      }
+      uint8_t* base = slots + (size_t)slot * kSlotBytes;
+      const uint32_t nb = Wt<WD>::bytes(cols);
+      if (lane == 0)
+        mbar_arrive_expect_tx(&hd.full[slot], (g.u_off ? 2 * g.cnt : g.cnt) * nb);
+      __syncwarp();
+      if (lane < 16 && g.has(lane))
+        bulk_load(base + lane * geo.wpitch,
+                  g.w + ((int64_t)g.row(lane) * g.K + c0) * Wt<WD>::kBits / 8, nb, &hd.full[slot]);
+      if constexpr (WD == MOE_INT4) {
+        // scales [K / 32][R]: two rows of a group a copy, into [group][16]
+        for (int i = lane; i < cols / 32 * 8; i += 32) {
+          const int grp = i >> 3, r = (i & 7) * 2;
+          if (!g.has(r)) continue;
+          const __nv_bfloat16* src =
+              (const __nv_bfloat16*)g.s + (int64_t)(c0 / 32 + grp) * g.R + g.row(r);
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                           smem_u32(base + geo.soff + grp * 32 + r * 2)),
+                       "l"(src)
+                       : "memory");
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                         smem_u32(&hd.full[slot]))
+                     : "memory");
+      }
+      ++issued;
+      if (n_pend == 0 && ready(g.dep)) {
+        load_acts(g, c0, cols, slot, geo.apitch, geo.aoff);
+      } else {
+        const int at = (pend0 + n_pend) % kSlots;
+        if (lane == 0) hd.pend[at] = Pending{g, c0, cols, slot, geo.apitch, geo.aoff};
+        ++n_pend;
+        __syncwarp();
+        flush(false);
+      }
+    }
+  }
+  // Copies what still waits; after a failure, waits for the copies in flight to land.
+  __device__ void finish() {
+    while (n_pend > 0 && !failed) {
+      int ok = 1;
+      if (lane == 0)
+        ok = counter_wait(p.bar + hd.pend[pend0].seg.dep, gridDim.x, &hd.abort, p.err);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) failed = true;
+      flush(false);
+    }
+    if (*(volatile int*)&hd.abort) failed = true;
+    if (!__any_sync(0xffffffffu, failed)) return;
+    flush(true);
+    for (uint32_t i = issued > kSlots ? issued - kSlots : 0; i < issued; ++i)
+      mbar_wait(&hd.full[i % kSlots], i / kSlots & 1u, nullptr, nullptr, kDrainLimitNs);
+  }
+};
+
+__device__ __forceinline__ uint4 lds16(const void* q) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(smem_u32(q)));
+  return v;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a),
+                             *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a),
+                             *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+
+// Four e4m3 codes as bf16: exponent and mantissa bits moved to bf16's places give value * 2^-120
+// (subnormals included), the product with 2^120 is exact.  A code of all ones is NaN.
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t x0 = __byte_perm(w, 0, 0x1404), x1 = __byte_perm(w, 0, 0x3424);
+  lo = mul_bf16x2(((x0 >> 4) & 0x07f007f0u) | (x0 & 0x80008000u), 0x7b807b80u);
+  hi = mul_bf16x2(((x1 >> 4) & 0x07f007f0u) | (x1 & 0x80008000u), 0x7b807b80u);
+  const uint32_t bad = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  if (bad) {
+    lo |= (bad & 0x80u ? 0x7fffu : 0u) | (bad & 0x8000u ? 0x7fff0000u : 0u);
+    hi |= (bad & 0x800000u ? 0x7fffu : 0u) | (bad & 0x80000000u ? 0x7fff0000u : 0u);
+  }
+}
+
+// Eight 4-bit codes (nibbles j and j + 4 are channels 2j and 2j + 1) times their scale: 128 + u is
+// bf16's 0x4300 | u, minus 136 exact, and the product rounds once.
+__device__ __forceinline__ void int4x8_to_bf16(uint32_t w, uint32_t sc, uint32_t (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = mul_bf16x2(sub_bf16x2(((w >> (4 * j)) & 0x000f000fu) | 0x43004300u, 0x43084308u), sc);
+}
+
+__device__ __forceinline__ void split_planes(float v, __nv_bfloat16& hi, __nv_bfloat16& lo) {
+  hi = __float2bfloat16_rn(v);
+  const float f = __bfloat162float(hi);
+  lo = __float2bfloat16_rn(isinf(f) ? 0.0f : v - f);
+}
+
+// The sixteen consumer warps.  NT: groups of 8 tokens.
+template <int WD, int NT>
+struct Consumer {
+  const FewParams& p;
+  StreamHead& hd;
+  const uint8_t* slots;
+  float* red;  // [kCons][NT][16 rows][8 tokens]
+  int warp, lane;
+  uint32_t used = 0;  // slots consumed so far
+  float acc[NT][4];
+  float ssq = 0.0f;   // of the latent features this thread has stored for its token
+
+  __device__ void begin() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+  }
+
+  __device__ void seg(const Seg& g) {
+    using W = Wt<WD>;
+    const Geo<WD> geo(g);
+    const int gr = lane >> 2, t4 = lane & 3;
+    const int n_act = __popc(g.mask);
+    int boff[NT];   // offset of this lane's token row among the activations, -1: absent
+    bool any[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int tok = n * 8 + gr;
+      boff[n] = g.mask >> tok & 1u ? geo.aoff + __popc(g.mask & ((1u << tok) - 1u)) * geo.apitch : -1;
+      any[n] = (g.mask >> (n * 8) & 0xffu) != 0;
+    }
+    const int plane = n_act * geo.apitch;
+    const bool two = g.act[1] != nullptr;
+    float d[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
+
+    for (int c0 = 0; c0 < g.K; c0 += geo.cols) {
+      const int cols = min(geo.cols, g.K - c0);
+      const int slot = used % kSlots;
+      mbar_wait_sleep(&hd.full[slot], used / kSlots & 1u, &hd.abort, p.err);
+      ++used;
+      const uint8_t* base = slots + (size_t)slot * kSlotBytes;
+      for (int u = warp * W::kUnit; u < cols; u += kCons * W::kUnit) {
+        float s0 = 0.0f, s1 = 0.0f;
+        float dd[NT][4];
+        if constexpr (WD == MOE_FP8_E4M3) {  // one scale block: its own sum
+          const float* s = (const float*)g.s + (c0 + u) / 128;
+          s0 = __ldg(s + (int64_t)(g.row(gr) / 128) * (g.K / 128));
+          s1 = __ldg(s + (int64_t)(g.row(gr + 8) / 128) * (g.K / 128));
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dd[n][i] = 0.0f;
+        }
+#pragma unroll
+        for (int st = 0; st < W::kUnit / W::kStep; ++st) {
+          const int col = u + st * W::kStep + t4 * W::kChunk;
+          const bool valid = col < cols;
+          uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
+          uint32_t sa = 0, sb = 0;
+          if (valid) {
+            ra = lds16(base + gr * geo.wpitch + W::bytes(col));
+            rb = lds16(base + (gr + 8) * geo.wpitch + W::bytes(col));
+            if constexpr (WD == MOE_INT4) {
+              const uint16_t* sc = (const uint16_t*)(base + geo.soff + (col >> 5) * 32);
+              sa = sc[gr] * 0x10001u;
+              sb = sc[gr + 8] * 0x10001u;
+            }
+          }
+          const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+#pragma unroll
+          for (int h = 0; h < W::kChunk / 8; ++h) {  // 8 channels: two products
+            uint32_t a[4], b[4];
+            if constexpr (WD == MOE_BF16) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                a[i] = wa[i];
+                b[i] = wb[i];
+              }
+            } else if constexpr (WD == MOE_FP8_E4M3) {
+              e4m3x4_to_bf16(wa[2 * h], a[0], a[1]);
+              e4m3x4_to_bf16(wa[2 * h + 1], a[2], a[3]);
+              e4m3x4_to_bf16(wb[2 * h], b[0], b[1]);
+              e4m3x4_to_bf16(wb[2 * h + 1], b[2], b[3]);
+            } else {
+              int4x8_to_bf16(wa[h], sa, a);
+              int4x8_to_bf16(wb[h], sb, b);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if (!any[n]) continue;
+              const bool on = valid && boff[n] >= 0;
+              const uint8_t* q = base + boff[n] + col * 2 + h * 16;
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (on) v = lds16(q);
+              float(&o)[4] = WD == MOE_FP8_E4M3 ? dd[n] : d[n];
+              mma16816(o, a[0], b[0], a[1], b[1], v.x, v.y);
+              mma16816(o, a[2], b[2], a[3], b[3], v.z, v.w);
+              if (two) {
+                if (on) v = lds16(q + plane);
+                mma16816(o, a[0], b[0], a[1], b[1], v.x, v.y);
+                mma16816(o, a[2], b[2], a[3], b[3], v.z, v.w);
+              }
+            }
+          }
+        }
+        if constexpr (WD == MOE_FP8_E4M3) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            d[n][0] = fmaf(s0, dd[n][0], d[n][0]);
+            d[n][1] = fmaf(s0, dd[n][1], d[n][1]);
+            d[n][2] = fmaf(s1, dd[n][2], d[n][2]);
+            d[n][3] = fmaf(s1, dd[n][3], d[n][3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&hd.empty[slot]);
+    }
+    if (g.scaled) mbar_wait_sleep(&hd.inv_bar, 0, &hd.abort, p.err);
+    // only the segment's own tokens: another token's zeros times an infinite weight are NaN
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tok = n * 8 + t4 * 2 + (i & 1);
+        if (g.mask >> tok & 1u) acc[n][i] += g.scaled ? d[n][i] * hd.inv[tok] : d[n][i];
+      }
+  }
+
+  __device__ void end(Kind kind, int f0, int cnt, uint32_t mask, int row0, bool gated) {
+    const int gr = lane >> 2, t4 = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float* r = red + (warp * NT + n) * 128 + gr * 8 + t4 * 2;
+      *reinterpret_cast<float2*>(r) = make_float2(acc[n][0], acc[n][1]);
+      *reinterpret_cast<float2*>(r + 64) = make_float2(acc[n][2], acc[n][3]);
+    }
+    named_barrier(1, kCons * 32);
+    const int c = warp * 32 + lane;
+    const bool pair = kind == kHid;
+    const int per = pair ? 64 : 128, nr = pair ? 8 : 16;
+    const int n = c / per, row = c % nr, tok = n * 8 + c / nr % 8;
+    const bool own = c < per * NT;
+    float v = 0.0f, up = 0.0f;
+    if (own) {
+      const float* r = red + n * 128 + row * 8 + tok % 8;
+#pragma unroll
+      for (int w = 0; w < kCons; ++w) v += r[w * NT * 128];
+      if (pair) {
+#pragma unroll
+        for (int w = 0; w < kCons; ++w) up += r[w * NT * 128 + 64];
+      }
+    }
+    named_barrier(1, kCons * 32);  // the partial sums have been read
+    const bool live = own && row < cnt && (mask >> tok & 1u);
+    const int f = f0 + row;
+    if (kind == kHid) {
+      if (!live) return;
+      const int hr = row0 + __popc(mask & ((1u << tok) - 1u));
+      v = silu_accurate(v) * up;
+      if (gated) v *= hd.sel.row_gate[hr];
+      __nv_bfloat16 hi, lo;
+      split_planes(v, hi, lo);
+      const int64_t at = (int64_t)hr * p.I + f;
+      p.h2[at] = hi;
+      p.h2[(int64_t)p.T * (p.k + 1) * p.I + at] = lo;
+    } else if (kind == kOut) {
+      if (live) static_cast<__nv_bfloat16*>(p.out)[(int64_t)tok * p.d + f] = __float2bfloat16_rn(v);
+    } else {
+      if (kind == kLat) {  // 16 consecutive lanes hold the tile's features of one token
+        float q = live ? v * v : 0.0f;
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
+        ssq += q;
+      }
+      if (!live) return;
+      __nv_bfloat16 hi, lo;
+      split_planes(v, hi, lo);
+      __nv_bfloat16* o = kind == kDown ? p.x_lat2 : p.y_lat2;
+      o[(int64_t)tok * p.L + f] = hi;
+      o[(int64_t)(p.T + tok) * p.L + f] = lo;
+    }
+  }
+
+  // Publishes what the CTA has stored so far: to the other CTAs' loads and bulk copies.
+  __device__ void done(int counter) {
+    const int c = warp * 32 + lane;
+    if (counter == kCntLat && c < 128 * NT && c % 16 == 0)
+      p.ssq[blockIdx.x * kMaxT + c / 128 * 8 + c / 16 % 8] = ssq;
+    asm volatile("fence.proxy.async;" ::: "memory");
+    __threadfence();
+    named_barrier(1, kCons * 32);
+    if (c == 0)
+      asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.bar + counter) : "memory");
+  }
+
+  __device__ bool selected() {
+    const bool ok = mbar_wait_sleep(&hd.sel_bar, 0, &hd.abort, p.err);
+    return named_barrier_and(1, kCons * 32, ok);  // all warps go on or none
+  }
+
+  // Router logits: a warp takes one expert's range of input channels.
+  __device__ void router() {
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
+    for (int u = warp * gridDim.x + blockIdx.x; u < p.E * p.parts; u += gridDim.x * kCons) {
+      const int e = u % p.E, q = u / p.E;
+      const int end = min(p.d, (q + 1) * p.part_cols);
+      const float* w = p.W_r + (int64_t)e * p.d;
+      float z[NT * 8];
+#pragma unroll
+      for (int t = 0; t < NT * 8; ++t) z[t] = 0.0f;
+#pragma unroll 4
+      for (int c = q * p.part_cols + lane * 4; c < end; c += 128) {
+        const float4 wv = __ldg(reinterpret_cast<const float4*>(w + c));
+#pragma unroll
+        for (int t = 0; t < NT * 8; ++t)
+          if (t < p.T) {
+            const uint2 xv = __ldg(reinterpret_cast<const uint2*>(x + (int64_t)t * p.d + c));
+            z[t] = fmaf(wv.x, __uint_as_float(xv.x << 16), z[t]);
+            z[t] = fmaf(wv.y, __uint_as_float(xv.x & 0xffff0000u), z[t]);
+            z[t] = fmaf(wv.z, __uint_as_float(xv.y << 16), z[t]);
+            z[t] = fmaf(wv.w, __uint_as_float(xv.y & 0xffff0000u), z[t]);
+          }
+      }
+#pragma unroll
+      for (int t = 0; t < NT * 8; ++t)
+        if (t < p.T) {
+          const float v = warp_sum(z[t]);
+          if (lane == 0) p.logits[((int64_t)q * p.T + t) * p.E + e] = v;
+        }
+    }
+  }
+};
+
+template <int WD, int NT>
+__global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const FewParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
+                                             ~uintptr_t(127));
+  StreamHead& hd = *reinterpret_cast<StreamHead*>(smem);
+  float* red = reinterpret_cast<float*>(smem + head_bytes());
+  uint8_t* slots = smem + head_bytes() + (size_t)kCons * NT * 512;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&hd.full[i], 2 + (WD == MOE_INT4 ? 32 : 0));  // weights, activations (+ scales)
+      mbar_init(&hd.empty[i], kCons);
+    }
+    mbar_init(&hd.sel_bar, kSelWarps);
+    mbar_init(&hd.inv_bar, kSelWarps);
+    hd.abort = 0;
+    hd.sel.n_active = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+
+  if (warp == 0) {
+    Producer<WD> v{p, hd, slots, lane};
+    walk<WD>(p, hd.sel, v);
+    v.finish();
+  } else if (warp < kFirstCons) {
+    int ok = 1;
+    if (lane == 0) ok = counter_wait(p.bar + kCntRouter, gridDim.x, &hd.abort, p.err);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    ok = named_barrier_and(2, kSelWarps * 32, ok);
+    if (!ok) return;
+    build_selection(p, hd.sel, threadIdx.x - 32, kSelWarps, 2);
+    if (lane == 0) mbar_arrive(&hd.sel_bar);
+    if (!p.L) return;
+    if (lane == 0) ok = counter_wait(p.bar + kCntLat, gridDim.x, &hd.abort, p.err);
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return;
+    for (int t = warp - 1; t < p.T; t += kSelWarps) {
+      float ss = 0.0f;
+      for (int c = lane; c < (int)gridDim.x; c += 32) ss += __ldcg(p.ssq + c * kMaxT + t);
+      ss = warp_sum(ss);
+      if (lane == 0) hd.inv[t] = p.latent_norm ? 1.0f / sqrtf(ss / (float)p.L + p.eps) : 1.0f;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&hd.inv_bar);
+  } else {
+    Consumer<WD, NT> v{p, hd, slots, red, warp - kFirstCons, lane};
+    v.router();
+    v.done(kCntRouter);
+    walk<WD>(p, hd.sel, v);
+  }
+}
+
+struct FewLayout {
+  size_t logits, x_lat, h, y_lat, ssq, total;
+  int parts, part_cols;
+};
+
+constexpr int kMaxCtas = 256;  // the grid is one CTA per SM, at most this many
 
 FewLayout few_layout(const moe_config_t* c) {
   FewLayout l;
@@ -417,10 +1151,21 @@ FewLayout few_layout(const moe_config_t* c) {
     return at;
   };
   const size_t T = (size_t)c->T;
-  l.logits = take(T * c->E * 4);
+  // router ranges: about one (expert, range) per consumer warp of 152 SMs, 128 channels at least
+  l.parts = 1;
+  l.part_cols = c->d;
+  if (c->act_dtype == MOE_BF16) {
+    int n = 152 * kCons / c->E;
+    n = n < 1 ? 1 : n > 8 ? 8 : n;
+    l.part_cols = ((c->d + n - 1) / n + 127) / 128 * 128;
+    l.parts = (c->d + l.part_cols - 1) / l.part_cols;
+  }
+  l.logits = take(l.parts * T * c->E * 4);
+  // 4 bytes a value: one fp32, or two bf16 planes
   l.x_lat = take(T * c->d_latent * 4);
   l.h = take((T * c->k + T) * c->I * 4);
   l.y_lat = take(T * c->d_latent * 4);
+  l.ssq = take(c->d_latent ? (size_t)kMaxCtas * kMaxT * 4 : 0);
   l.total = off;
   return l;
 }
@@ -449,19 +1194,33 @@ moe_status_t validate_few(const moe_config_t* c) {
   return MOE_OK;
 }
 
-template <typename TA, int WD>
-cudaError_t launch(FewParams& p, cudaStream_t st) {
+cudaError_t start(const void* kernel, FewParams& p, int threads, size_t smem, cudaStream_t st) {
+  if (smem) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(num_sms());
-  cfg.blockDim = dim3(kThreads);
+  const int sms = num_sms();
+  cfg.gridDim = dim3(sms < kMaxCtas ? sms : kMaxCtas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;  // every CTA resident at once: they wait for others
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  void* args[] = {&p};
   LaunchScope ls("few_layer", st);
-  return cudaLaunchKernelEx(&cfg, few_kernel<TA, WD>, (const FewParams)p);
+  return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+template <int WD>
+cudaError_t start_stream(FewParams& p, cudaStream_t st) {
+  if (p.T <= 8)
+    return start((const void*)few_stream_kernel<WD, 1>, p, kStreamThreads, stream_smem(1), st);
+  return start((const void*)few_stream_kernel<WD, 2>, p, kStreamThreads, stream_smem(2), st);
 }
 
 }  // namespace
@@ -527,18 +1286,24 @@ extern "C" moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, 
   p.err = reinterpret_cast<uint32_t*>(base);
   p.bar = reinterpret_cast<uint32_t*>(base + 128);
   p.logits = reinterpret_cast<float*>(base + l.logits);
+  p.parts = l.parts;
+  p.part_cols = l.part_cols;
   p.x_lat = reinterpret_cast<float*>(base + l.x_lat);
   p.h = reinterpret_cast<float*>(base + l.h);
   p.y_lat = reinterpret_cast<float*>(base + l.y_lat);
+  p.x_lat2 = reinterpret_cast<__nv_bfloat16*>(base + l.x_lat);
+  p.h2 = reinterpret_cast<__nv_bfloat16*>(base + l.h);
+  p.y_lat2 = reinterpret_cast<__nv_bfloat16*>(base + l.y_lat);
+  p.ssq = reinterpret_cast<float*>(base + l.ssq);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   (void)cudaGetLastError();  // start from a clean launch-error state
   cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);  // status word and barrier counters
   if (e != cudaSuccess) return status_from_cuda(e);
   switch (cfg->w_dtype) {
-    case MOE_F32: e = launch<float, MOE_F32>(p, st); break;
-    case MOE_BF16: e = launch<__nv_bfloat16, MOE_BF16>(p, st); break;
-    case MOE_FP8_E4M3: e = launch<__nv_bfloat16, MOE_FP8_E4M3>(p, st); break;
-    default: e = launch<__nv_bfloat16, MOE_INT4>(p, st); break;
+    case MOE_F32: e = start((const void*)few_kernel, p, kThreads, 0, st); break;
+    case MOE_BF16: e = start_stream<MOE_BF16>(p, st); break;
+    case MOE_FP8_E4M3: e = start_stream<MOE_FP8_E4M3>(p, st); break;
+    default: e = start_stream<MOE_INT4>(p, st); break;
   }
   return status_from_cuda(e);
 }
