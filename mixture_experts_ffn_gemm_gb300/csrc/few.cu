@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
 // ---------------------------------------------------------------------------------------------
 // bf16 activations: one stream of weights through shared memory per SM.
 //
-// A producer warp walks the CTA's share of every step and copies it (bulk asynchronous copies, a row
+// Producer warps walk the CTA's share of every step and copy it (bulk asynchronous copies, a row
 // piece each) into a ring of kSlots slots: 16 weight rows times up to a few thousand input channels,
 // and the same channels of the activations they meet.  Sixteen consumer warps split a slot's
 // channels, multiply 16 rows by 8 tokens with mma.sync m16n8k16 and, when a tile of rows is
@@ -417,11 +417,11 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
 // or more of each, where one bf16 would add a rounding of 2^-9.
 // ---------------------------------------------------------------------------------------------
 constexpr int kCons = 16;      // consumer warps
-constexpr int kSelWarps = 3;
-constexpr int kFirstCons = 1 + kSelWarps;
+constexpr int kSlots = 4;      // ring slots, one producer warp each
+constexpr int kSelWarps = 4;
+constexpr int kFirstCons = kSlots + kSelWarps;
 constexpr int kStreamThreads = 32 * (kFirstCons + kCons);
-constexpr int kSlots = 5;
-constexpr int kSlotBytes = 38912;
+constexpr int kSlotBytes = 48640;
 
 // Counters of the launch (FewParams::bar): arrivals of CTAs at the end of each part.
 enum : int { kCntRouter = 0, kCntDown = 1, kCntH = 2, kCntLat = 3 };
@@ -470,7 +470,9 @@ struct Geo {
     constexpr int per16 = 16 * Wt<WD>::kBits / 8 + (WD == MOE_INT4 ? 1 : 0);
     int c = (kSlotBytes - (16 + nr) * 64) / (per16 + 2 * nr);
     constexpr int half = 8 * Wt<WD>::kUnit;  // half a round of the consumer warps
-    c = c >= half ? c / half * half : c / Wt<WD>::kGran * Wt<WD>::kGran;
+    const int gran = c >= half ? half : Wt<WD>::kGran;
+    const int n = (g.K + c / gran * gran - 1) / (c / gran * gran);  // slots, evenly
+    c = ((g.K + n - 1) / n + gran - 1) / gran * gran;
     cols = c;
     wpitch = slot_pitch(Wt<WD>::bytes(c));
     apitch = slot_pitch(c * 2);
@@ -479,14 +481,8 @@ struct Geo {
   }
 };
 
-struct Pending {  // activations of a slot whose step is not complete yet
-  Seg seg;
-  int c0, cols, slot, apitch, aoff;
-};
-
 struct StreamHead {
   uint64_t full[kSlots], empty[kSlots], sel_bar, inv_bar;
-  Pending pend[kSlots];
   float inv[kMaxT];
   int abort;
   Selection sel;
@@ -646,96 +642,48 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// The producer warp.
+// A producer warp; warp i fills slot i, every kSlots-th slot of the stream.  (One copy instruction
+// takes its addresses from uniform registers, so a warp issues the 16 and more copies of a slot one
+// after another: one warp for all slots held the stream to 4.2 TB/s.)
 template <int WD>
 struct Producer {
   const FewParams& p;
   StreamHead& hd;
-  uint8_t* slots;
-  int lane;
-  uint32_t issued = 0;   // slots filled so far
-  int n_pend = 0, pend0 = 0;
+  uint8_t* base;         // this warp's slot
+  int slot, lane;
+  uint32_t count = 0;    // slots of the stream so far
+  uint32_t filled = 0;   // of them this warp's
   uint32_t complete = 0; // counters known to be complete
   bool failed = false;
 
-  // lane 0 asks, every lane gets the answer; the copies after it see what the counter published
-  __device__ bool ready(int dep) {
+  // Waits until a step is complete; the copies after it see what it published.
+  __device__ bool step_complete(int dep) {
     if (dep == kNoDep || (complete >> dep & 1u)) return true;
-    int r = 0;
-    if (lane == 0) r = counter_reached(p.bar + dep, gridDim.x);
-    r = __shfl_sync(0xffffffffu, r, 0);
-    if (r) {
-      complete |= 1u << dep;
-      asm volatile("fence.proxy.async;" ::: "memory");
-      __syncwarp();
-    }
-    return r != 0;
-  }
-  __device__ void load_acts(const Seg& g, int c0, int cols, int slot, int apitch, int aoff) {
-    const int n = __popc(g.mask), rows = n * g.planes();
-    if (lane == 0) mbar_arrive_expect_tx(&hd.full[slot], rows * cols * 2);
-    __syncwarp();
-    for (int i = lane; i < rows; i += 32) {
-      const int pl = i >= n, j = i - pl * n;
-      const int64_t src = g.row0 < 0 ? nth_token(g.mask, j) : g.row0 + j;
-      bulk_load(slots + (size_t)slot * kSlotBytes + aoff + i * apitch,
-                g.act[pl] + src * g.K + c0, cols * 2, &hd.full[slot]);
-    }
-  }
-  // Copies the waiting activations whose counters are complete (force: all of them).
-  __device__ void flush(bool force) {
-    while (n_pend > 0) {
-      const Pending& q = hd.pend[pend0];
-      if (!force && !ready(q.seg.dep)) return;
-      load_acts(q.seg, q.c0, q.cols, q.slot, q.apitch, q.aoff);
-      __syncwarp();
-      pend0 = pend0 + 1 == kSlots ? 0 : pend0 + 1;
-      --n_pend;
-    }
-  }
-  // Waits until the next slot is free, copying waiting activations meanwhile.
-  __device__ bool slot_free(int slot, uint32_t parity) {
-    uint64_t t0 = 0;
-    while (true) {
-      int r = 0;
-      if (lane == 0) {
-        if (mbar_test(&hd.empty[slot], parity)) {
-          r = 1;
-        } else if (*(volatile int*)&hd.abort) {
-          r = 2;
-        } else {
-          const uint64_t t = globaltimer_ns();
-          if (t0 == 0) t0 = t;
-          if (t - t0 > kWaitLimitNs) {
-            hd.abort = 1;
-            raise_flag(p.err, kErrTimeout);
-            r = 2;
-          }
-        }
-      }
-      r = __shfl_sync(0xffffffffu, r, 0);
-      if (r) return r == 1;
-      flush(false);
-    }
+    int ok = 1;
+    if (lane == 0) ok = counter_wait(p.bar + dep, gridDim.x, &hd.abort, p.err);
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+    complete |= 1u << dep;
+    asm volatile("fence.proxy.async;" ::: "memory");
+    return true;
   }
   __device__ void begin() {}
   __device__ void end(Kind, int, int, uint32_t, int, bool) {}
   __device__ void done(int) {}
   __device__ bool selected() {
-    if (failed || !mbar_wait(&hd.sel_bar, 0, &hd.abort, p.err)) failed = true;
-    failed = __any_sync(0xffffffffu, failed);
+    const bool ok = !failed && mbar_wait(&hd.sel_bar, 0, &hd.abort, p.err);
+    failed = __any_sync(0xffffffffu, !ok);
     return !failed;
   }
   __device__ void seg(const Seg& g) {
     const Geo<WD> geo(g);
-    for (int c0 = 0; c0 < g.K && !failed; c0 += geo.cols) {
+    for (int c0 = 0; c0 < g.K; c0 += geo.cols, ++count) {
+      if (count % kSlots != slot || failed) continue;
       const int cols = min(geo.cols, g.K - c0);
-      const int slot = issued % kSlots;
-      if (!slot_free(slot, (issued / kSlots & 1u) ^ 1u)) {
+      const bool ok = mbar_wait(&hd.empty[slot], (filled & 1u) ^ 1u, &hd.abort, p.err);
+      if (__any_sync(0xffffffffu, !ok)) {
         failed = true;
-        return;
+        continue;
       }
-      uint8_t* base = slots + (size_t)slot * kSlotBytes;
       const uint32_t nb = Wt<WD>::bytes(cols);
       if (lane == 0)
         mbar_arrive_expect_tx(&hd.full[slot], (g.u_off ? 2 * g.cnt : g.cnt) * nb);
@@ -759,32 +707,22 @@ struct Producer {
                          smem_u32(&hd.full[slot]))
                      : "memory");
       }
-      ++issued;
-      if (n_pend == 0 && ready(g.dep)) {
-        load_acts(g, c0, cols, slot, geo.apitch, geo.aoff);
-      } else {
-        const int at = (pend0 + n_pend) % kSlots;
-        if (lane == 0) hd.pend[at] = Pending{g, c0, cols, slot, geo.apitch, geo.aoff};
-        ++n_pend;
-        __syncwarp();
-        flush(false);
+      if (!step_complete(g.dep)) failed = true;  // then the copies bring what is there
+      const int n = __popc(g.mask), rows = n * g.planes();
+      if (lane == 0) mbar_arrive_expect_tx(&hd.full[slot], rows * cols * 2);
+      __syncwarp();
+      for (int i = lane; i < rows; i += 32) {
+        const int pl = i >= n, j = i - pl * n;
+        const int64_t src = g.row0 < 0 ? nth_token(g.mask, j) : g.row0 + j;
+        bulk_load(base + geo.aoff + i * geo.apitch, g.act[pl] + src * g.K + c0, cols * 2,
+                  &hd.full[slot]);
       }
+      ++filled;
     }
   }
-  // Copies what still waits; after a failure, waits for the copies in flight to land.
+  // After a failure the copies in flight still have to land before the CTA ends.
   __device__ void finish() {
-    while (n_pend > 0 && !failed) {
-      int ok = 1;
-      if (lane == 0)
-        ok = counter_wait(p.bar + hd.pend[pend0].seg.dep, gridDim.x, &hd.abort, p.err);
-      if (!__shfl_sync(0xffffffffu, ok, 0)) failed = true;
-      flush(false);
-    }
-    if (*(volatile int*)&hd.abort) failed = true;
-    if (!__any_sync(0xffffffffu, failed)) return;
-    flush(true);
-    for (uint32_t i = issued > kSlots ? issued - kSlots : 0; i < issued; ++i)
-      mbar_wait(&hd.full[i % kSlots], i / kSlots & 1u, nullptr, nullptr, kDrainLimitNs);
+    if (filled) mbar_wait(&hd.full[slot], (filled - 1) & 1u, nullptr, nullptr, kDrainLimitNs);
   }
 };
 
@@ -1104,8 +1042,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
   }
   __syncthreads();
 
-  if (warp == 0) {
-    Producer<WD> v{p, hd, slots, lane};
+  if (warp < kSlots) {
+    Producer<WD> v{p, hd, slots + (size_t)warp * kSlotBytes, warp, lane};
     walk<WD>(p, hd.sel, v);
     v.finish();
   } else if (warp < kFirstCons) {
@@ -1114,12 +1052,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
     ok = __shfl_sync(0xffffffffu, ok, 0);
     ok = named_barrier_and(2, kSelWarps * 32, ok);
     if (!ok) return;
-    build_selection(p, hd.sel, threadIdx.x - 32, kSelWarps, 2);
+    build_selection(p, hd.sel, threadIdx.x - 32 * kSlots, kSelWarps, 2);
     if (lane == 0) mbar_arrive(&hd.sel_bar);
     if (!p.L) return;
     if (lane == 0) ok = counter_wait(p.bar + kCntLat, gridDim.x, &hd.abort, p.err);
     if (!__shfl_sync(0xffffffffu, ok, 0)) return;
-    for (int t = warp - 1; t < p.T; t += kSelWarps) {
+    for (int t = warp - kSlots; t < p.T; t += kSelWarps) {
       float ss = 0.0f;
       for (int c = lane; c < (int)gridDim.x; c += 32) ss += __ldcg(p.ssq + c * kMaxT + t);
       ss = warp_sum(ss);
