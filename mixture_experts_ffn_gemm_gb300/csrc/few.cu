@@ -112,18 +112,27 @@ __device__ void select_token(const FewParams& p, int t, Selection& sel) {
   uint32_t key[N];
   float z[N];
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int e = lane + 32 * j;
-    z[j] = 0.0f;
-    if (e < p.E)
-      for (int q = 0; q < p.parts; ++q)
-        z[j] += __ldcg(p.logits + ((int64_t)q * p.T + t) * p.E + e);
+  for (int j = 0; j < N; ++j) z[j] = 0.0f;
+  constexpr int Q = N > 12 ? 1 : 2;
+  const float* lg = p.logits + (int64_t)t * p.E + lane;
+  for (int q = 0; q < p.parts; q += Q) {  // all loads of Q ranges in flight
+    float v[Q][N];
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        v[i][j] = q + i < p.parts && lane + 32 * j < p.E
+                      ? __ldcg(lg + (int64_t)(q + i) * p.T * p.E + 32 * j)
+                      : 0.0f;
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) z[j] += v[i][j];
   }
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const int e = lane + 32 * j;
     z[j] = 1.0f / (1.0f + expf(-z[j]));
-    key[j] = e < p.E ? key_bits(z[j] + p.b[e]) : 0u;
+    key[j] = lane + 32 * j < p.E ? key_bits(z[j] + __ldg(p.b + lane + 32 * j)) : 0u;
   }
   float my_s = 0.0f, den = 0.0f;
   int my_e = 0;
@@ -481,17 +490,34 @@ struct Geo {
   }
 };
 
+// What a slot holds, written by its producer for the consumers.
+enum : int {
+  kSegFirst = 1, kSegLast = 2, kTileFirst = 4, kTileLast = 8, kScaled = 16, kGated = 32,
+  kDone = 64,  // no data: the CTA's share of a part is complete, publish it (counter in kind)
+  kStop = 128  // no data: the stream ends
+};
+struct SlotInfo {
+  int cols, wpitch, apitch, aoff;
+  int soff, plane;   // int4 scales; distance of the activations' second plane (0: one plane)
+  uint32_t mask;     // tokens
+  int flags;
+  int f0, cnt, row0, kind;
+  const float* s;    // e4m3: scale of the matrix's row block 0 and the slot's first channel
+  int s_ld, u_off;   // scales per row block; distance of the W3 rows (0: no pairs)
+};
+
 struct StreamHead {
-  uint64_t full[kSlots], empty[kSlots], sel_bar, inv_bar;
+  uint64_t full[kSlots], empty[kSlots], sel_bar, inv_bar, red_full, red_empty;
+  SlotInfo info[kSlots];
   float inv[kMaxT];
   int abort;
+  uint32_t done[4];  // consumer warps through each part (a warp may be a part ahead of another)
   Selection sel;
 };
 constexpr size_t head_bytes() { return (sizeof(StreamHead) + 127) & ~size_t(127); }
 constexpr size_t stream_smem(int nt) {
   return 128 + head_bytes() + (size_t)kCons * nt * 512 + (size_t)kSlots * kSlotBytes;
 }
-
 static_assert(stream_smem(2) <= 227 * 1024, "one CTA's shared memory");
 
 enum Kind { kDown, kHid, kLat, kOut };
@@ -542,26 +568,24 @@ __device__ __forceinline__ Seg segment(const FewParams& p, const Selection& sel,
         g.dep = kCntDown;
       }
     }
-  } else if (part == kPartW2 ? s < sel.n_active : s == 1) {
-    if (part == kPartW2) {
-      w = p.W2;
-      g.s = p.s2;
-      e = sel.active[s];
-      g.row0 = sel.row0[s];
-      g.R = de;
-      g.K = p.I;
-      g.act[0] = p.h2;
-      g.act[1] = h_lo;
-      g.dep = kCntH;
-    } else {
-      w = p.W_up;
-      g.R = p.d;
-      g.K = p.L;
-      g.act[0] = p.y_lat2;
-      g.act[1] = p.y_lat2 + (int64_t)p.T * p.L;
-      g.dep = kCntLat;
-      g.scaled = true;
-    }
+  } else if (part == kPartW2 && s < sel.n_active) {
+    w = p.W2;
+    g.s = p.s2;
+    e = sel.active[s];
+    g.row0 = sel.row0[s];
+    g.R = de;
+    g.K = p.I;
+    g.act[0] = p.h2;
+    g.act[1] = h_lo;
+    g.dep = kCntH;
+  } else if (part == kPartUp && s == 1) {
+    w = p.W_up;
+    g.R = p.d;
+    g.K = p.L;
+    g.act[0] = p.y_lat2;
+    g.act[1] = p.y_lat2 + (int64_t)p.T * p.L;
+    g.dep = kCntLat;
+    g.scaled = true;
   } else {
     w = p.Ws2;
     g.s = p.ss2;
@@ -584,55 +608,6 @@ __device__ __forceinline__ Seg segment(const FewParams& p, const Selection& sel,
   return g;
 }
 
-// The CTA's share of the layer; the producer and the consumers follow it alike.
-// V: begin(), seg(Seg), end(kind, f0, cnt, mask, first h row, gated), done(counter), selected().
-template <int WD, typename V>
-__device__ __forceinline__ void walk(const FewParams& p, const Selection& sel, V& v) {
-  constexpr int G = WD == MOE_INT4 ? 2 : 1;  // 4-byte copies of the bf16 scales of two rows
-  const uint32_t all = (1u << p.T) - 1u;
-  const int P = p.T * p.k;
-#pragma unroll 1
-  for (int part = 0; part < kParts; ++part) {
-    if ((part == kPartDown || part == kPartUp) && !p.L) continue;
-    if (part == kPartShared && !p.n_shared) continue;
-    if (part == kPartRouted && !v.selected()) return;
-    const bool pair = part == kPartShared || part == kPartRouted;
-    const int64_t total = part == kPartShared   ? p.I
-                          : part == kPartRouted ? (int64_t)sel.n_active * p.I
-                          : part == kPartUp     ? p.d
-                                                : p.L ? p.L : p.d;
-    const int64_t u1 = total / G * (blockIdx.x + 1) / gridDim.x * G;
-    int n_seg = 1;
-    if (part == kPartW2) n_seg = sel.n_active + (p.L ? 0 : p.n_shared);
-    if (part == kPartUp) n_seg = 2;
-#pragma unroll 1
-    for (int64_t u = total / G * blockIdx.x / gridDim.x * G; u < u1;) {
-      int a = 0, f = (int)u, len = (int)(u1 - u);
-      if (part == kPartRouted) {
-        a = (int)(u / p.I);
-        f = (int)(u - (int64_t)a * p.I);
-        len = (int)min(u1 - u, (int64_t)(p.I - f));
-      }
-      const int n = (len + (pair ? 7 : 15)) / (pair ? 8 : 16);  // tiles left, evenly
-      const int cnt = (len / G + n - 1) / n * G;
-      v.begin();
-#pragma unroll 1
-      for (int s = part == kPartUp && !p.n_shared ? 1 : 0; s < n_seg; ++s)
-        v.seg(segment<WD>(p, sel, part, s, a, f, cnt));
-      const bool routed = part == kPartRouted;
-      v.end(part == kPartDown              ? kDown
-            : pair                         ? kHid
-            : part == kPartW2 && p.L       ? kLat
-                                           : kOut,
-            f, cnt, routed ? sel.mask[sel.active[a]] : all, routed ? sel.row0[a] : P, routed);
-      u += cnt;
-    }
-    if (part == kPartDown) v.done(kCntDown);
-    if (part == kPartRouted) v.done(kCntH);
-    if (part == kPartW2 && p.L) v.done(kCntLat);
-  }
-}
-
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
   asm volatile(
@@ -651,64 +626,92 @@ struct Producer {
   StreamHead& hd;
   uint8_t* base;         // this warp's slot
   int slot, lane;
-  uint32_t count = 0;    // slots of the stream so far
-  uint32_t filled = 0;   // of them this warp's
+  int turn = 0;          // slot of the stream's next piece
+  uint32_t filled = 0;   // times this warp has filled its slot
   uint32_t complete = 0; // counters known to be complete
   bool failed = false;
 
-  // Waits until a step is complete; the copies after it see what it published.
-  __device__ bool step_complete(int dep) {
-    if (dep == kNoDep || (complete >> dep & 1u)) return true;
-    int ok = 1;
-    if (lane == 0) ok = counter_wait(p.bar + dep, gridDim.x, &hd.abort, p.err);
-    if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
-    complete |= 1u << dep;
-    asm volatile("fence.proxy.async;" ::: "memory");
-    return true;
-  }
-  __device__ void begin() {}
-  __device__ void end(Kind, int, int, uint32_t, int, bool) {}
-  __device__ void done(int) {}
-  __device__ bool selected() {
-    const bool ok = !failed && mbar_wait(&hd.sel_bar, 0, &hd.abort, p.err);
-    failed = __any_sync(0xffffffffu, !ok);
+  // True when the stream's next piece is this warp's, with the slot free.
+  __device__ __forceinline__ bool mine() {
+    const bool m = turn == slot && !failed;
+    turn = turn + 1 == kSlots ? 0 : turn + 1;
+    if (!m) return false;
+    const bool ok = mbar_wait_sleep(&hd.empty[slot], (filled & 1u) ^ 1u, &hd.abort, p.err);
+    if (__any_sync(0xffffffffu, !ok)) failed = true;
     return !failed;
   }
-  __device__ void seg(const Seg& g) {
+  // Waits until a step is complete; the copies after it see what it published.
+  __device__ __forceinline__ void step_complete(int dep) {
+    if (dep == kNoDep || (complete >> dep & 1u)) return;
+    int ok = 1;
+    if (lane == 0) ok = counter_wait(p.bar + dep, gridDim.x, &hd.abort, p.err);
+    if (!__shfl_sync(0xffffffffu, ok, 0)) failed = true;  // the copies bring what is there
+    complete |= 1u << dep;
+    asm volatile("fence.proxy.async;" ::: "memory");
+  }
+  // A piece without data.
+  __device__ void control(int flags, int kind) {
+    if (!mine()) return;
+    if (lane == 0) {
+      hd.info[slot].flags = flags;
+      hd.info[slot].kind = kind;
+    }
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&hd.full[slot]);
+      mbar_arrive(&hd.full[slot]);
+    }
+    if constexpr (WD == MOE_INT4) mbar_arrive(&hd.full[slot]);
+    ++filled;
+  }
+  __device__ __forceinline__ void seg(const Seg& g, int flags, int kind, int h_row0) {
     const Geo<WD> geo(g);
-    for (int c0 = 0; c0 < g.K; c0 += geo.cols, ++count) {
-      if (count % kSlots != slot || failed) continue;
+    for (int c0 = 0; c0 < g.K; c0 += geo.cols) {
+      if (!mine()) continue;
       const int cols = min(geo.cols, g.K - c0);
-      const bool ok = mbar_wait(&hd.empty[slot], (filled & 1u) ^ 1u, &hd.abort, p.err);
-      if (__any_sync(0xffffffffu, !ok)) {
-        failed = true;
-        continue;
-      }
       const uint32_t nb = Wt<WD>::bytes(cols);
-      if (lane == 0)
+      const int n = __popc(g.mask), rows = n * g.planes();
+      if (lane == 0) {
+        SlotInfo& i = hd.info[slot];
+        i.cols = cols;
+        i.wpitch = geo.wpitch;
+        i.apitch = geo.apitch;
+        i.aoff = geo.aoff;
+        i.soff = geo.soff;
+        i.plane = g.act[1] ? n * geo.apitch : 0;
+        i.mask = g.mask;
+        i.flags = (flags & (kScaled | kGated)) |
+                  (c0 == 0 ? kSegFirst | (flags & kTileFirst) : 0) |
+                  (c0 + cols == g.K ? kSegLast | (flags & kTileLast) : 0);
+        i.f0 = g.f0;
+        i.cnt = g.cnt;
+        i.row0 = h_row0;
+        i.kind = kind;
+        i.s = WD == MOE_FP8_E4M3 ? static_cast<const float*>(g.s) + c0 / 128 : nullptr;
+        i.s_ld = g.K / 128;
+        i.u_off = g.u_off;
         mbar_arrive_expect_tx(&hd.full[slot], (g.u_off ? 2 * g.cnt : g.cnt) * nb);
+      }
       __syncwarp();
       if (lane < 16 && g.has(lane))
         bulk_load(base + lane * geo.wpitch,
                   g.w + ((int64_t)g.row(lane) * g.K + c0) * Wt<WD>::kBits / 8, nb, &hd.full[slot]);
       if constexpr (WD == MOE_INT4) {
         // scales [K / 32][R]: two rows of a group a copy, into [group][16]
-        for (int i = lane; i < cols / 32 * 8; i += 32) {
-          const int grp = i >> 3, r = (i & 7) * 2;
-          if (!g.has(r)) continue;
-          const __nv_bfloat16* src =
-              (const __nv_bfloat16*)g.s + (int64_t)(c0 / 32 + grp) * g.R + g.row(r);
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
-                           smem_u32(base + geo.soff + grp * 32 + r * 2)),
-                       "l"(src)
-                       : "memory");
+        const int r = (lane & 7) * 2;
+        if (g.has(r)) {
+          const __nv_bfloat16* src = (const __nv_bfloat16*)g.s +
+                                     (int64_t)(c0 / 32 + (lane >> 3)) * g.R + g.row(r);
+          uint32_t dst = smem_u32(base + geo.soff + (lane >> 3) * 32 + r * 2);
+          for (int i = lane >> 3; i < cols / 32; i += 4, src += 4 * (int64_t)g.R, dst += 128)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src)
+                         : "memory");
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                          smem_u32(&hd.full[slot]))
                      : "memory");
       }
-      if (!step_complete(g.dep)) failed = true;  // then the copies bring what is there
-      const int n = __popc(g.mask), rows = n * g.planes();
+      step_complete(g.dep);
       if (lane == 0) mbar_arrive_expect_tx(&hd.full[slot], rows * cols * 2);
       __syncwarp();
       for (int i = lane; i < rows; i += 32) {
@@ -720,8 +723,60 @@ struct Producer {
       ++filled;
     }
   }
-  // After a failure the copies in flight still have to land before the CTA ends.
-  __device__ void finish() {
+
+  // The CTA's share of the layer.
+  __device__ void run() {
+    constexpr int G = WD == MOE_INT4 ? 2 : 1;  // 4-byte copies of the bf16 scales of two rows
+    const Selection& sel = hd.sel;
+#pragma unroll 1
+    for (int part = 0; part < kParts && !failed; ++part) {
+      if ((part == kPartDown || part == kPartUp) && !p.L) continue;
+      if (part == kPartShared && !p.n_shared) continue;
+      if (part == kPartRouted) {
+        const bool ok = mbar_wait_sleep(&hd.sel_bar, 0, &hd.abort, p.err);
+        if (__any_sync(0xffffffffu, !ok)) {
+          failed = true;
+          break;
+        }
+      }
+      const bool pair = part == kPartShared || part == kPartRouted;
+      const int total = part == kPartShared   ? p.I
+                        : part == kPartRouted ? sel.n_active * p.I
+                        : part == kPartUp     ? p.d
+                                              : p.L ? p.L : p.d;
+      int u = (int)((int64_t)(total / G) * blockIdx.x / gridDim.x) * G;
+      const int u1 = (int)((int64_t)(total / G) * (blockIdx.x + 1) / gridDim.x) * G;
+      const int kind = part == kPartDown ? kDown : pair ? kHid : part == kPartW2 && p.L ? kLat : kOut;
+      const int s0 = part == kPartUp && !p.n_shared ? 1 : 0;
+      const int s1 = part == kPartW2   ? sel.n_active + (p.L ? 0 : p.n_shared)
+                     : part == kPartUp ? 2
+                                       : 1;
+#pragma unroll 1
+      while (u < u1) {
+        int a = 0, f = u, len = u1 - u;
+        if (part == kPartRouted) {
+          a = u / p.I;
+          f = u - a * p.I;
+          len = min(len, p.I - f);
+        }
+        const int n = (len + (pair ? 7 : 15)) / (pair ? 8 : 16);  // tiles left, evenly
+        const int cnt = (len / G + n - 1) / n * G;
+#pragma unroll 1
+        for (int s = s0; s < s1; ++s) {
+          const Seg g = segment<WD>(p, sel, part, s, a, f, cnt);
+          seg(g,
+              (s == s0 ? kTileFirst : 0) | (s == s1 - 1 ? kTileLast : 0) |
+                  (g.scaled ? kScaled : 0) | (part == kPartRouted ? kGated : 0),
+              kind, part == kPartRouted ? sel.row0[a] : p.T * p.k);
+        }
+        u += cnt;
+      }
+      if (part == kPartDown) control(kDone, kCntDown);
+      if (part == kPartRouted) control(kDone, kCntH);
+      if (part == kPartW2 && p.L) control(kDone, kCntLat);
+    }
+    control(kStop, 0);
+    // after a failure the copies in flight still have to land before the CTA ends
     if (filled) mbar_wait(&hd.full[slot], (filled - 1) & 1u, nullptr, nullptr, kDrainLimitNs);
   }
 };
@@ -781,7 +836,8 @@ __device__ __forceinline__ void split_planes(float v, __nv_bfloat16& hi, __nv_bf
   lo = __float2bfloat16_rn(isinf(f) ? 0.0f : v - f);
 }
 
-// The sixteen consumer warps.  NT: groups of 8 tokens.
+// The sixteen consumer warps.  NT: groups of 8 tokens.  Every wait gives up once the CTA's abort
+// flag is set, so the warps may leave one by one.
 template <int WD, int NT>
 struct Consumer {
   const FewParams& p;
@@ -789,161 +845,51 @@ struct Consumer {
   const uint8_t* slots;
   float* red;  // [kCons][NT][16 rows][8 tokens]
   int warp, lane;
-  uint32_t used = 0;  // slots consumed so far
-  float acc[NT][4];
+  uint32_t tiles = 0;
   float ssq = 0.0f;   // of the latent features this thread has stored for its token
 
-  __device__ void begin() {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    return mbar_wait_sleep(bar, parity, &hd.abort, p.err);
   }
 
-  __device__ void seg(const Seg& g) {
-    using W = Wt<WD>;
-    const Geo<WD> geo(g);
+  // Sums the warps' partial tiles in warp order and stores the tile's features.
+  __device__ __forceinline__ bool end(const float (&acc)[NT][4], int kind, int f0, int cnt,
+                                      uint32_t mask, int row0, bool gated) {
     const int gr = lane >> 2, t4 = lane & 3;
-    const int n_act = __popc(g.mask);
-    int boff[NT];   // offset of this lane's token row among the activations, -1: absent
-    bool any[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int tok = n * 8 + gr;
-      boff[n] = g.mask >> tok & 1u ? geo.aoff + __popc(g.mask & ((1u << tok) - 1u)) * geo.apitch : -1;
-      any[n] = (g.mask >> (n * 8) & 0xffu) != 0;
-    }
-    const int plane = n_act * geo.apitch;
-    const bool two = g.act[1] != nullptr;
-    float d[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
-
-    for (int c0 = 0; c0 < g.K; c0 += geo.cols) {
-      const int cols = min(geo.cols, g.K - c0);
-      const int slot = used % kSlots;
-      mbar_wait_sleep(&hd.full[slot], used / kSlots & 1u, &hd.abort, p.err);
-      ++used;
-      const uint8_t* base = slots + (size_t)slot * kSlotBytes;
-      for (int u = warp * W::kUnit; u < cols; u += kCons * W::kUnit) {
-        float s0 = 0.0f, s1 = 0.0f;
-        float dd[NT][4];
-        if constexpr (WD == MOE_FP8_E4M3) {  // one scale block: its own sum
-          const float* s = (const float*)g.s + (c0 + u) / 128;
-          s0 = __ldg(s + (int64_t)(g.row(gr) / 128) * (g.K / 128));
-          s1 = __ldg(s + (int64_t)(g.row(gr + 8) / 128) * (g.K / 128));
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dd[n][i] = 0.0f;
-        }
-#pragma unroll
-        for (int st = 0; st < W::kUnit / W::kStep; ++st) {
-          const int col = u + st * W::kStep + t4 * W::kChunk;
-          const bool valid = col < cols;
-          uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
-          uint32_t sa = 0, sb = 0;
-          if (valid) {
-            ra = lds16(base + gr * geo.wpitch + W::bytes(col));
-            rb = lds16(base + (gr + 8) * geo.wpitch + W::bytes(col));
-            if constexpr (WD == MOE_INT4) {
-              const uint16_t* sc = (const uint16_t*)(base + geo.soff + (col >> 5) * 32);
-              sa = sc[gr] * 0x10001u;
-              sb = sc[gr + 8] * 0x10001u;
-            }
-          }
-          const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
-#pragma unroll
-          for (int h = 0; h < W::kChunk / 8; ++h) {  // 8 channels: two products
-            uint32_t a[4], b[4];
-            if constexpr (WD == MOE_BF16) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                a[i] = wa[i];
-                b[i] = wb[i];
-              }
-            } else if constexpr (WD == MOE_FP8_E4M3) {
-              e4m3x4_to_bf16(wa[2 * h], a[0], a[1]);
-              e4m3x4_to_bf16(wa[2 * h + 1], a[2], a[3]);
-              e4m3x4_to_bf16(wb[2 * h], b[0], b[1]);
-              e4m3x4_to_bf16(wb[2 * h + 1], b[2], b[3]);
-            } else {
-              int4x8_to_bf16(wa[h], sa, a);
-              int4x8_to_bf16(wb[h], sb, b);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              if (!any[n]) continue;
-              const bool on = valid && boff[n] >= 0;
-              const uint8_t* q = base + boff[n] + col * 2 + h * 16;
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (on) v = lds16(q);
-              float(&o)[4] = WD == MOE_FP8_E4M3 ? dd[n] : d[n];
-              mma16816(o, a[0], b[0], a[1], b[1], v.x, v.y);
-              mma16816(o, a[2], b[2], a[3], b[3], v.z, v.w);
-              if (two) {
-                if (on) v = lds16(q + plane);
-                mma16816(o, a[0], b[0], a[1], b[1], v.x, v.y);
-                mma16816(o, a[2], b[2], a[3], b[3], v.z, v.w);
-              }
-            }
-          }
-        }
-        if constexpr (WD == MOE_FP8_E4M3) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            d[n][0] = fmaf(s0, dd[n][0], d[n][0]);
-            d[n][1] = fmaf(s0, dd[n][1], d[n][1]);
-            d[n][2] = fmaf(s1, dd[n][2], d[n][2]);
-            d[n][3] = fmaf(s1, dd[n][3], d[n][3]);
-          }
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&hd.empty[slot]);
-    }
-    if (g.scaled) mbar_wait_sleep(&hd.inv_bar, 0, &hd.abort, p.err);
-    // only the segment's own tokens: another token's zeros times an infinite weight are NaN
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = n * 8 + t4 * 2 + (i & 1);
-        if (g.mask >> tok & 1u) acc[n][i] += g.scaled ? d[n][i] * hd.inv[tok] : d[n][i];
-      }
-  }
-
-  __device__ void end(Kind kind, int f0, int cnt, uint32_t mask, int row0, bool gated) {
-    const int gr = lane >> 2, t4 = lane & 3;
+    if (!wait(&hd.red_empty, (tiles & 1u) ^ 1u)) return false;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float* r = red + (warp * NT + n) * 128 + gr * 8 + t4 * 2;
       *reinterpret_cast<float2*>(r) = make_float2(acc[n][0], acc[n][1]);
       *reinterpret_cast<float2*>(r + 64) = make_float2(acc[n][2], acc[n][3]);
     }
-    named_barrier(1, kCons * 32);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&hd.red_full);
     const int c = warp * 32 + lane;
     const bool pair = kind == kHid;
-    const int per = pair ? 64 : 128, nr = pair ? 8 : 16;
-    const int n = c / per, row = c % nr, tok = n * 8 + c / nr % 8;
-    const bool own = c < per * NT;
+    const int per = pair ? 64 : 128;
+    const bool own = c < per * NT;  // whole warps
+    const int n = pair ? c >> 6 : c >> 7, row = pair ? c & 7 : c & 15;
+    const int tok = n * 8 + ((pair ? c >> 3 : c >> 4) & 7);
     float v = 0.0f, up = 0.0f;
     if (own) {
-      const float* r = red + n * 128 + row * 8 + tok % 8;
+      if (!wait(&hd.red_full, tiles & 1u)) return false;
+      const float* r = red + n * 128 + row * 8 + (tok & 7);
 #pragma unroll
       for (int w = 0; w < kCons; ++w) v += r[w * NT * 128];
       if (pair) {
 #pragma unroll
         for (int w = 0; w < kCons; ++w) up += r[w * NT * 128 + 64];
       }
+      __syncwarp();
     }
-    named_barrier(1, kCons * 32);  // the partial sums have been read
-    const bool live = own && row < cnt && (mask >> tok & 1u);
+    ++tiles;
+    if (lane == 0) mbar_arrive(&hd.red_empty);
+    if (!own) return true;
+    const bool live = row < cnt && (mask >> tok & 1u);
     const int f = f0 + row;
     if (kind == kHid) {
-      if (!live) return;
+      if (!live) return true;
       const int hr = row0 + __popc(mask & ((1u << tok) - 1u));
       v = silu_accurate(v) * up;
       if (gated) v *= hd.sel.row_gate[hr];
@@ -961,54 +907,65 @@ struct Consumer {
         for (int off = 8; off > 0; off >>= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
         ssq += q;
       }
-      if (!live) return;
+      if (!live) return true;
       __nv_bfloat16 hi, lo;
       split_planes(v, hi, lo);
       __nv_bfloat16* o = kind == kDown ? p.x_lat2 : p.y_lat2;
       o[(int64_t)tok * p.L + f] = hi;
       o[(int64_t)(p.T + tok) * p.L + f] = lo;
     }
+    return true;
   }
 
-  // Publishes what the CTA has stored so far: to the other CTAs' loads and bulk copies.
+  // Publishes what the CTA has stored so far to the other CTAs' loads and bulk copies: the last of
+  // the warps to come adds the CTA to the counter.
   __device__ void done(int counter) {
     const int c = warp * 32 + lane;
     if (counter == kCntLat && c < 128 * NT && c % 16 == 0)
       p.ssq[blockIdx.x * kMaxT + c / 128 * 8 + c / 16 % 8] = ssq;
     asm volatile("fence.proxy.async;" ::: "memory");
     __threadfence();
-    named_barrier(1, kCons * 32);
-    if (c == 0)
+    __syncwarp();
+    if (lane == 0 && atomicAdd(&hd.done[counter], 1u) == kCons - 1) {
+      __threadfence();
       asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.bar + counter) : "memory");
+    }
   }
 
-  __device__ bool selected() {
-    const bool ok = mbar_wait_sleep(&hd.sel_bar, 0, &hd.abort, p.err);
-    return named_barrier_and(1, kCons * 32, ok);  // all warps go on or none
-  }
-
-  // Router logits: a warp takes one expert's range of input channels.
+  // Router logits: a warp takes one expert's range of input channels, its weights in flight at once.
   __device__ void router() {
+    constexpr int kMost = 10;
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
     for (int u = warp * gridDim.x + blockIdx.x; u < p.E * p.parts; u += gridDim.x * kCons) {
-      const int e = u % p.E, q = u / p.E;
+      const int q = u / p.E, e = u - q * p.E;
       const int end = min(p.d, (q + 1) * p.part_cols);
       const float* w = p.W_r + (int64_t)e * p.d;
       float z[NT * 8];
 #pragma unroll
       for (int t = 0; t < NT * 8; ++t) z[t] = 0.0f;
-#pragma unroll 4
-      for (int c = q * p.part_cols + lane * 4; c < end; c += 128) {
-        const float4 wv = __ldg(reinterpret_cast<const float4*>(w + c));
+      for (int c0 = q * p.part_cols + lane * 4; c0 < end; c0 += 128 * kMost) {
+        float4 wv[kMost];
 #pragma unroll
-        for (int t = 0; t < NT * 8; ++t)
-          if (t < p.T) {
-            const uint2 xv = __ldg(reinterpret_cast<const uint2*>(x + (int64_t)t * p.d + c));
-            z[t] = fmaf(wv.x, __uint_as_float(xv.x << 16), z[t]);
-            z[t] = fmaf(wv.y, __uint_as_float(xv.x & 0xffff0000u), z[t]);
-            z[t] = fmaf(wv.z, __uint_as_float(xv.y << 16), z[t]);
-            z[t] = fmaf(wv.w, __uint_as_float(xv.y & 0xffff0000u), z[t]);
+        for (int i = 0; i < kMost; ++i)
+          wv[i] = c0 + i * 128 < end ? __ldg(reinterpret_cast<const float4*>(w + c0 + i * 128))
+                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int t = 0; t < NT * 8; ++t) {
+          if (t >= p.T) break;
+          const __nv_bfloat16* xr = x + (int64_t)t * p.d + c0;
+          uint2 xv[kMost];
+#pragma unroll
+          for (int i = 0; i < kMost; ++i)
+            xv[i] = c0 + i * 128 < end ? __ldg(reinterpret_cast<const uint2*>(xr + i * 128))
+                                       : make_uint2(0, 0);
+#pragma unroll
+          for (int i = 0; i < kMost; ++i) {
+            z[t] = fmaf(wv[i].x, __uint_as_float(xv[i].x << 16), z[t]);
+            z[t] = fmaf(wv[i].y, __uint_as_float(xv[i].x & 0xffff0000u), z[t]);
+            z[t] = fmaf(wv[i].z, __uint_as_float(xv[i].y << 16), z[t]);
+            z[t] = fmaf(wv[i].w, __uint_as_float(xv[i].y & 0xffff0000u), z[t]);
           }
+        }
       }
 #pragma unroll
       for (int t = 0; t < NT * 8; ++t)
@@ -1017,6 +974,163 @@ struct Consumer {
           if (lane == 0) p.logits[((int64_t)q * p.T + t) * p.E + e] = v;
         }
     }
+  }
+
+  __device__ void run() {
+    using W = Wt<WD>;
+    const int gr = lane >> 2, t4 = lane & 3;
+    float acc[NT][4], d[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = d[n][i] = 0.0f;
+    int slot = 0;
+    uint32_t parity = 0;
+    while (true) {
+      if (!wait(&hd.full[slot], parity)) return;
+      const SlotInfo& si = hd.info[slot];
+      const int flags = si.flags;
+      if (flags & (kDone | kStop)) {
+        if (flags & kStop) return;
+        const int counter = si.kind;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&hd.empty[slot]);
+        done(counter);
+      } else {
+        const int cols = si.cols, f0 = si.f0, cnt = si.cnt, kind = si.kind, row0 = si.row0;
+        const uint32_t mask = si.mask;
+        const uint8_t* base = slots + (size_t)slot * kSlotBytes;
+        const uint8_t* wa_row = base + gr * si.wpitch;
+        const uint8_t* wb_row = wa_row + 8 * si.wpitch;
+        const uint8_t* sc_row = base + si.soff;
+        const int plane = si.plane;
+        const uint8_t* arow[NT];  // this lane's token row among the activations
+        bool on[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int tok = n * 8 + gr;
+          on[n] = mask >> tok & 1u;
+          arow[n] = base + si.aoff + __popc(mask & ((1u << tok) - 1u)) * si.apitch;
+        }
+        const float *s0p = nullptr, *s1p = nullptr;
+        if constexpr (WD == MOE_FP8_E4M3) {
+          const int r0 = f0 + min(gr, cnt - 1);
+          const int r1 = si.u_off ? r0 + si.u_off : f0 + min(gr + 8, cnt - 1);
+          s0p = si.s + (r0 >> 7) * si.s_ld;
+          s1p = si.s + (r1 >> 7) * si.s_ld;
+        }
+        if (flags & kSegFirst) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
+        }
+#pragma unroll 1
+        for (int u = warp * W::kUnit; u < cols; u += kCons * W::kUnit) {
+          float s0 = 0.0f, s1 = 0.0f;
+          float dd[NT][4];
+          if constexpr (WD == MOE_FP8_E4M3) {  // one scale block: its own sum
+            s0 = __ldg(s0p + (u >> 7));
+            s1 = __ldg(s1p + (u >> 7));
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) dd[n][i] = 0.0f;
+          }
+#pragma unroll
+          for (int st = 0; st < W::kUnit / W::kStep; ++st) {
+            const int col = u + st * W::kStep + t4 * W::kChunk;
+            const bool valid = col < cols;
+            uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
+            uint32_t sa = 0, sb = 0;
+            if (valid) {
+              ra = lds16(wa_row + W::bytes(col));
+              rb = lds16(wb_row + W::bytes(col));
+              if constexpr (WD == MOE_INT4) {
+                const uint16_t* sc = (const uint16_t*)(sc_row + col);  // 32 bytes a group of 32
+                sa = sc[gr] * 0x10001u;
+                sb = sc[gr + 8] * 0x10001u;
+              }
+            }
+            const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+#pragma unroll
+            for (int h = 0; h < W::kChunk / 8; ++h) {  // 8 channels: two products
+              uint32_t a[4], b[4];
+              if constexpr (WD == MOE_BF16) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  a[i] = wa[i];
+                  b[i] = wb[i];
+                }
+              } else if constexpr (WD == MOE_FP8_E4M3) {
+                e4m3x4_to_bf16(wa[2 * h], a[0], a[1]);
+                e4m3x4_to_bf16(wa[2 * h + 1], a[2], a[3]);
+                e4m3x4_to_bf16(wb[2 * h], b[0], b[1]);
+                e4m3x4_to_bf16(wb[2 * h + 1], b[2], b[3]);
+              } else {
+                int4x8_to_bf16(wa[h], sa, a);
+                int4x8_to_bf16(wb[h], sb, b);
+              }
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                if (NT > 1 && !(mask >> (n * 8) & 0xffu)) continue;
+                const bool ok = valid && on[n];
+                const uint8_t* q = arow[n] + col * 2 + h * 16;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (ok) v = lds16(q);
+                float(&o)[4] = WD == MOE_FP8_E4M3 ? dd[n] : d[n];
+                mma16816(o, a[0], b[0], a[1], b[1], v.x, v.y);
+                mma16816(o, a[2], b[2], a[3], b[3], v.z, v.w);
+                if (plane) {
+                  if (ok) v = lds16(q + plane);
+                  mma16816(o, a[0], b[0], a[1], b[1], v.x, v.y);
+                  mma16816(o, a[2], b[2], a[3], b[3], v.z, v.w);
+                }
+              }
+            }
+          }
+          if constexpr (WD == MOE_FP8_E4M3) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              d[n][0] = fmaf(s0, dd[n][0], d[n][0]);
+              d[n][1] = fmaf(s0, dd[n][1], d[n][1]);
+              d[n][2] = fmaf(s1, dd[n][2], d[n][2]);
+              d[n][3] = fmaf(s1, dd[n][3], d[n][3]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&hd.empty[slot]);
+        if (flags & kSegLast) {
+          const bool scaled = flags & kScaled;
+          if (scaled && !wait(&hd.inv_bar, 0)) return;
+          // only the segment's own tokens: another token's zeros times an infinite weight are NaN
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int tok = n * 8 + t4 * 2 + (i & 1);
+              const float v = scaled ? d[n][i] * hd.inv[tok] : d[n][i];
+              acc[n][i] += mask >> tok & 1u ? v : 0.0f;
+            }
+          if (flags & kTileLast) {
+            if (!end(acc, kind, f0, cnt, mask_of_tile(kind, mask), row0, flags & kGated)) return;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+          }
+        }
+      }
+      if (++slot == kSlots) {
+        slot = 0;
+        parity ^= 1u;
+      }
+    }
+  }
+  // The tokens of a whole tile: its only segment's, or all for sums over segments.
+  __device__ __forceinline__ uint32_t mask_of_tile(int kind, uint32_t mask) const {
+    return kind == kHid || kind == kDown ? mask : (1u << p.T) - 1u;
   }
 };
 
@@ -1036,16 +1150,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
     }
     mbar_init(&hd.sel_bar, kSelWarps);
     mbar_init(&hd.inv_bar, kSelWarps);
+    mbar_init(&hd.red_full, kCons);
+    mbar_init(&hd.red_empty, kCons);
     hd.abort = 0;
-    hd.sel.n_active = 0;
+    for (int i = 0; i < 4; ++i) hd.done[i] = 0;
     fence_barrier_init();
   }
   __syncthreads();
 
   if (warp < kSlots) {
     Producer<WD> v{p, hd, slots + (size_t)warp * kSlotBytes, warp, lane};
-    walk<WD>(p, hd.sel, v);
-    v.finish();
+    v.run();
   } else if (warp < kFirstCons) {
     int ok = 1;
     if (lane == 0) ok = counter_wait(p.bar + kCntRouter, gridDim.x, &hd.abort, p.err);
@@ -1069,7 +1184,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
     Consumer<WD, NT> v{p, hd, slots, red, warp - kFirstCons, lane};
     v.router();
     v.done(kCntRouter);
-    walk<WD>(p, hd.sel, v);
+    v.run();
   }
 }
 
