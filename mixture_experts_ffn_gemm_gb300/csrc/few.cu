@@ -38,8 +38,7 @@ struct FewParams {
   void* out;
   uint32_t* err;
   uint32_t* bar;   // one arrival counter per barrier, zeroed before the launch
-  float* logits;   // [parts][T][E]: sums over consecutive ranges of part_cols input channels
-  int parts, part_cols;
+  float* logits;   // [T][E], zeroed before the launch
   // fp32 kernel
   float* x_lat;    // [T][L]
   float* h;        // [T * k + T][I]: routed rows expert by expert, then the shared rows
@@ -51,6 +50,7 @@ struct FewParams {
 
 struct Selection {
   uint32_t mask[kMaxE + 1];      // tokens of each expert
+  float bias[kMaxE + 1];         // b
   int16_t slot[kMaxE + 1];       // its place in active
   int16_t active[kMaxPairs];     // distinct selected experts, ascending
   int16_t row0[kMaxPairs + 1];   // first h row of each
@@ -105,34 +105,41 @@ __device__ __forceinline__ uint32_t key_bits(float v) {
 }
 
 // One warp selects the experts of token t: k rounds of the largest key, ties to the lower index.
-// Lane l holds experts l, l + 32, ... in registers (N >= ceil(E / 32) of them).
+// Lane l holds experts l, l + 32, ... in registers (N >= ceil(E / 32) of them).  Its logits may still
+// be on their way: the launch starts with zeros in their place, no logit is stored as +0, and the
+// warp reads until none is left (one trip to memory instead of a counter's and then the logits').
 template <int N>
-__device__ void select_token(const FewParams& p, int t, Selection& sel) {
+__device__ bool select_token(const FewParams& p, int t, Selection& sel, volatile int* abort) {
   const int lane = threadIdx.x & 31;
   uint32_t key[N];
   float z[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) z[j] = 0.0f;
-  constexpr int Q = N > 12 ? 1 : 2;
   const float* lg = p.logits + (int64_t)t * p.E + lane;
-  for (int q = 0; q < p.parts; q += Q) {  // all loads of Q ranges in flight
-    float v[Q][N];
+  uint64_t t0 = 0;
+  while (true) {
+    bool all = true;
 #pragma unroll
-    for (int i = 0; i < Q; ++i)
+    for (int j = 0; j < N; ++j) {
+      z[j] = -0.0f;
+      if (lane + 32 * j < p.E)
+        asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(z[j]) : "l"(lg + 32 * j));
+    }
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        v[i][j] = q + i < p.parts && lane + 32 * j < p.E
-                      ? __ldcg(lg + (int64_t)(q + i) * p.T * p.E + 32 * j)
-                      : 0.0f;
-#pragma unroll
-    for (int i = 0; i < Q; ++i)
-#pragma unroll
-      for (int j = 0; j < N; ++j) z[j] += v[i][j];
+    for (int j = 0; j < N; ++j) all = all && __float_as_uint(z[j]) != 0u;
+    if (__all_sync(0xffffffffu, all)) break;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    bool stop = abort && *abort;
+    if (now - t0 > kWaitLimitNs) {
+      if (abort) *abort = 1;
+      raise_flag(p.err, kErrTimeout);
+      stop = true;
+    }
+    if (__any_sync(0xffffffffu, stop)) return false;
   }
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     z[j] = 1.0f / (1.0f + expf(-z[j]));
-    key[j] = lane + 32 * j < p.E ? key_bits(z[j] + __ldg(p.b + lane + 32 * j)) : 0u;
+    key[j] = lane + 32 * j < p.E ? key_bits(z[j] + sel.bias[lane + 32 * j]) : 0u;
   }
   float my_s = 0.0f, den = 0.0f;
   int my_e = 0;
@@ -164,23 +171,26 @@ __device__ void select_token(const FewParams& p, int t, Selection& sel) {
     sel.pair_e[t * p.k + lane] = (int16_t)my_e;
     sel.pair_g[t * p.k + lane] = p.gate_scale * my_s / den;
   }
+  return true;
 }
 
 // The CTA's copy of the selection, by n_warps warps of which this thread is number tid (barrier
 // `bar` is theirs): per-expert token masks, the distinct experts in index order, the first h row of
-// each and each row's gate.
-__device__ void build_selection(const FewParams& p, Selection& sel, int tid, int n_warps, int bar) {
+// each and each row's gate.  False when a wait for the logits gave up.
+__device__ bool build_selection(const FewParams& p, Selection& sel, int tid, int n_warps, int bar,
+                                volatile int* abort) {
   const int n = n_warps * 32, lane = tid & 31;
-  for (int e = tid; e < p.E; e += n) sel.mask[e] = 0;
-  for (int t = tid >> 5; t < p.T; t += n_warps) {
-    if (p.E <= 64)
-      select_token<2>(p, t, sel);
-    else if (p.E <= 384)
-      select_token<12>(p, t, sel);
-    else
-      select_token<32>(p, t, sel);
+  for (int e = tid; e < p.E; e += n) {
+    sel.mask[e] = 0;
+    sel.bias[e] = __ldg(p.b + e);
   }
   named_barrier(bar, n);
+  bool ok = true;
+  for (int t = tid >> 5; t < p.T && ok; t += n_warps)
+    ok = p.E <= 64    ? select_token<2>(p, t, sel, abort)
+         : p.E <= 384 ? select_token<12>(p, t, sel, abort)
+                      : select_token<32>(p, t, sel, abort);
+  if (!named_barrier_and(bar, n, ok)) return false;
   for (int i = tid; i < p.T * p.k; i += n) atomicOr(&sel.mask[sel.pair_e[i]], 1u << (i / p.k));
   named_barrier(bar, n);
   if (tid < 32) {  // compact: 32 experts at a time
@@ -214,7 +224,11 @@ __device__ void build_selection(const FewParams& p, Selection& sel, int tid, int
     sel.row_gate[sel.row0[sel.slot[e]] + __popc(sel.mask[e] & ((1u << t) - 1u))] = sel.pair_g[i];
   }
   named_barrier(bar, n);
+  return true;
 }
+
+// A logit as it is stored: +0 marks one that is not computed yet.
+__device__ __forceinline__ float stored_logit(float z) { return z == 0.0f ? -0.0f : z; }
 
 // 8 values that an earlier step of this kernel wrote (past L1).
 __device__ __forceinline__ void load8_cg(const float* p, float (&v)[8]) {
@@ -291,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
           const float z = warp_sum(acc[n]);
           if (lane == 0) {
             if (u < p.E)
-              p.logits[(int64_t)n * p.E + u] = z;
+              p.logits[(int64_t)n * p.E + u] = stored_logit(z);
             else
               p.x_lat[(int64_t)n * p.L + u - p.E] = z;
           }
@@ -312,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
   if (!grid_barrier(p.bar, p.err)) return;
 
   // B
-  build_selection(p, sel, threadIdx.x, kWarps, 1);
+  if (!build_selection(p, sel, threadIdx.x, kWarps, 1, nullptr)) return;
   for (int64_t u = gw; u < (int64_t)sel.n_active * p.I; u += nw) {
     const int a = (int)(u / p.I), f = (int)(u - (int64_t)a * p.I);
     const int64_t e = sel.active[a];
@@ -431,9 +445,10 @@ constexpr int kSelWarps = 4;
 constexpr int kFirstCons = kSlots + kSelWarps;
 constexpr int kStreamThreads = 32 * (kFirstCons + kCons);
 constexpr int kSlotBytes = 48640;
+static_assert(kCons == 4 * kSlots && (kSlots & (kSlots - 1)) == 0, "four consumer warps to a slot");
 
 // Counters of the launch (FewParams::bar): arrivals of CTAs at the end of each part.
-enum : int { kCntRouter = 0, kCntDown = 1, kCntH = 2, kCntLat = 3 };
+enum : int { kCntDown = 0, kCntH = 1, kCntLat = 2 };
 constexpr int kNoDep = -1;
 
 template <int WD>
@@ -450,68 +465,51 @@ struct Wt {
 // (two rows, four words each) meet different banks.
 __device__ __forceinline__ int slot_pitch(int bytes) { return ((bytes + 127) & ~127) + 64; }
 
-// 16 weight rows (pair: rows f0.. of W1 and of W3, eight each) times activation rows, over K.
-struct Seg {
-  const uint8_t* w;   // matrix [R][K]
-  const void* s;      // its scales
-  int R, K;
-  int f0, cnt, u_off; // features f0 .. f0+cnt; u_off > 0: pairs, W3 rows at + u_off
-  const __nv_bfloat16* act[2];  // planes; the second may be null
-  int row0;           // first activation row, or -1: the tokens of mask
-  uint32_t mask;      // tokens
-  int dep;            // counter that must be complete before the activations are read
-  bool scaled;        // multiply by the tokens' 1 / rms (latent up-projection)
-
-  __device__ __forceinline__ int planes() const { return act[1] ? 2 : 1; }
-  __device__ __forceinline__ int row(int i) const {  // feature row of slot row i (clamped)
-    if (u_off) return (i < 8 ? 0 : u_off) + f0 + min(i & 7, cnt - 1);
-    return f0 + min(i, cnt - 1);
-  }
-  __device__ __forceinline__ bool has(int i) const { return (u_off ? i & 7 : i) < cnt; }
-};
-
-// Geometry of a segment's slots.
+// Channels a slot of a segment takes (K in all, nr activation rows), cut evenly.
 template <int WD>
-struct Geo {
-  int cols, wpitch, apitch, soff, aoff;
-  __device__ __forceinline__ explicit Geo(const Seg& g) {
-    const int nr = __popc(g.mask) * g.planes();
-    constexpr int per16 = 16 * Wt<WD>::kBits / 8 + (WD == MOE_INT4 ? 1 : 0);
-    int c = (kSlotBytes - (16 + nr) * 64) / (per16 + 2 * nr);
-    constexpr int half = 8 * Wt<WD>::kUnit;  // half a round of the consumer warps
-    const int gran = c >= half ? half : Wt<WD>::kGran;
-    const int n = (g.K + c / gran * gran - 1) / (c / gran * gran);  // slots, evenly
-    c = ((g.K + n - 1) / n + gran - 1) / gran * gran;
-    cols = c;
-    wpitch = slot_pitch(Wt<WD>::bytes(c));
-    apitch = slot_pitch(c * 2);
-    soff = 16 * wpitch;
-    aoff = soff + (WD == MOE_INT4 ? c : 0);  // c / 32 groups of 16 bf16 scales
-  }
-};
+__device__ __forceinline__ int slot_cols(int K, int nr) {
+  constexpr int per16 = 16 * Wt<WD>::kBits / 8 + (WD == MOE_INT4 ? 1 : 0);
+  constexpr int round = 4 * Wt<WD>::kUnit;  // a round of the slot's four consumer warps
+  int c = (kSlotBytes - (16 + nr) * 64) / (per16 + 2 * nr);
+  const int gran = c >= 4 * round ? round : Wt<WD>::kGran;
+  c = c / gran * gran;
+  const int n = (K + c - 1) / c;
+  return ((K + n - 1) / n + gran - 1) / gran * gran;
+}
 
 // What a slot holds, written by its producer for the consumers.
-enum : int {
-  kSegFirst = 1, kSegLast = 2, kTileFirst = 4, kTileLast = 8, kScaled = 16, kGated = 32,
-  kDone = 64,  // no data: the CTA's share of a part is complete, publish it (counter in kind)
-  kStop = 128  // no data: the stream ends
-};
+enum : int { kScaled = 1, kStop = 2 };  // kStop: no data, the stream ends
 struct SlotInfo {
   int cols, wpitch, apitch, aoff;
   int soff, plane;   // int4 scales; distance of the activations' second plane (0: one plane)
   uint32_t mask;     // tokens
   int flags;
-  int f0, cnt, row0, kind;
+  int f0, cnt;
   const float* s;    // e4m3: scale of the matrix's row block 0 and the slot's first channel
   int s_ld, u_off;   // scales per row block; distance of the W3 rows (0: no pairs)
+  uint32_t tile;     // the tile it belongs to; the ones before it are complete in the stream
 };
 
+// A tile of features in stream order; kPublish: the CTA's share of a part is complete, add it to
+// counter f0.
+enum Kind { kDown, kHid, kLat, kOut, kPublish };
+struct Tile {
+  int kind, f0, cnt, row0;  // first h row
+  uint32_t mask;
+  int gated;
+};
+// Between two pieces of one slot the stream has kSlots - 1 others: at most that many tiles and the
+// three publishings; twice that for the piece the producer is ahead.
+constexpr int kTiles = 16;
+
 struct StreamHead {
-  uint64_t full[kSlots], empty[kSlots], sel_bar, inv_bar, red_full, red_empty;
+  uint64_t info_bar[kSlots], full[kSlots], empty[kSlots], sel_bar, inv_bar, red_full, red_empty;
   SlotInfo info[kSlots];
+  Tile tile[kSlots][kTiles];  // each producer's own, for its consumers
+  uint4 zeros;
   float inv[kMaxT];
   int abort;
-  uint32_t done[4];  // consumer warps through each part (a warp may be a part ahead of another)
+  uint32_t done[3];  // consumer warps through each part (a warp may be a part ahead of another)
   Selection sel;
 };
 constexpr size_t head_bytes() { return (sizeof(StreamHead) + 127) & ~size_t(127); }
@@ -520,93 +518,8 @@ constexpr size_t stream_smem(int nt) {
 }
 static_assert(stream_smem(2) <= 227 * 1024, "one CTA's shared memory");
 
-enum Kind { kDown, kHid, kLat, kOut };
-
 // The parts of the layer in stream order, each split evenly over the CTAs by features.
 enum Part { kPartDown, kPartShared, kPartRouted, kPartW2, kPartUp, kParts };
-
-// The s-th segment of a tile of features f0 .. f0 + cnt of a part (a: the routed expert's place).
-template <int WD>
-__device__ __forceinline__ Seg segment(const FewParams& p, const Selection& sel, int part, int s,
-                                       int a, int f0, int cnt) {
-  const uint32_t all = (1u << p.T) - 1u;
-  const int P = p.T * p.k, de = p.L ? p.L : p.d;
-  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
-  const __nv_bfloat16* h_lo = p.h2 + (int64_t)(P + p.T) * p.I;
-  Seg g;
-  g.s = nullptr;
-  g.f0 = f0;
-  g.cnt = cnt;
-  g.u_off = 0;
-  g.act[0] = x;
-  g.act[1] = nullptr;
-  g.row0 = 0;
-  g.mask = all;
-  g.dep = kNoDep;
-  g.scaled = false;
-  g.R = p.L;
-  g.K = p.d;
-  int64_t e = -1;  // routed expert
-  const void* w;
-  if (part == kPartDown) {
-    w = p.W_down;
-  } else if (part == kPartShared || part == kPartRouted) {
-    g.R = 2 * p.I;
-    g.u_off = p.I;
-    if (part == kPartShared) {
-      w = p.Ws13;
-      g.s = p.ss13;
-    } else {
-      w = p.W13;
-      g.s = p.s13;
-      e = sel.active[a];
-      g.K = de;
-      g.row0 = -1;
-      if (p.L) {
-        g.act[0] = p.x_lat2;
-        g.act[1] = p.x_lat2 + (int64_t)p.T * p.L;
-        g.dep = kCntDown;
-      }
-    }
-  } else if (part == kPartW2 && s < sel.n_active) {
-    w = p.W2;
-    g.s = p.s2;
-    e = sel.active[s];
-    g.row0 = sel.row0[s];
-    g.R = de;
-    g.K = p.I;
-    g.act[0] = p.h2;
-    g.act[1] = h_lo;
-    g.dep = kCntH;
-  } else if (part == kPartUp && s == 1) {
-    w = p.W_up;
-    g.R = p.d;
-    g.K = p.L;
-    g.act[0] = p.y_lat2;
-    g.act[1] = p.y_lat2 + (int64_t)p.T * p.L;
-    g.dep = kCntLat;
-    g.scaled = true;
-  } else {
-    w = p.Ws2;
-    g.s = p.ss2;
-    g.R = p.d;
-    g.K = p.I;
-    g.act[0] = p.h2;
-    g.act[1] = h_lo;
-    g.row0 = P;
-    g.dep = kCntH;
-  }
-  g.w = static_cast<const uint8_t*>(w);
-  if (e >= 0) {
-    g.mask = sel.mask[e];
-    g.w += e * g.R * g.K * Wt<WD>::kBits / 8;
-    if constexpr (WD == MOE_FP8_E4M3)
-      g.s = static_cast<const float*>(g.s) + e * (g.R / 128) * (g.K / 128);
-    if constexpr (WD == MOE_INT4)
-      g.s = static_cast<const __nv_bfloat16*>(g.s) + e * (g.K / 32) * g.R;
-  }
-  return g;
-}
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
@@ -626,16 +539,15 @@ struct Producer {
   StreamHead& hd;
   uint8_t* base;         // this warp's slot
   int slot, lane;
-  int turn = 0;          // slot of the stream's next piece
+  int turn = 0;          // slot of the stream's next piece (pieces go round the slots)
   uint32_t filled = 0;   // times this warp has filled its slot
+  uint32_t tile = 0;     // tiles begun
   uint32_t complete = 0; // counters known to be complete
   bool failed = false;
 
-  // True when the stream's next piece is this warp's, with the slot free.
-  __device__ __forceinline__ bool mine() {
-    const bool m = turn == slot && !failed;
-    turn = turn + 1 == kSlots ? 0 : turn + 1;
-    if (!m) return false;
+  // Waits until the consumers have left the slot.
+  __device__ __forceinline__ bool slot_free() {
+    if (failed) return false;
     const bool ok = mbar_wait_sleep(&hd.empty[slot], (filled & 1u) ^ 1u, &hd.abort, p.err);
     if (__any_sync(0xffffffffu, !ok)) failed = true;
     return !failed;
@@ -649,62 +561,98 @@ struct Producer {
     complete |= 1u << dep;
     asm volatile("fence.proxy.async;" ::: "memory");
   }
-  // A piece without data.
-  __device__ void control(int flags, int kind) {
-    if (!mine()) return;
-    if (lane == 0) {
-      hd.info[slot].flags = flags;
-      hd.info[slot].kind = kind;
-    }
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(&hd.full[slot]);
-      mbar_arrive(&hd.full[slot]);
-    }
-    if constexpr (WD == MOE_INT4) mbar_arrive(&hd.full[slot]);
-    ++filled;
+  __device__ __forceinline__ void next_tile(int kind, int f0, int cnt, int row0, uint32_t mask,
+                                            int gated) {
+    if (failed) return;  // no longer paced by the slot: the consumers still read what is there
+    if (lane == 0) hd.tile[slot][tile % kTiles] = Tile{kind, f0, cnt, row0, mask, gated};
+    ++tile;
   }
-  __device__ __forceinline__ void seg(const Seg& g, int flags, int kind, int h_row0) {
-    const Geo<WD> geo(g);
-    for (int c0 = 0; c0 < g.K; c0 += geo.cols) {
-      if (!mine()) continue;
-      const int cols = min(geo.cols, g.K - c0);
+
+  // Matrices [R][K] (one, or one of each expert) and the activation rows that they meet.
+  struct Source {
+    const uint8_t* w;
+    const void* s;             // scales
+    int R, K;
+    int u_off;                 // > 0: pairs of rows, the W3 rows at + u_off
+    const __nv_bfloat16* act;  // plane 0; plane 1 at + plane elements unless plane is 0
+    int64_t plane;
+    bool tokens;               // activation rows are the tokens of the mask, else row0 ...
+    int dep;                   // part that must be complete before the activations are read
+    bool scaled;               // multiply by the tokens' 1 / rms
+    int lane_cols;             // lane n - 1: slot_cols() for n tokens
+
+    __device__ __forceinline__ void fit(int lane) {
+      lane_cols = slot_cols<WD>(K, (lane % kMaxT + 1) * (plane ? 2 : 1));
+    }
+  };
+
+  // The segment of matrix e (-1: the only one) for features f0 .. f0 + cnt and the tokens of mask:
+  // this warp's pieces of it.
+  __device__ __forceinline__ void seg(const Source& g, int e, int f0, int cnt, uint32_t mask,
+                                      int row0) {
+    const int n = __popc(mask);
+    const int step = __shfl_sync(0xffffffffu, g.lane_cols, n - 1);
+    int c0 = ((slot - turn) & (kSlots - 1)) * step;  // the first that falls to this warp
+    int pieces = 0;  // without a division: K / step is small
+    for (int c = 0; c < g.K; c += step) ++pieces;
+    turn = (turn + pieces) & (kSlots - 1);
+    if (c0 >= g.K) return;
+    const uint8_t* w = g.w;
+    const void* sc = g.s;
+    if (e >= 0) {
+      w += (int64_t)e * g.R * g.K * Wt<WD>::kBits / 8;
+      if constexpr (WD == MOE_FP8_E4M3)
+        sc = static_cast<const float*>(sc) + (int64_t)e * (g.R >> 7) * (g.K >> 7);
+      if constexpr (WD == MOE_INT4)
+        sc = static_cast<const __nv_bfloat16*>(sc) + (int64_t)e * (g.K >> 5) * g.R;
+    }
+    const int wpitch = slot_pitch(Wt<WD>::bytes(step)), apitch = slot_pitch(step * 2);
+    const int soff = 16 * wpitch, aoff = soff + (WD == MOE_INT4 ? step : 0);
+    const int rows = n * (g.plane ? 2 : 1);
+    // this lane's weight row
+    const int r = g.u_off ? lane & 7 : lane;
+    const bool has = lane < 16 && r < cnt;
+    const uint8_t* w_row =
+        w + (int64_t)(f0 + r + (g.u_off && lane >= 8 ? g.u_off : 0)) * g.K * Wt<WD>::kBits / 8;
+    // this lane's activation row (rows <= 32)
+    const int pl = lane >= n, j = lane - pl * n;
+    const int a_src = lane < rows ? (g.tokens ? nth_token(mask, j) : row0 + j) : 0;
+    const __nv_bfloat16* a_row = g.act + pl * g.plane + (int64_t)a_src * g.K;
+    for (; c0 < g.K; c0 += kSlots * step) {
+      if (!slot_free()) return;
+      const int cols = min(step, g.K - c0);
       const uint32_t nb = Wt<WD>::bytes(cols);
-      const int n = __popc(g.mask), rows = n * g.planes();
       if (lane == 0) {
         SlotInfo& i = hd.info[slot];
         i.cols = cols;
-        i.wpitch = geo.wpitch;
-        i.apitch = geo.apitch;
-        i.aoff = geo.aoff;
-        i.soff = geo.soff;
-        i.plane = g.act[1] ? n * geo.apitch : 0;
-        i.mask = g.mask;
-        i.flags = (flags & (kScaled | kGated)) |
-                  (c0 == 0 ? kSegFirst | (flags & kTileFirst) : 0) |
-                  (c0 + cols == g.K ? kSegLast | (flags & kTileLast) : 0);
-        i.f0 = g.f0;
-        i.cnt = g.cnt;
-        i.row0 = h_row0;
-        i.kind = kind;
-        i.s = WD == MOE_FP8_E4M3 ? static_cast<const float*>(g.s) + c0 / 128 : nullptr;
-        i.s_ld = g.K / 128;
+        i.wpitch = wpitch;
+        i.apitch = apitch;
+        i.aoff = aoff;
+        i.soff = soff;
+        i.plane = g.plane ? n * apitch : 0;
+        i.mask = mask;
+        i.flags = g.scaled ? kScaled : 0;
+        i.f0 = f0;
+        i.cnt = cnt;
+        i.s = WD == MOE_FP8_E4M3 ? static_cast<const float*>(sc) + (c0 >> 7) : nullptr;
+        i.s_ld = g.K >> 7;
         i.u_off = g.u_off;
-        mbar_arrive_expect_tx(&hd.full[slot], (g.u_off ? 2 * g.cnt : g.cnt) * nb);
+        i.tile = tile - 1;
+        mbar_arrive(&hd.info_bar[slot]);
+        mbar_arrive_expect_tx(&hd.full[slot], (g.u_off ? 2 * cnt : cnt) * nb);
       }
       __syncwarp();
-      if (lane < 16 && g.has(lane))
-        bulk_load(base + lane * geo.wpitch,
-                  g.w + ((int64_t)g.row(lane) * g.K + c0) * Wt<WD>::kBits / 8, nb, &hd.full[slot]);
+      if (has) bulk_load(base + lane * wpitch, w_row + Wt<WD>::bytes(c0), nb, &hd.full[slot]);
       if constexpr (WD == MOE_INT4) {
-        // scales [K / 32][R]: two rows of a group a copy, into [group][16]
-        const int r = (lane & 7) * 2;
-        if (g.has(r)) {
-          const __nv_bfloat16* src = (const __nv_bfloat16*)g.s +
-                                     (int64_t)(c0 / 32 + (lane >> 3)) * g.R + g.row(r);
-          uint32_t dst = smem_u32(base + geo.soff + (lane >> 3) * 32 + r * 2);
-          for (int i = lane >> 3; i < cols / 32; i += 4, src += 4 * (int64_t)g.R, dst += 128)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src)
+        // scales [K / 32][R]: four rows of a group a copy, into [group][16]
+        const int q = (lane & 3) * 4, grp = lane >> 2;
+        if ((g.u_off ? q & 7 : q) < cnt) {
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(sc) +
+                                     (int64_t)((c0 >> 5) + grp) * g.R + f0 +
+                                     (g.u_off && q >= 8 ? g.u_off + q - 8 : q);
+          uint32_t dst = smem_u32(base + soff + grp * 32 + q * 2);
+          for (int i = grp; i < cols >> 5; i += 8, src += 8 * (int64_t)g.R, dst += 256)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src)
                          : "memory");
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
@@ -714,20 +662,19 @@ struct Producer {
       step_complete(g.dep);
       if (lane == 0) mbar_arrive_expect_tx(&hd.full[slot], rows * cols * 2);
       __syncwarp();
-      for (int i = lane; i < rows; i += 32) {
-        const int pl = i >= n, j = i - pl * n;
-        const int64_t src = g.row0 < 0 ? nth_token(g.mask, j) : g.row0 + j;
-        bulk_load(base + geo.aoff + i * geo.apitch, g.act[pl] + src * g.K + c0, cols * 2,
-                  &hd.full[slot]);
-      }
+      if (lane < rows) bulk_load(base + aoff + lane * apitch, a_row + c0, cols * 2, &hd.full[slot]);
       ++filled;
     }
   }
 
   // The CTA's share of the layer.
   __device__ void run() {
-    constexpr int G = WD == MOE_INT4 ? 2 : 1;  // 4-byte copies of the bf16 scales of two rows
+    constexpr int G = WD == MOE_INT4 ? 4 : 1;  // 8-byte copies of the bf16 scales of four rows
     const Selection& sel = hd.sel;
+    const uint32_t all = (1u << p.T) - 1u;
+    const int P = p.T * p.k, de = p.L ? p.L : p.d;
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
+    auto u8 = [](const void* q) { return static_cast<const uint8_t*>(q); };
 #pragma unroll 1
     for (int part = 0; part < kParts && !failed; ++part) {
       if ((part == kPartDown || part == kPartUp) && !p.L) continue;
@@ -739,18 +686,46 @@ struct Producer {
           break;
         }
       }
+      // one: every tile's own segment, or (W2) the segments of the selected experts; last: one more
+      Source one, last;
       const bool pair = part == kPartShared || part == kPartRouted;
-      const int total = part == kPartShared   ? p.I
-                        : part == kPartRouted ? sel.n_active * p.I
-                        : part == kPartUp     ? p.d
-                                              : p.L ? p.L : p.d;
+      int total, kind = kOut;
+      if (part == kPartDown) {
+        one = Source{u8(p.W_down), nullptr, p.L, p.d, 0, x, 0, true, kNoDep, false, 0};
+        total = p.L;
+        kind = kDown;
+      } else if (part == kPartShared) {
+        one = Source{u8(p.Ws13), p.ss13, 2 * p.I, p.d, p.I, x, 0, true, kNoDep, false, 0};
+        total = p.I;
+        kind = kHid;
+      } else if (part == kPartRouted) {
+        one = Source{u8(p.W13), p.s13, 2 * p.I, de, p.I, x, 0, true, kNoDep, false, 0};
+        if (p.L) {
+          one.act = p.x_lat2;
+          one.plane = (int64_t)p.T * p.L;
+          one.dep = kCntDown;
+        }
+        total = sel.n_active * p.I;
+        kind = kHid;
+      } else if (part == kPartW2) {
+        one = Source{u8(p.W2), p.s2, de, p.I, 0, p.h2, (int64_t)(P + p.T) * p.I, false, kCntH,
+                     false, 0};
+        total = de;
+        if (p.L) kind = kLat;
+      } else {
+        one = Source{u8(p.W_up), nullptr, p.d, p.L, 0, p.y_lat2, (int64_t)p.T * p.L, false, kCntLat,
+                     true, 0};
+        total = p.d;
+      }
+      one.fit(lane);
+      const bool with_shared = p.n_shared && (part == kPartUp || (part == kPartW2 && !p.L));
+      if (with_shared) {
+        last = Source{u8(p.Ws2), p.ss2, p.d, p.I, 0, p.h2, (int64_t)(P + p.T) * p.I, false, kCntH,
+                      false, 0};
+        last.fit(lane);
+      }
       int u = (int)((int64_t)(total / G) * blockIdx.x / gridDim.x) * G;
       const int u1 = (int)((int64_t)(total / G) * (blockIdx.x + 1) / gridDim.x) * G;
-      const int kind = part == kPartDown ? kDown : pair ? kHid : part == kPartW2 && p.L ? kLat : kOut;
-      const int s0 = part == kPartUp && !p.n_shared ? 1 : 0;
-      const int s1 = part == kPartW2   ? sel.n_active + (p.L ? 0 : p.n_shared)
-                     : part == kPartUp ? 2
-                                       : 1;
 #pragma unroll 1
       while (u < u1) {
         int a = 0, f = u, len = u1 - u;
@@ -761,38 +736,60 @@ struct Producer {
         }
         const int n = (len + (pair ? 7 : 15)) / (pair ? 8 : 16);  // tiles left, evenly
         const int cnt = (len / G + n - 1) / n * G;
+        const bool routed = part == kPartRouted;
+        const int e = routed ? sel.active[a] : -1;
+        const uint32_t mask = routed ? sel.mask[e] : all;
+        next_tile(kind, f, cnt, routed ? sel.row0[a] : P, mask, routed);
+        if (with_shared) seg(last, -1, f, cnt, all, P);
+        if (part == kPartW2) {
 #pragma unroll 1
-        for (int s = s0; s < s1; ++s) {
-          const Seg g = segment<WD>(p, sel, part, s, a, f, cnt);
-          seg(g,
-              (s == s0 ? kTileFirst : 0) | (s == s1 - 1 ? kTileLast : 0) |
-                  (g.scaled ? kScaled : 0) | (part == kPartRouted ? kGated : 0),
-              kind, part == kPartRouted ? sel.row0[a] : p.T * p.k);
+          for (int i = 0; i < sel.n_active; ++i) {
+            const int ei = sel.active[i];
+            seg(one, ei, f, cnt, sel.mask[ei], sel.row0[i]);
+          }
+        } else {
+          seg(one, e, f, cnt, mask, 0);
         }
         u += cnt;
       }
-      if (part == kPartDown) control(kDone, kCntDown);
-      if (part == kPartRouted) control(kDone, kCntH);
-      if (part == kPartW2 && p.L) control(kDone, kCntLat);
+      if (part == kPartDown) next_tile(kPublish, kCntDown, 0, 0, 0, 0);
+      if (part == kPartRouted) next_tile(kPublish, kCntH, 0, 0, 0, 0);
+      if (part == kPartW2 && p.L) next_tile(kPublish, kCntLat, 0, 0, 0, 0);
     }
-    control(kStop, 0);
+    if (slot_free() && lane == 0) {
+      hd.info[slot].flags = kStop;
+      hd.info[slot].tile = tile;
+      mbar_arrive(&hd.info_bar[slot]);
+    }
     // after a failure the copies in flight still have to land before the CTA ends
     if (filled) mbar_wait(&hd.full[slot], (filled - 1) & 1u, nullptr, nullptr, kDrainLimitNs);
   }
 };
 
-__device__ __forceinline__ uint4 lds16(const void* q) {
+// Shared-memory loads and products without side effects, which the compiler may schedule freely: the
+// addresses come from settle() after the wait for the slot, and the sums pass through settle()
+// before the slot is given back, so none leaves the time in which the slot is the consumers'.
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(smem_u32(q)));
+  asm("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "r"(addr));
   return v;
 }
+__device__ __forceinline__ uint32_t lds2(uint32_t addr) {
+  uint16_t v;
+  asm("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t settle(uint32_t v) {
+  asm volatile("" : "+r"(v)::"memory");
+  return v;
+}
+__device__ __forceinline__ void settle_sum(float& v) { asm volatile("" : "+f"(v)::"memory"); }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -810,16 +807,19 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
 }
 
 // Four e4m3 codes as bf16: exponent and mantissa bits moved to bf16's places give value * 2^-120
-// (subnormals included), the product with 2^120 is exact.  A code of all ones is NaN.
+// (subnormals included), the product with 2^120 is exact.  NaN codes are left to the caller.
 __device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   const uint32_t x0 = __byte_perm(w, 0, 0x1404), x1 = __byte_perm(w, 0, 0x3424);
   lo = mul_bf16x2(((x0 >> 4) & 0x07f007f0u) | (x0 & 0x80008000u), 0x7b807b80u);
   hi = mul_bf16x2(((x1 >> 4) & 0x07f007f0u) | (x1 & 0x80008000u), 0x7b807b80u);
-  const uint32_t bad = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-  if (bad) {
-    lo |= (bad & 0x80u ? 0x7fffu : 0u) | (bad & 0x8000u ? 0x7fff0000u : 0u);
-    hi |= (bad & 0x800000u ? 0x7fffu : 0u) | (bad & 0x80000000u ? 0x7fff0000u : 0u);
-  }
+}
+// Which of four codes are NaN (0x80 in their byte), and their bf16 values marked so.
+__device__ __forceinline__ uint32_t e4m3_nan(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+__device__ __forceinline__ void e4m3_mark_nan(uint32_t bad, uint32_t& lo, uint32_t& hi) {
+  lo |= (bad & 0x80u ? 0x7fffu : 0u) | (bad & 0x8000u ? 0x7fff0000u : 0u);
+  hi |= (bad & 0x800000u ? 0x7fffu : 0u) | (bad & 0x80000000u ? 0x7fff0000u : 0u);
 }
 
 // Eight 4-bit codes (nibbles j and j + 4 are channels 2j and 2j + 1) times their scale: 128 + u is
@@ -836,8 +836,10 @@ __device__ __forceinline__ void split_planes(float v, __nv_bfloat16& hi, __nv_bf
   lo = __float2bfloat16_rn(isinf(f) ? 0.0f : v - f);
 }
 
-// The sixteen consumer warps.  NT: groups of 8 tokens.  Every wait gives up once the CTA's abort
-// flag is set, so the warps may leave one by one.
+// The sixteen consumer warps: four to a slot, so that the latencies of a slot's few products and of
+// its bookkeeping overlap with three other slots'.  A warp adds its channels of a tile's segments
+// up over the pieces its slot gets; the tile's end brings the sixteen sums together.  NT: groups of
+// 8 tokens.  Every wait gives up once the CTA's abort flag is set, so the warps may leave one by one.
 template <int WD, int NT>
 struct Consumer {
   const FewParams& p;
@@ -845,16 +847,16 @@ struct Consumer {
   const uint8_t* slots;
   float* red;  // [kCons][NT][16 rows][8 tokens]
   int warp, lane;
-  uint32_t tiles = 0;
-  float ssq = 0.0f;   // of the latent features this thread has stored for its token
+  uint32_t tiles = 0;  // summed over warps so far
+  float ssq = 0.0f;    // of the latent features this thread has stored for its token
 
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
     return mbar_wait_sleep(bar, parity, &hd.abort, p.err);
   }
 
   // Sums the warps' partial tiles in warp order and stores the tile's features.
-  __device__ __forceinline__ bool end(const float (&acc)[NT][4], int kind, int f0, int cnt,
-                                      uint32_t mask, int row0, bool gated) {
+  __device__ __forceinline__ bool end(const float (&acc)[NT][4], const Tile& ti) {
+    const int kind = ti.kind;
     const int gr = lane >> 2, t4 = lane & 3;
     if (!wait(&hd.red_empty, (tiles & 1u) ^ 1u)) return false;
 #pragma unroll
@@ -865,7 +867,7 @@ struct Consumer {
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&hd.red_full);
-    const int c = warp * 32 + lane;
+    const int c = ((warp >> 2) + 4 * (warp & 3)) * 32 + lane;  // the first warp of every slot first
     const bool pair = kind == kHid;
     const int per = pair ? 64 : 128;
     const bool own = c < per * NT;  // whole warps
@@ -886,13 +888,13 @@ struct Consumer {
     ++tiles;
     if (lane == 0) mbar_arrive(&hd.red_empty);
     if (!own) return true;
-    const bool live = row < cnt && (mask >> tok & 1u);
-    const int f = f0 + row;
+    const bool live = row < ti.cnt && (ti.mask >> tok & 1u);
+    const int f = ti.f0 + row;
     if (kind == kHid) {
       if (!live) return true;
-      const int hr = row0 + __popc(mask & ((1u << tok) - 1u));
+      const int hr = ti.row0 + __popc(ti.mask & ((1u << tok) - 1u));
       v = silu_accurate(v) * up;
-      if (gated) v *= hd.sel.row_gate[hr];
+      if (ti.gated) v *= hd.sel.row_gate[hr];
       __nv_bfloat16 hi, lo;
       split_planes(v, hi, lo);
       const int64_t at = (int64_t)hr * p.I + f;
@@ -920,7 +922,7 @@ struct Consumer {
   // Publishes what the CTA has stored so far to the other CTAs' loads and bulk copies: the last of
   // the warps to come adds the CTA to the counter.
   __device__ void done(int counter) {
-    const int c = warp * 32 + lane;
+    const int c = ((warp >> 2) + 4 * (warp & 3)) * 32 + lane;
     if (counter == kCntLat && c < 128 * NT && c % 16 == 0)
       p.ssq[blockIdx.x * kMaxT + c / 128 * 8 + c / 16 % 8] = ssq;
     asm volatile("fence.proxy.async;" ::: "memory");
@@ -932,18 +934,23 @@ struct Consumer {
     }
   }
 
-  // Router logits: a warp takes one expert's range of input channels, its weights in flight at once.
+  // Router logits: the CTA takes every gridDim-th expert, an expert's input channels split over as
+  // many warps as there are for it; a warp's weights are in flight at once.
   __device__ void router() {
-    constexpr int kMost = 10;
+    constexpr int kMost = 8;
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
-    for (int u = warp * gridDim.x + blockIdx.x; u < p.E * p.parts; u += gridDim.x * kCons) {
-      const int q = u / p.E, e = u - q * p.E;
-      const int end = min(p.d, (q + 1) * p.part_cols);
+    const int n_e = (p.E + (int)gridDim.x - 1) / (int)gridDim.x;  // experts of a CTA, at most
+    const int S = max(kCons / n_e, 1), step = kCons / S;
+    const int part = ((p.d + S - 1) / S + 127) / 128 * 128;
+    for (int i0 = 0; i0 < n_e; i0 += step) {
+      const int q = warp % S, e = blockIdx.x + (i0 + warp / S) * (int)gridDim.x;
+      const bool on = warp / S < step && e < p.E;
+      const int end = on ? min(p.d, (q + 1) * part) : 0;
       const float* w = p.W_r + (int64_t)e * p.d;
       float z[NT * 8];
 #pragma unroll
       for (int t = 0; t < NT * 8; ++t) z[t] = 0.0f;
-      for (int c0 = q * p.part_cols + lane * 4; c0 < end; c0 += 128 * kMost) {
+      for (int c0 = q * part + lane * 4; c0 < end; c0 += 128 * kMost) {
         float4 wv[kMost];
 #pragma unroll
         for (int i = 0; i < kMost; ++i)
@@ -971,166 +978,195 @@ struct Consumer {
       for (int t = 0; t < NT * 8; ++t)
         if (t < p.T) {
           const float v = warp_sum(z[t]);
-          if (lane == 0) p.logits[((int64_t)q * p.T + t) * p.E + e] = v;
+          if (lane == 0) red[warp * kMaxT + t] = v;
         }
+      named_barrier(1, kCons * 32);
+      for (int i = warp * 32 + lane; i < step * p.T; i += kCons * 32) {
+        const int j = i / p.T, t = i - j * p.T, ej = blockIdx.x + (i0 + j) * (int)gridDim.x;
+        if (ej >= p.E) continue;
+        float v = 0.0f;
+        for (int r = 0; r < S; ++r) v += red[(j * S + r) * kMaxT + t];
+        p.logits[(int64_t)t * p.E + ej] = stored_logit(v);
+      }
+      named_barrier(1, kCons * 32);  // red has been read
     }
   }
 
-  __device__ void run() {
+  // A slot's 16 rows times its tokens, this warp's channels: added to d.
+  template <bool PLANES>
+  __device__ __forceinline__ void multiply(const SlotInfo& si, uint32_t base, int part,
+                                           float (&d)[NT][4]) {
     using W = Wt<WD>;
     const int gr = lane >> 2, t4 = lane & 3;
-    float acc[NT][4], d[NT][4];
+    const int cols = si.cols;
+    const uint32_t mask = si.mask;
+    const uint32_t wa_row = base + gr * si.wpitch, wb_row = wa_row + 8 * si.wpitch;
+    const uint32_t sc_row = base + si.soff + gr * 2;
+    const uint32_t zeros = settle(smem_u32(&hd.zeros));
+    uint32_t arow[NT];  // this lane's token row among the activations
+    bool on[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int tok = n * 8 + gr;
+      on[n] = mask >> tok & 1u;
+      arow[n] = base + si.aoff + __popc(mask & ((1u << tok) - 1u)) * si.apitch;
+    }
+    const float *s0p = nullptr, *s1p = nullptr;
+    if constexpr (WD == MOE_FP8_E4M3) {
+      const int r0 = si.f0 + min(gr, si.cnt - 1);
+      const int r1 = si.u_off ? r0 + si.u_off : si.f0 + min(gr + 8, si.cnt - 1);
+      s0p = si.s + (r0 >> 7) * si.s_ld;
+      s1p = si.s + (r1 >> 7) * si.s_ld;
+    }
+    const uint32_t plane = PLANES ? si.plane : 0;
+    // two bf16 units at a time, with sums of their own, so that their products overlap
+    constexpr int kPar = WD == MOE_BF16 ? 2 : 1;
+    constexpr int kSteps = WD == MOE_BF16 ? kPar : W::kUnit / W::kStep;
+    float o[kPar][NT][4];
+#pragma unroll
+    for (int i = 0; i < kPar; ++i) zero_sums(o[i]);
+#pragma unroll 1
+    for (int u0 = part * W::kUnit; u0 < cols; u0 += kPar * 4 * W::kUnit) {
+      float s0 = 0.0f, s1 = 0.0f;
+      if constexpr (WD == MOE_FP8_E4M3) {  // one scale block: its own sum
+        s0 = __ldg(s0p + (u0 >> 7));
+        s1 = __ldg(s1p + (u0 >> 7));
+        zero_sums(o[0]);
+      }
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) {
+        constexpr int stride = WD == MOE_BF16 ? 4 * W::kUnit : W::kStep;
+        if (WD == MOE_BF16 && u0 + st * stride >= cols) break;
+        const int col = u0 + st * stride + t4 * W::kChunk;
+        const uint4 ra = lds16(wa_row + W::bytes(col)), rb = lds16(wb_row + W::bytes(col));
+        // 4-bit: the channels past the end of K (some lanes of the last unit) count as zeros
+        const bool valid = WD != MOE_INT4 || col < cols;
+        uint32_t sa = 0, sb = 0;
+        if constexpr (WD == MOE_INT4) {
+          sa = valid ? lds2(sc_row + col) * 0x10001u : 0u;  // 32 bytes a group of 32 channels
+          sb = valid ? lds2(sc_row + 16 + col) * 0x10001u : 0u;
+        }
+        const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+        bool nan = false;
+        if constexpr (WD == MOE_FP8_E4M3) {
+          uint32_t bad = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            bad |= ((wa[i] & 0x7f7f7f7fu) + 0x01010101u) | ((wb[i] & 0x7f7f7f7fu) + 0x01010101u);
+          nan = bad & 0x80808080u;
+        }
+#pragma unroll
+        for (int h = 0; h < W::kChunk / 8; ++h) {  // 8 channels: two products
+          uint32_t a[4], b[4];
+          if constexpr (WD == MOE_BF16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a[i] = wa[i];
+              b[i] = wb[i];
+            }
+          } else if constexpr (WD == MOE_FP8_E4M3) {
+            e4m3x4_to_bf16(wa[2 * h], a[0], a[1]);
+            e4m3x4_to_bf16(wa[2 * h + 1], a[2], a[3]);
+            e4m3x4_to_bf16(wb[2 * h], b[0], b[1]);
+            e4m3x4_to_bf16(wb[2 * h + 1], b[2], b[3]);
+            if (nan) {
+              e4m3_mark_nan(e4m3_nan(wa[2 * h]), a[0], a[1]);
+              e4m3_mark_nan(e4m3_nan(wa[2 * h + 1]), a[2], a[3]);
+              e4m3_mark_nan(e4m3_nan(wb[2 * h]), b[0], b[1]);
+              e4m3_mark_nan(e4m3_nan(wb[2 * h + 1]), b[2], b[3]);
+            }
+          } else {
+            int4x8_to_bf16(wa[h], sa, a);
+            int4x8_to_bf16(wb[h], sb, b);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (NT > 1 && !(mask >> (n * 8) & 0xffu)) continue;
+            // a token without a row reads zeros
+            const uint32_t q = on[n] && valid ? arow[n] + col * 2 + h * 16 : zeros;
+            float(&sum)[4] = o[WD == MOE_BF16 ? st : 0][n];
+            const uint4 v = lds16(q);
+            mma16816(sum, a[0], b[0], a[1], b[1], v.x, v.y);
+            mma16816(sum, a[2], b[2], a[3], b[3], v.z, v.w);
+            if (PLANES) {
+              const uint4 v2 = lds16(on[n] && valid ? q + plane : zeros);
+              mma16816(sum, a[0], b[0], a[1], b[1], v2.x, v2.y);
+              mma16816(sum, a[2], b[2], a[3], b[3], v2.z, v2.w);
+            }
+          }
+        }
+      }
+      if constexpr (WD == MOE_FP8_E4M3) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[n][i] = fmaf(i < 2 ? s0 : s1, o[0][n][i], d[n][i]);
+      }
+    }
+    if constexpr (WD != MOE_FP8_E4M3) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < kPar; ++j) d[n][i] += o[j][n][i];
+    }
+  }
+
+  __device__ __forceinline__ static void zero_sums(float (&v)[NT][4]) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = d[n][i] = 0.0f;
-    int slot = 0;
-    uint32_t parity = 0;
-    while (true) {
-      if (!wait(&hd.full[slot], parity)) return;
-      const SlotInfo& si = hd.info[slot];
-      const int flags = si.flags;
-      if (flags & (kDone | kStop)) {
-        if (flags & kStop) return;
-        const int counter = si.kind;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&hd.empty[slot]);
-        done(counter);
-      } else {
-        const int cols = si.cols, f0 = si.f0, cnt = si.cnt, kind = si.kind, row0 = si.row0;
-        const uint32_t mask = si.mask;
-        const uint8_t* base = slots + (size_t)slot * kSlotBytes;
-        const uint8_t* wa_row = base + gr * si.wpitch;
-        const uint8_t* wb_row = wa_row + 8 * si.wpitch;
-        const uint8_t* sc_row = base + si.soff;
-        const int plane = si.plane;
-        const uint8_t* arow[NT];  // this lane's token row among the activations
-        bool on[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int tok = n * 8 + gr;
-          on[n] = mask >> tok & 1u;
-          arow[n] = base + si.aoff + __popc(mask & ((1u << tok) - 1u)) * si.apitch;
-        }
-        const float *s0p = nullptr, *s1p = nullptr;
-        if constexpr (WD == MOE_FP8_E4M3) {
-          const int r0 = f0 + min(gr, cnt - 1);
-          const int r1 = si.u_off ? r0 + si.u_off : f0 + min(gr + 8, cnt - 1);
-          s0p = si.s + (r0 >> 7) * si.s_ld;
-          s1p = si.s + (r1 >> 7) * si.s_ld;
-        }
-        if (flags & kSegFirst) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
-        }
-#pragma unroll 1
-        for (int u = warp * W::kUnit; u < cols; u += kCons * W::kUnit) {
-          float s0 = 0.0f, s1 = 0.0f;
-          float dd[NT][4];
-          if constexpr (WD == MOE_FP8_E4M3) {  // one scale block: its own sum
-            s0 = __ldg(s0p + (u >> 7));
-            s1 = __ldg(s1p + (u >> 7));
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) dd[n][i] = 0.0f;
-          }
-#pragma unroll
-          for (int st = 0; st < W::kUnit / W::kStep; ++st) {
-            const int col = u + st * W::kStep + t4 * W::kChunk;
-            const bool valid = col < cols;
-            uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
-            uint32_t sa = 0, sb = 0;
-            if (valid) {
-              ra = lds16(wa_row + W::bytes(col));
-              rb = lds16(wb_row + W::bytes(col));
-              if constexpr (WD == MOE_INT4) {
-                const uint16_t* sc = (const uint16_t*)(sc_row + col);  // 32 bytes a group of 32
-                sa = sc[gr] * 0x10001u;
-                sb = sc[gr + 8] * 0x10001u;
-              }
-            }
-            const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
-#pragma unroll
-            for (int h = 0; h < W::kChunk / 8; ++h) {  // 8 channels: two products
-              uint32_t a[4], b[4];
-              if constexpr (WD == MOE_BF16) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  a[i] = wa[i];
-                  b[i] = wb[i];
-                }
-              } else if constexpr (WD == MOE_FP8_E4M3) {
-                e4m3x4_to_bf16(wa[2 * h], a[0], a[1]);
-                e4m3x4_to_bf16(wa[2 * h + 1], a[2], a[3]);
-                e4m3x4_to_bf16(wb[2 * h], b[0], b[1]);
-                e4m3x4_to_bf16(wb[2 * h + 1], b[2], b[3]);
-              } else {
-                int4x8_to_bf16(wa[h], sa, a);
-                int4x8_to_bf16(wb[h], sb, b);
-              }
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                if (NT > 1 && !(mask >> (n * 8) & 0xffu)) continue;
-                const bool ok = valid && on[n];
-                const uint8_t* q = arow[n] + col * 2 + h * 16;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (ok) v = lds16(q);
-                float(&o)[4] = WD == MOE_FP8_E4M3 ? dd[n] : d[n];
-                mma16816(o, a[0], b[0], a[1], b[1], v.x, v.y);
-                mma16816(o, a[2], b[2], a[3], b[3], v.z, v.w);
-                if (plane) {
-                  if (ok) v = lds16(q + plane);
-                  mma16816(o, a[0], b[0], a[1], b[1], v.x, v.y);
-                  mma16816(o, a[2], b[2], a[3], b[3], v.z, v.w);
-                }
-              }
-            }
-          }
-          if constexpr (WD == MOE_FP8_E4M3) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              d[n][0] = fmaf(s0, dd[n][0], d[n][0]);
-              d[n][1] = fmaf(s0, dd[n][1], d[n][1]);
-              d[n][2] = fmaf(s1, dd[n][2], d[n][2]);
-              d[n][3] = fmaf(s1, dd[n][3], d[n][3]);
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&hd.empty[slot]);
-        if (flags & kSegLast) {
-          const bool scaled = flags & kScaled;
-          if (scaled && !wait(&hd.inv_bar, 0)) return;
-          // only the segment's own tokens: another token's zeros times an infinite weight are NaN
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int tok = n * 8 + t4 * 2 + (i & 1);
-              const float v = scaled ? d[n][i] * hd.inv[tok] : d[n][i];
-              acc[n][i] += mask >> tok & 1u ? v : 0.0f;
-            }
-          if (flags & kTileLast) {
-            if (!end(acc, kind, f0, cnt, mask_of_tile(kind, mask), row0, flags & kGated)) return;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-          }
-        }
-      }
-      if (++slot == kSlots) {
-        slot = 0;
-        parity ^= 1u;
-      }
-    }
+      for (int i = 0; i < 4; ++i) v[n][i] = 0.0f;
   }
-  // The tokens of a whole tile: its only segment's, or all for sums over segments.
-  __device__ __forceinline__ uint32_t mask_of_tile(int kind, uint32_t mask) const {
-    return kind == kHid || kind == kDown ? mask : (1u << p.T) - 1u;
+
+  __device__ void run() {
+    const int slot = warp >> 2, part = warp & 3, t4 = lane & 3;
+    const uint32_t base = smem_u32(slots) + slot * kSlotBytes;
+    const SlotInfo& si = hd.info[slot];
+    float acc[NT][4];
+    zero_sums(acc);
+    uint32_t tile = 0;
+    for (uint32_t parity = 0;; parity ^= 1u) {
+      if (!wait(&hd.info_bar[slot], parity)) return;
+      for (const uint32_t now = si.tile; tile != now; ++tile) {  // tiles that ended before it
+        const Tile& ti = hd.tile[slot][tile % kTiles];
+        if (ti.kind == kPublish) {
+          done(ti.f0);
+        } else {
+          if (!end(acc, ti)) return;
+          zero_sums(acc);
+        }
+      }
+      const int flags = si.flags;
+      if (flags & kStop) return;
+      if (!wait(&hd.full[slot], parity)) return;
+      float d[NT][4];
+      zero_sums(d);
+      const uint32_t addr = settle(base);
+      if (si.plane)
+        multiply<true>(si, addr, part, d);
+      else
+        multiply<false>(si, addr, part, d);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) settle_sum(d[n][i]);
+      const uint32_t mask = si.mask;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&hd.empty[slot]);
+      const bool scaled = flags & kScaled;
+      if (scaled && !wait(&hd.inv_bar, 0)) return;
+      // only the segment's own tokens: another token's zeros times an infinite weight are NaN
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = n * 8 + t4 * 2 + (i & 1);
+          const float v = scaled ? d[n][i] * hd.inv[tok] : d[n][i];
+          acc[n][i] += mask >> tok & 1u ? v : 0.0f;
+        }
+    }
   }
 };
 
@@ -1146,14 +1182,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&hd.full[i], 2 + (WD == MOE_INT4 ? 32 : 0));  // weights, activations (+ scales)
-      mbar_init(&hd.empty[i], kCons);
+      mbar_init(&hd.info_bar[i], 1);
+      mbar_init(&hd.empty[i], kCons / kSlots);
     }
     mbar_init(&hd.sel_bar, kSelWarps);
     mbar_init(&hd.inv_bar, kSelWarps);
     mbar_init(&hd.red_full, kCons);
     mbar_init(&hd.red_empty, kCons);
     hd.abort = 0;
-    for (int i = 0; i < 4; ++i) hd.done[i] = 0;
+    hd.zeros = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 3; ++i) hd.done[i] = 0;
     fence_barrier_init();
   }
   __syncthreads();
@@ -1162,14 +1200,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
     Producer<WD> v{p, hd, slots + (size_t)warp * kSlotBytes, warp, lane};
     v.run();
   } else if (warp < kFirstCons) {
-    int ok = 1;
-    if (lane == 0) ok = counter_wait(p.bar + kCntRouter, gridDim.x, &hd.abort, p.err);
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    ok = named_barrier_and(2, kSelWarps * 32, ok);
-    if (!ok) return;
-    build_selection(p, hd.sel, threadIdx.x - 32 * kSlots, kSelWarps, 2);
+    if (!build_selection(p, hd.sel, threadIdx.x - 32 * kSlots, kSelWarps, 2, &hd.abort)) return;
     if (lane == 0) mbar_arrive(&hd.sel_bar);
     if (!p.L) return;
+    int ok = 1;
     if (lane == 0) ok = counter_wait(p.bar + kCntLat, gridDim.x, &hd.abort, p.err);
     if (!__shfl_sync(0xffffffffu, ok, 0)) return;
     for (int t = warp - kSlots; t < p.T; t += kSelWarps) {
@@ -1183,14 +1217,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
   } else {
     Consumer<WD, NT> v{p, hd, slots, red, warp - kFirstCons, lane};
     v.router();
-    v.done(kCntRouter);
     v.run();
   }
 }
 
 struct FewLayout {
   size_t logits, x_lat, h, y_lat, ssq, total;
-  int parts, part_cols;
 };
 
 constexpr int kMaxCtas = 256;  // the grid is one CTA per SM, at most this many
@@ -1204,16 +1236,7 @@ FewLayout few_layout(const moe_config_t* c) {
     return at;
   };
   const size_t T = (size_t)c->T;
-  // router ranges: about one (expert, range) per consumer warp of 152 SMs, 128 channels at least
-  l.parts = 1;
-  l.part_cols = c->d;
-  if (c->act_dtype == MOE_BF16) {
-    int n = 152 * kCons / c->E;
-    n = n < 1 ? 1 : n > 8 ? 8 : n;
-    l.part_cols = ((c->d + n - 1) / n + 127) / 128 * 128;
-    l.parts = (c->d + l.part_cols - 1) / l.part_cols;
-  }
-  l.logits = take(l.parts * T * c->E * 4);
+  l.logits = take(T * c->E * 4);  // follows the status word: cleared with it
   // 4 bytes a value: one fp32, or two bf16 planes
   l.x_lat = take(T * c->d_latent * 4);
   l.h = take((T * c->k + T) * c->I * 4);
@@ -1339,8 +1362,6 @@ extern "C" moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, 
   p.err = reinterpret_cast<uint32_t*>(base);
   p.bar = reinterpret_cast<uint32_t*>(base + 128);
   p.logits = reinterpret_cast<float*>(base + l.logits);
-  p.parts = l.parts;
-  p.part_cols = l.part_cols;
   p.x_lat = reinterpret_cast<float*>(base + l.x_lat);
   p.h = reinterpret_cast<float*>(base + l.h);
   p.y_lat = reinterpret_cast<float*>(base + l.y_lat);
@@ -1350,7 +1371,8 @@ extern "C" moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, 
   p.ssq = reinterpret_cast<float*>(base + l.ssq);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   (void)cudaGetLastError();  // start from a clean launch-error state
-  cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);  // status word and barrier counters
+  // status word, barrier counters and the logits' places
+  cudaError_t e = cudaMemsetAsync(ws, 0, l.logits + (size_t)p.T * p.E * 4, st);
   if (e != cudaSuccess) return status_from_cuda(e);
   switch (cfg->w_dtype) {
     case MOE_F32: e = start((const void*)few_kernel, p, kThreads, 0, st); break;
