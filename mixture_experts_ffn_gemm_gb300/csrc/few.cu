@@ -53,6 +53,7 @@ struct Selection {
   float bias[kMaxE + 1];         // b
   int16_t slot[kMaxE + 1];       // its place in active
   int16_t active[kMaxPairs];     // distinct selected experts, ascending
+  uint16_t active_mask[kMaxPairs];  // their tokens
   int16_t row0[kMaxPairs + 1];   // first h row of each
   int16_t pair_e[kMaxPairs];
   float pair_g[kMaxPairs];
@@ -207,6 +208,7 @@ __device__ bool build_selection(const FewParams& p, Selection& sel, int tid, int
       if (m) {
         const int a = na + __popc(act & ((1u << lane) - 1u));
         sel.active[a] = (int16_t)(e0 + lane);
+        sel.active_mask[a] = (uint16_t)m;
         sel.row0[a] = (int16_t)(row + incl - __popc(m));
         sel.slot[e0 + lane] = (int16_t)a;
       }
@@ -441,10 +443,13 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
 // ---------------------------------------------------------------------------------------------
 constexpr int kCons = 16;      // consumer warps
 constexpr int kSlots = 4;      // ring slots, one producer warp each
-constexpr int kSelWarps = 4;
-constexpr int kFirstCons = kSlots + kSelWarps;
+constexpr int kSelWarps = 2;   // selection
+constexpr int kRedWarps = 2;   // sums of the finished tiles
+constexpr int kFirstCons = kSlots + kSelWarps + kRedWarps;
 constexpr int kStreamThreads = 32 * (kFirstCons + kCons);
-constexpr int kSlotBytes = 48640;
+constexpr int kRed = 2;        // tiles whose partial sums wait for the reducers
+// What is left of one CTA's shared memory, for 8 or 16 tokens.
+constexpr int slot_bytes(int nt) { return nt == 1 ? 48384 : 44288; }
 static_assert(kCons == 4 * kSlots && (kSlots & (kSlots - 1)) == 0, "four consumer warps to a slot");
 
 // Counters of the launch (FewParams::bar): arrivals of CTAs at the end of each part.
@@ -466,11 +471,11 @@ struct Wt {
 __device__ __forceinline__ int slot_pitch(int bytes) { return ((bytes + 127) & ~127) + 64; }
 
 // Channels a slot of a segment takes (K in all, nr activation rows), cut evenly.
-template <int WD>
+template <int WD, int NT>
 __device__ __forceinline__ int slot_cols(int K, int nr) {
   constexpr int per16 = 16 * Wt<WD>::kBits / 8 + (WD == MOE_INT4 ? 1 : 0);
   constexpr int round = 4 * Wt<WD>::kUnit;  // a round of the slot's four consumer warps
-  int c = (kSlotBytes - (16 + nr) * 64) / (per16 + 2 * nr);
+  int c = (slot_bytes(NT) - (16 + nr) * 64) / (per16 + 2 * nr);
   const int gran = c >= 4 * round ? round : Wt<WD>::kGran;
   c = c / gran * gran;
   const int n = (K + c - 1) / c;
@@ -491,32 +496,32 @@ struct SlotInfo {
 };
 
 // A tile of features in stream order; kPublish: the CTA's share of a part is complete, add it to
-// counter f0.
-enum Kind { kDown, kHid, kLat, kOut, kPublish };
+// counter f0; kEnd: the last.
+enum Kind { kDown, kHid, kLat, kOut, kPublish, kEnd };
 struct Tile {
   int kind, f0, cnt, row0;  // first h row
   uint32_t mask;
   int gated;
 };
 // Between two pieces of one slot the stream has kSlots - 1 others: at most that many tiles and the
-// three publishings; twice that for the piece the producer is ahead.
-constexpr int kTiles = 16;
+// three publishings; twice that for the piece the producer is ahead, and the reducers' kRed.
+constexpr int kTiles = 32;
 
 struct StreamHead {
-  uint64_t info_bar[kSlots], full[kSlots], empty[kSlots], sel_bar, inv_bar, red_full, red_empty;
+  uint64_t info_bar[kSlots], full[kSlots], empty[kSlots], sel_bar, inv_bar, red_full[kRed], red_empty[kRed];
   SlotInfo info[kSlots];
-  Tile tile[kSlots][kTiles];  // each producer's own, for its consumers
+  Tile tile[kSlots][kTiles];  // each producer's own, for its consumers (the reducers: slot 0's)
   uint4 zeros;
   float inv[kMaxT];
   int abort;
-  uint32_t done[3];  // consumer warps through each part (a warp may be a part ahead of another)
+  uint32_t done[3];  // reducer warps through each part
   Selection sel;
 };
 constexpr size_t head_bytes() { return (sizeof(StreamHead) + 127) & ~size_t(127); }
 constexpr size_t stream_smem(int nt) {
-  return 128 + head_bytes() + (size_t)kCons * nt * 512 + (size_t)kSlots * kSlotBytes;
+  return 128 + head_bytes() + (size_t)kRed * kCons * nt * 512 + (size_t)kSlots * slot_bytes(nt);
 }
-static_assert(stream_smem(2) <= 227 * 1024, "one CTA's shared memory");
+static_assert(stream_smem(1) <= 227 * 1024 && stream_smem(2) <= 227 * 1024, "one CTA's memory");
 
 // The parts of the layer in stream order, each split evenly over the CTAs by features.
 enum Part { kPartDown, kPartShared, kPartRouted, kPartW2, kPartUp, kParts };
@@ -533,7 +538,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // A producer warp; warp i fills slot i, every kSlots-th slot of the stream.  (One copy instruction
 // takes its addresses from uniform registers, so a warp issues the 16 and more copies of a slot one
 // after another: one warp for all slots held the stream to 4.2 TB/s.)
-template <int WD>
+template <int WD, int NT>
 struct Producer {
   const FewParams& p;
   StreamHead& hd;
@@ -579,10 +584,11 @@ struct Producer {
     bool tokens;               // activation rows are the tokens of the mask, else row0 ...
     int dep;                   // part that must be complete before the activations are read
     bool scaled;               // multiply by the tokens' 1 / rms
-    int lane_cols;             // lane n - 1: slot_cols() for n tokens
+    int lane_cols;             // lane n - 1: slot_cols() for n tokens and, above bit 20, the pieces
 
     __device__ __forceinline__ void fit(int lane) {
-      lane_cols = slot_cols<WD>(K, (lane % kMaxT + 1) * (plane ? 2 : 1));
+      const int c = slot_cols<WD, NT>(K, (lane % kMaxT + 1) * (plane ? 2 : 1));
+      lane_cols = c | (K + c - 1) / c << 20;
     }
   };
 
@@ -591,12 +597,12 @@ struct Producer {
   __device__ __forceinline__ void seg(const Source& g, int e, int f0, int cnt, uint32_t mask,
                                       int row0) {
     const int n = __popc(mask);
-    const int step = __shfl_sync(0xffffffffu, g.lane_cols, n - 1);
-    int c0 = ((slot - turn) & (kSlots - 1)) * step;  // the first that falls to this warp
-    int pieces = 0;  // without a division: K / step is small
-    for (int c = 0; c < g.K; c += step) ++pieces;
+    const int fit = __shfl_sync(0xffffffffu, g.lane_cols, n - 1);
+    const int step = fit & 0xfffff, pieces = fit >> 20;
+    const int first = (slot - turn) & (kSlots - 1);  // the first that falls to this warp
     turn = (turn + pieces) & (kSlots - 1);
-    if (c0 >= g.K) return;
+    if (first >= pieces) return;
+    int c0 = first * step;
     const uint8_t* w = g.w;
     const void* sc = g.s;
     if (e >= 0) {
@@ -644,15 +650,15 @@ struct Producer {
       __syncwarp();
       if (has) bulk_load(base + lane * wpitch, w_row + Wt<WD>::bytes(c0), nb, &hd.full[slot]);
       if constexpr (WD == MOE_INT4) {
-        // scales [K / 32][R]: four rows of a group a copy, into [group][16]
-        const int q = (lane & 3) * 4, grp = lane >> 2;
-        if ((g.u_off ? q & 7 : q) < cnt) {
+        // scales [K / 32][R]: eight rows of a group a copy, into [group][16]
+        const int q = lane & 1, grp = lane >> 1;
+        if (g.u_off || q * 8 < cnt) {
           const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(sc) +
                                      (int64_t)((c0 >> 5) + grp) * g.R + f0 +
-                                     (g.u_off && q >= 8 ? g.u_off + q - 8 : q);
-          uint32_t dst = smem_u32(base + soff + grp * 32 + q * 2);
-          for (int i = grp; i < cols >> 5; i += 8, src += 8 * (int64_t)g.R, dst += 256)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src)
+                                     (g.u_off ? q * g.u_off : q * 8);
+          uint32_t dst = smem_u32(base + soff + grp * 32 + q * 16);
+          for (int i = grp; i < cols >> 5; i += 16, src += 16 * (int64_t)g.R, dst += 512)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src)
                          : "memory");
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
@@ -669,7 +675,7 @@ struct Producer {
 
   // The CTA's share of the layer.
   __device__ void run() {
-    constexpr int G = WD == MOE_INT4 ? 4 : 1;  // 8-byte copies of the bf16 scales of four rows
+    constexpr int G = WD == MOE_INT4 ? 8 : 1;  // 16-byte copies of the bf16 scales of eight rows
     const Selection& sel = hd.sel;
     const uint32_t all = (1u << p.T) - 1u;
     const int P = p.T * p.k, de = p.L ? p.L : p.d;
@@ -738,15 +744,13 @@ struct Producer {
         const int cnt = (len / G + n - 1) / n * G;
         const bool routed = part == kPartRouted;
         const int e = routed ? sel.active[a] : -1;
-        const uint32_t mask = routed ? sel.mask[e] : all;
+        const uint32_t mask = routed ? sel.active_mask[a] : all;
         next_tile(kind, f, cnt, routed ? sel.row0[a] : P, mask, routed);
         if (with_shared) seg(last, -1, f, cnt, all, P);
         if (part == kPartW2) {
 #pragma unroll 1
-          for (int i = 0; i < sel.n_active; ++i) {
-            const int ei = sel.active[i];
-            seg(one, ei, f, cnt, sel.mask[ei], sel.row0[i]);
-          }
+          for (int i = 0; i < sel.n_active; ++i)
+            seg(one, sel.active[i], f, cnt, sel.active_mask[i], sel.row0[i]);
         } else {
           seg(one, e, f, cnt, mask, 0);
         }
@@ -756,6 +760,7 @@ struct Producer {
       if (part == kPartRouted) next_tile(kPublish, kCntH, 0, 0, 0, 0);
       if (part == kPartW2 && p.L) next_tile(kPublish, kCntLat, 0, 0, 0, 0);
     }
+    next_tile(kEnd, 0, 0, 0, 0, 0);
     if (slot_free() && lane == 0) {
       hd.info[slot].flags = kStop;
       hd.info[slot].tile = tile;
@@ -847,146 +852,98 @@ struct Consumer {
   const uint8_t* slots;
   float* red;  // [kCons][NT][16 rows][8 tokens]
   int warp, lane;
-  uint32_t tiles = 0;  // summed over warps so far
-  float ssq = 0.0f;    // of the latent features this thread has stored for its token
 
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
     return mbar_wait_sleep(bar, parity, &hd.abort, p.err);
   }
 
-  // Sums the warps' partial tiles in warp order and stores the tile's features.
-  __device__ __forceinline__ bool end(const float (&acc)[NT][4], const Tile& ti) {
-    const int kind = ti.kind;
+  // Hands this warp's sums of tile number t to the reducers.
+  __device__ __forceinline__ bool hand_over(const float (&acc)[NT][4], uint32_t t) {
     const int gr = lane >> 2, t4 = lane & 3;
-    if (!wait(&hd.red_empty, (tiles & 1u) ^ 1u)) return false;
+    if (!wait(&hd.red_empty[t % kRed], (t / kRed & 1u) ^ 1u)) return false;
+    if (hd.tile[warp >> 2][t % kTiles].kind < kPublish) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float* r = red + (warp * NT + n) * 128 + gr * 8 + t4 * 2;
-      *reinterpret_cast<float2*>(r) = make_float2(acc[n][0], acc[n][1]);
-      *reinterpret_cast<float2*>(r + 64) = make_float2(acc[n][2], acc[n][3]);
+      for (int n = 0; n < NT; ++n) {
+        float* r = red + ((t % kRed * kCons + warp) * NT + n) * 128 + gr * 8 + t4 * 2;
+        *reinterpret_cast<float2*>(r) = make_float2(acc[n][0], acc[n][1]);
+        *reinterpret_cast<float2*>(r + 64) = make_float2(acc[n][2], acc[n][3]);
+      }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&hd.red_full);
-    const int c = ((warp >> 2) + 4 * (warp & 3)) * 32 + lane;  // the first warp of every slot first
-    const bool pair = kind == kHid;
-    const int per = pair ? 64 : 128;
-    const bool own = c < per * NT;  // whole warps
-    const int n = pair ? c >> 6 : c >> 7, row = pair ? c & 7 : c & 15;
-    const int tok = n * 8 + ((pair ? c >> 3 : c >> 4) & 7);
-    float v = 0.0f, up = 0.0f;
-    if (own) {
-      if (!wait(&hd.red_full, tiles & 1u)) return false;
-      const float* r = red + n * 128 + row * 8 + (tok & 7);
-#pragma unroll
-      for (int w = 0; w < kCons; ++w) v += r[w * NT * 128];
-      if (pair) {
-#pragma unroll
-        for (int w = 0; w < kCons; ++w) up += r[w * NT * 128 + 64];
-      }
-      __syncwarp();
-    }
-    ++tiles;
-    if (lane == 0) mbar_arrive(&hd.red_empty);
-    if (!own) return true;
-    const bool live = row < ti.cnt && (ti.mask >> tok & 1u);
-    const int f = ti.f0 + row;
-    if (kind == kHid) {
-      if (!live) return true;
-      const int hr = ti.row0 + __popc(ti.mask & ((1u << tok) - 1u));
-      v = silu_accurate(v) * up;
-      if (ti.gated) v *= hd.sel.row_gate[hr];
-      __nv_bfloat16 hi, lo;
-      split_planes(v, hi, lo);
-      const int64_t at = (int64_t)hr * p.I + f;
-      p.h2[at] = hi;
-      p.h2[(int64_t)p.T * (p.k + 1) * p.I + at] = lo;
-    } else if (kind == kOut) {
-      if (live) static_cast<__nv_bfloat16*>(p.out)[(int64_t)tok * p.d + f] = __float2bfloat16_rn(v);
-    } else {
-      if (kind == kLat) {  // 16 consecutive lanes hold the tile's features of one token
-        float q = live ? v * v : 0.0f;
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
-        ssq += q;
-      }
-      if (!live) return true;
-      __nv_bfloat16 hi, lo;
-      split_planes(v, hi, lo);
-      __nv_bfloat16* o = kind == kDown ? p.x_lat2 : p.y_lat2;
-      o[(int64_t)tok * p.L + f] = hi;
-      o[(int64_t)(p.T + tok) * p.L + f] = lo;
-    }
+    if (lane == 0) mbar_arrive(&hd.red_full[t % kRed]);
     return true;
   }
 
-  // Publishes what the CTA has stored so far to the other CTAs' loads and bulk copies: the last of
-  // the warps to come adds the CTA to the counter.
-  __device__ void done(int counter) {
-    const int c = ((warp >> 2) + 4 * (warp & 3)) * 32 + lane;
-    if (counter == kCntLat && c < 128 * NT && c % 16 == 0)
-      p.ssq[blockIdx.x * kMaxT + c / 128 * 8 + c / 16 % 8] = ssq;
-    asm volatile("fence.proxy.async;" ::: "memory");
-    __threadfence();
-    __syncwarp();
-    if (lane == 0 && atomicAdd(&hd.done[counter], 1u) == kCons - 1) {
-      __threadfence();
-      asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.bar + counter) : "memory");
-    }
-  }
-
-  // Router logits: the CTA takes every gridDim-th expert, an expert's input channels split over as
-  // many warps as there are for it; a warp's weights are in flight at once.
+  // Router logits: the CTA takes every gridDim-th expert, kExp at a time; the warps split the input
+  // channels, so that a CTA reads the tokens once for them.
   __device__ void router() {
-    constexpr int kMost = 8;
+    constexpr int kExp = 3, kMost = 2;
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
-    const int n_e = (p.E + (int)gridDim.x - 1) / (int)gridDim.x;  // experts of a CTA, at most
-    const int S = max(kCons / n_e, 1), step = kCons / S;
-    const int part = ((p.d + S - 1) / S + 127) / 128 * 128;
-    for (int i0 = 0; i0 < n_e; i0 += step) {
-      const int q = warp % S, e = blockIdx.x + (i0 + warp / S) * (int)gridDim.x;
-      const bool on = warp / S < step && e < p.E;
-      const int end = on ? min(p.d, (q + 1) * part) : 0;
-      const float* w = p.W_r + (int64_t)e * p.d;
-      float z[NT * 8];
+    const int part = ((p.d + kCons - 1) / kCons + 31) / 32 * 32;
+    const int end = min(p.d, (warp + 1) * part);
+    for (int e0 = blockIdx.x; e0 < p.E; e0 += kExp * (int)gridDim.x) {
+#pragma unroll 1
+      for (int n = 0; n < NT; ++n) {
+        float z[kExp][8];
 #pragma unroll
-      for (int t = 0; t < NT * 8; ++t) z[t] = 0.0f;
-      for (int c0 = q * part + lane * 4; c0 < end; c0 += 128 * kMost) {
-        float4 wv[kMost];
+        for (int j = 0; j < kExp; ++j)
 #pragma unroll
-        for (int i = 0; i < kMost; ++i)
-          wv[i] = c0 + i * 128 < end ? __ldg(reinterpret_cast<const float4*>(w + c0 + i * 128))
-                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int t = 0; t < NT * 8; ++t) {
-          if (t >= p.T) break;
-          const __nv_bfloat16* xr = x + (int64_t)t * p.d + c0;
-          uint2 xv[kMost];
-#pragma unroll
-          for (int i = 0; i < kMost; ++i)
-            xv[i] = c0 + i * 128 < end ? __ldg(reinterpret_cast<const uint2*>(xr + i * 128))
-                                       : make_uint2(0, 0);
+          for (int t = 0; t < 8; ++t) z[j][t] = 0.0f;
+#pragma unroll 1
+        for (int c0 = warp * part + lane * 4; c0 < end; c0 += 128 * kMost) {
+          float4 wv[kMost][kExp];
+          uint2 xv[kMost][8];
 #pragma unroll
           for (int i = 0; i < kMost; ++i) {
-            z[t] = fmaf(wv[i].x, __uint_as_float(xv[i].x << 16), z[t]);
-            z[t] = fmaf(wv[i].y, __uint_as_float(xv[i].x & 0xffff0000u), z[t]);
-            z[t] = fmaf(wv[i].z, __uint_as_float(xv[i].y << 16), z[t]);
-            z[t] = fmaf(wv[i].w, __uint_as_float(xv[i].y & 0xffff0000u), z[t]);
+            const int c = c0 + i * 128;
+#pragma unroll
+            for (int j = 0; j < kExp; ++j) {
+              const int e = e0 + j * (int)gridDim.x;
+              wv[i][j] = c < end && e < p.E
+                             ? __ldg(reinterpret_cast<const float4*>(p.W_r + (int64_t)e * p.d + c))
+                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+              xv[i][t] = c < end && n * 8 + t < p.T
+                             ? __ldg(reinterpret_cast<const uint2*>(x + (int64_t)(n * 8 + t) * p.d + c))
+                             : make_uint2(0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < kMost; ++i)
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+              const float x0 = __uint_as_float(xv[i][t].x << 16),
+                          x1 = __uint_as_float(xv[i][t].x & 0xffff0000u),
+                          x2 = __uint_as_float(xv[i][t].y << 16),
+                          x3 = __uint_as_float(xv[i][t].y & 0xffff0000u);
+#pragma unroll
+              for (int j = 0; j < kExp; ++j) {
+                z[j][t] = fmaf(wv[i][j].x, x0, z[j][t]);
+                z[j][t] = fmaf(wv[i][j].y, x1, z[j][t]);
+                z[j][t] = fmaf(wv[i][j].z, x2, z[j][t]);
+                z[j][t] = fmaf(wv[i][j].w, x3, z[j][t]);
+              }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          if (n * 8 + t >= p.T) break;
+#pragma unroll
+          for (int j = 0; j < kExp; ++j) {
+            const float v = warp_sum(z[j][t]);
+            if (lane == 0) red[(warp * kExp + j) * kMaxT + n * 8 + t] = v;
           }
         }
       }
-#pragma unroll
-      for (int t = 0; t < NT * 8; ++t)
-        if (t < p.T) {
-          const float v = warp_sum(z[t]);
-          if (lane == 0) red[warp * kMaxT + t] = v;
-        }
       named_barrier(1, kCons * 32);
-      for (int i = warp * 32 + lane; i < step * p.T; i += kCons * 32) {
-        const int j = i / p.T, t = i - j * p.T, ej = blockIdx.x + (i0 + j) * (int)gridDim.x;
-        if (ej >= p.E) continue;
+      for (int i = warp * 32 + lane; i < kExp * p.T; i += kCons * 32) {
+        const int j = i / p.T, t = i - j * p.T, e = e0 + j * (int)gridDim.x;
+        if (e >= p.E) continue;
         float v = 0.0f;
-        for (int r = 0; r < S; ++r) v += red[(j * S + r) * kMaxT + t];
-        p.logits[(int64_t)t * p.E + ej] = stored_logit(v);
+#pragma unroll
+        for (int w = 0; w < kCons; ++w) v += red[(w * kExp + j) * kMaxT + t];
+        p.logits[(int64_t)t * p.E + e] = stored_logit(v);
       }
       named_barrier(1, kCons * 32);  // red has been read
     }
@@ -1122,7 +1079,7 @@ struct Consumer {
 
   __device__ void run() {
     const int slot = warp >> 2, part = warp & 3, t4 = lane & 3;
-    const uint32_t base = smem_u32(slots) + slot * kSlotBytes;
+    const uint32_t base = smem_u32(slots) + slot * slot_bytes(NT);
     const SlotInfo& si = hd.info[slot];
     float acc[NT][4];
     zero_sums(acc);
@@ -1130,13 +1087,8 @@ struct Consumer {
     for (uint32_t parity = 0;; parity ^= 1u) {
       if (!wait(&hd.info_bar[slot], parity)) return;
       for (const uint32_t now = si.tile; tile != now; ++tile) {  // tiles that ended before it
-        const Tile& ti = hd.tile[slot][tile % kTiles];
-        if (ti.kind == kPublish) {
-          done(ti.f0);
-        } else {
-          if (!end(acc, ti)) return;
-          zero_sums(acc);
-        }
+        if (!hand_over(acc, tile)) return;
+        zero_sums(acc);
       }
       const int flags = si.flags;
       if (flags & kStop) return;
@@ -1170,6 +1122,98 @@ struct Consumer {
   }
 };
 
+// The reducer warps: sum the consumer warps' partial tiles in warp order, store the tiles' features
+// and publish the parts.
+template <int NT>
+struct Reducer {
+  const FewParams& p;
+  StreamHead& hd;
+  const float* red;
+  int tid, lane;  // of kRedWarps warps
+  float ssq[2 * NT] = {};  // squares of the latent features of this thread's tokens
+
+  __device__ void run() {
+    for (uint32_t t = 0;; ++t) {
+      if (!mbar_wait_sleep(&hd.red_full[t % kRed], t / kRed & 1u, &hd.abort, p.err)) return;
+      const Tile ti = hd.tile[0][t % kTiles];
+      if (ti.kind == kEnd) return;
+      if (ti.kind == kPublish) {
+        publish(ti.f0);
+      } else if (ti.kind == kHid) {
+        hidden(ti, red + (t % kRed) * kCons * NT * 128);
+      } else {
+        rows(ti, red + (t % kRed) * kCons * NT * 128);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&hd.red_empty[t % kRed]);
+    }
+  }
+  static __device__ __forceinline__ float sum(const float* r) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kCons; ++w) v += r[w * NT * 128];
+    return v;
+  }
+  // 8 pairs of W1 and W3 features times 8 NT tokens, one a thread and turn
+  __device__ __forceinline__ void hidden(const Tile& ti, const float* r) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = tid & 7, tok = n * 8 + (tid >> 3);
+      const float* q = r + n * 128 + row * 8 + (tid >> 3);
+      const float g = sum(q), u = sum(q + 64);
+      if (row >= ti.cnt || !(ti.mask >> tok & 1u)) continue;
+      const int hr = ti.row0 + __popc(ti.mask & ((1u << tok) - 1u));
+      float v = silu_accurate(g) * u;
+      if (ti.gated) v *= hd.sel.row_gate[hr];
+      store_planes(p.h2 + (int64_t)hr * p.I + ti.f0 + row, (int64_t)p.T * (p.k + 1) * p.I, v);
+    }
+  }
+  // 16 features times 8 NT tokens, two a thread and token group
+  __device__ __forceinline__ void rows(const Tile& ti, const float* r) {
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) {
+      const int row = tid & 15, tok = i * 4 + (tid >> 4);
+      const float v = sum(r + (tok >> 3) * 128 + row * 8 + (tok & 7));
+      const bool live = row < ti.cnt && tok < p.T;
+      if (ti.kind == kLat) {  // 16 consecutive lanes hold one token's features
+        float q = live ? v * v : 0.0f;
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
+        ssq[i] += q;
+      }
+      if (!live) continue;
+      const int f = ti.f0 + row;
+      if (ti.kind == kOut)
+        static_cast<__nv_bfloat16*>(p.out)[(int64_t)tok * p.d + f] = __float2bfloat16_rn(v);
+      else
+        store_planes((ti.kind == kDown ? p.x_lat2 : p.y_lat2) + (int64_t)tok * p.L + f,
+                     (int64_t)p.T * p.L, v);
+    }
+  }
+  static __device__ __forceinline__ void store_planes(__nv_bfloat16* at, int64_t plane, float v) {
+    __nv_bfloat16 hi, lo;
+    split_planes(v, hi, lo);
+    at[0] = hi;
+    at[plane] = lo;
+  }
+  // Publishes what the CTA has stored so far to the other CTAs' loads and bulk copies.
+  __device__ void publish(int counter) {
+    if (counter == kCntLat && (tid & 15) == 0) {
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i)
+        p.ssq[blockIdx.x * kMaxT + i * 4 + (tid >> 4)] = ssq[i];
+    }
+    asm volatile("fence.proxy.async;" ::: "memory");
+    __threadfence();
+    __syncwarp();
+    // the last of the warps to come adds the CTA to the counter
+    if (lane == 0 && atomicAdd(&hd.done[counter], 1u) == kRedWarps - 1) {
+      __threadfence();
+      asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.bar + counter) : "memory");
+    }
+  }
+};
+
 template <int WD, int NT>
 __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const FewParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -1177,7 +1221,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
                                              ~uintptr_t(127));
   StreamHead& hd = *reinterpret_cast<StreamHead*>(smem);
   float* red = reinterpret_cast<float*>(smem + head_bytes());
-  uint8_t* slots = smem + head_bytes() + (size_t)kCons * NT * 512;
+  uint8_t* slots = smem + head_bytes() + (size_t)kRed * kCons * NT * 512;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
@@ -1187,8 +1231,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
     }
     mbar_init(&hd.sel_bar, kSelWarps);
     mbar_init(&hd.inv_bar, kSelWarps);
-    mbar_init(&hd.red_full, kCons);
-    mbar_init(&hd.red_empty, kCons);
+    for (int i = 0; i < kRed; ++i) {
+      mbar_init(&hd.red_full[i], kCons);
+      mbar_init(&hd.red_empty[i], kRedWarps);
+    }
     hd.abort = 0;
     hd.zeros = make_uint4(0, 0, 0, 0);
     for (int i = 0; i < 3; ++i) hd.done[i] = 0;
@@ -1197,9 +1243,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
   __syncthreads();
 
   if (warp < kSlots) {
-    Producer<WD> v{p, hd, slots + (size_t)warp * kSlotBytes, warp, lane};
+    Producer<WD, NT> v{p, hd, slots + (size_t)warp * slot_bytes(NT), warp, lane};
     v.run();
-  } else if (warp < kFirstCons) {
+  } else if (warp < kSlots + kSelWarps) {
     if (!build_selection(p, hd.sel, threadIdx.x - 32 * kSlots, kSelWarps, 2, &hd.abort)) return;
     if (lane == 0) mbar_arrive(&hd.sel_bar);
     if (!p.L) return;
@@ -1214,6 +1260,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&hd.inv_bar);
+  } else if (warp < kFirstCons) {
+    Reducer<NT> v{p, hd, red, (int)threadIdx.x - 32 * (kSlots + kSelWarps), lane};
+    v.run();
   } else {
     Consumer<WD, NT> v{p, hd, slots, red, warp - kFirstCons, lane};
     v.router();
