@@ -45,6 +45,7 @@ struct FewParams {
   float* y_lat;    // [T][L]
   // bf16 kernel: the same as two bf16 planes, value = plane 0 + plane 1 to 16 bits or more
   __nv_bfloat16 *x_lat2, *h2, *y_lat2;
+  float* y_sh;     // [T][d] shared expert's output
   float* ssq;      // [CTAs][16] sums of squares of each CTA's latent features
 };
 
@@ -105,38 +106,60 @@ __device__ __forceinline__ uint32_t key_bits(float v) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One warp selects the experts of token t: k rounds of the largest key, ties to the lower index.
-// Lane l holds experts l, l + 32, ... in registers (N >= ceil(E / 32) of them).  Its logits may still
-// be on their way: the launch starts with zeros in their place, no logit is stored as +0, and the
-// warp reads until none is left (one trip to memory instead of a counter's and then the logits').
+// One warp selects the experts of tokens t0, t0 + stride, ...: k rounds of the largest key, ties to
+// the lower index.  Lane l holds experts l, l + 32, ... in registers (N >= ceil(E / 32) of them).  The
+// logits may still be on their way: the launch starts with zeros in their place, no logit is stored
+// as +0, and the warp reads until none is left (one trip to memory instead of a counter's and then
+// the logits').  The next token's are read ahead.
 template <int N>
-__device__ bool select_token(const FewParams& p, int t, Selection& sel, volatile int* abort) {
+__device__ __forceinline__ void read_logits(const FewParams& p, int t, float (&z)[N]) {
+  const int lane = threadIdx.x & 31;
+  const float* lg = p.logits + (int64_t)t * p.E + lane;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    z[j] = -0.0f;
+    if (t < p.T && lane + 32 * j < p.E)
+      asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(z[j]) : "l"(lg + 32 * j));
+  }
+}
+template <int N>
+__device__ void choose(const FewParams& p, int t, float (&z)[N], Selection& sel);
+
+template <int N>
+__device__ bool select_tokens(const FewParams& p, int t0, int stride, Selection& sel,
+                              volatile int* abort) {
+  float z[N], next[N];
+  read_logits(p, t0, z);
+  uint64_t since = 0;
+  for (int t = t0; t < p.T; t += stride) {
+    read_logits(p, t + stride, next);
+    while (true) {
+      bool all = true;
+#pragma unroll
+      for (int j = 0; j < N; ++j) all = all && __float_as_uint(z[j]) != 0u;
+      if (__all_sync(0xffffffffu, all)) break;
+      const uint64_t now = globaltimer_ns();
+      if (since == 0) since = now;
+      bool stop = abort && *abort;
+      if (now - since > kWaitLimitNs) {
+        if (abort) *abort = 1;
+        raise_flag(p.err, kErrTimeout);
+        stop = true;
+      }
+      if (__any_sync(0xffffffffu, stop)) return false;
+      read_logits(p, t, z);
+    }
+    choose(p, t, z, sel);
+#pragma unroll
+    for (int j = 0; j < N; ++j) z[j] = next[j];
+  }
+  return true;
+}
+
+template <int N>
+__device__ void choose(const FewParams& p, int t, float (&z)[N], Selection& sel) {
   const int lane = threadIdx.x & 31;
   uint32_t key[N];
-  float z[N];
-  const float* lg = p.logits + (int64_t)t * p.E + lane;
-  uint64_t t0 = 0;
-  while (true) {
-    bool all = true;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      z[j] = -0.0f;
-      if (lane + 32 * j < p.E)
-        asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(z[j]) : "l"(lg + 32 * j));
-    }
-#pragma unroll
-    for (int j = 0; j < N; ++j) all = all && __float_as_uint(z[j]) != 0u;
-    if (__all_sync(0xffffffffu, all)) break;
-    const uint64_t now = globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    bool stop = abort && *abort;
-    if (now - t0 > kWaitLimitNs) {
-      if (abort) *abort = 1;
-      raise_flag(p.err, kErrTimeout);
-      stop = true;
-    }
-    if (__any_sync(0xffffffffu, stop)) return false;
-  }
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     z[j] = 1.0f / (1.0f + expf(-z[j]));
@@ -172,7 +195,6 @@ __device__ bool select_token(const FewParams& p, int t, Selection& sel, volatile
     sel.pair_e[t * p.k + lane] = (int16_t)my_e;
     sel.pair_g[t * p.k + lane] = p.gate_scale * my_s / den;
   }
-  return true;
 }
 
 // The CTA's copy of the selection, by n_warps warps of which this thread is number tid (barrier
@@ -186,11 +208,10 @@ __device__ bool build_selection(const FewParams& p, Selection& sel, int tid, int
     sel.bias[e] = __ldg(p.b + e);
   }
   named_barrier(bar, n);
-  bool ok = true;
-  for (int t = tid >> 5; t < p.T && ok; t += n_warps)
-    ok = p.E <= 64    ? select_token<2>(p, t, sel, abort)
-         : p.E <= 384 ? select_token<12>(p, t, sel, abort)
-                      : select_token<32>(p, t, sel, abort);
+  const int w = tid >> 5;
+  const bool ok = p.E <= 64    ? select_tokens<2>(p, w, n_warps, sel, abort)
+                  : p.E <= 384 ? select_tokens<12>(p, w, n_warps, sel, abort)
+                               : select_tokens<32>(p, w, n_warps, sel, abort);
   if (!named_barrier_and(bar, n, ok)) return false;
   for (int i = tid; i < p.T * p.k; i += n) atomicOr(&sel.mask[sel.pair_e[i]], 1u << (i / p.k));
   named_barrier(bar, n);
@@ -453,7 +474,7 @@ constexpr int slot_bytes(int nt) { return nt == 1 ? 48384 : 44288; }
 static_assert(kCons == 4 * kSlots && (kSlots & (kSlots - 1)) == 0, "four consumer warps to a slot");
 
 // Counters of the launch (FewParams::bar): arrivals of CTAs at the end of each part.
-enum : int { kCntDown = 0, kCntH = 1, kCntLat = 2 };
+enum : int { kCntDown = 0, kCntH = 1, kCntLat = 2, kCntShared = 3, kCounters = 4 };
 constexpr int kNoDep = -1;
 
 template <int WD>
@@ -497,24 +518,24 @@ struct SlotInfo {
 
 // A tile of features in stream order; kPublish: the CTA's share of a part is complete, add it to
 // counter f0; kEnd: the last.
-enum Kind { kDown, kHid, kLat, kOut, kPublish, kEnd };
+enum Kind { kDown, kHid, kLat, kShOut, kOut, kPublish, kEnd };
 struct Tile {
   int kind, f0, cnt, row0;  // first h row
   uint32_t mask;
   int gated;
 };
 // Between two pieces of one slot the stream has kSlots - 1 others: at most that many tiles and the
-// three publishings; twice that for the piece the producer is ahead, and the reducers' kRed.
+// four publishings; twice that for the piece the producer is ahead, and the reducers' kRed.
 constexpr int kTiles = 32;
 
 struct StreamHead {
-  uint64_t info_bar[kSlots], full[kSlots], empty[kSlots], sel_bar, inv_bar, red_full[kRed], red_empty[kRed];
+  uint64_t info_bar[kSlots], full[kSlots], empty[kSlots], sel_bar, inv_bar, start_bar, red_full[kRed], red_empty[kRed];
   SlotInfo info[kSlots];
   Tile tile[kSlots][kTiles];  // each producer's own, for its consumers (the reducers: slot 0's)
   uint4 zeros;
   float inv[kMaxT];
   int abort;
-  uint32_t done[3];  // reducer warps through each part
+  uint32_t done[kCounters];  // reducer warps through each part
   Selection sel;
 };
 constexpr size_t head_bytes() { return (sizeof(StreamHead) + 127) & ~size_t(127); }
@@ -524,7 +545,9 @@ constexpr size_t stream_smem(int nt) {
 static_assert(stream_smem(1) <= 227 * 1024 && stream_smem(2) <= 227 * 1024, "one CTA's memory");
 
 // The parts of the layer in stream order, each split evenly over the CTAs by features.
-enum Part { kPartDown, kPartShared, kPartRouted, kPartW2, kPartUp, kParts };
+// The shared expert's W2 needs nothing of the step before it: its weights pass by while the last CTAs
+// finish that step (K2: before W2; latent: before W_up).
+enum Part { kPartDown, kPartShared, kPartRouted, kPartShOut, kPartW2, kPartShOutLat, kPartUp, kParts };
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
@@ -676,6 +699,9 @@ struct Producer {
   // The CTA's share of the layer.
   __device__ void run() {
     constexpr int G = WD == MOE_INT4 ? 8 : 1;  // 16-byte copies of the bf16 scales of eight rows
+    // the stream starts behind the router's loads (see Consumer::router)
+    if (!mbar_wait_sleep(&hd.start_bar, 0, &hd.abort, p.err)) failed = true;
+    failed = __any_sync(0xffffffffu, failed);
     const Selection& sel = hd.sel;
     const uint32_t all = (1u << p.T) - 1u;
     const int P = p.T * p.k, de = p.L ? p.L : p.d;
@@ -685,6 +711,9 @@ struct Producer {
     for (int part = 0; part < kParts && !failed; ++part) {
       if ((part == kPartDown || part == kPartUp) && !p.L) continue;
       if (part == kPartShared && !p.n_shared) continue;
+      if ((part == kPartShOut || part == kPartShOutLat) &&
+          (!p.n_shared || (part == kPartShOutLat) != (p.L != 0)))
+        continue;
       if (part == kPartRouted) {
         const bool ok = mbar_wait_sleep(&hd.sel_bar, 0, &hd.abort, p.err);
         if (__any_sync(0xffffffffu, !ok)) {
@@ -692,44 +721,42 @@ struct Producer {
           break;
         }
       }
-      // one: every tile's own segment, or (W2) the segments of the selected experts; last: one more
-      Source one, last;
+      Source src;
       const bool pair = part == kPartShared || part == kPartRouted;
       int total, kind = kOut;
       if (part == kPartDown) {
-        one = Source{u8(p.W_down), nullptr, p.L, p.d, 0, x, 0, true, kNoDep, false, 0};
+        src = Source{u8(p.W_down), nullptr, p.L, p.d, 0, x, 0, true, kNoDep, false, 0};
         total = p.L;
         kind = kDown;
       } else if (part == kPartShared) {
-        one = Source{u8(p.Ws13), p.ss13, 2 * p.I, p.d, p.I, x, 0, true, kNoDep, false, 0};
+        src = Source{u8(p.Ws13), p.ss13, 2 * p.I, p.d, p.I, x, 0, true, kNoDep, false, 0};
         total = p.I;
         kind = kHid;
       } else if (part == kPartRouted) {
-        one = Source{u8(p.W13), p.s13, 2 * p.I, de, p.I, x, 0, true, kNoDep, false, 0};
+        src = Source{u8(p.W13), p.s13, 2 * p.I, de, p.I, x, 0, true, kNoDep, false, 0};
         if (p.L) {
-          one.act = p.x_lat2;
-          one.plane = (int64_t)p.T * p.L;
-          one.dep = kCntDown;
+          src.act = p.x_lat2;
+          src.plane = (int64_t)p.T * p.L;
+          src.dep = kCntDown;
         }
         total = sel.n_active * p.I;
         kind = kHid;
       } else if (part == kPartW2) {
-        one = Source{u8(p.W2), p.s2, de, p.I, 0, p.h2, (int64_t)(P + p.T) * p.I, false, kCntH,
+        src = Source{u8(p.W2), p.s2, de, p.I, 0, p.h2, (int64_t)(P + p.T) * p.I, false, kCntH,
                      false, 0};
         total = de;
         if (p.L) kind = kLat;
-      } else {
-        one = Source{u8(p.W_up), nullptr, p.d, p.L, 0, p.y_lat2, (int64_t)p.T * p.L, false, kCntLat,
+      } else if (part == kPartUp) {
+        src = Source{u8(p.W_up), nullptr, p.d, p.L, 0, p.y_lat2, (int64_t)p.T * p.L, false, kCntLat,
                      true, 0};
         total = p.d;
+      } else {
+        src = Source{u8(p.Ws2), p.ss2, p.d, p.I, 0, p.h2, (int64_t)(P + p.T) * p.I, false,
+                     kCntShared, false, 0};
+        total = p.d;
+        kind = kShOut;
       }
-      one.fit(lane);
-      const bool with_shared = p.n_shared && (part == kPartUp || (part == kPartW2 && !p.L));
-      if (with_shared) {
-        last = Source{u8(p.Ws2), p.ss2, p.d, p.I, 0, p.h2, (int64_t)(P + p.T) * p.I, false, kCntH,
-                      false, 0};
-        last.fit(lane);
-      }
+      src.fit(lane);
       int u = (int)((int64_t)(total / G) * blockIdx.x / gridDim.x) * G;
       const int u1 = (int)((int64_t)(total / G) * (blockIdx.x + 1) / gridDim.x) * G;
 #pragma unroll 1
@@ -746,17 +773,17 @@ struct Producer {
         const int e = routed ? sel.active[a] : -1;
         const uint32_t mask = routed ? sel.active_mask[a] : all;
         next_tile(kind, f, cnt, routed ? sel.row0[a] : P, mask, routed);
-        if (with_shared) seg(last, -1, f, cnt, all, P);
         if (part == kPartW2) {
 #pragma unroll 1
           for (int i = 0; i < sel.n_active; ++i)
-            seg(one, sel.active[i], f, cnt, sel.active_mask[i], sel.row0[i]);
+            seg(src, sel.active[i], f, cnt, sel.active_mask[i], sel.row0[i]);
         } else {
-          seg(one, e, f, cnt, mask, 0);
+          seg(src, e, f, cnt, mask, part == kPartUp ? 0 : P);
         }
         u += cnt;
       }
       if (part == kPartDown) next_tile(kPublish, kCntDown, 0, 0, 0, 0);
+      if (part == kPartShared) next_tile(kPublish, kCntShared, 0, 0, 0, 0);
       if (part == kPartRouted) next_tile(kPublish, kCntH, 0, 0, 0, 0);
       if (part == kPartW2 && p.L) next_tile(kPublish, kCntLat, 0, 0, 0, 0);
     }
@@ -875,12 +902,15 @@ struct Consumer {
   }
 
   // Router logits: the CTA takes every gridDim-th expert, kExp at a time; the warps split the input
-  // channels, so that a CTA reads the tokens once for them.
+  // channels, so that a CTA reads the tokens once for them.  The stream starts when the first
+  // kExp experts' loads are in: behind a full ring they would wait for all of it (the selection was
+  // ready at 18 us instead of XX).
   __device__ void router() {
     constexpr int kExp = 3, kMost = 2;
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
     const int part = ((p.d + kCons - 1) / kCons + 31) / 32 * 32;
     const int end = min(p.d, (warp + 1) * part);
+    if ((int)blockIdx.x >= p.E && lane == 0) mbar_arrive(&hd.start_bar);
     for (int e0 = blockIdx.x; e0 < p.E; e0 += kExp * (int)gridDim.x) {
 #pragma unroll 1
       for (int n = 0; n < NT; ++n) {
@@ -936,6 +966,7 @@ struct Consumer {
           }
         }
       }
+      if (e0 == (int)blockIdx.x && lane == 0) mbar_arrive(&hd.start_bar);
       named_barrier(1, kCons * 32);
       for (int i = warp * 32 + lane; i < kExp * p.T; i += kCons * 32) {
         const int j = i / p.T, t = i - j * p.T, e = e0 + j * (int)gridDim.x;
@@ -1183,8 +1214,11 @@ struct Reducer {
       }
       if (!live) continue;
       const int f = ti.f0 + row;
-      if (ti.kind == kOut)
-        static_cast<__nv_bfloat16*>(p.out)[(int64_t)tok * p.d + f] = __float2bfloat16_rn(v);
+      if (ti.kind == kShOut)  // for this very thread: the features' tiles are the same
+        p.y_sh[(int64_t)tok * p.d + f] = v;
+      else if (ti.kind == kOut)
+        static_cast<__nv_bfloat16*>(p.out)[(int64_t)tok * p.d + f] =
+            __float2bfloat16_rn(p.n_shared ? v + p.y_sh[(int64_t)tok * p.d + f] : v);
       else
         store_planes((ti.kind == kDown ? p.x_lat2 : p.y_lat2) + (int64_t)tok * p.L + f,
                      (int64_t)p.T * p.L, v);
@@ -1231,13 +1265,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
     }
     mbar_init(&hd.sel_bar, kSelWarps);
     mbar_init(&hd.inv_bar, kSelWarps);
+    mbar_init(&hd.start_bar, kCons);
     for (int i = 0; i < kRed; ++i) {
       mbar_init(&hd.red_full[i], kCons);
       mbar_init(&hd.red_empty[i], kRedWarps);
     }
     hd.abort = 0;
     hd.zeros = make_uint4(0, 0, 0, 0);
-    for (int i = 0; i < 3; ++i) hd.done[i] = 0;
+    for (int i = 0; i < kCounters; ++i) hd.done[i] = 0;
     fence_barrier_init();
   }
   __syncthreads();
@@ -1271,7 +1306,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
 }
 
 struct FewLayout {
-  size_t logits, x_lat, h, y_lat, ssq, total;
+  size_t logits, x_lat, h, y_lat, y_sh, ssq, total;
 };
 
 constexpr int kMaxCtas = 256;  // the grid is one CTA per SM, at most this many
@@ -1290,6 +1325,7 @@ FewLayout few_layout(const moe_config_t* c) {
   l.x_lat = take(T * c->d_latent * 4);
   l.h = take((T * c->k + T) * c->I * 4);
   l.y_lat = take(T * c->d_latent * 4);
+  l.y_sh = take(c->act_dtype == MOE_BF16 && c->n_shared ? T * c->d * 4 : 0);
   l.ssq = take(c->d_latent ? (size_t)kMaxCtas * kMaxT * 4 : 0);
   l.total = off;
   return l;
@@ -1417,6 +1453,7 @@ extern "C" moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, 
   p.x_lat2 = reinterpret_cast<__nv_bfloat16*>(base + l.x_lat);
   p.h2 = reinterpret_cast<__nv_bfloat16*>(base + l.h);
   p.y_lat2 = reinterpret_cast<__nv_bfloat16*>(base + l.y_lat);
+  p.y_sh = reinterpret_cast<float*>(base + l.y_sh);
   p.ssq = reinterpret_cast<float*>(base + l.ssq);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   (void)cudaGetLastError();  // start from a clean launch-error state
