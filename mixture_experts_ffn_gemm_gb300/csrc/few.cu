@@ -463,15 +463,17 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
 // or more of each, where one bf16 would add a rounding of 2^-9.
 // ---------------------------------------------------------------------------------------------
 constexpr int kCons = 16;      // consumer warps
-constexpr int kSlots = 4;      // ring slots, one producer warp each
+constexpr int kLanes = 4;      // lanes of the stream: a producer warp, four consumer warps, kBufs slots
+constexpr int kBufs = 2;
+constexpr int kSlots = kLanes * kBufs;
 constexpr int kSelWarps = 2;   // selection
 constexpr int kRedWarps = 2;   // sums of the finished tiles
-constexpr int kFirstCons = kSlots + kSelWarps + kRedWarps;
+constexpr int kFirstCons = kLanes + kSelWarps + kRedWarps;
 constexpr int kStreamThreads = 32 * (kFirstCons + kCons);
 constexpr int kRed = 2;        // tiles whose partial sums wait for the reducers
 // What is left of one CTA's shared memory, for 8 or 16 tokens.
-constexpr int slot_bytes(int nt) { return nt == 1 ? 48384 : 44288; }
-static_assert(kCons == 4 * kSlots && (kSlots & (kSlots - 1)) == 0, "four consumer warps to a slot");
+constexpr int slot_bytes(int nt) { return nt == 1 ? 24192 : 22016; }
+static_assert(kCons == 4 * kLanes && (kLanes & (kLanes - 1)) == 0, "four consumer warps to a lane");
 
 // Counters of the launch (FewParams::bar): arrivals of CTAs at the end of each part.
 enum : int { kCntDown = 0, kCntH = 1, kCntLat = 2, kCntShared = 3, kCounters = 4 };
@@ -495,9 +497,9 @@ __device__ __forceinline__ int slot_pitch(int bytes) { return ((bytes + 127) & ~
 template <int WD, int NT>
 __device__ __forceinline__ int slot_cols(int K, int nr) {
   constexpr int per16 = 16 * Wt<WD>::kBits / 8 + (WD == MOE_INT4 ? 1 : 0);
-  constexpr int round = 4 * Wt<WD>::kUnit;  // a round of the slot's four consumer warps
+  constexpr int round = 4 * Wt<WD>::kUnit;  // a round of the lane's four consumer warps
   int c = (slot_bytes(NT) - (16 + nr) * 64) / (per16 + 2 * nr);
-  const int gran = c >= 4 * round ? round : Wt<WD>::kGran;
+  const int gran = c >= 2 * round ? round : Wt<WD>::kGran;
   c = c / gran * gran;
   const int n = (K + c - 1) / c;
   return ((K + n - 1) / n + gran - 1) / gran * gran;
@@ -524,14 +526,15 @@ struct Tile {
   uint32_t mask;
   int gated;
 };
-// Between two pieces of one slot the stream has kSlots - 1 others: at most that many tiles and the
-// four publishings; twice that for the piece the producer is ahead, and the reducers' kRed.
+// Between two pieces of one lane the stream has kLanes - 1 others: at most kLanes tiles begin, and
+// three times that for the pieces the producer is ahead, with the publishings, the end and the
+// reducers' kRed: fewer than kTiles.
 constexpr int kTiles = 32;
 
 struct StreamHead {
   uint64_t info_bar[kSlots], full[kSlots], empty[kSlots], sel_bar, inv_bar, start_bar, red_full[kRed], red_empty[kRed];
   SlotInfo info[kSlots];
-  Tile tile[kSlots][kTiles];  // each producer's own, for its consumers (the reducers: slot 0's)
+  Tile tile[kLanes][kTiles];  // each producer's own, for its consumers (the reducers: lane 0's)
   uint4 zeros;
   float inv[kMaxT];
   int abort;
@@ -558,25 +561,26 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// A producer warp; warp i fills slot i, every kSlots-th slot of the stream.  (One copy instruction
-// takes its addresses from uniform registers, so a warp issues the 16 and more copies of a slot one
-// after another: one warp for all slots held the stream to 4.2 TB/s.)
+// A producer warp; warp i fills the slots of lane i, in turn, with every kLanes-th piece of the stream.
+// (One copy instruction takes its addresses from uniform registers, so a warp issues the 16 and more
+// copies of a slot one after another: one warp for all slots held the stream to 4.2 TB/s.)
 template <int WD, int NT>
 struct Producer {
   const FewParams& p;
   StreamHead& hd;
-  uint8_t* base;         // this warp's slot
-  int slot, lane;
-  int turn = 0;          // slot of the stream's next piece (pieces go round the slots)
-  uint32_t filled = 0;   // times this warp has filled its slot
+  uint8_t* slots;        // the lane's
+  int slot, lane;        // slot: lane of the stream
+  int turn = 0;          // lane of the stream's next piece (pieces go round the lanes)
+  uint32_t filled = 0;   // slots this warp has filled
   uint32_t tile = 0;     // tiles begun
   uint32_t complete = 0; // counters known to be complete
   bool failed = false;
 
-  // Waits until the consumers have left the slot.
+  __device__ __forceinline__ int at() const { return slot * kBufs + filled % kBufs; }
+  // Waits until the consumers have left the next slot.
   __device__ __forceinline__ bool slot_free() {
     if (failed) return false;
-    const bool ok = mbar_wait_sleep(&hd.empty[slot], (filled & 1u) ^ 1u, &hd.abort, p.err);
+    const bool ok = mbar_wait_sleep(&hd.empty[at()], (filled / kBufs & 1u) ^ 1u, &hd.abort, p.err);
     if (__any_sync(0xffffffffu, !ok)) failed = true;
     return !failed;
   }
@@ -622,8 +626,8 @@ struct Producer {
     const int n = __popc(mask);
     const int fit = __shfl_sync(0xffffffffu, g.lane_cols, n - 1);
     const int step = fit & 0xfffff, pieces = fit >> 20;
-    const int first = (slot - turn) & (kSlots - 1);  // the first that falls to this warp
-    turn = (turn + pieces) & (kSlots - 1);
+    const int first = (slot - turn) & (kLanes - 1);  // the first that falls to this warp
+    turn = (turn + pieces) & (kLanes - 1);
     if (first >= pieces) return;
     int c0 = first * step;
     const uint8_t* w = g.w;
@@ -647,12 +651,14 @@ struct Producer {
     const int pl = lane >= n, j = lane - pl * n;
     const int a_src = lane < rows ? (g.tokens ? nth_token(mask, j) : row0 + j) : 0;
     const __nv_bfloat16* a_row = g.act + pl * g.plane + (int64_t)a_src * g.K;
-    for (; c0 < g.K; c0 += kSlots * step) {
+    for (; c0 < g.K; c0 += kLanes * step) {
       if (!slot_free()) return;
+      uint8_t* base = slots + filled % kBufs * slot_bytes(NT);
+      uint64_t* full = &hd.full[at()];
       const int cols = min(step, g.K - c0);
       const uint32_t nb = Wt<WD>::bytes(cols);
       if (lane == 0) {
-        SlotInfo& i = hd.info[slot];
+        SlotInfo& i = hd.info[at()];
         i.cols = cols;
         i.wpitch = wpitch;
         i.apitch = apitch;
@@ -667,11 +673,11 @@ struct Producer {
         i.s_ld = g.K >> 7;
         i.u_off = g.u_off;
         i.tile = tile - 1;
-        mbar_arrive(&hd.info_bar[slot]);
-        mbar_arrive_expect_tx(&hd.full[slot], (g.u_off ? 2 * cnt : cnt) * nb);
+        mbar_arrive(&hd.info_bar[at()]);
+        mbar_arrive_expect_tx(full, (g.u_off ? 2 * cnt : cnt) * nb);
       }
       __syncwarp();
-      if (has) bulk_load(base + lane * wpitch, w_row + Wt<WD>::bytes(c0), nb, &hd.full[slot]);
+      if (has) bulk_load(base + lane * wpitch, w_row + Wt<WD>::bytes(c0), nb, full);
       if constexpr (WD == MOE_INT4) {
         // scales [K / 32][R]: eight rows of a group a copy, into [group][16]
         const int q = lane & 1, grp = lane >> 1;
@@ -685,13 +691,13 @@ struct Producer {
                          : "memory");
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                         smem_u32(&hd.full[slot]))
+                         smem_u32(full))
                      : "memory");
       }
       step_complete(g.dep);
-      if (lane == 0) mbar_arrive_expect_tx(&hd.full[slot], rows * cols * 2);
+      if (lane == 0) mbar_arrive_expect_tx(full, rows * cols * 2);
       __syncwarp();
-      if (lane < rows) bulk_load(base + aoff + lane * apitch, a_row + c0, cols * 2, &hd.full[slot]);
+      if (lane < rows) bulk_load(base + aoff + lane * apitch, a_row + c0, cols * 2, full);
       ++filled;
     }
   }
@@ -789,12 +795,13 @@ struct Producer {
     }
     next_tile(kEnd, 0, 0, 0, 0, 0);
     if (slot_free() && lane == 0) {
-      hd.info[slot].flags = kStop;
-      hd.info[slot].tile = tile;
-      mbar_arrive(&hd.info_bar[slot]);
+      hd.info[at()].flags = kStop;
+      hd.info[at()].tile = tile;
+      mbar_arrive(&hd.info_bar[at()]);
     }
     // after a failure the copies in flight still have to land before the CTA ends
-    if (filled) mbar_wait(&hd.full[slot], (filled - 1) & 1u, nullptr, nullptr, kDrainLimitNs);
+    for (uint32_t i = filled > kBufs ? filled - kBufs : 0; i < filled; ++i)
+      mbar_wait(&hd.full[slot * kBufs + i % kBufs], i / kBufs & 1u, nullptr, nullptr, kDrainLimitNs);
   }
 };
 
@@ -868,9 +875,9 @@ __device__ __forceinline__ void split_planes(float v, __nv_bfloat16& hi, __nv_bf
   lo = __float2bfloat16_rn(isinf(f) ? 0.0f : v - f);
 }
 
-// The sixteen consumer warps: four to a slot, so that the latencies of a slot's few products and of
-// its bookkeeping overlap with three other slots'.  A warp adds its channels of a tile's segments
-// up over the pieces its slot gets; the tile's end brings the sixteen sums together.  NT: groups of
+// The sixteen consumer warps: four to a lane of the stream, so that the latencies of a slot's few
+// products and of its bookkeeping overlap with three other lanes', while the lane's other slot fills.
+// A warp adds its channels of a tile's segments up over the pieces its lane gets; the tile's end brings the sixteen sums together.  NT: groups of
 // 8 tokens.  Every wait gives up once the CTA's abort flag is set, so the warps may leave one by one.
 template <int WD, int NT>
 struct Consumer {
@@ -1110,23 +1117,24 @@ struct Consumer {
 
   __device__ void run() {
     const int slot = warp >> 2, part = warp & 3, t4 = lane & 3;
-    const uint32_t base = smem_u32(slots) + slot * slot_bytes(NT);
-    const SlotInfo& si = hd.info[slot];
     float acc[NT][4];
     zero_sums(acc);
     uint32_t tile = 0;
-    for (uint32_t parity = 0;; parity ^= 1u) {
-      if (!wait(&hd.info_bar[slot], parity)) return;
+    for (uint32_t piece = 0;; ++piece) {
+      const int at = slot * kBufs + piece % kBufs;
+      const uint32_t parity = piece / kBufs & 1u;
+      const SlotInfo& si = hd.info[at];
+      if (!wait(&hd.info_bar[at], parity)) return;
       for (const uint32_t now = si.tile; tile != now; ++tile) {  // tiles that ended before it
         if (!hand_over(acc, tile)) return;
         zero_sums(acc);
       }
       const int flags = si.flags;
       if (flags & kStop) return;
-      if (!wait(&hd.full[slot], parity)) return;
+      if (!wait(&hd.full[at], parity)) return;
       float d[NT][4];
       zero_sums(d);
-      const uint32_t addr = settle(base);
+      const uint32_t addr = settle(smem_u32(slots) + at * slot_bytes(NT));
       if (si.plane)
         multiply<true>(si, addr, part, d);
       else
@@ -1137,7 +1145,7 @@ struct Consumer {
         for (int i = 0; i < 4; ++i) settle_sum(d[n][i]);
       const uint32_t mask = si.mask;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&hd.empty[slot]);
+      if (lane == 0) mbar_arrive(&hd.empty[at]);
       const bool scaled = flags & kScaled;
       if (scaled && !wait(&hd.inv_bar, 0)) return;
       // only the segment's own tokens: another token's zeros times an infinite weight are NaN
@@ -1261,7 +1269,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&hd.full[i], 2 + (WD == MOE_INT4 ? 32 : 0));  // weights, activations (+ scales)
       mbar_init(&hd.info_bar[i], 1);
-      mbar_init(&hd.empty[i], kCons / kSlots);
+      mbar_init(&hd.empty[i], kCons / kLanes);
     }
     mbar_init(&hd.sel_bar, kSelWarps);
     mbar_init(&hd.inv_bar, kSelWarps);
@@ -1277,17 +1285,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
   }
   __syncthreads();
 
-  if (warp < kSlots) {
-    Producer<WD, NT> v{p, hd, slots + (size_t)warp * slot_bytes(NT), warp, lane};
+  if (warp < kLanes) {
+    Producer<WD, NT> v{p, hd, slots + (size_t)warp * kBufs * slot_bytes(NT), warp, lane};
     v.run();
-  } else if (warp < kSlots + kSelWarps) {
-    if (!build_selection(p, hd.sel, threadIdx.x - 32 * kSlots, kSelWarps, 2, &hd.abort)) return;
+  } else if (warp < kLanes + kSelWarps) {
+    if (!build_selection(p, hd.sel, threadIdx.x - 32 * kLanes, kSelWarps, 2, &hd.abort)) return;
     if (lane == 0) mbar_arrive(&hd.sel_bar);
     if (!p.L) return;
     int ok = 1;
     if (lane == 0) ok = counter_wait(p.bar + kCntLat, gridDim.x, &hd.abort, p.err);
     if (!__shfl_sync(0xffffffffu, ok, 0)) return;
-    for (int t = warp - kSlots; t < p.T; t += kSelWarps) {
+    for (int t = warp - kLanes; t < p.T; t += kSelWarps) {
       float ss = 0.0f;
       for (int c = lane; c < (int)gridDim.x; c += 32) ss += __ldcg(p.ssq + c * kMaxT + t);
       ss = warp_sum(ss);
@@ -1296,7 +1304,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
     __syncwarp();
     if (lane == 0) mbar_arrive(&hd.inv_bar);
   } else if (warp < kFirstCons) {
-    Reducer<NT> v{p, hd, red, (int)threadIdx.x - 32 * (kSlots + kSelWarps), lane};
+    Reducer<NT> v{p, hd, red, (int)threadIdx.x - 32 * (kLanes + kSelWarps), lane};
     v.run();
   } else {
     Consumer<WD, NT> v{p, hd, slots, red, warp - kFirstCons, lane};
