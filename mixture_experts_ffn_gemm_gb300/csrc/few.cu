@@ -507,7 +507,7 @@ __device__ __forceinline__ int slot_cols(int K, int nr) {
 
 // What a slot holds, written by its producer for the consumers.
 enum : int { kScaled = 1, kStop = 2 };  // kStop: no data, the stream ends
-struct SlotInfo {
+struct alignas(16) SlotInfo {  // written in four 16-byte stores
   int cols, wpitch, apitch, aoff;
   int soff, plane;   // int4 scales; distance of the activations' second plane (0: one plane)
   uint32_t mask;     // tokens
@@ -516,7 +516,9 @@ struct SlotInfo {
   const float* s;    // e4m3: scale of the matrix's row block 0 and the slot's first channel
   int s_ld, u_off;   // scales per row block; distance of the W3 rows (0: no pairs)
   uint32_t tile;     // the tile it belongs to; the ones before it are complete in the stream
+  int pad_;
 };
+static_assert(sizeof(SlotInfo) == 64, "four 16-byte stores");
 
 // A tile of features in stream order; kPublish: the CTA's share of a part is complete, add it to
 // counter f0; kEnd: the last.
@@ -612,10 +614,13 @@ struct Producer {
     int dep;                   // part that must be complete before the activations are read
     bool scaled;               // multiply by the tokens' 1 / rms
     int lane_cols;             // lane n - 1: slot_cols() for n tokens and, above bit 20, the pieces
+    int64_t w_step, s_step;    // bytes from one expert's matrix and scales to the next
 
     __device__ __forceinline__ void fit(int lane) {
       const int c = slot_cols<WD, NT>(K, (lane % kMaxT + 1) * (plane ? 2 : 1));
       lane_cols = c | (K + c - 1) / c << 20;
+      w_step = (int64_t)R * Wt<WD>::bytes(K);
+      s_step = WD == MOE_FP8_E4M3 ? (int64_t)(R >> 7) * (K >> 7) * 4 : (int64_t)(K >> 5) * R * 2;
     }
   };
 
@@ -633,11 +638,8 @@ struct Producer {
     const uint8_t* w = g.w;
     const void* sc = g.s;
     if (e >= 0) {
-      w += (int64_t)e * g.R * g.K * Wt<WD>::kBits / 8;
-      if constexpr (WD == MOE_FP8_E4M3)
-        sc = static_cast<const float*>(sc) + (int64_t)e * (g.R >> 7) * (g.K >> 7);
-      if constexpr (WD == MOE_INT4)
-        sc = static_cast<const __nv_bfloat16*>(sc) + (int64_t)e * (g.K >> 5) * g.R;
+      w += e * g.w_step;
+      if constexpr (WD != MOE_BF16) sc = static_cast<const uint8_t*>(sc) + e * g.s_step;
     }
     const int wpitch = slot_pitch(Wt<WD>::bytes(step)), apitch = slot_pitch(step * 2);
     const int soff = 16 * wpitch, aoff = soff + (WD == MOE_INT4 ? step : 0);
@@ -658,21 +660,14 @@ struct Producer {
       const int cols = min(step, g.K - c0);
       const uint32_t nb = Wt<WD>::bytes(cols);
       if (lane == 0) {
-        SlotInfo& i = hd.info[at()];
-        i.cols = cols;
-        i.wpitch = wpitch;
-        i.apitch = apitch;
-        i.aoff = aoff;
-        i.soff = soff;
-        i.plane = g.plane ? n * apitch : 0;
-        i.mask = mask;
-        i.flags = g.scaled ? kScaled : 0;
-        i.f0 = f0;
-        i.cnt = cnt;
-        i.s = WD == MOE_FP8_E4M3 ? static_cast<const float*>(sc) + (c0 >> 7) : nullptr;
-        i.s_ld = g.K >> 7;
-        i.u_off = g.u_off;
-        i.tile = tile - 1;
+        int4* i = reinterpret_cast<int4*>(&hd.info[at()]);
+        const uint64_t sp = WD == MOE_FP8_E4M3
+                                ? reinterpret_cast<uint64_t>(static_cast<const float*>(sc) + (c0 >> 7))
+                                : 0;
+        i[0] = make_int4(cols, wpitch, apitch, aoff);
+        i[1] = make_int4(soff, g.plane ? n * apitch : 0, (int)mask, g.scaled ? kScaled : 0);
+        i[2] = make_int4(f0, cnt, (int)(uint32_t)sp, (int)(sp >> 32));
+        i[3] = make_int4(g.K >> 7, g.u_off, (int)(tile - 1), 0);
         mbar_arrive(&hd.info_bar[at()]);
         mbar_arrive_expect_tx(full, (g.u_off ? 2 * cnt : cnt) * nb);
       }
@@ -731,15 +726,15 @@ struct Producer {
       const bool pair = part == kPartShared || part == kPartRouted;
       int total, kind = kOut;
       if (part == kPartDown) {
-        src = Source{u8(p.W_down), nullptr, p.L, p.d, 0, x, 0, true, kNoDep, false, 0};
+        src = Source{u8(p.W_down), nullptr, p.L, p.d, 0, x, 0, true, kNoDep, false, 0, 0, 0};
         total = p.L;
         kind = kDown;
       } else if (part == kPartShared) {
-        src = Source{u8(p.Ws13), p.ss13, 2 * p.I, p.d, p.I, x, 0, true, kNoDep, false, 0};
+        src = Source{u8(p.Ws13), p.ss13, 2 * p.I, p.d, p.I, x, 0, true, kNoDep, false, 0, 0, 0};
         total = p.I;
         kind = kHid;
       } else if (part == kPartRouted) {
-        src = Source{u8(p.W13), p.s13, 2 * p.I, de, p.I, x, 0, true, kNoDep, false, 0};
+        src = Source{u8(p.W13), p.s13, 2 * p.I, de, p.I, x, 0, true, kNoDep, false, 0, 0, 0};
         if (p.L) {
           src.act = p.x_lat2;
           src.plane = (int64_t)p.T * p.L;
@@ -749,16 +744,16 @@ struct Producer {
         kind = kHid;
       } else if (part == kPartW2) {
         src = Source{u8(p.W2), p.s2, de, p.I, 0, p.h2, (int64_t)(P + p.T) * p.I, false, kCntH,
-                     false, 0};
+                     false, 0, 0, 0};
         total = de;
         if (p.L) kind = kLat;
       } else if (part == kPartUp) {
         src = Source{u8(p.W_up), nullptr, p.d, p.L, 0, p.y_lat2, (int64_t)p.T * p.L, false, kCntLat,
-                     true, 0};
+                     true, 0, 0, 0};
         total = p.d;
       } else {
         src = Source{u8(p.Ws2), p.ss2, p.d, p.I, 0, p.h2, (int64_t)(P + p.T) * p.I, false,
-                     kCntShared, false, 0};
+                     kCntShared, false, 0, 0, 0};
         total = p.d;
         kind = kShOut;
       }
@@ -845,20 +840,31 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
-// Four e4m3 codes as bf16: exponent and mantissa bits moved to bf16's places give value * 2^-120
-// (subnormals included), the product with 2^120 is exact.  NaN codes are left to the caller.
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t x0 = __byte_perm(w, 0, 0x1404), x1 = __byte_perm(w, 0, 0x3424);
-  lo = mul_bf16x2(((x0 >> 4) & 0x07f007f0u) | (x0 & 0x80008000u), 0x7b807b80u);
-  hi = mul_bf16x2(((x1 >> 4) & 0x07f007f0u) | (x1 & 0x80008000u), 0x7b807b80u);
+// Four e4m3 codes as bf16, the pairs of codes 0, 2 and 1, 3: exponent and mantissa bits moved to
+// bf16's places give value * 2^-120 (subnormals included), the product with 2^120 is exact.  The
+// integer pipe runs at half rate and bounds the e4m3 layer, so the left shifts are multiplications
+// (k16 and k256 are 16 and 256, unknown to the compiler).  top collects the largest magnitude of the
+// codes in each half: 0x7f, a NaN, is marked by the caller.
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t k16, uint32_t k256, uint32_t& p02,
+                                               uint32_t& p13, uint32_t& top) {
+  const uint32_t e02 = w & 0x007f007fu, e13 = (w >> 8) & 0x007f007fu;
+  top = __vmaxu2(top, __vmaxu2(e02, e13));
+  p02 = mul_bf16x2(e02 * k16 + (w & 0x00800080u) * k256, 0x7b807b80u);
+  p13 = mul_bf16x2(e13 * k16 + (w & 0x80008000u), 0x7b807b80u);
 }
-// Which of four codes are NaN (0x80 in their byte), and their bf16 values marked so.
-__device__ __forceinline__ uint32_t e4m3_nan(uint32_t w) {
-  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+__device__ __forceinline__ bool e4m3_any_nan(uint32_t top) {
+  return (top & 0xffffu) == 0x7fu || top >> 16 == 0x7fu;
 }
-__device__ __forceinline__ void e4m3_mark_nan(uint32_t bad, uint32_t& lo, uint32_t& hi) {
-  lo |= (bad & 0x80u ? 0x7fffu : 0u) | (bad & 0x8000u ? 0x7fff0000u : 0u);
-  hi |= (bad & 0x800000u ? 0x7fffu : 0u) | (bad & 0x80000000u ? 0x7fff0000u : 0u);
+__device__ __forceinline__ void e4m3_mark_nan(uint32_t w, uint32_t& p02, uint32_t& p13) {
+  const uint32_t bad = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  p02 |= (bad & 0x80u ? 0x7fffu : 0u) | (bad & 0x800000u ? 0x7fff0000u : 0u);
+  p13 |= (bad & 0x8000u ? 0x7fffu : 0u) | (bad & 0x80000000u ? 0x7fff0000u : 0u);
+}
+// The order in which h is stored for the e4m3 layer: features 4i, 4i + 2, 4i + 1, 4i + 3, the pairs
+// that e4m3x4_to_bf16 gives.
+template <int WD>
+__device__ __forceinline__ int h_place(int f) {
+  return WD == MOE_FP8_E4M3 && ((f ^ (f >> 1)) & 1) ? f ^ 3 : f;
 }
 
 // Eight 4-bit codes (nibbles j and j + 4 are channels 2j and 2j + 1) times their scale: 128 + u is
@@ -1014,6 +1020,7 @@ struct Consumer {
       s1p = si.s + (r1 >> 7) * si.s_ld;
     }
     const uint32_t plane = PLANES ? si.plane : 0;
+    const uint32_t k16 = settle(16u), k256 = settle(256u);
     // two bf16 units at a time, with sums of their own, so that their products overlap
     constexpr int kPar = WD == MOE_BF16 ? 2 : 1;
     constexpr int kSteps = WD == MOE_BF16 ? kPar : W::kUnit / W::kStep;
@@ -1042,13 +1049,21 @@ struct Consumer {
           sb = valid ? lds2(sc_row + 16 + col) * 0x10001u : 0u;
         }
         const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
-        bool nan = false;
+        uint32_t cva[8], cvb[8];  // e4m3: all 16 channels as bf16
         if constexpr (WD == MOE_FP8_E4M3) {
-          uint32_t bad = 0;
+          uint32_t top = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            bad |= ((wa[i] & 0x7f7f7f7fu) + 0x01010101u) | ((wb[i] & 0x7f7f7f7fu) + 0x01010101u);
-          nan = bad & 0x80808080u;
+          for (int i = 0; i < 4; ++i) {
+            e4m3x4_to_bf16(wa[i], k16, k256, cva[2 * i], cva[2 * i + 1], top);
+            e4m3x4_to_bf16(wb[i], k16, k256, cvb[2 * i], cvb[2 * i + 1], top);
+          }
+          if (e4m3_any_nan(top)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              e4m3_mark_nan(wa[i], cva[2 * i], cva[2 * i + 1]);
+              e4m3_mark_nan(wb[i], cvb[2 * i], cvb[2 * i + 1]);
+            }
+          }
         }
 #pragma unroll
         for (int h = 0; h < W::kChunk / 8; ++h) {  // 8 channels: two products
@@ -1060,15 +1075,10 @@ struct Consumer {
               b[i] = wb[i];
             }
           } else if constexpr (WD == MOE_FP8_E4M3) {
-            e4m3x4_to_bf16(wa[2 * h], a[0], a[1]);
-            e4m3x4_to_bf16(wa[2 * h + 1], a[2], a[3]);
-            e4m3x4_to_bf16(wb[2 * h], b[0], b[1]);
-            e4m3x4_to_bf16(wb[2 * h + 1], b[2], b[3]);
-            if (nan) {
-              e4m3_mark_nan(e4m3_nan(wa[2 * h]), a[0], a[1]);
-              e4m3_mark_nan(e4m3_nan(wa[2 * h + 1]), a[2], a[3]);
-              e4m3_mark_nan(e4m3_nan(wb[2 * h]), b[0], b[1]);
-              e4m3_mark_nan(e4m3_nan(wb[2 * h + 1]), b[2], b[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a[i] = cva[4 * h + i];
+              b[i] = cvb[4 * h + i];
             }
           } else {
             int4x8_to_bf16(wa[h], sa, a);
@@ -1080,7 +1090,14 @@ struct Consumer {
             // a token without a row reads zeros
             const uint32_t q = on[n] && valid ? arow[n] + col * 2 + h * 16 : zeros;
             float(&sum)[4] = o[WD == MOE_BF16 ? st : 0][n];
-            const uint4 v = lds16(q);
+            uint4 v = lds16(q);
+            if (WD == MOE_FP8_E4M3 && !PLANES) {  // x: to the order of the converted pairs
+              const uint4 u = v;
+              v.x = __byte_perm(u.x, u.y, 0x5410);
+              v.y = __byte_perm(u.x, u.y, 0x7632);
+              v.z = __byte_perm(u.z, u.w, 0x5410);
+              v.w = __byte_perm(u.z, u.w, 0x7632);
+            }
             mma16816(sum, a[0], b[0], a[1], b[1], v.x, v.y);
             mma16816(sum, a[2], b[2], a[3], b[3], v.z, v.w);
             if (PLANES) {
@@ -1163,7 +1180,7 @@ struct Consumer {
 
 // The reducer warps: sum the consumer warps' partial tiles in warp order, store the tiles' features
 // and publish the parts.
-template <int NT>
+template <int WD, int NT>
 struct Reducer {
   const FewParams& p;
   StreamHead& hd;
@@ -1204,7 +1221,7 @@ struct Reducer {
       const int hr = ti.row0 + __popc(ti.mask & ((1u << tok) - 1u));
       float v = silu_accurate(g) * u;
       if (ti.gated) v *= hd.sel.row_gate[hr];
-      store_planes(p.h2 + (int64_t)hr * p.I + ti.f0 + row, (int64_t)p.T * (p.k + 1) * p.I, v);
+      store_planes(p.h2 + (int64_t)hr * p.I + h_place<WD>(ti.f0 + row), (int64_t)p.T * (p.k + 1) * p.I, v);
     }
   }
   // 16 features times 8 NT tokens, two a thread and token group
@@ -1304,7 +1321,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
     __syncwarp();
     if (lane == 0) mbar_arrive(&hd.inv_bar);
   } else if (warp < kFirstCons) {
-    Reducer<NT> v{p, hd, red, (int)threadIdx.x - 32 * (kLanes + kSelWarps), lane};
+    Reducer<WD, NT> v{p, hd, red, (int)threadIdx.x - 32 * (kLanes + kSelWarps), lane};
     v.run();
   } else {
     Consumer<WD, NT> v{p, hd, slots, red, warp - kFirstCons, lane};
