@@ -463,17 +463,17 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
 // or more of each, where one bf16 would add a rounding of 2^-9.
 // ---------------------------------------------------------------------------------------------
 constexpr int kCons = 16;      // consumer warps
-constexpr int kLanes = 4;      // lanes of the stream: a producer warp, four consumer warps, kBufs slots
+constexpr int kLanes = 4;      // lanes of the stream: four consumer warps and kBufs slots each
 constexpr int kBufs = 2;
-constexpr int kSlots = kLanes * kBufs;
+constexpr int kSlots = kLanes * kBufs;  // one producer warp each
 constexpr int kSelWarps = 2;   // selection
 constexpr int kRedWarps = 2;   // sums of the finished tiles
-constexpr int kFirstCons = kLanes + kSelWarps + kRedWarps;
+constexpr int kFirstCons = kSlots + kSelWarps + kRedWarps;
 constexpr int kStreamThreads = 32 * (kFirstCons + kCons);
 constexpr int kRed = 2;        // tiles whose partial sums wait for the reducers
 // What is left of one CTA's shared memory, for 8 or 16 tokens.
-constexpr int slot_bytes(int nt) { return nt == 1 ? 24192 : 22016; }
-static_assert(kCons == 4 * kLanes && (kLanes & (kLanes - 1)) == 0, "four consumer warps to a lane");
+constexpr int slot_bytes(int nt) { return nt == 1 ? 24064 : 22016; }
+static_assert(kCons == 4 * kLanes && (kSlots & (kSlots - 1)) == 0, "four consumer warps to a lane");
 
 // Counters of the launch (FewParams::bar): arrivals of CTAs at the end of each part.
 enum : int { kCntDown = 0, kCntH = 1, kCntLat = 2, kCntShared = 3, kCounters = 4 };
@@ -505,6 +505,16 @@ __device__ __forceinline__ int slot_cols(int K, int nr) {
   return ((K + n - 1) / n + gran - 1) / gran * gran;
 }
 
+// The most activation rows (both planes of every token) leave room for one unit of channels at least.
+template <int WD>
+constexpr bool slot_fits(int nt) {
+  return (slot_bytes(nt) - (16 + 16 * nt) * 64) /
+             (16 * Wt<WD>::kBits / 8 + (WD == MOE_INT4 ? 1 : 0) + 2 * 16 * nt) >= Wt<WD>::kGran;
+}
+static_assert(slot_fits<MOE_BF16>(1) && slot_fits<MOE_FP8_E4M3>(1) && slot_fits<MOE_INT4>(1) &&
+                  slot_fits<MOE_BF16>(2) && slot_fits<MOE_FP8_E4M3>(2) && slot_fits<MOE_INT4>(2),
+              "a slot takes one unit of channels");
+
 // What a slot holds, written by its producer for the consumers.
 enum : int { kScaled = 1, kStop = 2 };  // kStop: no data, the stream ends
 struct alignas(16) SlotInfo {  // written in four 16-byte stores
@@ -524,19 +534,19 @@ static_assert(sizeof(SlotInfo) == 64, "four 16-byte stores");
 // counter f0; kEnd: the last.
 enum Kind { kDown, kHid, kLat, kShOut, kOut, kPublish, kEnd };
 struct Tile {
-  int kind, f0, cnt, row0;  // first h row
-  uint32_t mask;
-  int gated;
+  int f0;
+  uint16_t row0, mask;  // first h row, tokens
+  uint8_t kind, cnt, gated, pad_;
 };
-// Between two pieces of one lane the stream has kLanes - 1 others: at most kLanes tiles begin, and
-// three times that for the pieces the producer is ahead, with the publishings, the end and the
-// reducers' kRed: fewer than kTiles.
+// Between two pieces of one producer the stream has kSlots - 1 others: at most kSlots tiles begin, and
+// twice that while it is a piece ahead, with the publishings and the end: fewer than kTiles.
 constexpr int kTiles = 32;
 
 struct StreamHead {
   uint64_t info_bar[kSlots], full[kSlots], empty[kSlots], sel_bar, inv_bar, start_bar, red_full[kRed], red_empty[kRed];
   SlotInfo info[kSlots];
-  Tile tile[kLanes][kTiles];  // each producer's own, for its consumers (the reducers: lane 0's)
+  Tile tile[kSlots][kTiles];  // each producer's own, for its consumers
+  Tile red_tile[kRed];        // for the reducers
   uint4 zeros;
   float inv[kMaxT];
   int abort;
@@ -563,26 +573,25 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// A producer warp; warp i fills the slots of lane i, in turn, with every kLanes-th piece of the stream.
-// (One copy instruction takes its addresses from uniform registers, so a warp issues the 16 and more
-// copies of a slot one after another: one warp for all slots held the stream to 4.2 TB/s.)
+// A producer warp; warp i fills slot i with every kSlots-th piece of the stream.  (A copy instruction
+// takes its addresses from uniform registers, so a warp issues the 16 and more copies of a slot one
+// after another, about 60 clocks each: one warp for all slots held the stream to 4.2 TB/s.)
 template <int WD, int NT>
 struct Producer {
   const FewParams& p;
   StreamHead& hd;
-  uint8_t* slots;        // the lane's
-  int slot, lane;        // slot: lane of the stream
-  int turn = 0;          // lane of the stream's next piece (pieces go round the lanes)
-  uint32_t filled = 0;   // slots this warp has filled
+  uint8_t* base;         // this warp's slot
+  int slot, lane;
+  int turn = 0;          // slot of the stream's next piece (pieces go round the slots)
+  uint32_t filled = 0;   // times this warp has filled its slot
   uint32_t tile = 0;     // tiles begun
   uint32_t complete = 0; // counters known to be complete
   bool failed = false;
 
-  __device__ __forceinline__ int at() const { return slot * kBufs + filled % kBufs; }
-  // Waits until the consumers have left the next slot.
+  // Waits until the consumers have left the slot.
   __device__ __forceinline__ bool slot_free() {
     if (failed) return false;
-    const bool ok = mbar_wait_sleep(&hd.empty[at()], (filled / kBufs & 1u) ^ 1u, &hd.abort, p.err);
+    const bool ok = mbar_wait_sleep(&hd.empty[slot], (filled & 1u) ^ 1u, &hd.abort, p.err);
     if (__any_sync(0xffffffffu, !ok)) failed = true;
     return !failed;
   }
@@ -598,7 +607,7 @@ struct Producer {
   __device__ __forceinline__ void next_tile(int kind, int f0, int cnt, int row0, uint32_t mask,
                                             int gated) {
     if (failed) return;  // no longer paced by the slot: the consumers still read what is there
-    if (lane == 0) hd.tile[slot][tile % kTiles] = Tile{kind, f0, cnt, row0, mask, gated};
+    if (lane == 0) hd.tile[slot][tile % kTiles] = Tile{f0, (uint16_t)row0, (uint16_t)mask, (uint8_t)kind, (uint8_t)cnt, (uint8_t)gated, 0};
     ++tile;
   }
 
@@ -631,8 +640,8 @@ struct Producer {
     const int n = __popc(mask);
     const int fit = __shfl_sync(0xffffffffu, g.lane_cols, n - 1);
     const int step = fit & 0xfffff, pieces = fit >> 20;
-    const int first = (slot - turn) & (kLanes - 1);  // the first that falls to this warp
-    turn = (turn + pieces) & (kLanes - 1);
+    const int first = (slot - turn) & (kSlots - 1);  // the first that falls to this warp
+    turn = (turn + pieces) & (kSlots - 1);
     if (first >= pieces) return;
     int c0 = first * step;
     const uint8_t* w = g.w;
@@ -653,14 +662,13 @@ struct Producer {
     const int pl = lane >= n, j = lane - pl * n;
     const int a_src = lane < rows ? (g.tokens ? nth_token(mask, j) : row0 + j) : 0;
     const __nv_bfloat16* a_row = g.act + pl * g.plane + (int64_t)a_src * g.K;
-    for (; c0 < g.K; c0 += kLanes * step) {
+    uint64_t* full = &hd.full[slot];
+    for (; c0 < g.K; c0 += kSlots * step) {
       if (!slot_free()) return;
-      uint8_t* base = slots + filled % kBufs * slot_bytes(NT);
-      uint64_t* full = &hd.full[at()];
       const int cols = min(step, g.K - c0);
       const uint32_t nb = Wt<WD>::bytes(cols);
       if (lane == 0) {
-        int4* i = reinterpret_cast<int4*>(&hd.info[at()]);
+        int4* i = reinterpret_cast<int4*>(&hd.info[slot]);
         const uint64_t sp = WD == MOE_FP8_E4M3
                                 ? reinterpret_cast<uint64_t>(static_cast<const float*>(sc) + (c0 >> 7))
                                 : 0;
@@ -668,7 +676,7 @@ struct Producer {
         i[1] = make_int4(soff, g.plane ? n * apitch : 0, (int)mask, g.scaled ? kScaled : 0);
         i[2] = make_int4(f0, cnt, (int)(uint32_t)sp, (int)(sp >> 32));
         i[3] = make_int4(g.K >> 7, g.u_off, (int)(tile - 1), 0);
-        mbar_arrive(&hd.info_bar[at()]);
+        mbar_arrive(&hd.info_bar[slot]);
         mbar_arrive_expect_tx(full, (g.u_off ? 2 * cnt : cnt) * nb);
       }
       __syncwarp();
@@ -790,13 +798,12 @@ struct Producer {
     }
     next_tile(kEnd, 0, 0, 0, 0, 0);
     if (slot_free() && lane == 0) {
-      hd.info[at()].flags = kStop;
-      hd.info[at()].tile = tile;
-      mbar_arrive(&hd.info_bar[at()]);
+      hd.info[slot].flags = kStop;
+      hd.info[slot].tile = tile;
+      mbar_arrive(&hd.info_bar[slot]);
     }
     // after a failure the copies in flight still have to land before the CTA ends
-    for (uint32_t i = filled > kBufs ? filled - kBufs : 0; i < filled; ++i)
-      mbar_wait(&hd.full[slot * kBufs + i % kBufs], i / kBufs & 1u, nullptr, nullptr, kDrainLimitNs);
+    if (filled) mbar_wait(&hd.full[slot], (filled - 1) & 1u, nullptr, nullptr, kDrainLimitNs);
   }
 };
 
@@ -848,7 +855,7 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t k16, uint32_t k256, uint32_t& p02,
                                                uint32_t& p13, uint32_t& top) {
   const uint32_t e02 = w & 0x007f007fu, e13 = (w >> 8) & 0x007f007fu;
-  top = __vmaxu2(top, __vmaxu2(e02, e13));
+  top = __vimax3_u16x2(top, e02, e13);
   p02 = mul_bf16x2(e02 * k16 + (w & 0x00800080u) * k256, 0x7b807b80u);
   p13 = mul_bf16x2(e13 * k16 + (w & 0x80008000u), 0x7b807b80u);
 }
@@ -898,10 +905,11 @@ struct Consumer {
   }
 
   // Hands this warp's sums of tile number t to the reducers.
-  __device__ __forceinline__ bool hand_over(const float (&acc)[NT][4], uint32_t t) {
+  __device__ __forceinline__ bool hand_over(const float (&acc)[NT][4], uint32_t t, const Tile& ti) {
     const int gr = lane >> 2, t4 = lane & 3;
     if (!wait(&hd.red_empty[t % kRed], (t / kRed & 1u) ^ 1u)) return false;
-    if (hd.tile[warp >> 2][t % kTiles].kind < kPublish) {
+    if (warp == 0 && lane == 0) hd.red_tile[t % kRed] = ti;
+    if (ti.kind < kPublish) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float* r = red + ((t % kRed * kCons + warp) * NT + n) * 128 + gr * 8 + t4 * 2;
@@ -1133,17 +1141,17 @@ struct Consumer {
   }
 
   __device__ void run() {
-    const int slot = warp >> 2, part = warp & 3, t4 = lane & 3;
+    const int line = warp >> 2, part = warp & 3, t4 = lane & 3;
     float acc[NT][4];
     zero_sums(acc);
     uint32_t tile = 0;
     for (uint32_t piece = 0;; ++piece) {
-      const int at = slot * kBufs + piece % kBufs;
+      const int at = line + piece % kBufs * kLanes;  // pieces go round the slots, kLanes apart here
       const uint32_t parity = piece / kBufs & 1u;
       const SlotInfo& si = hd.info[at];
       if (!wait(&hd.info_bar[at], parity)) return;
       for (const uint32_t now = si.tile; tile != now; ++tile) {  // tiles that ended before it
-        if (!hand_over(acc, tile)) return;
+        if (!hand_over(acc, tile, hd.tile[at][tile % kTiles])) return;
         zero_sums(acc);
       }
       const int flags = si.flags;
@@ -1191,7 +1199,7 @@ struct Reducer {
   __device__ void run() {
     for (uint32_t t = 0;; ++t) {
       if (!mbar_wait_sleep(&hd.red_full[t % kRed], t / kRed & 1u, &hd.abort, p.err)) return;
-      const Tile ti = hd.tile[0][t % kTiles];
+      const Tile ti = hd.red_tile[t % kRed];
       if (ti.kind == kEnd) return;
       if (ti.kind == kPublish) {
         publish(ti.f0);
@@ -1302,17 +1310,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
   }
   __syncthreads();
 
-  if (warp < kLanes) {
-    Producer<WD, NT> v{p, hd, slots + (size_t)warp * kBufs * slot_bytes(NT), warp, lane};
+  if (warp < kSlots) {
+    Producer<WD, NT> v{p, hd, slots + (size_t)warp * slot_bytes(NT), warp, lane};
     v.run();
-  } else if (warp < kLanes + kSelWarps) {
-    if (!build_selection(p, hd.sel, threadIdx.x - 32 * kLanes, kSelWarps, 2, &hd.abort)) return;
+  } else if (warp < kSlots + kSelWarps) {
+    if (!build_selection(p, hd.sel, threadIdx.x - 32 * kSlots, kSelWarps, 2, &hd.abort)) return;
     if (lane == 0) mbar_arrive(&hd.sel_bar);
     if (!p.L) return;
     int ok = 1;
     if (lane == 0) ok = counter_wait(p.bar + kCntLat, gridDim.x, &hd.abort, p.err);
     if (!__shfl_sync(0xffffffffu, ok, 0)) return;
-    for (int t = warp - kLanes; t < p.T; t += kSelWarps) {
+    for (int t = warp - kSlots; t < p.T; t += kSelWarps) {
       float ss = 0.0f;
       for (int c = lane; c < (int)gridDim.x; c += 32) ss += __ldcg(p.ssq + c * kMaxT + t);
       ss = warp_sum(ss);
@@ -1321,7 +1329,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
     __syncwarp();
     if (lane == 0) mbar_arrive(&hd.inv_bar);
   } else if (warp < kFirstCons) {
-    Reducer<WD, NT> v{p, hd, red, (int)threadIdx.x - 32 * (kLanes + kSelWarps), lane};
+    Reducer<WD, NT> v{p, hd, red, (int)threadIdx.x - 32 * (kSlots + kSelWarps), lane};
     v.run();
   } else {
     Consumer<WD, NT> v{p, hd, slots, red, warp - kFirstCons, lane};
