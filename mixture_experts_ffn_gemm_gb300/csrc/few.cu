@@ -547,7 +547,7 @@ struct StreamHead {
   SlotInfo info[kSlots];
   Tile tile[kSlots][kTiles];  // each producer's own, for its consumers
   Tile red_tile[kRed];        // for the reducers
-  uint4 zeros;
+  uint4 zeros[4];
   float inv[kMaxT];
   int abort;
   uint32_t done[kCounters];  // reducer warps through each part
@@ -766,30 +766,34 @@ struct Producer {
         kind = kShOut;
       }
       src.fit(lane);
-      int u = (int)((int64_t)(total / G) * blockIdx.x / gridDim.x) * G;
+      const int u0 = (int)((int64_t)(total / G) * blockIdx.x / gridDim.x) * G;
       const int u1 = (int)((int64_t)(total / G) * (blockIdx.x + 1) / gridDim.x) * G;
+      const bool routed = part == kPartRouted;
+      int a = routed ? u0 / p.I : 0, f = u0 - a * p.I * (routed ? 1 : 0), left = u1 - u0;
 #pragma unroll 1
-      while (u < u1) {
-        int a = 0, f = u, len = u1 - u;
-        if (part == kPartRouted) {
-          a = u / p.I;
-          f = u - a * p.I;
-          len = min(len, p.I - f);
-        }
-        const int n = (len + (pair ? 7 : 15)) / (pair ? 8 : 16);  // tiles left, evenly
-        const int cnt = (len / G + n - 1) / n * G;
-        const bool routed = part == kPartRouted;
+      while (left > 0) {  // spans of one matrix (routed: of one expert), in tiles of nearly one size
+        const int len = routed ? min(left, p.I - f) : left;
+        const int n = (len + (pair ? 7 : 15)) >> (pair ? 3 : 4);
+        const int size = len / G / n, more = len / G - size * n;
         const int e = routed ? sel.active[a] : -1;
         const uint32_t mask = routed ? sel.active_mask[a] : all;
-        next_tile(kind, f, cnt, routed ? sel.row0[a] : P, mask, routed);
-        if (part == kPartW2) {
+        const int h_row = routed ? sel.row0[a] : P;
 #pragma unroll 1
-          for (int i = 0; i < sel.n_active; ++i)
-            seg(src, sel.active[i], f, cnt, sel.active_mask[i], sel.row0[i]);
-        } else {
-          seg(src, e, f, cnt, mask, part == kPartUp ? 0 : P);
+        for (int i = 0; i < n; ++i) {
+          const int cnt = (size + (i < more)) * G;
+          next_tile(kind, f, cnt, h_row, mask, routed);
+          if (part == kPartW2) {
+#pragma unroll 1
+            for (int j = 0; j < sel.n_active; ++j)
+              seg(src, sel.active[j], f, cnt, sel.active_mask[j], sel.row0[j]);
+          } else {
+            seg(src, e, f, cnt, mask, part == kPartUp ? 0 : P);
+          }
+          f += cnt;
         }
-        u += cnt;
+        left -= len;
+        ++a;
+        if (routed) f = 0;
       }
       if (part == kPartDown) next_tile(kPublish, kCntDown, 0, 0, 0, 0);
       if (part == kPartShared) next_tile(kPublish, kCntShared, 0, 0, 0, 0);
@@ -851,7 +855,7 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
 // bf16's places give value * 2^-120 (subnormals included), the product with 2^120 is exact.  The
 // integer pipe runs at half rate and bounds the e4m3 layer, so the left shifts are multiplications
 // (k16 and k256 are 16 and 256, unknown to the compiler).  top collects the largest magnitude of the
-// codes in each half: 0x7f, a NaN, is marked by the caller.
+// codes in each half: 0x7f is NaN.
 __device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t k16, uint32_t k256, uint32_t& p02,
                                                uint32_t& p13, uint32_t& top) {
   const uint32_t e02 = w & 0x007f007fu, e13 = (w >> 8) & 0x007f007fu;
@@ -861,11 +865,6 @@ __device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t k16, uint32_
 }
 __device__ __forceinline__ bool e4m3_any_nan(uint32_t top) {
   return (top & 0xffffu) == 0x7fu || top >> 16 == 0x7fu;
-}
-__device__ __forceinline__ void e4m3_mark_nan(uint32_t w, uint32_t& p02, uint32_t& p13) {
-  const uint32_t bad = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-  p02 |= (bad & 0x80u ? 0x7fffu : 0u) | (bad & 0x800000u ? 0x7fff0000u : 0u);
-  p13 |= (bad & 0x8000u ? 0x7fffu : 0u) | (bad & 0x80000000u ? 0x7fff0000u : 0u);
 }
 // The order in which h is stored for the e4m3 layer: features 4i, 4i + 2, 4i + 1, 4i + 3, the pairs
 // that e4m3x4_to_bf16 gives.
@@ -1011,7 +1010,7 @@ struct Consumer {
     const uint32_t mask = si.mask;
     const uint32_t wa_row = base + gr * si.wpitch, wb_row = wa_row + 8 * si.wpitch;
     const uint32_t sc_row = base + si.soff + gr * 2;
-    const uint32_t zeros = settle(smem_u32(&hd.zeros));
+    const uint32_t zeros = settle(smem_u32(hd.zeros));
     uint32_t arow[NT];  // this lane's token row among the activations
     bool on[NT];
 #pragma unroll
@@ -1029,6 +1028,7 @@ struct Consumer {
     }
     const uint32_t plane = PLANES ? si.plane : 0;
     const uint32_t k16 = settle(16u), k256 = settle(256u);
+    uint32_t top_a = 0, top_b = 0;  // largest e4m3 magnitudes of the two rows
     // two bf16 units at a time, with sums of their own, so that their products overlap
     constexpr int kPar = WD == MOE_BF16 ? 2 : 1;
     constexpr int kSteps = WD == MOE_BF16 ? kPar : W::kUnit / W::kStep;
@@ -1057,21 +1057,11 @@ struct Consumer {
           sb = valid ? lds2(sc_row + 16 + col) * 0x10001u : 0u;
         }
         const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
-        uint32_t cva[8], cvb[8];  // e4m3: all 16 channels as bf16
-        if constexpr (WD == MOE_FP8_E4M3) {
-          uint32_t top = 0;
+        uint32_t q[NT], q2[NT];  // this lane's channels of its tokens, plane by plane
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            e4m3x4_to_bf16(wa[i], k16, k256, cva[2 * i], cva[2 * i + 1], top);
-            e4m3x4_to_bf16(wb[i], k16, k256, cvb[2 * i], cvb[2 * i + 1], top);
-          }
-          if (e4m3_any_nan(top)) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              e4m3_mark_nan(wa[i], cva[2 * i], cva[2 * i + 1]);
-              e4m3_mark_nan(wb[i], cvb[2 * i], cvb[2 * i + 1]);
-            }
-          }
+        for (int n = 0; n < NT; ++n) {
+          q[n] = on[n] && valid ? arow[n] + col * 2 : zeros;  // a token without a row reads zeros
+          q2[n] = on[n] && valid ? q[n] + plane : zeros;
         }
 #pragma unroll
         for (int h = 0; h < W::kChunk / 8; ++h) {  // 8 channels: two products
@@ -1083,11 +1073,10 @@ struct Consumer {
               b[i] = wb[i];
             }
           } else if constexpr (WD == MOE_FP8_E4M3) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              a[i] = cva[4 * h + i];
-              b[i] = cvb[4 * h + i];
-            }
+            e4m3x4_to_bf16(wa[2 * h], k16, k256, a[0], a[1], top_a);
+            e4m3x4_to_bf16(wa[2 * h + 1], k16, k256, a[2], a[3], top_a);
+            e4m3x4_to_bf16(wb[2 * h], k16, k256, b[0], b[1], top_b);
+            e4m3x4_to_bf16(wb[2 * h + 1], k16, k256, b[2], b[3], top_b);
           } else {
             int4x8_to_bf16(wa[h], sa, a);
             int4x8_to_bf16(wb[h], sb, b);
@@ -1095,10 +1084,8 @@ struct Consumer {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             if (NT > 1 && !(mask >> (n * 8) & 0xffu)) continue;
-            // a token without a row reads zeros
-            const uint32_t q = on[n] && valid ? arow[n] + col * 2 + h * 16 : zeros;
             float(&sum)[4] = o[WD == MOE_BF16 ? st : 0][n];
-            uint4 v = lds16(q);
+            uint4 v = lds16(q[n] + h * 16);
             if (WD == MOE_FP8_E4M3 && !PLANES) {  // x: to the order of the converted pairs
               const uint4 u = v;
               v.x = __byte_perm(u.x, u.y, 0x5410);
@@ -1109,7 +1096,7 @@ struct Consumer {
             mma16816(sum, a[0], b[0], a[1], b[1], v.x, v.y);
             mma16816(sum, a[2], b[2], a[3], b[3], v.z, v.w);
             if (PLANES) {
-              const uint4 v2 = lds16(on[n] && valid ? q + plane : zeros);
+              const uint4 v2 = lds16(q2[n] + h * 16);
               mma16816(sum, a[0], b[0], a[1], b[1], v2.x, v2.y);
               mma16816(sum, a[2], b[2], a[3], b[3], v2.z, v2.w);
             }
@@ -1130,6 +1117,18 @@ struct Consumer {
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int j = 0; j < kPar; ++j) d[n][i] += o[j][n][i];
+    } else {
+      // a NaN code that any of a row's four lanes has met makes the row's sums NaN
+      const uint32_t bad = (e4m3_any_nan(top_a) ? 1u : 0u) | (e4m3_any_nan(top_b) ? 2u : 0u);
+      if (__any_sync(0xffffffffu, bad != 0)) {
+        const uint32_t ba = __ballot_sync(0xffffffffu, bad & 1u) >> (gr * 4) & 15u;
+        const uint32_t bb = __ballot_sync(0xffffffffu, bad & 2u) >> (gr * 4) & 15u;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < 2 ? ba : bb) d[n][i] = __uint_as_float(0x7fffffffu);
+      }
     }
   }
 
@@ -1304,7 +1303,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
       mbar_init(&hd.red_empty[i], kRedWarps);
     }
     hd.abort = 0;
-    hd.zeros = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 4; ++i) hd.zeros[i] = make_uint4(0, 0, 0, 0);
     for (int i = 0; i < kCounters; ++i) hd.done[i] = 0;
     fence_barrier_init();
   }
