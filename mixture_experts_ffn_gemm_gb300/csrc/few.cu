@@ -23,7 +23,8 @@ constexpr int kMaxT = MOE_FEW_MAX_TOKENS;
 constexpr int kMaxE = 1023;
 constexpr int kMaxPairs = kMaxT * 32;
 constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = kThreads / 32;  // consumers of the stream, too
+static_assert(kWarps >= kMaxT, "one for each token");
 
 struct FewParams {
   int T, d, E, k, I, L;  // L: latent width, 0 on the K2 path
@@ -38,7 +39,7 @@ struct FewParams {
   void* out;
   uint32_t* err;
   uint32_t* bar;   // one arrival counter per barrier, zeroed before the launch
-  float* logits;   // [T][E], zeroed before the launch
+  float* scores;   // [T][E] sigma(z), zeroed before the launch
   // fp32 kernel
   float* x_lat;    // [T][L]
   float* h;        // [T * k + T][I]: routed rows expert by expert, then the shared rows
@@ -106,113 +107,133 @@ __device__ __forceinline__ uint32_t key_bits(float v) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One warp selects the experts of tokens t0, t0 + stride, ...: k rounds of the largest key, ties to
-// the lower index.  Lane l holds experts l, l + 32, ... in registers (N >= ceil(E / 32) of them).  The
-// logits may still be on their way: the launch starts with zeros in their place, no logit is stored
-// as +0, and the warp reads until none is left (one trip to memory instead of a counter's and then
-// the logits').  The next token's are read ahead.
+// One warp selects the experts of token t: k rounds of the largest key, ties to the lower index.
+// Lane l holds experts l, l + 32, ... in registers (N >= ceil(E / 32) of them).  The scores may still
+// be on their way: the launch starts with zeros in their place, no score is stored as +0, and the
+// warp reads until none is left (one trip to memory instead of a counter's and then the scores').
 template <int N>
-__device__ __forceinline__ void read_logits(const FewParams& p, int t, float (&z)[N]) {
-  const int lane = threadIdx.x & 31;
-  const float* lg = p.logits + (int64_t)t * p.E + lane;
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    z[j] = -0.0f;
-    if (t < p.T && lane + 32 * j < p.E)
-      asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(z[j]) : "l"(lg + 32 * j));
-  }
-}
-template <int N>
-__device__ void choose(const FewParams& p, int t, float (&z)[N], Selection& sel);
-
-template <int N>
-__device__ bool select_tokens(const FewParams& p, int t0, int stride, Selection& sel,
-                              volatile int* abort) {
-  float z[N], next[N];
-  read_logits(p, t0, z);
-  uint64_t since = 0;
-  for (int t = t0; t < p.T; t += stride) {
-    read_logits(p, t + stride, next);
-    while (true) {
-      bool all = true;
-#pragma unroll
-      for (int j = 0; j < N; ++j) all = all && __float_as_uint(z[j]) != 0u;
-      if (__all_sync(0xffffffffu, all)) break;
-      const uint64_t now = globaltimer_ns();
-      if (since == 0) since = now;
-      bool stop = abort && *abort;
-      if (now - since > kWaitLimitNs) {
-        if (abort) *abort = 1;
-        raise_flag(p.err, kErrTimeout);
-        stop = true;
-      }
-      if (__any_sync(0xffffffffu, stop)) return false;
-      read_logits(p, t, z);
-    }
-    choose(p, t, z, sel);
-#pragma unroll
-    for (int j = 0; j < N; ++j) z[j] = next[j];
-  }
-  return true;
-}
-
-template <int N>
-__device__ void choose(const FewParams& p, int t, float (&z)[N], Selection& sel) {
+__device__ bool select_token(const FewParams& p, int t, Selection& sel, volatile int* abort) {
   const int lane = threadIdx.x & 31;
   uint32_t key[N];
+  float z[N];
+  const float* sc = p.scores + (int64_t)t * p.E + lane;
+  uint64_t since = 0;
+  while (true) {
+    bool all = true;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      z[j] = -0.0f;
+      if (lane + 32 * j < p.E)
+        asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(z[j]) : "l"(sc + 32 * j));
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) all = all && __float_as_uint(z[j]) != 0u;
+    if (__all_sync(0xffffffffu, all)) break;
+    const uint64_t now = globaltimer_ns();
+    if (since == 0) since = now;
+    bool stop = abort && *abort;
+    if (now - since > kWaitLimitNs) {
+      if (abort) *abort = 1;
+      raise_flag(p.err, kErrTimeout);
+      stop = true;
+    }
+    if (__any_sync(0xffffffffu, stop)) return false;
+  }
+  uint32_t top = 0;  // this lane's largest key left, its place j (the lowest) and score
+  int top_j = 0;
+  float top_s = 0.0f;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    z[j] = 1.0f / (1.0f + expf(-z[j]));
     key[j] = lane + 32 * j < p.E ? key_bits(z[j] + sel.bias[lane + 32 * j]) : 0u;
+    if (key[j] > top) {
+      top = key[j];
+      top_j = j;
+      top_s = z[j];
+    }
   }
   float my_s = 0.0f, den = 0.0f;
   int my_e = 0;
   for (int slot = 0; slot < p.k; ++slot) {
-    uint32_t best = 0;
-#pragma unroll
-    for (int j = 0; j < N; ++j) best = max(best, key[j]);
-    best = __reduce_max_sync(0xffffffffu, best);
-    uint32_t e = 0xffffffffu;
-#pragma unroll
-    for (int j = N - 1; j >= 0; --j)
-      if (key[j] == best) e = lane + 32 * j;
-    e = __reduce_min_sync(0xffffffffu, e);  // best >= 1: always an expert not taken yet
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if ((int)e == lane + 32 * j) {
-        s = z[j];
-        key[j] = 0;
-      }
-    s = __shfl_sync(0xffffffffu, s, e & 31);
+    const uint32_t best = __reduce_max_sync(0xffffffffu, top);  // >= 1: an expert is left
+    const uint32_t e = __reduce_min_sync(0xffffffffu, top == best ? (uint32_t)(lane + 32 * top_j) : 0xffffffffu);
+    const float s = __shfl_sync(0xffffffffu, top_s, e & 31);
     if (lane == slot) {
       my_e = (int)e;
       my_s = s;
     }
     den += s;
+    if (lane == (int)(e & 31)) {
+      const int was = top_j;
+      top = 0;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        if (j == was) key[j] = 0;
+        if (key[j] > top) {
+          top = key[j];
+          top_j = j;
+          top_s = z[j];
+        }
+      }
+    }
+    __syncwarp();
   }
   if (lane < p.k) {
     sel.pair_e[t * p.k + lane] = (int16_t)my_e;
     sel.pair_g[t * p.k + lane] = p.gate_scale * my_s / den;
   }
+  return true;
 }
 
-// The CTA's copy of the selection, by n_warps warps of which this thread is number tid (barrier
-// `bar` is theirs): per-expert token masks, the distinct experts in index order, the first h row of
-// each and each row's gate.  False when a wait for the logits gave up.
-__device__ bool build_selection(const FewParams& p, Selection& sel, int tid, int n_warps, int bar,
-                                volatile int* abort) {
-  const int n = n_warps * 32, lane = tid & 31;
+// The CTA's copy of the selection, by the kWarps warps of which this thread is number tid (barrier 1
+// is theirs), one for each token: per-expert token masks, the distinct experts in index order, the
+// first h row of each and each row's gate.  False when a wait for the scores gave up.
+__device__ bool build_selection(const FewParams& p, Selection& sel, int tid, volatile int* abort) {
+  constexpr int n = kWarps * 32, bar = 1;
+  const int lane = tid & 31, t = tid >> 5;
   for (int e = tid; e < p.E; e += n) {
     sel.mask[e] = 0;
     sel.bias[e] = __ldg(p.b + e);
   }
   named_barrier(bar, n);
-  const int w = tid >> 5;
-  const bool ok = p.E <= 64    ? select_tokens<2>(p, w, n_warps, sel, abort)
-                  : p.E <= 384 ? select_tokens<12>(p, w, n_warps, sel, abort)
-                               : select_tokens<32>(p, w, n_warps, sel, abort);
+  bool ok = true;
+  if (t < p.T)
+    ok = p.E <= 64    ? select_token<2>(p, t, sel, abort)
+         : p.E <= 384 ? select_token<12>(p, t, sel, abort)
+                      : select_token<32>(p, t, sel, abort);
   if (!named_barrier_and(bar, n, ok)) return false;
+  if (p.T * p.k <= 32) {  // few pairs: one lane each, ordered by comparing every two
+    if (tid < 32) {
+      const int P = p.T * p.k, tok = lane / p.k;
+      const int e = lane < P ? sel.pair_e[lane] : 0x7fff;
+      int rows = 0, place = 0;  // pairs and distinct experts before this one's
+      uint32_t mask = 0, first = 0xffffffffu;
+      for (int j = P - 1; j >= 0; --j) {
+        const int ej = __shfl_sync(0xffffffffu, e, j);
+        if (ej == e) {
+          mask |= 1u << (j / p.k);
+          first = j;
+        }
+        rows += ej < e;
+      }
+      const uint32_t leaders = __ballot_sync(0xffffffffu, lane < P && (int)first == lane);
+      for (uint32_t m = leaders; m; m &= m - 1)
+        place += __shfl_sync(0xffffffffu, e, __ffs(m) - 1) < e;
+      if (lane < P) {
+        if ((int)first == lane) {
+          sel.active[place] = (int16_t)e;
+          sel.active_mask[place] = (uint16_t)mask;
+          sel.row0[place] = (int16_t)rows;
+        }
+        sel.row_gate[rows + __popc(mask & ((1u << tok) - 1u))] = sel.pair_g[lane];
+      }
+      if (lane == 0) {
+        sel.n_active = __popc(leaders);
+        sel.row0[__popc(leaders)] = (int16_t)P;
+      }
+    }
+    named_barrier(bar, n);
+    return true;
+  }
   for (int i = tid; i < p.T * p.k; i += n) atomicOr(&sel.mask[sel.pair_e[i]], 1u << (i / p.k));
   named_barrier(bar, n);
   if (tid < 32) {  // compact: 32 experts at a time
@@ -243,15 +264,18 @@ __device__ bool build_selection(const FewParams& p, Selection& sel, int tid, int
   }
   named_barrier(bar, n);
   for (int i = tid; i < p.T * p.k; i += n) {
-    const int e = sel.pair_e[i], t = i / p.k;
-    sel.row_gate[sel.row0[sel.slot[e]] + __popc(sel.mask[e] & ((1u << t) - 1u))] = sel.pair_g[i];
+    const int e = sel.pair_e[i], tok = i / p.k;
+    sel.row_gate[sel.row0[sel.slot[e]] + __popc(sel.mask[e] & ((1u << tok) - 1u))] = sel.pair_g[i];
   }
   named_barrier(bar, n);
   return true;
 }
 
-// A logit as it is stored: +0 marks one that is not computed yet.
-__device__ __forceinline__ float stored_logit(float z) { return z == 0.0f ? -0.0f : z; }
+// sigma of a logit as it is stored: +0 marks one that is not computed yet.
+__device__ __forceinline__ float stored_score(float z) {
+  const float s = 1.0f / (1.0f + expf(-z));
+  return s == 0.0f ? -0.0f : s;
+}
 
 // 8 values that an earlier step of this kernel wrote (past L1).
 __device__ __forceinline__ void load8_cg(const float* p, float (&v)[8]) {
@@ -328,7 +352,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
           const float z = warp_sum(acc[n]);
           if (lane == 0) {
             if (u < p.E)
-              p.logits[(int64_t)n * p.E + u] = stored_logit(z);
+              p.scores[(int64_t)n * p.E + u] = stored_score(z);
             else
               p.x_lat[(int64_t)n * p.L + u - p.E] = z;
           }
@@ -349,12 +373,12 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
   if (!grid_barrier(p.bar, p.err)) return;
 
   // B
-  if (!build_selection(p, sel, threadIdx.x, kWarps, 1, nullptr)) return;
+  if (!build_selection(p, sel, threadIdx.x, nullptr)) return;
   for (int64_t u = gw; u < (int64_t)sel.n_active * p.I; u += nw) {
     const int a = (int)(u / p.I), f = (int)(u - (int64_t)a * p.I);
     const int64_t e = sel.active[a];
     const int row0 = sel.row0[a], n_e = sel.row0[a + 1] - row0;
-    const uint32_t mask = sel.mask[e];
+    const uint32_t mask = sel.active_mask[a];
     zero(acc);
     zero(acu);
     auto act = [&](int n, int c, float(&v)[8]) {
@@ -385,7 +409,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
     for (int a = 0; a < sel.n_active; ++a) {
       const int64_t e = sel.active[a];
       const int row0 = sel.row0[a], n_e = sel.row0[a + 1] - row0;
-      const uint32_t mask = sel.mask[e];
+      const uint32_t mask = sel.active_mask[a];
       float part[kMaxT];
       zero(part);
       auto act = [&](int n, int c, float(&v)[8]) {
@@ -462,13 +486,12 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
 // hi = bf16(v) and lo = bf16(v - hi), and multiplied plane by plane into the same fp32 sum: 16 bits
 // or more of each, where one bf16 would add a rounding of 2^-9.
 // ---------------------------------------------------------------------------------------------
-constexpr int kCons = 16;      // consumer warps
+constexpr int kCons = kWarps;  // consumer warps
 constexpr int kLanes = 4;      // lanes of the stream: four consumer warps and kBufs slots each
 constexpr int kBufs = 2;
 constexpr int kSlots = kLanes * kBufs;  // one producer warp each
-constexpr int kSelWarps = 2;   // selection
 constexpr int kRedWarps = 2;   // sums of the finished tiles
-constexpr int kFirstCons = kSlots + kSelWarps + kRedWarps;
+constexpr int kFirstCons = kSlots + kRedWarps;
 constexpr int kStreamThreads = 32 * (kFirstCons + kCons);
 constexpr int kRed = 2;        // tiles whose partial sums wait for the reducers
 // What is left of one CTA's shared memory, for 8 or 16 tokens.
@@ -926,23 +949,23 @@ struct Consumer {
   // kExp experts' loads are in: behind a full ring they would wait for all of it (the selection was
   // ready at 18 us instead of XX).
   __device__ void router() {
-    constexpr int kExp = 3, kMost = 2;
+    constexpr int kExp = 3, kMost = 2, kTok = 4;  // loads in flight, in registers
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
     const int part = ((p.d + kCons - 1) / kCons + 31) / 32 * 32;
     const int end = min(p.d, (warp + 1) * part);
     if ((int)blockIdx.x >= p.E && lane == 0) mbar_arrive(&hd.start_bar);
     for (int e0 = blockIdx.x; e0 < p.E; e0 += kExp * (int)gridDim.x) {
 #pragma unroll 1
-      for (int n = 0; n < NT; ++n) {
-        float z[kExp][8];
+      for (int n = 0; n < p.T; n += kTok) {
+        float z[kExp][kTok];
 #pragma unroll
         for (int j = 0; j < kExp; ++j)
 #pragma unroll
-          for (int t = 0; t < 8; ++t) z[j][t] = 0.0f;
+          for (int t = 0; t < kTok; ++t) z[j][t] = 0.0f;
 #pragma unroll 1
         for (int c0 = warp * part + lane * 4; c0 < end; c0 += 128 * kMost) {
           float4 wv[kMost][kExp];
-          uint2 xv[kMost][8];
+          uint2 xv[kMost][kTok];
 #pragma unroll
           for (int i = 0; i < kMost; ++i) {
             const int c = c0 + i * 128;
@@ -954,15 +977,15 @@ struct Consumer {
                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
-              xv[i][t] = c < end && n * 8 + t < p.T
-                             ? __ldg(reinterpret_cast<const uint2*>(x + (int64_t)(n * 8 + t) * p.d + c))
+            for (int t = 0; t < kTok; ++t)
+              xv[i][t] = c < end && n + t < p.T
+                             ? __ldg(reinterpret_cast<const uint2*>(x + (int64_t)(n + t) * p.d + c))
                              : make_uint2(0, 0);
           }
 #pragma unroll
           for (int i = 0; i < kMost; ++i)
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
+            for (int t = 0; t < kTok; ++t) {
               const float x0 = __uint_as_float(xv[i][t].x << 16),
                           x1 = __uint_as_float(xv[i][t].x & 0xffff0000u),
                           x2 = __uint_as_float(xv[i][t].y << 16),
@@ -977,12 +1000,12 @@ struct Consumer {
             }
         }
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          if (n * 8 + t >= p.T) break;
+        for (int t = 0; t < kTok; ++t) {
+          if (n + t >= p.T) break;
 #pragma unroll
           for (int j = 0; j < kExp; ++j) {
             const float v = warp_sum(z[j][t]);
-            if (lane == 0) red[(warp * kExp + j) * kMaxT + n * 8 + t] = v;
+            if (lane == 0) red[(warp * kExp + j) * kMaxT + n + t] = v;
           }
         }
       }
@@ -994,7 +1017,7 @@ struct Consumer {
         float v = 0.0f;
 #pragma unroll
         for (int w = 0; w < kCons; ++w) v += red[(w * kExp + j) * kMaxT + t];
-        p.logits[(int64_t)t * p.E + e] = stored_logit(v);
+        p.scores[(int64_t)t * p.E + e] = stored_score(v);
       }
       named_barrier(1, kCons * 32);  // red has been read
     }
@@ -1277,6 +1300,21 @@ struct Reducer {
       __threadfence();
       asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.bar + counter) : "memory");
     }
+    if (counter == kCntLat) inverse_rms();
+  }
+  // 1 / rms of the tokens' latent sums, once every CTA has published its squares.
+  __device__ void inverse_rms() {
+    int ok = 1;
+    if (lane == 0) ok = counter_wait(p.bar + kCntLat, gridDim.x, &hd.abort, p.err);
+    if (!__shfl_sync(0xffffffffu, ok, 0)) return;
+    for (int t = tid >> 5; t < p.T; t += kRedWarps) {
+      float ss = 0.0f;
+      for (int c = lane; c < (int)gridDim.x; c += 32) ss += __ldcg(p.ssq + c * kMaxT + t);
+      ss = warp_sum(ss);
+      if (lane == 0) hd.inv[t] = p.latent_norm ? 1.0f / sqrtf(ss / (float)p.L + p.eps) : 1.0f;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&hd.inv_bar);
   }
 };
 
@@ -1295,8 +1333,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
       mbar_init(&hd.info_bar[i], 1);
       mbar_init(&hd.empty[i], kCons / kLanes);
     }
-    mbar_init(&hd.sel_bar, kSelWarps);
-    mbar_init(&hd.inv_bar, kSelWarps);
+    mbar_init(&hd.sel_bar, kCons);
+    mbar_init(&hd.inv_bar, kRedWarps);
     mbar_init(&hd.start_bar, kCons);
     for (int i = 0; i < kRed; ++i) {
       mbar_init(&hd.red_full[i], kCons);
@@ -1312,33 +1350,20 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
   if (warp < kSlots) {
     Producer<WD, NT> v{p, hd, slots + (size_t)warp * slot_bytes(NT), warp, lane};
     v.run();
-  } else if (warp < kSlots + kSelWarps) {
-    if (!build_selection(p, hd.sel, threadIdx.x - 32 * kSlots, kSelWarps, 2, &hd.abort)) return;
-    if (lane == 0) mbar_arrive(&hd.sel_bar);
-    if (!p.L) return;
-    int ok = 1;
-    if (lane == 0) ok = counter_wait(p.bar + kCntLat, gridDim.x, &hd.abort, p.err);
-    if (!__shfl_sync(0xffffffffu, ok, 0)) return;
-    for (int t = warp - kSlots; t < p.T; t += kSelWarps) {
-      float ss = 0.0f;
-      for (int c = lane; c < (int)gridDim.x; c += 32) ss += __ldcg(p.ssq + c * kMaxT + t);
-      ss = warp_sum(ss);
-      if (lane == 0) hd.inv[t] = p.latent_norm ? 1.0f / sqrtf(ss / (float)p.L + p.eps) : 1.0f;
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&hd.inv_bar);
   } else if (warp < kFirstCons) {
-    Reducer<WD, NT> v{p, hd, red, (int)threadIdx.x - 32 * (kSlots + kSelWarps), lane};
+    Reducer<WD, NT> v{p, hd, red, (int)threadIdx.x - 32 * kSlots, lane};
     v.run();
   } else {
     Consumer<WD, NT> v{p, hd, slots, red, warp - kFirstCons, lane};
     v.router();
+    if (!build_selection(p, hd.sel, threadIdx.x - 32 * kFirstCons, &hd.abort)) return;
+    if (lane == 0) mbar_arrive(&hd.sel_bar);
     v.run();
   }
 }
 
 struct FewLayout {
-  size_t logits, x_lat, h, y_lat, y_sh, ssq, total;
+  size_t scores, x_lat, h, y_lat, y_sh, ssq, total;
 };
 
 constexpr int kMaxCtas = 256;  // the grid is one CTA per SM, at most this many
@@ -1352,7 +1377,7 @@ FewLayout few_layout(const moe_config_t* c) {
     return at;
   };
   const size_t T = (size_t)c->T;
-  l.logits = take(T * c->E * 4);  // follows the status word: cleared with it
+  l.scores = take(T * c->E * 4);  // follows the status word: cleared with it
   // 4 bytes a value: one fp32, or two bf16 planes
   l.x_lat = take(T * c->d_latent * 4);
   l.h = take((T * c->k + T) * c->I * 4);
@@ -1478,7 +1503,7 @@ extern "C" moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, 
   p.out = out;
   p.err = reinterpret_cast<uint32_t*>(base);
   p.bar = reinterpret_cast<uint32_t*>(base + 128);
-  p.logits = reinterpret_cast<float*>(base + l.logits);
+  p.scores = reinterpret_cast<float*>(base + l.scores);
   p.x_lat = reinterpret_cast<float*>(base + l.x_lat);
   p.h = reinterpret_cast<float*>(base + l.h);
   p.y_lat = reinterpret_cast<float*>(base + l.y_lat);
@@ -1489,8 +1514,8 @@ extern "C" moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, 
   p.ssq = reinterpret_cast<float*>(base + l.ssq);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   (void)cudaGetLastError();  // start from a clean launch-error state
-  // status word, barrier counters and the logits' places
-  cudaError_t e = cudaMemsetAsync(ws, 0, l.logits + (size_t)p.T * p.E * 4, st);
+  // status word, barrier counters and the scores' places
+  cudaError_t e = cudaMemsetAsync(ws, 0, l.scores + (size_t)p.T * p.E * 4, st);
   if (e != cudaSuccess) return status_from_cuda(e);
   switch (cfg->w_dtype) {
     case MOE_F32: e = start((const void*)few_kernel, p, kThreads, 0, st); break;
