@@ -13,6 +13,8 @@
 //      read once for all of its tokens; h = G SiLU(g) u per (expert, token) row
 //   C  W2: each output feature's sum over every selected expert (and the shared one)
 //   D  (latent) W_up rows and the shared expert's W2 rows
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -277,42 +279,10 @@ __device__ __forceinline__ float stored_score(float z) {
   return s == 0.0f ? -0.0f : s;
 }
 
-// 8 values that an earlier step of this kernel wrote (past L1).
-__device__ __forceinline__ void load8_cg(const float* p, float (&v)[8]) {
-  const float4 a = __ldcg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   return v;
-}
-
-// acc[n] += dot(weight row, activation row n) over this lane's columns; act(n, c, v) loads 8.
-template <typename Act>
-__device__ __forceinline__ void dot_rows(float (&acc)[kMaxT], int n, const float* w, int K,
-                                         Act act) {
-  for (int c = (threadIdx.x & 31) * 8; c < K; c += 256) {
-    float v[8];
-    load8(w + c, v);
-#pragma unroll
-    for (int i = 0; i < kMaxT; ++i) {
-      if (i < n) {
-        float a[8];
-        act(i, c, a);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i] = fmaf(v[j], a[j], acc[i]);
-      }
-    }
-  }
-}
-
-__device__ __forceinline__ void zero(float (&acc)[kMaxT]) {
-#pragma unroll
-  for (int i = 0; i < kMaxT; ++i) acc[i] = 0.0f;
 }
 
 // The n-th token of a mask.
@@ -321,13 +291,72 @@ __device__ __forceinline__ int nth_token(uint32_t mask, int n) {
   return __ffs(mask) - 1;
 }
 
-// The fp32 layer: a warp computes one feature, lanes stride over its weight row(s), a shuffle at the
-// end.  For small models, whose weights sit in L2: bound by the steps' latency.
+// acc[r][n] += this lane's part of dot(w[r], act(n)) for R weight rows and N activation rows of K.
+template <int R, int N, typename Act>
+__device__ __forceinline__ void dot_rows(float (&acc)[R][N], const float* const (&w)[R], int K,
+                                         Act act) {
+  const float* a[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) a[n] = act(n);
+#pragma unroll(N <= 2 ? 4 : N <= 4 ? 2 : 1)
+  for (int c = (threadIdx.x & 31) * 4; c < K; c += 128) {
+    float4 wv[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) wv[r] = __ldg(reinterpret_cast<const float4*>(w[r] + c));
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a[n] + c));
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        acc[r][n] = fmaf(wv[r].x, v.x, acc[r][n]);
+        acc[r][n] = fmaf(wv[r].y, v.y, acc[r][n]);
+        acc[r][n] = fmaf(wv[r].z, v.z, acc[r][n]);
+        acc[r][n] = fmaf(wv[r].w, v.w, acc[r][n]);
+      }
+    }
+  }
+}
+
+// The same for n rows, n known at run time, in passes of 8, 4 or 1 rows; out(sums, n) on every
+// lane, with the warp's sums.
+template <int R, typename Act, typename Out>
+__device__ __forceinline__ void dots(const float* const (&w)[R], int K, int n, Act act, Out out) {
+  auto pass = [&](auto width, int n0) {
+    constexpr int N = decltype(width)::value;
+    float acc[R][N];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[r][i] = 0.0f;
+    // rows past the last read the last and are dropped
+    dot_rows<R, N>(acc, w, K, [&](int i) { return act(min(n0 + i, n - 1)); });
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (n0 + i >= n) break;
+      float v[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) v[r] = warp_sum(acc[r][i]);
+      out(v, n0 + i);
+    }
+  };
+  if (n == 1)
+    pass(std::integral_constant<int, 1>{}, 0);
+  else if (n <= 4)
+    pass(std::integral_constant<int, 4>{}, 0);
+  else
+    for (int n0 = 0; n0 < n; n0 += 8) pass(std::integral_constant<int, 8>{}, n0);
+}
+
+// The fp32 layer, for small models: a warp computes a feature of W1|W3 for all tokens of its expert,
+// and a feature of the sums over experts is split over up to 16 warps of a CTA when there are fewer
+// features than warps.  Bound by the steps' latency as long as the weights sit in L2.
 __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
   __shared__ Selection sel;
   __shared__ float inv_rms[kMaxT];
-  const int lane = threadIdx.x & 31;
-  const int gw = blockIdx.x * kWarps + (threadIdx.x >> 5), nw = gridDim.x * kWarps;
+  __shared__ float red[2][kWarps][kMaxT];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // features in CTA-major order: neighbours of a step with few features land on different SMs
+  const int gw = warp * gridDim.x + blockIdx.x, nw = gridDim.x * kWarps;
   const int de = p.L ? p.L : p.d;
   const int P = p.T * p.k;
   const float* x = static_cast<const float*>(p.x);
@@ -336,132 +365,137 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
               *W_down = static_cast<const float*>(p.W_down),
               *W_up = static_cast<const float*>(p.W_up);
   float* out = static_cast<float*>(p.out);
-  float acc[kMaxT], acu[kMaxT];
 
   // A
   const int nA = p.E + p.L + (p.n_shared ? p.I : 0);
-  auto act_x = [&](int n, int c, float(&a)[8]) { load8(x + (int64_t)n * p.d + c, a); };
+  auto token = [&](int n) { return x + (int64_t)n * p.d; };
   for (int u = gw; u < nA; u += nw) {
-    zero(acc);
     if (u < p.E + p.L) {
-      const float* w = u < p.E ? p.W_r + (int64_t)u * p.d : W_down + (int64_t)(u - p.E) * p.d;
-      dot_rows(acc, p.T, w, p.d, act_x);
-#pragma unroll
-      for (int n = 0; n < kMaxT; ++n)
-        if (n < p.T) {
-          const float z = warp_sum(acc[n]);
-          if (lane == 0) {
-            if (u < p.E)
-              p.scores[(int64_t)n * p.E + u] = stored_score(z);
-            else
-              p.x_lat[(int64_t)n * p.L + u - p.E] = z;
-          }
-        }
+      const float* w[1] = {u < p.E ? p.W_r + (int64_t)u * p.d : W_down + (int64_t)(u - p.E) * p.d};
+      dots<1>(w, p.d, p.T, token, [&](const float (&v)[1], int n) {
+        if (lane) return;
+        if (u < p.E)
+          p.scores[(int64_t)n * p.E + u] = stored_score(v[0]);
+        else
+          p.x_lat[(int64_t)n * p.L + u - p.E] = v[0];
+      });
     } else {
       const int f = u - p.E - p.L;
-      zero(acu);
-      dot_rows(acc, p.T, Ws13 + (int64_t)f * p.d, p.d, act_x);
-      dot_rows(acu, p.T, Ws13 + (int64_t)(p.I + f) * p.d, p.d, act_x);
-#pragma unroll
-      for (int n = 0; n < kMaxT; ++n)
-        if (n < p.T) {
-          const float g = warp_sum(acc[n]), q = warp_sum(acu[n]);
-          if (lane == 0) p.h[(int64_t)(P + n) * p.I + f] = silu_accurate(g) * q;
-        }
+      const float* w[2] = {Ws13 + (int64_t)f * p.d, Ws13 + (int64_t)(p.I + f) * p.d};
+      dots<2>(w, p.d, p.T, token, [&](const float (&v)[2], int n) {
+        if (lane == 0) p.h[(int64_t)(P + n) * p.I + f] = silu_accurate(v[0]) * v[1];
+      });
     }
   }
-  if (!grid_barrier(p.bar, p.err)) return;
+  // the scores are waited for by themselves; x_lat needs the barrier
+  if (p.L && !grid_barrier(p.bar, p.err)) return;
 
   // B
   if (!build_selection(p, sel, threadIdx.x, nullptr)) return;
-  for (int64_t u = gw; u < (int64_t)sel.n_active * p.I; u += nw) {
-    const int a = (int)(u / p.I), f = (int)(u - (int64_t)a * p.I);
+  for (int u = gw; u < sel.n_active * p.I; u += nw) {
+    const int a = u / p.I, f = u - a * p.I;
     const int64_t e = sel.active[a];
     const int row0 = sel.row0[a], n_e = sel.row0[a + 1] - row0;
     const uint32_t mask = sel.active_mask[a];
-    zero(acc);
-    zero(acu);
-    auto act = [&](int n, int c, float(&v)[8]) {
-      const int t = nth_token(mask, n);
-      if (p.L)
-        load8_cg(p.x_lat + (int64_t)t * p.L + c, v);
-      else
-        load8(x + (int64_t)t * p.d + c, v);
-    };
-    dot_rows(acc, n_e, W13 + (e * 2 * p.I + f) * de, de, act);
-    dot_rows(acu, n_e, W13 + (e * 2 * p.I + p.I + f) * de, de, act);
-#pragma unroll
-    for (int n = 0; n < kMaxT; ++n)
-      if (n < n_e) {
-        const float g = warp_sum(acc[n]), q = warp_sum(acu[n]);
-        if (lane == 0)
-          p.h[(int64_t)(row0 + n) * p.I + f] = sel.row_gate[row0 + n] * (silu_accurate(g) * q);
-      }
+    const float* w[2] = {W13 + (e * 2 * p.I + f) * de, W13 + (e * 2 * p.I + p.I + f) * de};
+    dots<2>(
+        w, de, n_e,
+        [&](int n) { return (p.L ? p.x_lat : x) + (int64_t)nth_token(mask, n) * de; },
+        [&](const float (&v)[2], int n) {
+          if (lane == 0)
+            p.h[(int64_t)(row0 + n) * p.I + f] = sel.row_gate[row0 + n] * (silu_accurate(v[0]) * v[1]);
+        });
   }
   if (!grid_barrier(p.bar + 1, p.err)) return;
 
-  // C: per token the sum over its experts, in expert order (K2: then the shared expert)
-  auto act_sh = [&](int n, int c, float(&v)[8]) {
-    load8_cg(p.h + (int64_t)(P + n) * p.I + c, v);
-  };
-  for (int f = gw; f < de; f += nw) {
-    zero(acc);
-    for (int a = 0; a < sel.n_active; ++a) {
-      const int64_t e = sel.active[a];
-      const int row0 = sel.row0[a], n_e = sel.row0[a + 1] - row0;
-      const uint32_t mask = sel.active_mask[a];
-      float part[kMaxT];
-      zero(part);
-      auto act = [&](int n, int c, float(&v)[8]) {
-        load8_cg(p.h + (int64_t)(row0 + n) * p.I + c, v);
-      };
-      dot_rows(part, n_e, W2 + (e * de + f) * p.I, p.I, act);
-#pragma unroll
-      for (int t = 0; t < kMaxT; ++t) {
-        const int n = __popc(mask & ((1u << t) - 1u));
-#pragma unroll
-        for (int i = 0; i < kMaxT; ++i)
-          if ((mask >> t & 1u) && i == n) acc[t] += part[i];
+  // Sums over segments: feature f of a step is the sum of segments 0 .. n_seg (seg(s, f, acc) adds
+  // one to acc), taken by S <= most warps of a CTA by the segments' keys and joined in warp order;
+  // store(t, f, v).  Neither S nor a segment's warp depends on the other tokens' experts, so neither
+  // does the order of a token's sum.
+  auto features = [&](int n_f, int n_seg, int most, auto key, auto seg, auto store) {
+    int S = 1;
+    while (S < kWarps && S < most && 2 * S * n_f <= nw) S *= 2;
+    const int at_once = kWarps / S * gridDim.x;  // features of all CTAs
+    int turn = 0;
+    for (int f0 = 0; f0 < n_f; f0 += at_once, turn ^= 1) {
+      const int f = f0 + warp / S * gridDim.x + blockIdx.x;
+      float mine = 0.0f;  // lane t: token t
+      if (f < n_f)
+        for (int s = 0; s < n_seg; ++s)
+          if (key(s) % S == warp % S) seg(s, f, mine);
+      if (S > 1) {
+        if (lane < kMaxT) red[turn][warp][lane] = mine;
+        __syncthreads();
+        if (warp % S == 0 && lane < kMaxT)
+          for (int i = 1; i < S; ++i) mine += red[turn][warp + i][lane];
       }
+      if (f < n_f && warp % S == 0 && lane < p.T) store(lane, f, mine);
     }
-    if (!p.L && p.n_shared) dot_rows(acc, p.T, Ws2 + (int64_t)f * p.I, p.I, act_sh);
-#pragma unroll
-    for (int t = 0; t < kMaxT; ++t)
-      if (t < p.T) {
-        const float v = warp_sum(acc[t]);
-        if (lane == 0) (p.L ? p.y_lat : out)[(int64_t)t * de + f] = v;
-      }
+  };
+  auto expert_seg = [&](int a, int f, float& mine) {
+    const int64_t e = sel.active[a];
+    const int row0 = sel.row0[a], n_e = sel.row0[a + 1] - row0;
+    const uint32_t mask = sel.active_mask[a];
+    const float* w[1] = {W2 + (e * de + f) * p.I};
+    dots<1>(
+        w, p.I, n_e, [&](int n) { return p.h + (int64_t)(row0 + n) * p.I; },
+        [&](const float (&v)[1], int n) {
+          if (lane == nth_token(mask, n)) mine += v[0];
+        });
+  };
+  auto shared_seg = [&](int f, float& mine) {
+    const float* w[1] = {Ws2 + (int64_t)f * p.I};
+    dots<1>(
+        w, p.I, p.T, [&](int n) { return p.h + (int64_t)(P + n) * p.I; },
+        [&](const float (&v)[1], int n) {
+          if (lane == n) mine += v[0];
+        });
+  };
+
+  // C: per token the sum over its experts, in expert order (K2: then the shared expert)
+  if (!p.L) {
+    features(
+        p.d, sel.n_active + p.n_shared, P + p.n_shared,
+        [&](int s) { return s < sel.n_active ? (int)sel.active[s] : p.E; },
+        [&](int s, int f, float& mine) {
+          if (s < sel.n_active)
+            expert_seg(s, f, mine);
+          else
+            shared_seg(f, mine);
+        },
+        [&](int t, int f, float v) { out[(int64_t)t * p.d + f] = v; });
+    return;
   }
-  if (!p.L) return;
+  features(p.L, sel.n_active, P, [&](int s) { return (int)sel.active[s]; }, expert_seg,
+           [&](int t, int f, float v) { p.y_lat[(int64_t)t * p.L + f] = v; });
   if (!grid_barrier(p.bar + 2, p.err)) return;
 
   // D
-  for (int t = threadIdx.x >> 5; t < p.T; t += kWarps) {
+  if (warp < p.T) {
     float ss = 0.0f;
     for (int c = lane; c < p.L; c += 32) {
-      const float v = __ldcg(p.y_lat + (int64_t)t * p.L + c);
+      const float v = __ldcg(p.y_lat + (int64_t)warp * p.L + c);
       ss = fmaf(v, v, ss);
     }
     ss = warp_sum(ss);
-    if (lane == 0) inv_rms[t] = p.latent_norm ? 1.0f / sqrtf(ss / (float)p.L + p.eps) : 1.0f;
+    if (lane == 0) inv_rms[warp] = p.latent_norm ? 1.0f / sqrtf(ss / (float)p.L + p.eps) : 1.0f;
   }
   __syncthreads();
-  auto act_u = [&](int n, int c, float(&v)[8]) {
-    load8_cg(p.y_lat + (int64_t)n * p.L + c, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= inv_rms[n];
-  };
-  for (int f = gw; f < p.d; f += nw) {
-    zero(acc);
-    dot_rows(acc, p.T, W_up + (int64_t)f * p.L, p.L, act_u);
-    if (p.n_shared) dot_rows(acc, p.T, Ws2 + (int64_t)f * p.I, p.I, act_sh);
-#pragma unroll
-    for (int t = 0; t < kMaxT; ++t)
-      if (t < p.T) {
-        const float v = warp_sum(acc[t]);
-        if (lane == 0) out[(int64_t)t * p.d + f] = v;
-      }
-  }
+  features(
+      p.d, 1 + p.n_shared, 2, [](int s) { return s; },
+      [&](int s, int f, float& mine) {
+        if (s == 1) {
+          shared_seg(f, mine);
+          return;
+        }
+        const float* w[1] = {W_up + (int64_t)f * p.L};
+        dots<1>(
+            w, p.L, p.T, [&](int n) { return p.y_lat + (int64_t)n * p.L; },
+            [&](const float (&v)[1], int n) {
+              if (lane == n) mine += v[0] * inv_rms[n];
+            });
+      },
+      [&](int t, int f, float v) { out[(int64_t)t * p.d + f] = v; });
 }
 
 // ---------------------------------------------------------------------------------------------
