@@ -577,7 +577,7 @@ enum : int { kScaled = 1, kStop = 2 };  // kStop: no data, the stream ends
 struct alignas(16) SlotInfo {  // written in four 16-byte stores
   int cols, wpitch, apitch, aoff;
   int soff, plane;   // int4 scales; distance of the activations' second plane (0: one plane)
-  uint32_t mask;     // tokens
+  uint32_t mask;     // columns in use: tokens, or their places
   int flags;
   int f0, cnt;
   const float* s;    // e4m3: scale of the matrix's row block 0 and the slot's first channel
@@ -592,7 +592,7 @@ static_assert(sizeof(SlotInfo) == 64, "four 16-byte stores");
 enum Kind { kDown, kHid, kLat, kShOut, kOut, kPublish, kEnd };
 struct Tile {
   int f0;
-  uint16_t row0, mask;  // first h row, tokens
+  uint16_t row0, mask;  // first h row, columns in use
   uint8_t kind, cnt, gated, pad_;
 };
 // Between two pieces of one producer the stream has kSlots - 1 others: at most kSlots tiles begin, and
@@ -730,7 +730,10 @@ struct Producer {
                                 ? reinterpret_cast<uint64_t>(static_cast<const float*>(sc) + (c0 >> 7))
                                 : 0;
         i[0] = make_int4(cols, wpitch, apitch, aoff);
-        i[1] = make_int4(soff, g.plane ? n * apitch : 0, (int)mask, g.scaled ? kScaled : 0);
+        // W1|W3 and W_down: a product's column is the token's place among the segment's, so that 8
+        // tokens take one group of columns; sums over segments need columns of tokens
+        i[1] = make_int4(soff, g.plane ? n * apitch : 0, (int)(g.tokens ? (1u << n) - 1u : mask),
+                         g.scaled ? kScaled : 0);
         i[2] = make_int4(f0, cnt, (int)(uint32_t)sp, (int)(sp >> 32));
         i[3] = make_int4(g.K >> 7, g.u_off, (int)(tile - 1), 0);
         mbar_arrive(&hd.info_bar[slot]);
@@ -838,7 +841,7 @@ struct Producer {
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
           const int cnt = (size + (i < more)) * G;
-          next_tile(kind, f, cnt, h_row, mask, routed);
+          next_tile(kind, f, cnt, h_row, (1u << __popc(mask)) - 1u, routed);
           if (part == kPartW2) {
 #pragma unroll 1
             for (int j = 0; j < sel.n_active; ++j)
