@@ -556,7 +556,7 @@ __device__ __forceinline__ int slot_cols(int K, int nr) {
   constexpr int per16 = 16 * Wt<WD>::kBits / 8 + (WD == MOE_INT4 ? 1 : 0);
   constexpr int round = 4 * Wt<WD>::kUnit;  // a round of the lane's four consumer warps
   int c = (slot_bytes(NT) - (16 + nr) * 64) / (per16 + 2 * nr);
-  const int gran = c >= 2 * round ? round : Wt<WD>::kGran;
+  const int gran = c >= round ? round : Wt<WD>::kGran;
   c = c / gran * gran;
   const int n = (K + c - 1) / c;
   return ((K + n - 1) / n + gran - 1) / gran * gran;
