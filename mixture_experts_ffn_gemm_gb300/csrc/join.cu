@@ -209,6 +209,110 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 256) join_kernel(const JoinPara
   }
 }
 
+// Many wide rows: a row on a CTA of a quarter as many threads as it has chunks, and as many CTAs on
+// an SM as its shared memory holds rows.  A row's operands arrive by asynchronous copies without a
+// register, and r' takes their place between the norms; a thread reads only what it has copied, so
+// that the sums' barriers are the only ones.  (Rows held in registers: at most four CTAs an SM, and
+// 159 us where this takes XX for 16384 x 7168 bf16 rows with a gate per channel.)
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// 8 elements to shared memory: 16-byte word i of chunk c at word i * chunks + c of the array.
+template <typename T>
+__device__ __forceinline__ void copy8(uint4* dst, int chunks, int c, const T* src) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+    copy16(dst + i * chunks + c, reinterpret_cast<const uint4*>(src) + i);
+}
+template <typename T>
+__device__ __forceinline__ void read8(const uint4* src, int chunks, int c, float (&v)[8]) {
+  Raw<T, 8> w;
+  if constexpr (sizeof(T) == 2) {
+    w.q = src[c];
+  } else {
+    w.q[0] = src[c];
+    w.q[1] = src[chunks + c];
+  }
+  w.get(v);
+}
+
+template <typename TA, typename TR>
+__global__ void __launch_bounds__(1024) join_rows_kernel(const JoinParams p) {
+  extern __shared__ uint4 row4[];
+  __shared__ float red[2][32];
+  const int chunks = p.d >> 3;
+  const int64_t t = blockIdx.x;
+  const bool el = p.gate == MOE_GATE_ELEMENT;
+  uint4* ys = row4;
+  uint4* rs = ys + chunks * (int)(sizeof(TA) / 2);
+  uint4* gs = rs + chunks * (int)(sizeof(TR) / 2);
+  const TA* y = static_cast<const TA*>(p.branch) + t * p.ld_y;
+  const TR* r = static_cast<const TR*>(p.resid) + t * p.ld_r;
+  const TA* pw = static_cast<const TA*>(p.post_w);
+  const TA* qw = static_cast<const TA*>(p.pre_w);
+  const TA* gp = static_cast<const TA*>(p.g);
+  for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+    copy8(ys, chunks, c, y + c * 8);
+    copy8(rs, chunks, c, r + c * 8);
+    if (el) copy8(gs, chunks, c, gp + t * p.ld_g + c * 8);
+  }
+  float tg = p.b;
+  if (p.gate == MOE_GATE_TOKEN) {
+    const float v = to_f32<TA>(gp[t]);
+    tg *= p.sigmoid ? 1.0f / (1.0f + expf(-v)) : v;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  float inv = 1.0f;
+  if (pw) {
+    float ss = 0.0f;
+    for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+      float v[8];
+      read8<TA>(ys, chunks, c, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+    }
+    inv = 1.0f / sqrtf(row_sum<true>(ss, 0, red[0]) / (float)p.d + p.eps);
+  }
+  float ss = 0.0f;
+  for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+    float v[8], x[8];
+    read8<TA>(ys, chunks, c, v);
+    if (pw) {
+      load8(pw + c * 8, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * x[e];
+    }
+    if (el || p.gate == MOE_GATE_CHANNEL) {
+      if (el)
+        read8<TA>(gs, chunks, c, x);
+      else
+        load8(gp + c * 8, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= p.sigmoid ? 1.0f / (1.0f + expf(-x[e])) : x[e];
+    }
+    read8<TR>(rs, chunks, c, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] = p.a * x[e] + tg * v[e];
+      ss = fmaf(v[e], v[e], ss);
+    }
+    put(static_cast<TR*>(p.resid_out) + t * p.ld_ro + c * 8, v);
+    ys[c] = *reinterpret_cast<const uint4*>(v);
+    rs[c] = *reinterpret_cast<const uint4*>(v + 4);
+  }
+  if (!p.normed) return;
+  const float ninv = 1.0f / sqrtf(row_sum<true>(ss, 0, red[1]) / (float)p.d + p.eps);
+  for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+    float v[8], x[8];
+    *reinterpret_cast<uint4*>(v) = ys[c];
+    *reinterpret_cast<uint4*>(v + 4) = rs[c];
+    load8(qw + c * 8, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * ninv * x[e];
+    put(static_cast<TA*>(p.normed) + t * p.ld_n + c * 8, v);
+  }
+}
+
 // Rows too wide for registers without wide loads: r' waits in shared memory between the norms, each
 // thread reading back its own columns.
 template <typename TA, typename TR>
@@ -294,6 +398,19 @@ cudaError_t launch_rows(const JoinParams& p, int chunks, cudaStream_t st) {
 template <typename TA, typename TR>
 cudaError_t launch(const JoinParams& p, bool wide_loads, cudaStream_t st) {
   LaunchScope ls("block_join", st);
+  const size_t row_bytes =
+      (size_t)p.d * (sizeof(TA) * (p.gate == MOE_GATE_ELEMENT ? 2 : 1) + sizeof(TR));
+  if (wide_loads && p.T > num_sms() && p.d > 1024 && row_bytes <= 100 * 1024) {
+    if (row_bytes > 48 * 1024) {
+      cudaError_t e = cudaFuncSetAttribute(join_rows_kernel<TA, TR>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
+      if (e != cudaSuccess) return e;
+    }
+    int threads = (p.d / 32 + 31) / 32 * 32;
+    if (threads > 1024) threads = 1024;
+    join_rows_kernel<TA, TR><<<(unsigned)p.T, threads, row_bytes, st>>>(p);
+    return cudaGetLastError();
+  }
   if (wide_loads) return launch_rows<TA, TR, 8>(p, p.d / 8, st);  // d <= 32768: 4096 chunks
   if (p.d <= 8192) return launch_rows<TA, TR, 1>(p, p.d, st);
   const size_t smem = (size_t)p.d * sizeof(float);
