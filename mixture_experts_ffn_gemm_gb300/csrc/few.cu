@@ -984,7 +984,7 @@ struct Consumer {
   // Router logits: the CTA takes every gridDim-th expert, kExp at a time; the warps split the input
   // channels, so that a CTA reads the tokens once for them.  The stream starts when the first
   // kExp experts' loads are in: behind a full ring they would wait for all of it (the selection was
-  // ready at 18 us instead of XX).
+  // ready at 18 us, in a full ring's wake).
   __device__ void router() {
     constexpr int kExp = 3, kMost = 2, kTok = 4;  // loads in flight, in registers
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);

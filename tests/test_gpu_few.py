@@ -254,3 +254,83 @@ def test_zero_tokens_and_one_launch(cuda_device):
     B.moe_reset_launch_count()
     few(L)
     assert B.moe_launch_count() == 1
+
+
+def test_every_e4m3_code(cuda_device):
+    """Weights of every finite e4m3 code, subnormals and both zeros among them."""
+    L = S.make_layer(_workload("fp8", 3, d=256, E=4, k=2, I=128), seed=15, device="cuda")
+    codes = torch.arange(256, device="cuda", dtype=torch.int16)
+    codes = codes[(codes & 0x7F) != 0x7F].to(torch.uint8)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for m, s in ((L.W13, L.W13_scale), (L.W2, L.W2_scale), (L.Ws13, L.Ws13_scale),
+                 (L.Ws2, L.Ws2_scale)):
+        pick = torch.randint(0, codes.numel(), m.shape, generator=g, device="cuda")
+        m.view(torch.uint8).copy_(codes[pick])
+        s.copy_(torch.rand(s.shape, generator=g, device="cuda") * 2e-3)
+    out, _ = few(L)
+    compare(out, *reference(L))
+
+
+@pytest.mark.parametrize("tokens", [3, 12])
+def test_e4m3_nan_codes(cuda_device, tokens):
+    """A NaN code makes the tokens of its expert NaN (W2: in its feature), the others keep their bits."""
+    def run(edit):
+        L = S.make_layer(_workload("fp8", tokens, d=256, E=32, k=2, I=128), seed=16, device="cuda")
+        key = torch.sigmoid(L.x.double() @ L.W_r.double().t()) + L.b.double()
+        idx = key.topk(2, dim=1).indices
+        e = int(idx[0, 0])
+        edit(L, e)
+        return few(L)[0], (idx == e).any(1)
+
+    clean, users = run(lambda L, e: None)
+    assert users.any() and not users.all()
+
+    def w13(L, e):
+        L.W13.view(torch.uint8)[e, 200, 77] = 0xFF
+
+    out, _ = run(w13)
+    assert out[users].isnan().all() and torch.equal(out[~users], clean[~users])
+
+    def w2(L, e):
+        L.W2.view(torch.uint8)[e, 201, 3] = 0x7F
+
+    out, _ = run(w2)
+    other = torch.arange(256, device="cuda") != 201
+    assert out[users][:, 201].isnan().all() and torch.equal(out[~users], clean[~users])
+    assert torch.equal(out[:, other], clean[:, other])
+
+
+def test_int4_scales_of_all_sizes(cuda_device):
+    """Scales from subnormal to large, and zero: the weight is the product rounded to bf16."""
+    L = S.make_layer(_workload("int4", 2, d=256, E=4, k=2, I=128), seed=17, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for m, s in ((L.W13, L.W13_scale), (L.W2, L.W2_scale), (L.Ws13, L.Ws13_scale),
+                 (L.Ws2, L.Ws2_scale)):
+        m.copy_(torch.randint(0, 256, m.shape, generator=g, device="cuda").to(torch.uint8))
+        e = torch.randint(-12, 0, s.shape, generator=g, device="cuda").float()
+        s.copy_(torch.exp2(e) * (1 + torch.rand(s.shape, generator=g, device="cuda")))
+        s.view(-1)[::7] = 0
+        s.view(-1)[::11] = 1e-39
+    out, _ = few(L)
+    compare(out, *reference(L))
+
+
+@pytest.mark.parametrize("scale", [1e-6, 1e6])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
+def test_small_and_large_activations(cuda_device, kind, scale):
+    """The 16 bits of h do not depend on its size."""
+    L = S.make_layer(_workload(kind, 4), seed=18, device="cuda")
+    L.x.mul_(scale)
+    L.W_r.div_(scale)
+    out, _ = few(L)
+    compare(out, *reference(L))
+
+
+def test_64_bit_weight_offsets(cuda_device):
+    """Experts past 2^32 bytes of stacked weights."""
+    w = replace(S.WORKLOADS["k2_decode_bf16"], T=2, E=100, k=2, w_init="fan_in")
+    L = S.make_layer(w, seed=19, device="cuda")
+    L.b.fill_(-2.0)
+    L.b[-3:] = 2.0  # the last experts only
+    out, _ = few(L)
+    compare(out, *reference(L))
