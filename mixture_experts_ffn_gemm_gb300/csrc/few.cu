@@ -13,6 +13,8 @@
 //      read once for all of its tokens; h = G SiLU(g) u per (expert, token) row
 //   C  W2: each output feature's sum over every selected expert (and the shared one)
 //   D  (latent) W_up rows and the shared expert's W2 rows
+#include <cuda_fp16.h>
+
 #include <type_traits>
 
 #include "common.cuh"
@@ -49,6 +51,9 @@ struct FewParams {
   // bf16 kernel: the same as two bf16 planes, value = plane 0 + plane 1 to 16 bits or more
   __nv_bfloat16 *x_lat2, *h2, *y_lat2;
   float* y_sh;     // [T][d] shared expert's output
+  // e4m3 experts: the tokens in fp16, each divided by a power of two, and those powers
+  __half* x16;
+  float* x_scale;  // [16]
   float* ssq;      // [CTAs][16] sums of squares of each CTA's latent features
 };
 
@@ -62,6 +67,7 @@ struct Selection {
   int16_t pair_e[kMaxPairs];
   float pair_g[kMaxPairs];
   float row_gate[kMaxPairs];
+  uint8_t row_token[kMaxPairs];
   int n_active;
 };
 
@@ -227,6 +233,7 @@ __device__ bool build_selection(const FewParams& p, Selection& sel, int tid, vol
           sel.row0[place] = (int16_t)rows;
         }
         sel.row_gate[rows + __popc(mask & ((1u << tok) - 1u))] = sel.pair_g[lane];
+        sel.row_token[rows + __popc(mask & ((1u << tok) - 1u))] = (uint8_t)tok;
       }
       if (lane == 0) {
         sel.n_active = __popc(leaders);
@@ -267,7 +274,9 @@ __device__ bool build_selection(const FewParams& p, Selection& sel, int tid, vol
   named_barrier(bar, n);
   for (int i = tid; i < p.T * p.k; i += n) {
     const int e = sel.pair_e[i], tok = i / p.k;
-    sel.row_gate[sel.row0[sel.slot[e]] + __popc(sel.mask[e] & ((1u << tok) - 1u))] = sel.pair_g[i];
+    const int row = sel.row0[sel.slot[e]] + __popc(sel.mask[e] & ((1u << tok) - 1u));
+    sel.row_gate[row] = sel.pair_g[i];
+    sel.row_token[row] = (uint8_t)tok;
   }
   named_barrier(bar, n);
   return true;
@@ -533,7 +542,7 @@ constexpr int slot_bytes(int nt) { return nt == 1 ? 24064 : 22016; }
 static_assert(kCons == 4 * kLanes && (kSlots & (kSlots - 1)) == 0, "four consumer warps to a lane");
 
 // Counters of the launch (FewParams::bar): arrivals of CTAs at the end of each part.
-enum : int { kCntDown = 0, kCntH = 1, kCntLat = 2, kCntShared = 3, kCounters = 4 };
+enum : int { kCntDown = 0, kCntH = 1, kCntLat = 2, kCntShared = 3, kCntX = 4, kCounters = 5 };
 constexpr int kNoDep = -1;
 
 template <int WD>
@@ -605,6 +614,7 @@ struct StreamHead {
   Tile tile[kSlots][kTiles];  // each producer's own, for its consumers
   Tile red_tile[kRed];        // for the reducers
   uint4 zeros[4];
+  uint32_t x_top;
   float inv[kMaxT];
   int abort;
   uint32_t done[kCounters];  // reducer warps through each part
@@ -775,6 +785,9 @@ struct Producer {
     const uint32_t all = (1u << p.T) - 1u;
     const int P = p.T * p.k, de = p.L ? p.L : p.d;
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
+    const __nv_bfloat16* x13 =
+        WD == MOE_FP8_E4M3 ? reinterpret_cast<const __nv_bfloat16*>(p.x16) : x;
+    const int dep13 = WD == MOE_FP8_E4M3 ? kCntX : kNoDep;
     auto u8 = [](const void* q) { return static_cast<const uint8_t*>(q); };
 #pragma unroll 1
     for (int part = 0; part < kParts && !failed; ++part) {
@@ -798,11 +811,11 @@ struct Producer {
         total = p.L;
         kind = kDown;
       } else if (part == kPartShared) {
-        src = Source{u8(p.Ws13), p.ss13, 2 * p.I, p.d, p.I, x, 0, true, kNoDep, false, 0, 0, 0};
+        src = Source{u8(p.Ws13), p.ss13, 2 * p.I, p.d, p.I, x13, 0, true, dep13, false, 0, 0, 0};
         total = p.I;
         kind = kHid;
       } else if (part == kPartRouted) {
-        src = Source{u8(p.W13), p.s13, 2 * p.I, de, p.I, x, 0, true, kNoDep, false, 0, 0, 0};
+        src = Source{u8(p.W13), p.s13, 2 * p.I, de, p.I, x13, 0, true, dep13, false, 0, 0, 0};
         if (p.L) {
           src.act = p.x_lat2;
           src.plane = (int64_t)p.T * p.L;
@@ -898,6 +911,24 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four e4m3 codes as fp16, in order (exact, NaN included).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& p01, uint32_t& p23) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}\n"
+      : "=r"(p01), "=r"(p23)
+      : "r"(w));
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -1133,10 +1164,17 @@ struct Consumer {
               b[i] = wb[i];
             }
           } else if constexpr (WD == MOE_FP8_E4M3) {
-            e4m3x4_to_bf16(wa[2 * h], k16, k256, a[0], a[1], top_a);
-            e4m3x4_to_bf16(wa[2 * h + 1], k16, k256, a[2], a[3], top_a);
-            e4m3x4_to_bf16(wb[2 * h], k16, k256, b[0], b[1], top_b);
-            e4m3x4_to_bf16(wb[2 * h + 1], k16, k256, b[2], b[3], top_b);
+            if constexpr (PLANES) {
+              e4m3x4_to_bf16(wa[2 * h], k16, k256, a[0], a[1], top_a);
+              e4m3x4_to_bf16(wa[2 * h + 1], k16, k256, a[2], a[3], top_a);
+              e4m3x4_to_bf16(wb[2 * h], k16, k256, b[0], b[1], top_b);
+              e4m3x4_to_bf16(wb[2 * h + 1], k16, k256, b[2], b[3], top_b);
+            } else {
+              e4m3x4_to_f16(wa[2 * h], a[0], a[1]);
+              e4m3x4_to_f16(wa[2 * h + 1], a[2], a[3]);
+              e4m3x4_to_f16(wb[2 * h], b[0], b[1]);
+              e4m3x4_to_f16(wb[2 * h + 1], b[2], b[3]);
+            }
           } else {
             int4x8_to_bf16(wa[h], sa, a);
             int4x8_to_bf16(wb[h], sb, b);
@@ -1145,16 +1183,14 @@ struct Consumer {
           for (int n = 0; n < NT; ++n) {
             if (NT > 1 && !(mask >> (n * 8) & 0xffu)) continue;
             float(&sum)[4] = o[WD == MOE_BF16 ? st : 0][n];
-            uint4 v = lds16(q[n] + h * 16);
-            if (WD == MOE_FP8_E4M3 && !PLANES) {  // x: to the order of the converted pairs
-              const uint4 u = v;
-              v.x = __byte_perm(u.x, u.y, 0x5410);
-              v.y = __byte_perm(u.x, u.y, 0x7632);
-              v.z = __byte_perm(u.z, u.w, 0x5410);
-              v.w = __byte_perm(u.z, u.w, 0x7632);
+            const uint4 v = lds16(q[n] + h * 16);
+            if constexpr (WD == MOE_FP8_E4M3 && !PLANES) {
+              mma16816_f16(sum, a[0], b[0], a[1], b[1], v.x, v.y);
+              mma16816_f16(sum, a[2], b[2], a[3], b[3], v.z, v.w);
+            } else {
+              mma16816(sum, a[0], b[0], a[1], b[1], v.x, v.y);
+              mma16816(sum, a[2], b[2], a[3], b[3], v.z, v.w);
             }
-            mma16816(sum, a[0], b[0], a[1], b[1], v.x, v.y);
-            mma16816(sum, a[2], b[2], a[3], b[3], v.z, v.w);
             if (PLANES) {
               const uint4 v2 = lds16(q2[n] + h * 16);
               mma16816(sum, a[0], b[0], a[1], b[1], v2.x, v2.y);
@@ -1177,7 +1213,7 @@ struct Consumer {
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int j = 0; j < kPar; ++j) d[n][i] += o[j][n][i];
-    } else {
+    } else if constexpr (PLANES) {
       // a NaN code that any of a row's four lanes has met makes the row's sums NaN
       const uint32_t bad = (e4m3_any_nan(top_a) ? 1u : 0u) | (e4m3_any_nan(top_b) ? 2u : 0u);
       if (__any_sync(0xffffffffu, bad != 0)) {
@@ -1256,6 +1292,10 @@ struct Reducer {
   float ssq[2 * NT] = {};  // squares of the latent features of this thread's tokens
 
   __device__ void run() {
+    if constexpr (WD == MOE_FP8_E4M3) {
+      if ((int)blockIdx.x < p.T) token_to_f16(blockIdx.x);
+      publish(kCntX);
+    }
     for (uint32_t t = 0;; ++t) {
       if (!mbar_wait_sleep(&hd.red_full[t % kRed], t / kRed & 1u, &hd.abort, p.err)) return;
       const Tile ti = hd.red_tile[t % kRed];
@@ -1286,7 +1326,13 @@ struct Reducer {
       const float g = sum(q), u = sum(q + 64);
       if (row >= ti.cnt || !(ti.mask >> tok & 1u)) continue;
       const int hr = ti.row0 + __popc(ti.mask & ((1u << tok) - 1u));
-      float v = silu_accurate(g) * u;
+      float v;
+      if constexpr (WD == MOE_FP8_E4M3) {
+        const float xs = __ldcg(p.x_scale + (ti.gated ? hd.sel.row_token[hr] : tok));
+        v = silu_accurate(g * xs) * (u * xs);
+      } else {
+        v = silu_accurate(g) * u;
+      }
       if (ti.gated) v *= hd.sel.row_gate[hr];
       store_planes(p.h2 + (int64_t)hr * p.I + h_place<WD>(ti.f0 + row), (int64_t)p.T * (p.k + 1) * p.I, v);
     }
@@ -1315,6 +1361,40 @@ struct Reducer {
         store_planes((ti.kind == kDown ? p.x_lat2 : p.y_lat2) + (int64_t)tok * p.L + f,
                      (int64_t)p.T * p.L, v);
     }
+  }
+  // The token for the products with e4m3 weights, which convert to fp16 in a fifth of the
+  // instructions that bf16 takes: divided by the power of two that brings its largest magnitude to
+  // 2^13 .. 2^14, so that nothing overflows and what is lost of small values is below 2^-38 of the
+  // largest.  A row with an infinity or a NaN is taken as it is.
+  __device__ void token_to_f16(int t) {
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + (int64_t)t * p.d;
+    uint32_t top = 0;  // bits of the largest magnitude
+    for (int c = tid * 8; c < p.d; c += kRedWarps * 256) {
+      float v[8];
+      load8(x + c, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) atomicMax(&hd.x_top, top);
+    named_barrier(3, kRedWarps * 32);
+    top = *(volatile uint32_t*)&hd.x_top;
+    int e = top == 0 || top >= 0x7f800000u ? 0 : (int)(top >> 23) - 127 - 13;
+    e = max(e, -110);
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+    for (int c = tid * 8; c < p.d; c += kRedWarps * 256) {
+      float v[8];
+      load8(x + c, v);
+      uint4 h;
+      uint32_t* w = &h.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 q = __floats2half2_rn(v[2 * i] * down, v[2 * i + 1] * down);
+        w[i] = *reinterpret_cast<const uint32_t*>(&q);
+      }
+      *reinterpret_cast<uint4*>(p.x16 + (int64_t)t * p.d + c) = h;
+    }
+    if (tid == 0) p.x_scale[t] = __uint_as_float((uint32_t)(127 + e) << 23);
   }
   static __device__ __forceinline__ void store_planes(__nv_bfloat16* at, int64_t plane, float v) {
     __nv_bfloat16 hi, lo;
@@ -1378,6 +1458,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
       mbar_init(&hd.red_empty[i], kRedWarps);
     }
     hd.abort = 0;
+    hd.x_top = 0;
     for (int i = 0; i < 4; ++i) hd.zeros[i] = make_uint4(0, 0, 0, 0);
     for (int i = 0; i < kCounters; ++i) hd.done[i] = 0;
     fence_barrier_init();
@@ -1400,7 +1481,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
 }
 
 struct FewLayout {
-  size_t scores, x_lat, h, y_lat, y_sh, ssq, total;
+  size_t scores, x_lat, h, y_lat, y_sh, x16, x_scale, ssq, total;
 };
 
 constexpr int kMaxCtas = 256;  // the grid is one CTA per SM, at most this many
@@ -1420,6 +1501,8 @@ FewLayout few_layout(const moe_config_t* c) {
   l.h = take((T * c->k + T) * c->I * 4);
   l.y_lat = take(T * c->d_latent * 4);
   l.y_sh = take(c->act_dtype == MOE_BF16 && c->n_shared ? T * c->d * 4 : 0);
+  l.x16 = take(c->w_dtype == MOE_FP8_E4M3 ? T * c->d * 2 : 0);
+  l.x_scale = take(c->w_dtype == MOE_FP8_E4M3 ? kMaxT * 4 : 0);
   l.ssq = take(c->d_latent ? (size_t)kMaxCtas * kMaxT * 4 : 0);
   l.total = off;
   return l;
@@ -1548,6 +1631,8 @@ extern "C" moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, 
   p.h2 = reinterpret_cast<__nv_bfloat16*>(base + l.h);
   p.y_lat2 = reinterpret_cast<__nv_bfloat16*>(base + l.y_lat);
   p.y_sh = reinterpret_cast<float*>(base + l.y_sh);
+  p.x16 = reinterpret_cast<__half*>(base + l.x16);
+  p.x_scale = reinterpret_cast<float*>(base + l.x_scale);
   p.ssq = reinterpret_cast<float*>(base + l.ssq);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   (void)cudaGetLastError();  // start from a clean launch-error state
