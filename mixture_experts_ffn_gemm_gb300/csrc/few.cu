@@ -586,7 +586,7 @@ enum : int { kScaled = 1, kStop = 2 };  // kStop: no data, the stream ends
 struct alignas(16) SlotInfo {  // written in four 16-byte stores
   int cols, wpitch, apitch, aoff;
   int soff, plane;   // int4 scales; distance of the activations' second plane (0: one plane)
-  uint32_t mask;     // columns in use: tokens, or their places
+  uint32_t mask;     // sums over segments: the tokens; else one bit for each
   int flags;
   int f0, cnt;
   const float* s;    // e4m3: scale of the matrix's row block 0 and the slot's first channel
@@ -740,8 +740,6 @@ struct Producer {
                                 ? reinterpret_cast<uint64_t>(static_cast<const float*>(sc) + (c0 >> 7))
                                 : 0;
         i[0] = make_int4(cols, wpitch, apitch, aoff);
-        // W1|W3 and W_down: a product's column is the token's place among the segment's, so that 8
-        // tokens take one group of columns; sums over segments need columns of tokens
         i[1] = make_int4(soff, g.plane ? n * apitch : 0, (int)(g.tokens ? (1u << n) - 1u : mask),
                          g.scaled ? kScaled : 0);
         i[2] = make_int4(f0, cnt, (int)(uint32_t)sp, (int)(sp >> 32));
@@ -1098,17 +1096,17 @@ struct Consumer {
     using W = Wt<WD>;
     const int gr = lane >> 2, t4 = lane & 3;
     const int cols = si.cols;
-    const uint32_t mask = si.mask;
+    const int n_act = __popc(si.mask);
     const uint32_t wa_row = base + gr * si.wpitch, wb_row = wa_row + 8 * si.wpitch;
     const uint32_t sc_row = base + si.soff + gr * 2;
     const uint32_t zeros = settle(smem_u32(hd.zeros));
-    uint32_t arow[NT];  // this lane's token row among the activations
+    // a column of a product is a token's place among the segment's: 8 tokens to a group of columns
+    uint32_t arow[NT];
     bool on[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int tok = n * 8 + gr;
-      on[n] = mask >> tok & 1u;
-      arow[n] = base + si.aoff + __popc(mask & ((1u << tok) - 1u)) * si.apitch;
+      on[n] = n * 8 + gr < n_act;
+      arow[n] = base + si.aoff + (n * 8 + gr) * si.apitch;
     }
     const float *s0p = nullptr, *s1p = nullptr;
     if constexpr (WD == MOE_FP8_E4M3) {
@@ -1181,7 +1179,7 @@ struct Consumer {
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            if (NT > 1 && !(mask >> (n * 8) & 0xffu)) continue;
+            if (NT > 1 && n * 8 >= n_act) continue;
             float(&sum)[4] = o[WD == MOE_BF16 ? st : 0][n];
             const uint4 v = lds16(q[n] + h * 16);
             if constexpr (WD == MOE_FP8_E4M3 && !PLANES) {
@@ -1268,15 +1266,37 @@ struct Consumer {
       if (lane == 0) mbar_arrive(&hd.empty[at]);
       const bool scaled = flags & kScaled;
       if (scaled && !wait(&hd.inv_bar, 0)) return;
-      // only the segment's own tokens: another token's zeros times an infinite weight are NaN
+      if ((mask & (mask + 1u)) == 0) {  // places are tokens, or those of the tile's only segment
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int tok = n * 8 + t4 * 2 + (i & 1);
-          const float v = scaled ? d[n][i] * hd.inv[tok] : d[n][i];
-          acc[n][i] += mask >> tok & 1u ? v : 0.0f;
+          for (int i = 0; i < 4; ++i) {
+            // not the columns past the last: their zeros times an infinite weight are NaN
+            const int tok = n * 8 + t4 * 2 + (i & 1);
+            const float v = scaled ? d[n][i] * hd.inv[tok] : d[n][i];
+            acc[n][i] += mask >> tok & 1u ? v : 0.0f;
+          }
+      } else {  // each place's sums to the lanes that hold its token's
+        uint32_t m = mask;
+        for (int j = 0; m; ++j, m &= m - 1) {
+          const int tok = __ffs(m) - 1, src = (lane & ~3) | (j & 7) >> 1;
+          float lo = j & 1 ? d[0][1] : d[0][0], hi = j & 1 ? d[0][3] : d[0][2];
+          if (NT > 1 && j >= 8) {
+            lo = j & 1 ? d[NT - 1][1] : d[NT - 1][0];
+            hi = j & 1 ? d[NT - 1][3] : d[NT - 1][2];
+          }
+          lo = __shfl_sync(0xffffffffu, lo, src);
+          hi = __shfl_sync(0xffffffffu, hi, src);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (tok == n * 8 + t4 * 2 + i) {
+                acc[n][i] += lo;
+                acc[n][2 + i] += hi;
+              }
         }
+      }
     }
   }
 };
