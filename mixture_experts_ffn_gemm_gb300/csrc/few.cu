@@ -4,17 +4,19 @@
 //   E_i(x) = (SiLU(x W1_i) * (x W3_i)) W2_i ;  y = sum_sel G_i E_i(x) + E_shared(x)
 //   latent: experts on x W_down; y = RMSNorm(sum_sel G_i E_i) W_up + E_shared(x)
 //
-// Bound by memory: with T tokens a weight is used at most T times, so the layer is one pass over
-// the selected experts' weights.  Two kernels, both one CTA per SM with equal calls giving equal
-// bits: few_stream_kernel (bf16 activations) keeps that pass going through all steps; few_kernel
-// (fp32, small models) is plain.  Steps, each needing what every CTA wrote in the one before:
-//   A  router logits; W_down rows; the shared expert's W1|W3 rows
+// With T tokens a weight is used at most T times, so the layer is one pass over the selected experts'
+// weights, bound by memory (4-bit weights: by their conversion).  Two kernels, both one CTA per SM,
+// equal calls giving equal bits: few_stream_kernel (bf16 activations) keeps that pass going through
+// all steps; few_kernel (fp32, small models) is plain.  Steps, each needing what every CTA wrote in
+// the one before:
+//   A  router scores; W_down rows; the shared expert's W1|W3 rows
 //   B  every CTA repeats the selection, then W1|W3 rows of the distinct selected experts, each
 //      read once for all of its tokens; h = G SiLU(g) u per (expert, token) row
 //   C  W2: each output feature's sum over every selected expert (and the shared one)
 //   D  (latent) W_up rows and the shared expert's W2 rows
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -511,26 +513,33 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
 // bf16 activations: one stream of weights through shared memory per SM.
 //
 // Producer warps walk the CTA's share of every step and copy it (bulk asynchronous copies, a row
-// piece each) into a ring of kSlots slots: 16 weight rows times up to a few thousand input channels,
-// and the same channels of the activations they meet.  Sixteen consumer warps split a slot's
-// channels, multiply 16 rows by 8 tokens with mma.sync m16n8k16 and, when a tile of rows is
-// complete, add their partial sums in a fixed order through shared memory.  The products' K index
-// may be permuted as long as both operands agree, so a lane takes 16 consecutive bytes of its row
-// (8 bf16, 16 e4m3 or 32 4-bit weights) and the same channels of its token: shared memory is read
-// in 16-byte words with no transposition.  (tcgen05 would need 16 token rows of shared memory and
-// tensor memory round trips for one or two tokens per expert; nothing here is bound by products.)
+// piece each) into a ring of slots: 16 weight rows times as many input channels as 22-24 KB hold, and
+// the same channels of the activations they meet.  Consumer warps split a slot's channels and
+// multiply 16 rows by 8 tokens with mma.sync m16n8k16; when a tile of rows is complete, reducer warps
+// add the partial sums in a fixed order and store.  The products' K index may be permuted as long as
+// both operands agree, so a lane takes 16 consecutive bytes of its row (8 bf16, 16 e4m3 or 32 4-bit
+// weights) and the same channels of its token: shared memory is read in 16-byte words with no
+// transposition.  (A tcgen05 product would want 16 token rows in shared memory and a trip through
+// tensor memory for the one or two tokens that an expert has; products bound nothing here.)
 //
 // The stream does not stop at the steps' barriers.  Weights are copied ahead of them and only the
-// activations' copies wait for the barrier (each slot's barrier counts two arrivals, weights and
-// activations); four more warps wait for the router logits and repeat the selection while the
-// shared expert's weights pass by.
+// activations' copies wait (each slot's barrier counts two arrivals, weights and activations); the
+// selection runs on the consumer warps, a warp a token, while the ring fills with the shared expert's
+// weights; and the shared expert's W2 stands where the last CTAs of a step are waited for.
+//
+// Measured (384 experts of d 7168, I 2048, top 8): one token 130 us (118 of them the
+// weights at the measured copy bandwidth), 16 tokens 1250 us, four tokens with e4m3 weights 266 us (209),
+// one token with 4-bit weights 93 us (35); latent width 3584, four tokens 256 us (231).
 //
 // Values that one step leaves to the next (h, the latent activations) are kept as two bf16 planes,
 // hi = bf16(v) and lo = bf16(v - hi), and multiplied plane by plane into the same fp32 sum: 16 bits
 // or more of each, where one bf16 would add a rounding of 2^-9.
 // ---------------------------------------------------------------------------------------------
 constexpr int kCons = kWarps;  // consumer warps
-constexpr int kLanes = 4;      // lanes of the stream: four consumer warps and kBufs slots each
+// Four lanes of the stream, each four consumer warps and two slots, of which one fills while the other
+// is multiplied: one slot after another on all sixteen warps left the latencies of a slot's few
+// products and of its bookkeeping in the open (int4, one token: 128 us instead of 93).
+constexpr int kLanes = 4;
 constexpr int kBufs = 2;
 constexpr int kSlots = kLanes * kBufs;  // one producer warp each
 constexpr int kRedWarps = 2;   // sums of the finished tiles
@@ -609,12 +618,13 @@ struct Tile {
 constexpr int kTiles = 32;
 
 struct StreamHead {
-  uint64_t info_bar[kSlots], full[kSlots], empty[kSlots], sel_bar, inv_bar, start_bar, red_full[kRed], red_empty[kRed];
+  uint64_t info_bar[kSlots], full[kSlots], empty[kSlots], red_full[kRed], red_empty[kRed];
+  uint64_t sel_bar, inv_bar, start_bar;
   SlotInfo info[kSlots];
   Tile tile[kSlots][kTiles];  // each producer's own, for its consumers
   Tile red_tile[kRed];        // for the reducers
   uint4 zeros[4];
-  uint32_t x_top;
+  uint32_t x_top;             // bits of the token's largest magnitude (token_to_f16)
   float inv[kMaxT];
   int abort;
   uint32_t done[kCounters];  // reducer warps through each part
@@ -674,7 +684,9 @@ struct Producer {
   __device__ __forceinline__ void next_tile(int kind, int f0, int cnt, int row0, uint32_t mask,
                                             int gated) {
     if (failed) return;  // no longer paced by the slot: the consumers still read what is there
-    if (lane == 0) hd.tile[slot][tile % kTiles] = Tile{f0, (uint16_t)row0, (uint16_t)mask, (uint8_t)kind, (uint8_t)cnt, (uint8_t)gated, 0};
+    if (lane == 0)
+      hd.tile[slot][tile % kTiles] = Tile{f0,           (uint16_t)row0, (uint16_t)mask, (uint8_t)kind,
+                                          (uint8_t)cnt, (uint8_t)gated, 0};
     ++tile;
   }
 
@@ -761,8 +773,7 @@ struct Producer {
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src)
                          : "memory");
         }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                         smem_u32(full))
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full))
                      : "memory");
       }
       step_complete(g.dep);
@@ -1012,8 +1023,7 @@ struct Consumer {
 
   // Router logits: the CTA takes every gridDim-th expert, kExp at a time; the warps split the input
   // channels, so that a CTA reads the tokens once for them.  The stream starts when the first
-  // kExp experts' loads are in: behind a full ring they would wait for all of it (the selection was
-  // ready at 18 us, in a full ring's wake).
+  // kExp experts' loads are in: in the wake of a full ring they took 7 us instead of 4.
   __device__ void router() {
     constexpr int kExp = 3, kMost = 2, kTok = 4;  // loads in flight, in registers
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x);
@@ -1553,11 +1563,6 @@ moe_status_t validate_few(const moe_config_t* c) {
 }
 
 cudaError_t start(const void* kernel, FewParams& p, int threads, size_t smem, cudaStream_t st) {
-  if (smem) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
   const int sms = num_sms();
   cfg.gridDim = dim3(sms < kMaxCtas ? sms : kMaxCtas);
@@ -1576,9 +1581,22 @@ cudaError_t start(const void* kernel, FewParams& p, int threads, size_t smem, cu
 
 template <int WD>
 cudaError_t start_stream(FewParams& p, cudaStream_t st) {
-  if (p.T <= 8)
-    return start((const void*)few_stream_kernel<WD, 1>, p, kStreamThreads, stream_smem(1), st);
-  return start((const void*)few_stream_kernel<WD, 2>, p, kStreamThreads, stream_smem(2), st);
+  // 8 or 16 tokens: the second group of columns costs registers and shared memory
+  const int nt = p.T <= 8 ? 1 : 2;
+  const void* kernel = nt == 1 ? (const void*)few_stream_kernel<WD, 1>
+                               : (const void*)few_stream_kernel<WD, 2>;
+  static std::atomic<uint64_t> ready[2];  // devices whose kernel has its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(ready[nt - 1].load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)stream_smem(nt));
+    if (e != cudaSuccess) return e;
+    ready[nt - 1].fetch_or(bit, std::memory_order_relaxed);
+  }
+  return start(kernel, p, kStreamThreads, stream_smem(nt), st);
 }
 
 }  // namespace
