@@ -236,13 +236,53 @@ __device__ __forceinline__ void read8(const uint4* src, int chunks, int c, float
   w.get(v);
 }
 
+// Two fp32 operations an instruction, each rounded as the single one: the kernel below issues more
+// instructions than its memory traffic has time for otherwise.
+struct F2 {
+  uint64_t v;
+  __device__ __forceinline__ F2() = default;
+  __device__ __forceinline__ F2(float a, float b) {
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  }
+  __device__ __forceinline__ explicit F2(float a) : F2(a, a) {}
+  __device__ __forceinline__ void get(float& a, float& b) const {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+  }
+};
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ void pairs(const float (&x)[8], F2 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = F2(x[2 * i], x[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ void put2(T* p, const F2 (&v)[4]) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i].get(x[2 * i], x[2 * i + 1]);
+  store8(p, x);
+}
+__device__ __forceinline__ float total(F2 s) {
+  float a, b;
+  s.get(a, b);
+  return a + b;
+}
+
 template <typename TA, typename TR>
 __global__ void __launch_bounds__(1024) join_rows_kernel(const JoinParams p) {
   extern __shared__ uint4 row4[];
   __shared__ float red[2][32];
   const int chunks = p.d >> 3;
   const int64_t t = blockIdx.x;
-  const bool el = p.gate == MOE_GATE_ELEMENT;
+  const bool el = p.gate == MOE_GATE_ELEMENT, gated = el || p.gate == MOE_GATE_CHANNEL;
   uint4* ys = row4;
   uint4* rs = ys + chunks * (int)(sizeof(TA) / 2);
   uint4* gs = rs + chunks * (int)(sizeof(TR) / 2);
@@ -251,65 +291,80 @@ __global__ void __launch_bounds__(1024) join_rows_kernel(const JoinParams p) {
   const TA* pw = static_cast<const TA*>(p.post_w);
   const TA* qw = static_cast<const TA*>(p.pre_w);
   const TA* gp = static_cast<const TA*>(p.g);
+  TR* ro = static_cast<TR*>(p.resid_out) + t * p.ld_ro;
+  TA* no = static_cast<TA*>(p.normed) + t * p.ld_n;
   for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
     copy8(ys, chunks, c, y + c * 8);
     copy8(rs, chunks, c, r + c * 8);
     if (el) copy8(gs, chunks, c, gp + t * p.ld_g + c * 8);
   }
-  float tg = p.b;
+  float scale = p.b;  // of the branch: b, the token's gate, 1 / rms
   if (p.gate == MOE_GATE_TOKEN) {
     const float v = to_f32<TA>(gp[t]);
-    tg *= p.sigmoid ? 1.0f / (1.0f + expf(-v)) : v;
+    scale *= p.sigmoid ? 1.0f / (1.0f + expf(-v)) : v;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  float inv = 1.0f;
+  float x[8];
+  F2 v[4], w[4];
   if (pw) {
-    float ss = 0.0f;
+    F2 ss(0.0f);
     for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
-      float v[8];
-      read8<TA>(ys, chunks, c, v);
+      read8<TA>(ys, chunks, c, x);
+      pairs(x, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+      for (int e = 0; e < 4; ++e) ss = fma2(v[e], v[e], ss);
     }
-    inv = 1.0f / sqrtf(row_sum<true>(ss, 0, red[0]) / (float)p.d + p.eps);
+    scale *= 1.0f / sqrtf(row_sum<true>(total(ss), 0, red[0]) / (float)p.d + p.eps);
   }
-  float ss = 0.0f;
+  const F2 scale2(scale), a2(p.a);
+  F2 ss(0.0f);
   for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
-    float v[8], x[8];
-    read8<TA>(ys, chunks, c, v);
+    read8<TA>(ys, chunks, c, x);
+    pairs(x, v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = v[e] * scale2;
     if (pw) {
       load8(pw + c * 8, x);
+      pairs(x, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * x[e];
+      for (int e = 0; e < 4; ++e) v[e] = v[e] * w[e];
     }
-    if (el || p.gate == MOE_GATE_CHANNEL) {
+    if (gated) {
       if (el)
         read8<TA>(gs, chunks, c, x);
       else
         load8(gp + c * 8, x);
+      if (p.sigmoid) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= p.sigmoid ? 1.0f / (1.0f + expf(-x[e])) : x[e];
+        for (int e = 0; e < 8; ++e) x[e] = 1.0f / (1.0f + expf(-x[e]));
+      }
+      pairs(x, w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = v[e] * w[e];
     }
     read8<TR>(rs, chunks, c, x);
+    pairs(x, w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      v[e] = p.a * x[e] + tg * v[e];
-      ss = fmaf(v[e], v[e], ss);
+    for (int e = 0; e < 4; ++e) {
+      v[e] = fma2(a2, w[e], v[e]);
+      ss = fma2(v[e], v[e], ss);
     }
-    put(static_cast<TR*>(p.resid_out) + t * p.ld_ro + c * 8, v);
-    ys[c] = *reinterpret_cast<const uint4*>(v);
-    rs[c] = *reinterpret_cast<const uint4*>(v + 4);
+    put2(ro + c * 8, v);
+    if (p.normed) {
+      ys[c] = *reinterpret_cast<const uint4*>(v);
+      rs[c] = *reinterpret_cast<const uint4*>(v + 2);
+    }
   }
   if (!p.normed) return;
-  const float ninv = 1.0f / sqrtf(row_sum<true>(ss, 0, red[1]) / (float)p.d + p.eps);
+  const F2 ninv(1.0f / sqrtf(row_sum<true>(total(ss), 0, red[1]) / (float)p.d + p.eps));
   for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
-    float v[8], x[8];
     *reinterpret_cast<uint4*>(v) = ys[c];
-    *reinterpret_cast<uint4*>(v + 4) = rs[c];
+    *reinterpret_cast<uint4*>(v + 2) = rs[c];
     load8(qw + c * 8, x);
+    pairs(x, w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = v[e] * ninv * x[e];
-    put(static_cast<TA*>(p.normed) + t * p.ld_n + c * 8, v);
+    for (int e = 0; e < 4; ++e) v[e] = v[e] * ninv * w[e];
+    put2(no + c * 8, v);
   }
 }
 
