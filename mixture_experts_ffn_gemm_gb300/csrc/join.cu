@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 256) join_kernel(const JoinPara
 // an SM as its shared memory holds rows.  A row's operands arrive by asynchronous copies without a
 // register, and r' takes their place between the norms; a thread reads only what it has copied, so
 // that the sums' barriers are the only ones.  (Rows held in registers: at most four CTAs an SM, and
-// 159 us where this takes 155 for 16384 x 7168 bf16 rows with a gate per channel, 6.1 TB/s.)
+// 159 us where this takes 153 for 16384 x 7168 bf16 rows with a gate per channel, 6.1 TB/s.)
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
