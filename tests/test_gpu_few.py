@@ -334,3 +334,9 @@ def test_64_bit_weight_offsets(cuda_device):
     L.b[-3:] = 2.0  # the last experts only
     out, _ = few(L)
     compare(out, *reference(L))
+
+
+@pytest.mark.parametrize("kind,E", [("f32", 40), ("bf16", 1023), ("fp8", 64), ("int4", 33)])
+def test_most_pairs(cuda_device, kind, E):
+    """16 tokens of 32 experts each: 512 pairs."""
+    check(_workload(kind, 16, d=128, E=E, k=32, I=128), seed=20)
