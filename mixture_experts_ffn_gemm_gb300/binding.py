@@ -323,9 +323,10 @@ def _pitched(t, T: int, d: int, ld: int, name: str) -> Optional[int]:
         return None
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    if tuple(t.shape) != (T, d):
+    if t.shape != (T, d):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, the configuration says {(T, d)}")
-    if (d > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) != (ld or d)):
+    rows, cols = t.stride()
+    if (cols != 1 and d > 1) or (rows != (ld or d) and T > 1):
         raise ValueError(f"{name}: strides {t.stride()} do not match the row pitch {ld or d}")
     return t.data_ptr()
 
