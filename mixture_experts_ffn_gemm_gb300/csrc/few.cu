@@ -61,8 +61,10 @@ struct FewParams {
 
 struct Selection {
   uint32_t mask[kMaxE + 1];      // tokens of each expert
-  float bias[kMaxE + 1];         // b
-  int16_t slot[kMaxE + 1];       // its place in active
+  union {
+    float bias[kMaxE + 1];       // b, until the choice
+    int16_t slot[kMaxE + 1];     // then each expert's place in active
+  };
   int16_t active[kMaxPairs];     // distinct selected experts, ascending
   uint16_t active_mask[kMaxPairs];  // their tokens
   int16_t row0[kMaxPairs + 1];   // first h row of each
@@ -71,6 +73,9 @@ struct Selection {
   float row_gate[kMaxPairs];
   uint8_t row_token[kMaxPairs];
   int n_active;
+  // The stream's split of the selected experts' W1|W3 features over the CTAs: what a feature of each
+  // place costs, and the sums before it.
+  uint16_t cost[kMaxPairs], before[kMaxPairs + 1];
 };
 
 // Waits (bounded) until `counter` reaches `want`; one thread.
@@ -641,6 +646,56 @@ static_assert(stream_smem(1) <= 227 * 1024 && stream_smem(2) <= 227 * 1024, "one
 // finish that step (K2: before W2; latent: before W_up).
 enum Part { kPartDown, kPartShared, kPartRouted, kPartShOut, kPartW2, kPartShOutLat, kPartUp, kParts };
 
+// The costs of the selected experts' features, by one warp.  An expert of many tokens has less of a
+// slot for its weights: more pieces for the same bytes, and a CTA that gets such experts by their
+// bytes alone finishes last (16 tokens over 96 experts, bf16: 744 us after a mean of 604).  A feature
+// counts half by its bytes and half by its pieces, in eighths of one with one token.
+template <int WD, int NT>
+__device__ __forceinline__ void split_by_cost(const FewParams& p, Selection& sel, int lane) {
+  const int K = p.L ? p.L : p.d, planes = p.L ? 2 : 1;
+  const int n = lane % kMaxT + 1;
+  const int step = slot_cols<WD, NT>(K, n * planes);
+  const int pieces = (K + step - 1) / step;
+  const int one = __shfl_sync(0xffffffffu, pieces, 0);
+  const int mine = min(4 + 4 * pieces / one, 64);
+  int sum = 0;
+  for (int a0 = 0; a0 < sel.n_active; a0 += 32) {
+    const int a = a0 + lane;
+    const uint32_t m = a < sel.n_active ? sel.active_mask[a] : 1u;
+    int c = __shfl_sync(0xffffffffu, mine, __popc(m) - 1);
+    if (a >= sel.n_active) c = 0;
+    int incl = c;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += v;
+    }
+    if (a < sel.n_active) {
+      sel.cost[a] = (uint16_t)c;
+      sel.before[a] = (uint16_t)(sum + incl - c);
+    }
+    sum += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) sel.before[sel.n_active] = (uint16_t)sum;
+  __syncwarp();  // before lane 0 announces the selection
+}
+
+// Where CTA `cta`'s share of the selected experts' features begins: place * I + feature.
+template <int G>
+__device__ __forceinline__ int routed_begin(const FewParams& p, const Selection& sel, int cta,
+                                            int lane) {
+  const int64_t at = (int64_t)sel.before[sel.n_active] * p.I * cta / gridDim.x;
+  int a = 0;  // the last place that begins at or before it
+  for (int a0 = 0; a0 < sel.n_active; a0 += 32) {
+    const int i = a0 + lane;
+    const uint32_t in = __ballot_sync(0xffffffffu, i < sel.n_active && (int64_t)sel.before[i] * p.I <= at);
+    if (in) a = a0 + 31 - __clz(in);
+  }
+  if (cta == (int)gridDim.x) return sel.n_active * p.I;
+  const int f = (int)((at - (int64_t)sel.before[a] * p.I) / sel.cost[a]);
+  return a * p.I + min(f, p.I) / G * G;
+}
+
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
   asm volatile(
@@ -848,9 +903,15 @@ struct Producer {
         kind = kShOut;
       }
       src.fit(lane);
-      const int u0 = (int)((int64_t)(total / G) * blockIdx.x / gridDim.x) * G;
-      const int u1 = (int)((int64_t)(total / G) * (blockIdx.x + 1) / gridDim.x) * G;
       const bool routed = part == kPartRouted;
+      int u0, u1;
+      if (routed) {
+        u0 = routed_begin<G>(p, sel, blockIdx.x, lane);
+        u1 = routed_begin<G>(p, sel, blockIdx.x + 1, lane);
+      } else {
+        u0 = (int)((int64_t)(total / G) * blockIdx.x / gridDim.x) * G;
+        u1 = (int)((int64_t)(total / G) * (blockIdx.x + 1) / gridDim.x) * G;
+      }
       int a = routed ? u0 / p.I : 0, f = u0 - a * p.I * (routed ? 1 : 0), left = u1 - u0;
 #pragma unroll 1
       while (left > 0) {  // spans of one matrix (routed: of one expert), in tiles of nearly one size
@@ -1505,6 +1566,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) few_stream_kernel(const Few
     Consumer<WD, NT> v{p, hd, slots, red, warp - kFirstCons, lane};
     v.router();
     if (!build_selection(p, hd.sel, threadIdx.x - 32 * kFirstCons, &hd.abort)) return;
+    if (warp == kFirstCons) split_by_cost<WD, NT>(p, hd.sel, lane);
     if (lane == 0) mbar_arrive(&hd.sel_bar);
     v.run();
   }
