@@ -648,8 +648,9 @@ enum Part { kPartDown, kPartShared, kPartRouted, kPartShOut, kPartW2, kPartShOut
 
 // The costs of the selected experts' features, by one warp.  An expert of many tokens has less of a
 // slot for its weights: more pieces for the same bytes, and a CTA that gets such experts by their
-// bytes alone finishes last (16 tokens over 96 experts, bf16: 744 us after a mean of 604).  A feature
-// counts half by its bytes and half by its pieces, in eighths of one with one token.
+// bytes alone finishes last (16 tokens over 96 experts, bf16: 744 us after a mean of 604; the whole
+// layer takes 960 us instead of 1075 with this).  A feature
+// counts a quarter by its bytes and the rest by its pieces, in eighths of one with one token.
 template <int WD, int NT>
 __device__ __forceinline__ void split_by_cost(const FewParams& p, Selection& sel, int lane) {
   const int K = p.L ? p.L : p.d, planes = p.L ? 2 : 1;
@@ -657,7 +658,7 @@ __device__ __forceinline__ void split_by_cost(const FewParams& p, Selection& sel
   const int step = slot_cols<WD, NT>(K, n * planes);
   const int pieces = (K + step - 1) / step;
   const int one = __shfl_sync(0xffffffffu, pieces, 0);
-  const int mine = min(4 + 4 * pieces / one, 64);
+  const int mine = min(2 + 6 * pieces / one, 64);
   int sum = 0;
   for (int a0 = 0; a0 < sel.n_active; a0 += 32) {
     const int a = a0 + lane;
