@@ -1161,8 +1161,8 @@ struct Consumer {
     }
   }
 
-  // A slot's 16 rows times its tokens, this warp's channels: added to d.
-  template <bool PLANES>
+  // A slot's 16 rows times its tokens (NG groups of 8), this warp's channels: added to d.
+  template <bool PLANES, int NG>
   __device__ __forceinline__ void multiply(const SlotInfo& si, uint32_t base, int part,
                                            float (&d)[NT][4]) {
     using W = Wt<WD>;
@@ -1173,10 +1173,10 @@ struct Consumer {
     const uint32_t sc_row = base + si.soff + gr * 2;
     const uint32_t zeros = settle(smem_u32(hd.zeros));
     // a column of a product is a token's place among the segment's: 8 tokens to a group of columns
-    uint32_t arow[NT];
-    bool on[NT];
+    uint32_t arow[NG];
+    bool on[NG];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < NG; ++n) {
       on[n] = n * 8 + gr < n_act;
       arow[n] = base + si.aoff + (n * 8 + gr) * si.apitch;
     }
@@ -1193,7 +1193,7 @@ struct Consumer {
     // two bf16 units at a time, with sums of their own, so that their products overlap
     constexpr int kPar = WD == MOE_BF16 ? 2 : 1;
     constexpr int kSteps = WD == MOE_BF16 ? kPar : W::kUnit / W::kStep;
-    float o[kPar][NT][4];
+    float o[kPar][NG][4];
 #pragma unroll
     for (int i = 0; i < kPar; ++i) zero_sums(o[i]);
 #pragma unroll 1
@@ -1218,9 +1218,9 @@ struct Consumer {
           sb = valid ? lds2(sc_row + 16 + col) * 0x10001u : 0u;
         }
         const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
-        uint32_t q[NT], q2[NT];  // this lane's channels of its tokens, plane by plane
+        uint32_t q[NG], q2[NG];  // this lane's channels of its tokens, plane by plane
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NG; ++n) {
           q[n] = on[n] && valid ? arow[n] + col * 2 : zeros;  // a token without a row reads zeros
           q2[n] = on[n] && valid ? q[n] + plane : zeros;
         }
@@ -1250,8 +1250,7 @@ struct Consumer {
             int4x8_to_bf16(wb[h], sb, b);
           }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (NT > 1 && n * 8 >= n_act) continue;
+          for (int n = 0; n < NG; ++n) {
             float(&sum)[4] = o[WD == MOE_BF16 ? st : 0][n];
             const uint4 v = lds16(q[n] + h * 16);
             if constexpr (WD == MOE_FP8_E4M3 && !PLANES) {
@@ -1271,14 +1270,14 @@ struct Consumer {
       }
       if constexpr (WD == MOE_FP8_E4M3) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NG; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[n][i] = fmaf(i < 2 ? s0 : s1, o[0][n][i], d[n][i]);
       }
     }
     if constexpr (WD != MOE_FP8_E4M3) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NG; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -1290,7 +1289,7 @@ struct Consumer {
         const uint32_t ba = __ballot_sync(0xffffffffu, bad & 1u) >> (gr * 4) & 15u;
         const uint32_t bb = __ballot_sync(0xffffffffu, bad & 2u) >> (gr * 4) & 15u;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NG; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (i < 2 ? ba : bb) d[n][i] = __uint_as_float(0x7fffffffu);
@@ -1298,9 +1297,10 @@ struct Consumer {
     }
   }
 
-  __device__ __forceinline__ static void zero_sums(float (&v)[NT][4]) {
+  template <int N>
+  __device__ __forceinline__ static void zero_sums(float (&v)[N][4]) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[n][i] = 0.0f;
   }
@@ -1325,10 +1325,11 @@ struct Consumer {
       float d[NT][4];
       zero_sums(d);
       const uint32_t addr = settle(smem_u32(slots) + at * slot_bytes(NT));
-      if (si.plane)
-        multiply<true>(si, addr, part, d);
-      else
-        multiply<false>(si, addr, part, d);
+      if (NT > 1 && __popc(si.mask) > 8) {
+        si.plane ? multiply<true, NT>(si, addr, part, d) : multiply<false, NT>(si, addr, part, d);
+      } else {
+        si.plane ? multiply<true, 1>(si, addr, part, d) : multiply<false, 1>(si, addr, part, d);
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
