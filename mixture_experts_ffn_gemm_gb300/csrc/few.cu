@@ -1007,6 +1007,12 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
                              *reinterpret_cast<__nv_bfloat162*>(&b));
   return *reinterpret_cast<uint32_t*>(&r);
 }
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  __nv_bfloat162 r = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&a),
+                             *reinterpret_cast<__nv_bfloat162*>(&b),
+                             *reinterpret_cast<__nv_bfloat162*>(&c));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
   __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a),
                              *reinterpret_cast<__nv_bfloat162*>(&b));
@@ -1035,8 +1041,28 @@ __device__ __forceinline__ int h_place(int f) {
   return WD == MOE_FP8_E4M3 && ((f ^ (f >> 1)) & 1) ? f ^ 3 : f;
 }
 
-// Eight 4-bit codes (nibbles j and j + 4 are channels 2j and 2j + 1) times their scale: 128 + u is
-// bf16's 0x4300 | u, minus 136 exact, and the product rounds once.
+// Eight 4-bit codes (nibbles j and j + 4 are channels 2j and 2j + 1) times their scale, rounded once.
+// 0x00 to 0xff are bf16's multiples of 2^-133 without a gap (the subnormals and the first binade), so a
+// nibble at bit 0 or 4 is u * 2^-133 or u * 2^-129 as it stands, and one fma with the scale times
+// 2^133 or 2^129 and -8 times the scale, both exact, gives (u - 8) * scale.  Scales of 2^-5 and more,
+// whose multiples end past the largest bf16, take the other form: 128 + u is 0x4300 | u, minus 136
+// exact.  (15 operations a word there, 9 here and 4 a scale.)
+struct Int4Scale {
+  uint32_t low, high, minus8;
+  __device__ __forceinline__ static bool fits(uint32_t sc) { return (sc & 0x7fffu) < 0x3d00u; }
+  __device__ __forceinline__ void set(uint32_t sc) {  // two copies of the scale
+    high = mul_bf16x2(mul_bf16x2(sc, 0x60006000u), 0x5f805f80u);  // 2^65, 2^64
+    low = mul_bf16x2(high, 0x41804180u);                           // 2^4
+    minus8 = mul_bf16x2(sc, 0xc100c100u);
+  }
+};
+__device__ __forceinline__ void int4x8_to_bf16(uint32_t w, const Int4Scale& sc, uint32_t (&v)[4]) {
+  const uint32_t w8 = w >> 8;
+  v[0] = fma_bf16x2(w & 0x000f000fu, sc.low, sc.minus8);
+  v[1] = fma_bf16x2(w & 0x00f000f0u, sc.high, sc.minus8);
+  v[2] = fma_bf16x2(w8 & 0x000f000fu, sc.low, sc.minus8);
+  v[3] = fma_bf16x2(w8 & 0x00f000f0u, sc.high, sc.minus8);
+}
 __device__ __forceinline__ void int4x8_to_bf16(uint32_t w, uint32_t sc, uint32_t (&v)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -1224,48 +1250,62 @@ struct Consumer {
           q[n] = on[n] && valid ? arow[n] + col * 2 : zeros;  // a token without a row reads zeros
           q2[n] = on[n] && valid ? q[n] + plane : zeros;
         }
+        auto products = [&](const auto& fa, const auto& fb) {
 #pragma unroll
-        for (int h = 0; h < W::kChunk / 8; ++h) {  // 8 channels: two products
-          uint32_t a[4], b[4];
-          if constexpr (WD == MOE_BF16) {
+          for (int h = 0; h < W::kChunk / 8; ++h) {  // 8 channels: two products
+            uint32_t a[4], b[4];
+            if constexpr (WD == MOE_BF16) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              a[i] = wa[i];
-              b[i] = wb[i];
-            }
-          } else if constexpr (WD == MOE_FP8_E4M3) {
-            if constexpr (PLANES) {
-              e4m3x4_to_bf16(wa[2 * h], k16, k256, a[0], a[1], top_a);
-              e4m3x4_to_bf16(wa[2 * h + 1], k16, k256, a[2], a[3], top_a);
-              e4m3x4_to_bf16(wb[2 * h], k16, k256, b[0], b[1], top_b);
-              e4m3x4_to_bf16(wb[2 * h + 1], k16, k256, b[2], b[3], top_b);
+              for (int i = 0; i < 4; ++i) {
+                a[i] = wa[i];
+                b[i] = wb[i];
+              }
+            } else if constexpr (WD == MOE_FP8_E4M3) {
+              if constexpr (PLANES) {
+                e4m3x4_to_bf16(wa[2 * h], k16, k256, a[0], a[1], top_a);
+                e4m3x4_to_bf16(wa[2 * h + 1], k16, k256, a[2], a[3], top_a);
+                e4m3x4_to_bf16(wb[2 * h], k16, k256, b[0], b[1], top_b);
+                e4m3x4_to_bf16(wb[2 * h + 1], k16, k256, b[2], b[3], top_b);
+              } else {
+                e4m3x4_to_f16(wa[2 * h], a[0], a[1]);
+                e4m3x4_to_f16(wa[2 * h + 1], a[2], a[3]);
+                e4m3x4_to_f16(wb[2 * h], b[0], b[1]);
+                e4m3x4_to_f16(wb[2 * h + 1], b[2], b[3]);
+              }
             } else {
-              e4m3x4_to_f16(wa[2 * h], a[0], a[1]);
-              e4m3x4_to_f16(wa[2 * h + 1], a[2], a[3]);
-              e4m3x4_to_f16(wb[2 * h], b[0], b[1]);
-              e4m3x4_to_f16(wb[2 * h + 1], b[2], b[3]);
+              int4x8_to_bf16(wa[h], fa, a);
+              int4x8_to_bf16(wb[h], fb, b);
             }
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+              float(&sum)[4] = o[WD == MOE_BF16 ? st : 0][n];
+              const uint4 v = lds16(q[n] + h * 16);
+              if constexpr (WD == MOE_FP8_E4M3 && !PLANES) {
+                mma16816_f16(sum, a[0], b[0], a[1], b[1], v.x, v.y);
+                mma16816_f16(sum, a[2], b[2], a[3], b[3], v.z, v.w);
+              } else {
+                mma16816(sum, a[0], b[0], a[1], b[1], v.x, v.y);
+                mma16816(sum, a[2], b[2], a[3], b[3], v.z, v.w);
+              }
+              if (PLANES) {
+                const uint4 v2 = lds16(q2[n] + h * 16);
+                mma16816(sum, a[0], b[0], a[1], b[1], v2.x, v2.y);
+                mma16816(sum, a[2], b[2], a[3], b[3], v2.z, v2.w);
+              }
+            }
+          }
+        };
+        if constexpr (WD == MOE_INT4) {
+          if (__all_sync(0xffffffffu, Int4Scale::fits(sa) && Int4Scale::fits(sb))) {
+            Int4Scale fa, fb;
+            fa.set(sa);
+            fb.set(sb);
+            products(fa, fb);
           } else {
-            int4x8_to_bf16(wa[h], sa, a);
-            int4x8_to_bf16(wb[h], sb, b);
+            products(sa, sb);
           }
-#pragma unroll
-          for (int n = 0; n < NG; ++n) {
-            float(&sum)[4] = o[WD == MOE_BF16 ? st : 0][n];
-            const uint4 v = lds16(q[n] + h * 16);
-            if constexpr (WD == MOE_FP8_E4M3 && !PLANES) {
-              mma16816_f16(sum, a[0], b[0], a[1], b[1], v.x, v.y);
-              mma16816_f16(sum, a[2], b[2], a[3], b[3], v.z, v.w);
-            } else {
-              mma16816(sum, a[0], b[0], a[1], b[1], v.x, v.y);
-              mma16816(sum, a[2], b[2], a[3], b[3], v.z, v.w);
-            }
-            if (PLANES) {
-              const uint4 v2 = lds16(q2[n] + h * 16);
-              mma16816(sum, a[0], b[0], a[1], b[1], v2.x, v2.y);
-              mma16816(sum, a[2], b[2], a[3], b[3], v2.z, v2.w);
-            }
-          }
+        } else {
+          products(0, 0);
         }
       }
       if constexpr (WD == MOE_FP8_E4M3) {

@@ -340,3 +340,18 @@ def test_64_bit_weight_offsets(cuda_device):
 def test_most_pairs(cuda_device, kind, E):
     """16 tokens of 32 experts each: 512 pairs."""
     check(_workload(kind, 16, d=128, E=E, k=32, I=128), seed=20)
+
+
+@pytest.mark.parametrize("lo,hi", [(-12, -5), (-133, -120), (-6, -4), (100, 104)])
+def test_int4_scales_of_a_range(cuda_device, lo, hi):
+    """Scales of one range throughout: ordinary ones, subnormals, those about 2^-5, large ones."""
+    L = S.make_layer(_workload("int4", 3, d=256, E=4, k=2, I=128), seed=18, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for m, s in ((L.W13, L.W13_scale), (L.Ws13, L.Ws13_scale)):
+        # the gate's rows keep ordinary scales: the output is of the other rows' size
+        m.copy_(torch.randint(0, 256, m.shape, generator=g, device="cuda").to(torch.uint8))
+        up = s[..., s.shape[-1] // 2:]
+        e = torch.randint(lo, hi, up.shape, generator=g, device="cuda").double()
+        up.copy_(torch.exp2(e) * (1 + torch.rand(up.shape, generator=g, device="cuda")))
+    out, _ = few(L)
+    compare(out, *reference(L))
