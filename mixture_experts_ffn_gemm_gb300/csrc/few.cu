@@ -1029,26 +1029,15 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
-// Four e4m3 codes as bf16, the pairs of codes 0, 2 and 1, 3: exponent and mantissa bits moved to
-// bf16's places give value * 2^-120 (subnormals included), the product with 2^120 is exact.  The
-// integer pipe runs at half rate and bounds the e4m3 layer, so the left shifts are multiplications
-// (k16 and k256 are 16 and 256, unknown to the compiler).  top collects the largest magnitude of the
-// codes in each half: 0x7f is NaN.
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t k16, uint32_t k256, uint32_t& p02,
-                                               uint32_t& p13, uint32_t& top) {
-  const uint32_t e02 = w & 0x007f007fu, e13 = (w >> 8) & 0x007f007fu;
-  top = __vimax3_u16x2(top, e02, e13);
-  p02 = mul_bf16x2(e02 * k16 + (w & 0x00800080u) * k256, 0x7b807b80u);
-  p13 = mul_bf16x2(e13 * k16 + (w & 0x80008000u), 0x7b807b80u);
-}
-__device__ __forceinline__ bool e4m3_any_nan(uint32_t top) {
-  return (top & 0xffffu) == 0x7fu || top >> 16 == 0x7fu;
-}
-// The order in which h is stored for the e4m3 layer: features 4i, 4i + 2, 4i + 1, 4i + 3, the pairs
-// that e4m3x4_to_bf16 gives.
-template <int WD>
-__device__ __forceinline__ int h_place(int f) {
-  return WD == MOE_FP8_E4M3 && ((f ^ (f >> 1)) & 1) ? f ^ 3 : f;
+// Four e4m3 codes as bf16, in order (exact, NaN included).
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& p01, uint32_t& p23) {
+  uint32_t h[2];
+  e4m3x4_to_f16(w, h[0], h[1]);
+  const float2 a = __half22float2(*reinterpret_cast<__half2*>(&h[0]));
+  const float2 b = __half22float2(*reinterpret_cast<__half2*>(&h[1]));
+  const __nv_bfloat162 l = __float22bfloat162_rn(a), u = __float22bfloat162_rn(b);
+  p01 = *reinterpret_cast<const uint32_t*>(&l);
+  p23 = *reinterpret_cast<const uint32_t*>(&u);
 }
 
 // Eight 4-bit codes (nibbles j and j + 4 are channels 2j and 2j + 1) times their scale, rounded once.
@@ -1225,8 +1214,6 @@ struct Consumer {
       s1p = si.s + (r1 >> 7) * si.s_ld;
     }
     const uint32_t plane = PLANES ? si.plane : 0;
-    const uint32_t k16 = settle(16u), k256 = settle(256u);
-    uint32_t top_a = 0, top_b = 0;  // largest e4m3 magnitudes of the two rows
     // two bf16 units at a time, with sums of their own, so that their products overlap
     constexpr int kPar = WD == MOE_BF16 ? 2 : 1;
     constexpr int kSteps = WD == MOE_BF16 ? kPar : W::kUnit / W::kStep;
@@ -1280,10 +1267,10 @@ struct Consumer {
               }
             } else if constexpr (WD == MOE_FP8_E4M3) {
               if constexpr (PLANES) {
-                e4m3x4_to_bf16(wa[2 * h], k16, k256, a[0], a[1], top_a);
-                e4m3x4_to_bf16(wa[2 * h + 1], k16, k256, a[2], a[3], top_a);
-                e4m3x4_to_bf16(wb[2 * h], k16, k256, b[0], b[1], top_b);
-                e4m3x4_to_bf16(wb[2 * h + 1], k16, k256, b[2], b[3], top_b);
+                e4m3x4_to_bf16(wa[2 * h], a[0], a[1]);
+                e4m3x4_to_bf16(wa[2 * h + 1], a[2], a[3]);
+                e4m3x4_to_bf16(wb[2 * h], b[0], b[1]);
+                e4m3x4_to_bf16(wb[2 * h + 1], b[2], b[3]);
               } else {
                 e4m3x4_to_f16(wa[2 * h], a[0], a[1]);
                 e4m3x4_to_f16(wa[2 * h + 1], a[2], a[3]);
@@ -1340,18 +1327,6 @@ struct Consumer {
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int j = 0; j < kPar; ++j) d[n][i] += o[j][n][i];
-    } else if constexpr (PLANES) {
-      // a NaN code that any of a row's four lanes has met makes the row's sums NaN
-      const uint32_t bad = (e4m3_any_nan(top_a) ? 1u : 0u) | (e4m3_any_nan(top_b) ? 2u : 0u);
-      if (__any_sync(0xffffffffu, bad != 0)) {
-        const uint32_t ba = __ballot_sync(0xffffffffu, bad & 1u) >> (gr * 4) & 15u;
-        const uint32_t bb = __ballot_sync(0xffffffffu, bad & 2u) >> (gr * 4) & 15u;
-#pragma unroll
-        for (int n = 0; n < NG; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < 2 ? ba : bb) d[n][i] = __uint_as_float(0x7fffffffu);
-      }
     }
   }
 
@@ -1485,7 +1460,7 @@ struct Reducer {
         v = silu_accurate(g) * u;
       }
       if (ti.gated) v *= hd.sel.row_gate[hr];
-      store_planes(p.h2 + (int64_t)hr * p.I + h_place<WD>(ti.f0 + row), (int64_t)p.T * (p.k + 1) * p.I, v);
+      store_planes(p.h2 + (int64_t)hr * p.I + ti.f0 + row, (int64_t)p.T * (p.k + 1) * p.I, v);
     }
   }
   // 16 features times 8 NT tokens, two a thread and token group
