@@ -569,9 +569,13 @@ struct Wt {
   static __device__ __forceinline__ int bytes(int cols) { return cols * kBits / 8; }
 };
 
-// Row pitch in a slot: 64 bytes past a multiple of 128, so that the 16-byte loads of eight lanes
-// (two rows, four words each) meet different banks.
-__device__ __forceinline__ int slot_pitch(int bytes) { return ((bytes + 127) & ~127) + 64; }
+// Row pitch in a slot: past a multiple of 128 bytes by what keeps the 16-byte loads of eight lanes
+// (two rows, four words each) on different banks: 64 bytes where the words follow one another (weights,
+// bf16 layer's activations), 16 where they are 32 bytes apart (e4m3 layer's activations).  4-bit
+// layer's activations: 64 bytes apart, two words meet, with 16 not also the rows.
+__device__ __forceinline__ int slot_pitch(int bytes, int past) {
+  return ((bytes + 127) & ~127) + past;
+}
 
 // Channels a slot of a segment takes (K in all, nr activation rows), cut evenly.
 template <int WD, int NT>
@@ -785,7 +789,8 @@ struct Producer {
       w += e * g.w_step;
       if constexpr (WD != MOE_BF16) sc = static_cast<const uint8_t*>(sc) + e * g.s_step;
     }
-    const int wpitch = slot_pitch(Wt<WD>::bytes(step)), apitch = slot_pitch(step * 2);
+    const int wpitch = slot_pitch(Wt<WD>::bytes(step), 64);
+    const int apitch = slot_pitch(step * 2, WD == MOE_BF16 ? 64 : 16);
     const int soff = 16 * wpitch, aoff = soff + (WD == MOE_INT4 ? step : 0);
     const int rows = n * (g.plane ? 2 : 1);
     // this lane's weight row
