@@ -1191,8 +1191,13 @@ struct Consumer {
     }
   }
 
+  // How a product takes the activations' planes: the only one; both in turn; or, with up to four
+  // tokens, the first in columns 0 to 3 and the second in 4 to 7, which saves half of the products and
+  // loads, and adds the columns up at the end.
+  enum Planes { kOne, kInTurn, kSideBySide };
+
   // A slot's 16 rows times its tokens (NG groups of 8), this warp's channels: added to d.
-  template <bool PLANES, int NG>
+  template <Planes PLANES, int NG>
   __device__ __forceinline__ void multiply(const SlotInfo& si, uint32_t base, int part,
                                            float (&d)[NT][4]) {
     using W = Wt<WD>;
@@ -1208,8 +1213,10 @@ struct Consumer {
     bool on[NG];
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
-      on[n] = n * 8 + gr < n_act;
-      arow[n] = base + si.aoff + (n * 8 + gr) * si.apitch;
+      const int col = PLANES == kSideBySide ? gr & 3 : n * 8 + gr;
+      on[n] = col < n_act;
+      arow[n] = base + si.aoff + col * si.apitch;
+      if (PLANES == kSideBySide && gr >= 4) arow[n] += si.plane;
     }
     const float *s0p = nullptr, *s1p = nullptr;
     if constexpr (WD == MOE_FP8_E4M3) {
@@ -1218,7 +1225,7 @@ struct Consumer {
       s0p = si.s + (r0 >> 7) * si.s_ld;
       s1p = si.s + (r1 >> 7) * si.s_ld;
     }
-    const uint32_t plane = PLANES ? si.plane : 0;
+    const uint32_t plane = PLANES == kInTurn ? si.plane : 0;
     // two bf16 units at a time, with sums of their own, so that their products overlap
     constexpr int kPar = WD == MOE_BF16 ? 2 : 1;
     constexpr int kSteps = WD == MOE_BF16 ? kPar : W::kUnit / W::kStep;
@@ -1271,7 +1278,7 @@ struct Consumer {
                 b[i] = wb[i];
               }
             } else if constexpr (WD == MOE_FP8_E4M3) {
-              if constexpr (PLANES) {
+              if constexpr (PLANES != kOne) {
                 e4m3x4_to_bf16(wa[2 * h], a[0], a[1]);
                 e4m3x4_to_bf16(wa[2 * h + 1], a[2], a[3]);
                 e4m3x4_to_bf16(wb[2 * h], b[0], b[1]);
@@ -1290,14 +1297,14 @@ struct Consumer {
             for (int n = 0; n < NG; ++n) {
               float(&sum)[4] = o[WD == MOE_BF16 ? st : 0][n];
               const uint4 v = token(q[n] + h * 16, n);
-              if constexpr (WD == MOE_FP8_E4M3 && !PLANES) {
+              if constexpr (WD == MOE_FP8_E4M3 && PLANES == kOne) {
                 mma16816_f16(sum, a[0], b[0], a[1], b[1], v.x, v.y);
                 mma16816_f16(sum, a[2], b[2], a[3], b[3], v.z, v.w);
               } else {
                 mma16816(sum, a[0], b[0], a[1], b[1], v.x, v.y);
                 mma16816(sum, a[2], b[2], a[3], b[3], v.z, v.w);
               }
-              if (PLANES) {
+              if (PLANES == kInTurn) {
                 const uint4 v2 = token(q2[n] + h * 16, n);
                 mma16816(sum, a[0], b[0], a[1], b[1], v2.x, v2.y);
                 mma16816(sum, a[2], b[2], a[3], b[3], v2.z, v2.w);
@@ -1363,11 +1370,14 @@ struct Consumer {
       float d[NT][4];
       zero_sums(d);
       const uint32_t addr = settle(smem_u32(slots) + at * slot_bytes(NT));
-      if (NT > 1 && __popc(si.mask) > 8) {
-        si.plane ? multiply<true, NT>(si, addr, part, d) : multiply<false, NT>(si, addr, part, d);
-      } else {
-        si.plane ? multiply<true, 1>(si, addr, part, d) : multiply<false, 1>(si, addr, part, d);
-      }
+      const int n_act = __popc(si.mask);
+      const bool side = si.plane && n_act <= 4;
+      if (side)
+        multiply<kSideBySide, 1>(si, addr, part, d);
+      else if (NT > 1 && n_act > 8)
+        si.plane ? multiply<kInTurn, NT>(si, addr, part, d) : multiply<kOne, NT>(si, addr, part, d);
+      else
+        si.plane ? multiply<kInTurn, 1>(si, addr, part, d) : multiply<kOne, 1>(si, addr, part, d);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -1375,6 +1385,10 @@ struct Consumer {
       const uint32_t mask = si.mask;
       __syncwarp();
       if (lane == 0) mbar_arrive(&hd.empty[at]);
+      if (side) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[0][i] += __shfl_xor_sync(0xffffffffu, d[0][i], 2);
+      }
       const bool scaled = flags & kScaled;
       if (scaled && !wait(&hd.inv_bar, 0)) return;
       if ((mask & (mask + 1u)) == 0) {  // places are tokens, or those of the tile's only segment
