@@ -1338,7 +1338,7 @@ struct Consumer {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < kPar; ++j) d[n][i] += o[j][n][i];
+          for (int j = 0; j < kPar; ++j) d[n][i] = j ? d[n][i] + o[j][n][i] : o[0][n][i];
     }
   }
 
@@ -1358,8 +1358,11 @@ struct Consumer {
     for (uint32_t piece = 0;; ++piece) {
       const int at = line + piece % kBufs * kLanes;  // pieces go round the slots, kLanes apart here
       const uint32_t parity = piece / kBufs & 1u;
-      const SlotInfo& si = hd.info[at];
       if (!wait(&hd.info_bar[at], parity)) return;
+      SlotInfo si;  // in four loads
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        reinterpret_cast<int4*>(&si)[i] = reinterpret_cast<const int4*>(&hd.info[at])[i];
       for (const uint32_t now = si.tile; tile != now; ++tile) {  // tiles that ended before it
         if (!hand_over(acc, tile, hd.tile[at][tile % kTiles])) return;
         zero_sums(acc);
