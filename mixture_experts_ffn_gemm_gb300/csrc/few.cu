@@ -532,9 +532,9 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
 // selection runs on the consumer warps, a warp a token, while the ring fills with the shared expert's
 // weights; and the shared expert's W2 stands where the last CTAs of a step are waited for.
 //
-// Measured (384 experts of d 7168, I 2048, top 8): one token 130 us (118 of them the
-// weights at the measured copy bandwidth), 16 tokens 1250 us, four tokens with e4m3 weights 266 us (209),
-// one token with 4-bit weights 93 us (35); latent width 3584, four tokens 256 us (231).
+// Measured (384 experts of d 7168, I 2048, top 8; in brackets the bytes at the measured copy bandwidth):
+// one token 130 us (118), 16 tokens 1230 us (1240), four tokens with e4m3 weights 238 us (200), one
+// token with 4-bit weights 83 us (35); latent width 3584, four tokens 247 us (222).
 //
 // Values that one step leaves to the next (h, the latent activations) are kept as two bf16 planes,
 // hi = bf16(v) and lo = bf16(v - hi), and multiplied plane by plane into the same fp32 sum: 16 bits
@@ -543,7 +543,8 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
 constexpr int kCons = kWarps;  // consumer warps
 // Four lanes of the stream, each four consumer warps and two slots, of which one fills while the other
 // is multiplied: one slot after another on all sixteen warps left the latencies of a slot's few
-// products and of its bookkeeping in the open (int4, one token: 128 us instead of 93).
+// products and of its bookkeeping in the open (int4, one token: 128 us instead of 93 at
+// that time).
 constexpr int kLanes = 4;
 constexpr int kBufs = 2;
 constexpr int kSlots = kLanes * kBufs;  // one producer warp each
@@ -653,8 +654,8 @@ enum Part { kPartDown, kPartShared, kPartRouted, kPartShOut, kPartW2, kPartShOut
 // The costs of the selected experts' features, by one warp.  An expert of many tokens has less of a
 // slot for its weights: more pieces for the same bytes, and a CTA that gets such experts by their
 // bytes alone finishes last (16 tokens over 96 experts, bf16: 744 us after a mean of 604; the whole
-// layer takes 960 us instead of 1075 with this).  A feature
-// counts a quarter by its bytes and the rest by its pieces, in eighths of one with one token.
+// layer took 960 us instead of 1075 with this).  A feature counts a quarter by its bytes and the rest
+// by its pieces, in eighths of one with one token.
 template <int WD, int NT>
 __device__ __forceinline__ void split_by_cost(const FewParams& p, Selection& sel, int lane) {
   const int K = p.L ? p.L : p.d, planes = p.L ? 2 : 1;
@@ -1081,7 +1082,8 @@ __device__ __forceinline__ void split_planes(float v, __nv_bfloat16& hi, __nv_bf
 
 // The sixteen consumer warps: four to a lane of the stream, so that the latencies of a slot's few
 // products and of its bookkeeping overlap with three other lanes', while the lane's other slot fills.
-// A warp adds its channels of a tile's segments up over the pieces its lane gets; the tile's end brings the sixteen sums together.  NT: groups of
+// A warp adds its channels of a tile's segments up over the pieces its lane gets; the tile's end brings
+// the sixteen sums together.  NT: groups of
 // 8 tokens.  Every wait gives up once the CTA's abort flag is set, so the warps may leave one by one.
 template <int WD, int NT>
 struct Consumer {
