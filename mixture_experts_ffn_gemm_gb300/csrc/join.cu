@@ -11,6 +11,10 @@
 namespace moe {
 namespace {
 
+// Partial sums of a row's two norms, one float for each warp of a CTA.
+constexpr int kRowSumBytes = 2 * 32 * sizeof(float);
+constexpr int kRowsSmem = 100 * 1024;  // a row's operands in join_rows_kernel, two rows an SM at least
+
 struct JoinParams {
   int64_t T;
   int d;
@@ -280,6 +284,7 @@ template <typename TA, typename TR>
 __global__ void __launch_bounds__(1024) join_rows_kernel(const JoinParams p) {
   extern __shared__ uint4 row4[];
   __shared__ float red[2][32];
+  static_assert(sizeof(red) == kRowSumBytes, "counted when the launch sets its limit");
   const int chunks = p.d >> 3;
   const int64_t t = blockIdx.x;
   const bool el = p.gate == MOE_GATE_ELEMENT, gated = el || p.gate == MOE_GATE_CHANNEL;
@@ -455,10 +460,11 @@ cudaError_t launch(const JoinParams& p, bool wide_loads, cudaStream_t st) {
   LaunchScope ls("block_join", st);
   const size_t row_bytes =
       (size_t)p.d * (sizeof(TA) * (p.gate == MOE_GATE_ELEMENT ? 2 : 1) + sizeof(TR));
-  if (wide_loads && p.T > num_sms() && p.d > 1024 && row_bytes <= 100 * 1024) {
-    if (row_bytes > 48 * 1024) {
+  if (wide_loads && p.T > num_sms() && p.d > 1024 && row_bytes <= kRowsSmem) {
+    // 48 KB without the attribute: the kernel's own arrays and the launch's together
+    if (row_bytes + kRowSumBytes > 48 * 1024) {
       cudaError_t e = cudaFuncSetAttribute(join_rows_kernel<TA, TR>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
       if (e != cudaSuccess) return e;
     }
     int threads = (p.d / 32 + 31) / 32 * 32;

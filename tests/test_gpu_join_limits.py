@@ -1,0 +1,68 @@
+"""GPU tests of the block join where a launch's shared memory comes near the 48 KB that need no
+attribute.  The formula in 64 bits and the tolerances are those of the join's other tests."""
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+
+from conftest import ROOT  # noqa: E402
+from test_gpu_join import BF16, F32, TYPES, _check, _make, _reference, _run  # noqa: E402
+
+from mixture_experts_ffn_gemm_gb300 import binding as B  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+GATES = ("none", "channel", "token", "element")
+ROWS = 200  # more rows than the device has SMs: the kernel that keeps rows in shared memory
+
+
+def _row_bytes(act, res, gate):
+    """Shared memory a column takes there: branch, residual and an element gate."""
+    size = {F32: 4, BF16: 2}
+    return size[act] * (2 if gate == "element" else 1) + size[res]
+
+
+def _one(act, res, gate, d, seed):
+    cfg, st = _make(ROWS, d, act, res, gate, gate == "element", True, True, seed=seed)
+    ref = _reference(st, gate, gate == "element")
+    _run(cfg, st)
+    _check(cfg, st, ref)
+
+
+def _near_48k():
+    """Every type and gate at the widths whose rows take the last 256 bytes below 48 KB, in a process that
+    has launched no larger row before."""
+    for act, res in TYPES:
+        for gate in GATES:
+            last = 48 * 1024 // _row_bytes(act, res, gate) // 8 * 8
+            first = (48 * 1024 - 256) // _row_bytes(act, res, gate) // 8 * 8
+            for d in sorted({first, first + 8, last}):
+                try:
+                    _one(act, res, gate, d, 1)
+                except B.MoEError as e:
+                    print(f"refused: {act} {res} {gate} {d}: {e}")
+                    return 1
+    return 0
+
+
+def test_rows_near_48k_as_first_calls(cuda_device):
+    r = subprocess.run([sys.executable, os.path.abspath(__file__)], cwd=ROOT, capture_output=True,
+                       text=True, timeout=600)
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("d", [4096, 6144, 8192, 12288, 16384])
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("act,res", TYPES)
+def test_usual_widths(cuda_device, act, res, gate, d):
+    _one(act, res, gate, d, 2)
+
+
+if __name__ == "__main__":
+    from mixture_experts_ffn_gemm_gb300 import build
+    build.build()
+    sys.exit(_near_48k())
