@@ -474,11 +474,13 @@ cudaError_t launch(const JoinParams& p, bool wide_loads, cudaStream_t st) {
   }
   if (wide_loads) return launch_rows<TA, TR, 8>(p, p.d / 8, st);  // d <= 32768: 4096 chunks
   if (p.d <= 8192) return launch_rows<TA, TR, 1>(p, p.d, st);
-  const size_t smem = (size_t)p.d * sizeof(float);
+  // the widest row's, whatever this one takes: a limit of the call's own would be lowered by another
+  // host thread's narrower row between here and the launch
   cudaError_t e = cudaFuncSetAttribute(join_wide_kernel<TA, TR>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       MOE_JOIN_MAX_D * (int)sizeof(float));
   if (e != cudaSuccess) return e;
-  join_wide_kernel<TA, TR><<<(unsigned)p.T, 1024, smem, st>>>(p);
+  join_wide_kernel<TA, TR><<<(unsigned)p.T, 1024, (size_t)p.d * sizeof(float), st>>>(p);
   return cudaGetLastError();
 }
 

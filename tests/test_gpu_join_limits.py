@@ -1,8 +1,11 @@
 """GPU tests of the block join where a launch's shared memory comes near the 48 KB that need no
-attribute.  The formula in 64 bits and the tolerances are those of the join's other tests."""
+attribute, and of calls from several host threads.  The formula in 64 bits and the tolerances are those
+of the join's other tests."""
+import ctypes
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
 import torch
@@ -60,6 +63,33 @@ def test_rows_near_48k_as_first_calls(cuda_device):
 @pytest.mark.parametrize("act,res", TYPES)
 def test_usual_widths(cuda_device, act, res, gate, d):
     _one(act, res, gate, d, 2)
+
+
+def test_wide_odd_rows_from_two_threads(cuda_device):
+    """Odd widths beyond 8192 take d x 4 bytes of shared memory each: calls of different widths from two
+    threads do not lower each other's limit."""
+    lib = B.load_library()
+    calls, bad = 5000, []
+    buf = {d: [torch.randn(1, d, device="cuda").to(BF16) for _ in range(4)] for d in (8193, 32767)}
+
+    def work(d):
+        r, y, ro, n = buf[d]
+        w = torch.ones(d, dtype=BF16, device="cuda")
+        cfg = B.make_join_config(1, d)
+        stream = torch.cuda.Stream().cuda_stream
+        for _ in range(calls):
+            s = lib.moe_block_join(ctypes.byref(cfg), r.data_ptr(), y.data_ptr(), None, None,
+                                   w.data_ptr(), ro.data_ptr(), n.data_ptr(), stream)
+            if s != B.MOE_OK:
+                bad.append((d, s))
+        torch.cuda.synchronize()
+
+    threads = [threading.Thread(target=work, args=(d,)) for d in buf]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, (len(bad), bad[0])
 
 
 if __name__ == "__main__":
