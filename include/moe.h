@@ -334,6 +334,7 @@ typedef enum {
 } moe_gate_t;
 #define MOE_JOIN_GATE_SIGMOID 0x1u /* g = 1 / (1 + exp(-gate)) */
 #define MOE_JOIN_MAX_D 32768
+#define MOE_JOIN_MAX_LD_NORMED 1048576
 typedef struct {
   int64_t T;            /* rows, >= 0; T == 0 is a no-op                                      */
   int32_t d;            /* row width, 1 .. MOE_JOIN_MAX_D                                     */
@@ -344,7 +345,10 @@ typedef struct {
   float resid_scale;
   float branch_scale;
   float rms_eps;
-  int64_t ld_resid, ld_branch, ld_gate, ld_resid_out, ld_normed; /* row pitches; 0: d          */
+  /* Row pitches, 0: d.  At least d; T times a pitch at most 2^60, so that a row may be one position
+   * of a long buffer; ld_normed, whose reader takes rows that follow one another, at most
+   * MOE_JOIN_MAX_LD_NORMED. */
+  int64_t ld_resid, ld_branch, ld_gate, ld_resid_out, ld_normed;
 } moe_join_config_t;
 /*   resid [T][d], branch [T][d]; post_w [d] or NULL; gate as its kind says (NULL without);
  *   pre_w [d] and normed [T][d], both or neither; resid_out [T][d].

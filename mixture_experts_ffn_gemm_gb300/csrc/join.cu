@@ -502,11 +502,12 @@ extern "C" moe_status_t moe_block_join(const moe_join_config_t* cfg, const void*
   if (cfg->flags & ~MOE_JOIN_GATE_SIGMOID) return MOE_ERR_INVALID_ARG;
   if (cfg->d > MOE_JOIN_MAX_D || cfg->T > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (cfg->act_dtype == MOE_F32 && cfg->resid_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
-  const int64_t d = cfg->d, max_ld = (int64_t)1 << 20;
-  const int64_t lds[] = {cfg->ld_resid, cfg->ld_branch, cfg->ld_gate, cfg->ld_resid_out,
-                         cfg->ld_normed};
-  for (int64_t ld : lds)
+  // Offsets are 64-bit: the last row's, in bytes, stays below 2^62.
+  const int64_t d = cfg->d, max_ld = ((int64_t)1 << 60) / (cfg->T > 0 ? cfg->T : 1);
+  for (int64_t ld : {cfg->ld_resid, cfg->ld_branch, cfg->ld_gate, cfg->ld_resid_out})
     if (ld != 0 && (ld < d || ld > max_ld)) return MOE_ERR_INVALID_ARG;
+  if (cfg->ld_normed != 0 && (cfg->ld_normed < d || cfg->ld_normed > MOE_JOIN_MAX_LD_NORMED))
+    return MOE_ERR_INVALID_ARG;
   if (cfg->T == 0) return MOE_OK;
   if (!resid || !branch || !resid_out) return MOE_ERR_INVALID_ARG;
   if ((cfg->gate != MOE_GATE_NONE) != (gate != nullptr)) return MOE_ERR_INVALID_ARG;

@@ -1,6 +1,6 @@
 """GPU tests of the block join where a launch's shared memory comes near the 48 KB that need no
-attribute, and of calls from several host threads.  The formula in 64 bits and the tolerances are those
-of the join's other tests."""
+attribute, of calls from several host threads, and of wide row pitches.  The formula in 64 bits and the
+tolerances are those of the join's other tests."""
 import ctypes
 import os
 import subprocess
@@ -90,6 +90,34 @@ def test_wide_odd_rows_from_two_threads(cuda_device):
     for t in threads:
         t.join()
     assert not bad, (len(bad), bad[0])
+
+
+@pytest.mark.parametrize("act,res", TYPES)
+@pytest.mark.parametrize("d,more", [(7168, 0), (1001, 1)])
+def test_one_position_of_a_long_buffer(cuda_device, act, res, d, more):
+    """Rows more than 2^20 elements apart, as the last position of every sequence is."""
+    T, ld = 3, (1 << 20) + 4096 + more
+    cfg, st = _make(T, d, act, res, "element", False, True, True, ld - d, seed=3)
+    cfg.ld_normed = 0
+    st["normed"] = torch.empty(T, d, dtype=act, device="cuda")
+    ref = _reference(st, "element", False)
+    _run(cfg, st)
+    _check(cfg, st, ref)
+
+
+def test_pitch_past_32_bits(cuda_device):
+    """Two rows more than 2^31 elements apart, in place."""
+    T, d, ld = 2, 2048, (1 << 31) + 64
+    cfg, st = _make(T, d, BF16, BF16, "channel", False, True, True, seed=4)
+    ref = _reference(st, "channel", False)
+    for name in ("resid", "branch"):
+        buf = torch.empty(ld + d, dtype=BF16, device="cuda").as_strided((T, d), (ld, 1))
+        buf.copy_(st[name])
+        st[name] = buf
+    st["resid_out"] = st["resid"]
+    cfg.ld_resid = cfg.ld_branch = cfg.ld_resid_out = ld
+    _run(cfg, st)
+    _check(cfg, st, ref)
 
 
 if __name__ == "__main__":
