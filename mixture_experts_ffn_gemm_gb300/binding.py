@@ -201,7 +201,7 @@ def _dev(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:  # the current stream's handle without building a Stream object (3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -317,12 +317,17 @@ def make_join_config(T: int, d: int, act_dtype: torch.dtype = torch.bfloat16,
                              int(ld_normed))
 
 
-def _pitched(t, T: int, d: int, ld: int, name: str) -> Optional[int]:
-    """Address of a [T][d] tensor whose rows lie `ld` (0: d) elements apart."""
+_DTYPES = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
+
+
+def _pitched(t, T: int, d: int, ld: int, dtype, name: str) -> Optional[int]:
+    """Address of a [T][d] tensor of `dtype` whose rows lie `ld` (0: d) elements apart."""
     if t is None:
         return None
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: type {t.dtype}, the configuration says {dtype}")
     if t.shape != (T, d):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, the configuration says {(T, d)}")
     rows, cols = t.stride()
@@ -331,17 +336,31 @@ def _pitched(t, T: int, d: int, ld: int, name: str) -> Optional[int]:
     return t.data_ptr()
 
 
+def _vector(t, n: int, dtype, name: str) -> Optional[int]:
+    """Address of n consecutive elements of `dtype`."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: {tuple(t.shape)} of {t.dtype} with strides {t.stride()}, the "
+                         f"configuration says {n} consecutive elements of {dtype}")
+    return t.data_ptr()
+
+
 def moe_block_join(cfg: moe_join_config_t, resid, branch, post_w, gate, pre_w, resid_out, normed,
                    stream=None):
     """r' = resid_scale resid + branch_scale g RMSNorm(branch) post_w; normed = RMSNorm(r') pre_w."""
-    T, d = cfg.T, cfg.d
-    g = (_pitched(gate, T, d, cfg.ld_gate, "gate") if cfg.gate == MOE_GATE_ELEMENT
-         else _dev(gate))
+    T, d, kind = cfg.T, cfg.d, cfg.gate
+    act, res = _DTYPES.get(cfg.act_dtype), _DTYPES.get(cfg.resid_dtype)
+    g = (_pitched(gate, T, d, cfg.ld_gate, act, "gate") if kind == MOE_GATE_ELEMENT
+         else _vector(gate, T if kind == MOE_GATE_TOKEN else d, act, "gate"))
     _check(load_library().moe_block_join(
-        ctypes.byref(cfg), _pitched(resid, T, d, cfg.ld_resid, "resid"),
-        _pitched(branch, T, d, cfg.ld_branch, "branch"), _dev(post_w), g, _dev(pre_w),
-        _pitched(resid_out, T, d, cfg.ld_resid_out, "resid_out"),
-        _pitched(normed, T, d, cfg.ld_normed, "normed"), _stream(stream)), "moe_block_join")
+        ctypes.byref(cfg), _pitched(resid, T, d, cfg.ld_resid, res, "resid"),
+        _pitched(branch, T, d, cfg.ld_branch, act, "branch"), _vector(post_w, d, act, "post_w"), g,
+        _vector(pre_w, d, act, "pre_w"),
+        _pitched(resid_out, T, d, cfg.ld_resid_out, res, "resid_out"),
+        _pitched(normed, T, d, cfg.ld_normed, act, "normed"), _stream(stream)), "moe_block_join")
 
 
 def moe_forward_host_io(cfg, x_host, W_r, b, W13, W2, W13_scale, W2_scale, Ws13, Ws2,
