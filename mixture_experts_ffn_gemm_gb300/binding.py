@@ -1,4 +1,5 @@
-"""ctypes binding of the C ABI in ``include/moe.h`` (argument marshalling only).
+"""ctypes binding of the C ABI in ``include/moe.h`` (argument marshalling; moe_forward_few and
+moe_block_join also refuse operands that are shorter than their configuration).
 
 Every function has the name of its C entry point and takes torch tensors (device memory) or
 ``None`` for a NULL pointer; the stream defaults to torch's current CUDA stream.  All compute runs
@@ -8,6 +9,7 @@ there is no fallback of any kind.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -288,14 +290,48 @@ def alloc_few_workspace(cfg: moe_config_t, device="cuda") -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
+_FEW_OPERANDS = ("x", "W_r", "b", "W13", "W2", "W13_scale", "W2_scale", "Ws13", "Ws2", "Ws13_scale",
+                 "Ws2_scale", "W_down", "W_up", "out")
+
+
+@functools.lru_cache(maxsize=64)
+def _few_bytes(cfg: bytes) -> tuple:
+    """What each of _FEW_OPERANDS holds at least, in bytes (0: not read), by a moe_config_t's bytes."""
+    c = moe_config_t.from_buffer_copy(cfg)
+    T, d, E, I, n_shared, L, act, wt = (c.T, c.d, c.E, c.I, c.n_shared, c.d_latent, c.act_dtype,
+                                        c.w_dtype)
+    a, de = 4 if act == MOE_F32 else 2, L or d
+    bits = {MOE_F32: 32, MOE_BF16: 16, MOE_FP8_E4M3: 8, MOE_INT4: 4}.get(wt, 0)
+
+    def scales(rows, cols):
+        return (rows // 128 * (cols // 128) * 4 if wt == MOE_FP8_E4M3 else
+                cols // 32 * rows * 2 if wt == MOE_INT4 else 0)
+
+    return (T * d * a, E * d * 4, E * 4, E * 2 * I * de * bits // 8, E * de * I * bits // 8,
+            E * scales(2 * I, de), E * scales(de, I), n_shared * 2 * I * d * bits // 8,
+            n_shared * d * I * bits // 8, n_shared * scales(2 * I, d), n_shared * scales(d, I),
+            L * d * a, d * L * a, T * d * a)
+
+
+def _refuse_few(ops, need):
+    for t, n, name in zip(ops, need, _FEW_OPERANDS):
+        _dev(t)
+        if t is not None and t.nbytes < n:
+            raise ValueError(f"{name}: {t.nbytes} bytes, the configuration takes {n}")
+
+
 def moe_forward_few(cfg, x, W_r, b, W13, W2, W13_scale, W2_scale, Ws13, Ws2, Ws13_scale,
                     Ws2_scale, W_down, W_up, out, ws, stream=None):
     """moe_forward for T <= MOE_FEW_MAX_TOKENS tokens in one kernel launch; ws from
     alloc_few_workspace."""
-    _check(load_library().moe_forward_few(
-        ctypes.byref(cfg), _dev(x), _dev(W_r), _dev(b), _dev(W13), _dev(W2), _dev(W13_scale),
-        _dev(W2_scale), _dev(Ws13), _dev(Ws2), _dev(Ws13_scale), _dev(Ws2_scale), _dev(W_down),
-        _dev(W_up), _dev(out), _dev(ws), ws.numel(), _stream(stream)), "moe_forward_few")
+    ops = (x, W_r, b, W13, W2, W13_scale, W2_scale, Ws13, Ws2, Ws13_scale, Ws2_scale, W_down, W_up,
+           out)
+    need = _few_bytes(bytes(cfg))
+    args = [None if t is None else
+            t.data_ptr() if t.is_cuda and t.nbytes >= n and t.is_contiguous() else
+            _refuse_few(ops, need) for t, n in zip(ops, need)]
+    _check(load_library().moe_forward_few(ctypes.byref(cfg), *args, _dev(ws), ws.numel(),
+                                          _stream(stream)), "moe_forward_few")
 
 
 _GATES = {"none": MOE_GATE_NONE, "channel": MOE_GATE_CHANNEL, "token": MOE_GATE_TOKEN,
