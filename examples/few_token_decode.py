@@ -38,7 +38,11 @@ class FewTokenStack:
 
         self.layers = layers
         self.cfg = B.config_for(w)
-        self.ws = B.alloc_few_workspace(self.cfg, dev)
+        # a workspace a block: every call clears its workspace's status word, which `status` collects
+        ws = torch.stack([B.alloc_few_workspace(self.cfg, dev) for _ in layers])
+        self.ws = list(ws)
+        self._flags = ws.view(torch.int32)[:, :1]
+        self.status = torch.zeros(len(layers), 64, dtype=torch.int32, device=dev)
         self.ffn_norm = [vector() for _ in layers]
         self.post_norm = [vector() for _ in layers]
         self.next_norm = [vector() for _ in layers]
@@ -60,9 +64,17 @@ class FewTokenStack:
         for i, layer in enumerate(self.layers):
             B.moe_block_join(self.before, self.resid, self.attn[i], None, None, self.ffn_norm[i],
                              self.resid, self._n)
-            B.moe_forward_few(self.cfg, self._n, *B.layer_weights(layer), self._y, self.ws)
+            B.moe_forward_few(self.cfg, self._n, *B.layer_weights(layer), self._y, self.ws[i])
             B.moe_block_join(self.after, self.resid, self._y, self.post_norm[i], self.gate[i],
                              self.next_norm[i], self.resid, self.normed)
+        self.status[:, :1].bitwise_or_(self._flags)
+
+    def check(self):
+        """Raises if a layer call of any step so far gave up a wait (synchronises)."""
+        for i, word in enumerate(self.status):
+            status = B.moe_device_status(word.view(torch.uint8))
+            if status != B.MOE_OK:
+                raise B.MoEError(status, f"block {i}")
 
     def capture(self):
         """Captures step() into a CUDA graph that replay() runs."""
@@ -108,7 +120,7 @@ def main():
         stack.replay()
     stop.record()
     torch.cuda.synchronize()
-    assert B.moe_device_status(stack.ws) == B.MOE_OK
+    stack.check()
     print(f"{a.blocks} blocks, {a.tokens} tokens: {start.elapsed_time(stop) / a.steps * 1e3:.1f} us "
           f"a step, |normed| rms {stack.normed.float().pow(2).mean().sqrt().item():.3f}")
 

@@ -302,7 +302,8 @@ moe_status_t moe_dense_mlp(int64_t T, int32_t d, int32_t I, moe_dtype_t act_dtyp
  *     the output is rounded once.  e4m3 experts take the bf16 activations as they are (moe_forward
  *     quantises them), so both stay within that layer's tolerance of each other.
  *   - ws: moe_few_workspace_size() bytes, laid out differently from moe_workspace_size()'s.  One
- *     workspace serves one call at a time.
+ *     workspace serves one call at a time.  The device status word is cleared on entry, as by
+ *     moe_forward: it tells about the last call on that workspace.
  *   - The launch is cooperative (one thread block on each SM, which wait for one another between
  *     the layer's steps); it can be captured into a CUDA graph.  Every wait is bounded: a wait that
  *     expires raises MOE_ERR_TIMEOUT in the device status and the output is incomplete.
