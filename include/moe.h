@@ -307,7 +307,10 @@ moe_status_t moe_dense_mlp(int64_t T, int32_t d, int32_t I, moe_dtype_t act_dtyp
  *   - The launch is cooperative (one thread block on each SM, which wait for one another between
  *     the layer's steps); it can be captured into a CUDA graph.  Every wait is bounded: a wait that
  *     expires raises MOE_ERR_TIMEOUT in the device status and the output is incomplete.
- * The result depends on nothing but the arguments: equal calls give equal bits. */
+ * The result depends on nothing but the arguments: equal calls give equal bits.  A token's last bits
+ * may differ between calls in which other tokens share the layer with it: with bf16 activations the
+ * order of its sums follows how many tokens its experts have and which experts the others select; with
+ * fp32 it follows T alone.  Both stay within the arithmetic stated above. */
 #define MOE_FEW_MAX_TOKENS 16
 size_t moe_few_workspace_size(const moe_config_t* cfg);
 moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, const float* W_r,
@@ -323,7 +326,9 @@ moe_status_t moe_forward_few(const moe_config_t* cfg, const void* x, const float
  *   r' = resid_scale * resid + branch_scale * g * v
  *   normed = r' * pre_w / sqrt(mean(r'^2) + rms_eps)             (without normed: not computed)
  * with g = 1, the gate's value, or its sigmoid.  All in fp32; r' is rounded once to resid_dtype and
- * normed, computed from the unrounded r', once to act_dtype.
+ * normed, computed from the unrounded r', once to act_dtype.  Rows do not mix and equal calls give
+ * equal bits; the order of a row's fp32 products and sums, and so its last bits, may differ between
+ * calls of few and of many rows, and of other alignment.
  * Unlike the layer's buffers, rows may lie in wider buffers (the ld_* pitches, in elements) and
  * pointers need only their element's alignment; 16-byte aligned pointers and pitches with
  * d % 8 == 0 run wide loads. */
