@@ -422,7 +422,7 @@ template <typename TA, typename TR, int V, int NC>
 void start_rows(const JoinParams& p, bool block, int lanes, cudaStream_t st) {
   if (block)
     join_kernel<TA, TR, V, NC, true><<<(unsigned)p.T, lanes, 0, st>>>(p, lanes);
-  else
+  else if constexpr (NC <= 4)  // eight chunks a thread only for rows of more than 4096 of them
     join_kernel<TA, TR, V, NC, false>
         <<<(unsigned)((p.T + 256 / lanes - 1) / (256 / lanes)), 256, 0, st>>>(p, lanes);
 }
