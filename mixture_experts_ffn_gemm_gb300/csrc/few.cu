@@ -533,8 +533,8 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewParams p) {
 // weights; and the shared expert's W2 stands where the last CTAs of a step are waited for.
 //
 // Measured (384 experts of d 7168, I 2048, top 8; in brackets the bytes at the measured copy bandwidth):
-// one token 130 us (118), 16 tokens 1230 us (1240), four tokens with e4m3 weights 238 us (200), one
-// token with 4-bit weights 83 us (35); latent width 3584, four tokens 247 us (222).
+// one token 130 us (118), 16 tokens 1230 us (1240), four tokens with e4m3 weights 238-247 us (200), 16
+// 812 us (626), one token with 4-bit weights 83 us (35); latent width 3584, four tokens 247-258 us (222).
 //
 // Values that one step leaves to the next (h, the latent activations) are kept as two bf16 planes,
 // hi = bf16(v) and lo = bf16(v - hi), and multiplied plane by plane into the same fp32 sum: 16 bits
