@@ -6,8 +6,9 @@ quant    Microscaled 4-bit floating point: rows in blocks of B channels, each bl
          "mx": B = 32, S = 2^(floor(log2 amax) - 2) (a power of two held as its exponent);
          "nv": B = 16, S = s g with s = e4m3(amax / (6 g)) and a factor g of the whole tensor.
          c = x / S rounded to nearest (ties to the even code), at most 6.  Rows may be gathered: row r
-         is source row perm_src[r] / k, the order in which the experts take their tokens.  The pass
-         goes to codes and scales and back to the values that they stand for.
+         is source row perm_src[r] / k, and row t goes to the k rows dest[t], the order in which the
+         experts take their tokens.  The pass goes to codes and scales and back to the values that
+         they stand for.
 micro    The experts' product on such operands: row r of expert e gives out[r][n] = sum_k x[r][k]
          W_e[n][k], x quantised from the tokens' rows within the pass, W_e held in 4 bits; with SwiGLU
          out = SiLU(x W1_e) * (x W3_e).
@@ -128,16 +129,19 @@ def _tokens(g, T, K, pad, dtype):
 
 
 def _routing(g, T, k, E):
-    """Each token's k experts, some experts more popular: (perm_src int32 [T k], offsets as a list)."""
+    """Each token's k experts, some experts more popular: (perm_src int32 [T k], its inverse dest, and
+    offsets as a list)."""
     like = torch.randn(E, device=DEV, generator=g) * 0.5
     u = torch.rand(T, E, device=DEV, generator=g).clamp_(1e-7, 1.0 - 1e-7)
     idx = (like - torch.log(-torch.log(u))).topk(k, dim=1).indices.reshape(-1)
-    perm = torch.sort(idx, stable=True).indices.to(torch.int32)
+    perm = torch.sort(idx, stable=True).indices
+    dest = torch.empty_like(perm)
+    dest[perm] = torch.arange(T * k, device=DEV)
     counts = torch.bincount(idx, minlength=E).cpu().tolist()
     offsets = [0]
     for c in counts:
         offsets.append(offsets[-1] + c)
-    return perm, offsets
+    return perm.to(torch.int32), dest.to(torch.int32), offsets
 
 
 def _tiled_scales(s, rows_of_group):
@@ -161,7 +165,7 @@ def _prepare_quant(case, seed):
     g = _generator(seed)
     T, K, k, E = (case[n] for n in ("T", "K", "k", "E"))
     st = {"case": case, "x": _tokens(g, T, K, case["pad"], _DT[case["act"]])}
-    st["perm"], st["offs"] = _routing(g, T, k, E)
+    st["perm"], st["dest"], st["offs"] = _routing(g, T, k, E)
     st["g"] = None
     if case["fmt"] == "nv":  # the factor that brings the tensor's largest block scale to 448
         st["g"] = (st["x"].abs().amax().float() / (6.0 * 448.0)).reshape(1)
@@ -170,7 +174,7 @@ def _prepare_quant(case, seed):
         st["offsets"] = torch.tensor(st["offs"], dtype=torch.int32, device=DEV)
         st["cfg"] = B.make_micro_config(rows=T * k, K=K, format=case["fmt"], groups=E,
                                         dtype=_DT[case["act"]], ld=K + case["pad"], src_rows=T,
-                                        index_div=k)
+                                        copies=k)
         st["back"] = B.make_micro_config(rows=T * k, K=K, format=case["fmt"], groups=E,
                                          dtype=_DT[case["out"]])
         st["codes"], st["scales"] = B.alloc_micro(st["cfg"], DEV)
@@ -183,7 +187,7 @@ def _prepare_micro(case, seed):
     g = _generator(seed)
     T, k, E, N, K, fmt = (case[n] for n in ("T", "k", "E", "N", "K", "fmt"))
     st = {"case": case, "x": _tokens(g, T, K, 0, torch.bfloat16)}
-    st["perm"], st["offs"] = _routing(g, T, k, E)
+    st["perm"], st["dest"], st["offs"] = _routing(g, T, k, E)
     rows = N * (2 if case["swiglu"] else 1)
     st["w"] = torch.empty(E * rows, K // 2, dtype=torch.uint8, device=DEV)
     flat = st["w"].view(-1)
@@ -213,7 +217,7 @@ def _prepare_micro(case, seed):
         st["offsets"] = torch.tensor(st["offs"], dtype=torch.int32, device=DEV)
         st["w_scales"] = _tiled_scales(st["s"], rows)
         st["qcfg"] = B.make_micro_config(rows=T * k, K=K, format=fmt, groups=E, src_rows=T,
-                                         index_div=k)
+                                         copies=k)
         st["codes"], st["scales"] = B.alloc_micro(st["qcfg"], DEV)
         st["cfg"] = B.make_micro_product_config(rows=T * k, E=E, N=N, K=K, format=fmt,
                                                 out_dtype=_DT[case["out"]],
@@ -228,7 +232,7 @@ def _prepare_grouped(case, seed):
     T, k, E, N, K, kind, pad = (case[n] for n in ("T", "k", "E", "N", "K", "kind", "pad"))
     R = T * k
     st = {"case": case}
-    _, st["offs"] = _routing(g, T, k, E)
+    _, _, st["offs"] = _routing(g, T, k, E)
     x = dy = w = None
     if kind != "grad_x":
         x = _normal(g, (R, K + pad), 1.0, torch.bfloat16)[:, :K]
@@ -350,12 +354,12 @@ def run(state):
         return {"quant": _plain_quant, "micro": _plain_micro, "grouped": _plain_grouped}[op](st)
     from mixture_experts_ffn_gemm_gb300 import binding as B
     if op == "quant":
-        B.moe_micro_quantize(st["cfg"], st["x"], st["perm"], st["offsets"], st["g"], st["codes"],
+        B.moe_micro_quantize(st["cfg"], st["x"], st["dest"], st["offsets"], st["g"], st["codes"],
                              st["scales"], st["ws"])
         B.moe_micro_dequantize(st["back"], st["codes"], st["scales"], st["offsets"], st["g"],
                                st["out"], st["ws"])
     elif op == "micro":
-        B.moe_micro_quantize(st["qcfg"], st["x"], st["perm"], st["offsets"], st["gx"], st["codes"],
+        B.moe_micro_quantize(st["qcfg"], st["x"], st["dest"], st["offsets"], st["gx"], st["codes"],
                              st["scales"], st["ws"])
         B.moe_micro_product(st["cfg"], st["offsets"], st["codes"], st["scales"], st["gx"], st["w"],
                             st["w_scales"], st["gw"], st["out"], st["ws"])
