@@ -365,6 +365,125 @@ moe_status_t moe_block_join(const moe_join_config_t* cfg, const void* resid, con
                             const void* post_w, const void* gate, const void* pre_w,
                             void* resid_out, void* normed, void* stream);
 
+/* Products grouped by expert, rows [offsets[e], offsets[e+1]) of expert e, bf16 operands and fp32 sums:
+ *   MOE_PRODUCT_FORWARD  out = y  [rows][N]:  y[r][n]    = sum_k a[r][k] b_e[n][k]
+ *                        a = x [rows][K], b = W [E][N][K]
+ *   MOE_PRODUCT_GRAD_X   out = dx [rows][K]:  dx[r][k]   = sum_n a[r][n] b_e[n][k]
+ *                        a = dy [rows][N], b = W [E][N][K]
+ *   MOE_PRODUCT_GRAD_W   out = dW [E][N][K]:  dW_e[n][k] = sum_r a[r][n] b[r][k]
+ *                        a = dy [rows][N], b = x [rows][K]
+ * Each output is rounded once, from its fp32 sum, to out_dtype (MOE_BF16 or MOE_F32).
+ *   offsets [E+1] int32, as moe_permute gives them: not decreasing, from 0 on, at most `rows`.  Rows
+ *           from offsets[E] on belong to no expert: they are not read into any result and their
+ *           outputs are left as they are.  An expert without rows has a dW of zeros.
+ *   N and K are multiples of 8 up to 131072, E is at most 1023, rows at most 2^26; ld_x and ld_y are the
+ *           row pitches in elements of the [rows][K] and [rows][N] buffers (0: K, N), multiples of 8.
+ *           Pointers are 16-byte aligned.  W and dW are dense.
+ *   MOE_PRODUCT_ACCUMULATE (GRAD_W with fp32 outputs): dW is added onto what `out` holds.
+ *   ws      moe_product_workspace_size() bytes; its first word is the device status.  The call raises
+ *           flags there and clears none (moe_reset_device_status does), so one status can watch a run
+ *           of calls: MOE_ERR_TIMEOUT (a bounded wait expired, the output is incomplete),
+ *           MOE_ERR_DEVICE_CHECK (an offset outside its range, taken as the nearest allowed one).
+ * `out` may not overlap an operand.  rows == 0 is a no-op, but for GRAD_W without ACCUMULATE, which
+ * writes zeros.  Equal calls give equal bits. */
+typedef enum {
+  MOE_PRODUCT_FORWARD = 0,
+  MOE_PRODUCT_GRAD_X = 1,
+  MOE_PRODUCT_GRAD_W = 2
+} moe_product_t;
+#define MOE_PRODUCT_ACCUMULATE 0x1u
+typedef struct {
+  int64_t rows;      /* rows of the row buffers, >= 0         */
+  int32_t E, N, K;   /* experts, W's rows and columns         */
+  int32_t kind;      /* MOE_PRODUCT_*                         */
+  int32_t out_dtype; /* MOE_BF16 or MOE_F32                   */
+  uint32_t flags;    /* MOE_PRODUCT_ACCUMULATE                */
+  int64_t ld_x, ld_y;
+} moe_product_config_t;
+size_t moe_product_workspace_size(const moe_product_config_t* cfg);
+moe_status_t moe_grouped_product(const moe_product_config_t* cfg, const int32_t* offsets,
+                                 const void* a, const void* b, void* out, void* ws,
+                                 size_t ws_bytes, void* stream);
+
+/* Microscaled 4-bit floating point.  A row of K channels is cut into blocks of B; a block has one
+ * scale S, a channel one 4-bit code c of e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 as 0..7, bit 3 the sign),
+ * and the value is c S:
+ *   MOE_MICRO_MX  B = 32, S = 2^(byte - 127) (e8m0; 255: NaN), S = 2^(floor(log2 amax) - 2), the
+ *                 byte at least 0; 1 for a block of zeros
+ *   MOE_MICRO_NV  B = 16, S = s g: s an e4m3 byte (at most 448; 127: NaN), s = amax / (6 g) rounded to
+ *                 nearest (ties to even), g a factor of the whole tensor in [2^-100, 2^100]
+ * with amax the block's largest magnitude.  c is x / S rounded to nearest, ties to the even code, at
+ * most 6; where s is zero all codes are.  The roundings are those of the exact quotients.  A block that
+ * holds a NaN or an infinity has the scale NaN and codes 0: every value of it reads as NaN.  A factor
+ * outside its range makes every block NaN (and raises MOE_ERR_DEVICE_CHECK).
+ *   codes   [rows][K/2] bytes, channel 2i in the low half of byte i
+ *   scales  bytes in tiles of 128 rows x 4 scale columns (512 bytes), in which the tensor cores take
+ *           them: the scale of row r of a group and column c (channels cB .. cB+B-1) is byte
+ *             ((first + r / 128) * ceil(K / (4 B)) + c / 4) * 512 + r % 32 * 16 + r % 128 / 32 * 4 + c % 4
+ *           with first = (the group's first row) / 128 + (the group's number); quotients rounded
+ *           down.  moe_micro_scales_size() bytes; bytes of rows outside the groups are not written.
+ *   Groups are the experts' rows: offsets [groups+1] (as moe_permute gives them), or with offsets
+ *           NULL, `groups` groups of rows / groups rows each (a stack of weight matrices).
+ * K is a multiple of 64. */
+typedef enum { MOE_MICRO_MX = 0, MOE_MICRO_NV = 1 } moe_micro_format_t;
+#define MOE_MICRO_MAX_COPIES 32
+typedef struct {
+  int64_t rows;     /* coded rows, 0 .. 2^26                                                       */
+  int64_t src_rows; /* quantise: rows of x, 0 .. 2^26                                              */
+  int32_t K;        /* channels of a row, a multiple of 64 up to 131072                            */
+  int32_t format;   /* MOE_MICRO_*                                                                 */
+  int32_t dtype;    /* x or the values: MOE_F32 or MOE_BF16                                        */
+  int32_t groups;   /* 1 .. 1023                                                                   */
+  int32_t copies;   /* quantise: coded rows of each row of x, 1 .. MOE_MICRO_MAX_COPIES            */
+  uint32_t flags;   /* 0                                                                           */
+  int64_t ld;       /* row pitch of x or the values in elements (0: K), a multiple of 8            */
+} moe_micro_config_t;
+/* Bytes of the scales (0 for an invalid configuration). */
+size_t moe_micro_scales_size(const moe_micro_config_t* cfg);
+/* Rows of x to codes and scales.
+ *   x      [src_rows][K] dtype;  dest [src_rows][copies] int32: the coded rows that take source row t
+ *          (perm_dst of moe_permute with copies = k: the experts' rows, each token quantised once), or
+ *          NULL with copies == 1 and src_rows == rows: row t.  Coded rows that no entry names are left
+ *          as they are; an entry outside the groups' rows is skipped and raises MOE_ERR_DEVICE_CHECK.
+ *          Two entries may not name one row.
+ *   factor g, one fp32 on the device (MOE_MICRO_NV; NULL: 1).  Ignored for MOE_MICRO_MX.
+ *   ws     at least 256 bytes, the device status as for moe_grouped_product. */
+moe_status_t moe_micro_quantize(const moe_micro_config_t* cfg, const void* x, const int32_t* dest,
+                                const int32_t* offsets, const float* factor, void* codes,
+                                void* scales, void* ws, size_t ws_bytes, void* stream);
+/* The values that codes and scales stand for, out [rows][K] dtype: c s exactly, times g rounded once to
+ * fp32, and once more to bf16.  Rows outside the groups are left as they are; copies and src_rows are
+ * not used. */
+moe_status_t moe_micro_dequantize(const moe_micro_config_t* cfg, const void* codes,
+                                  const void* scales, const int32_t* offsets, const float* factor,
+                                  void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* The experts' product on microscaled operands: out[r][n] = g_a g_w[e] sum_k a[r][k] w_e[n][k] for the rows
+ * of expert e, the tensor cores' block-scaled products and fp32 sums, one rounding to out_dtype.
+ * MOE_MICRO_SWIGLU: w_e has 2N rows, the N of W1 and then the N of W3, and
+ * out[r][n] = SiLU(x W1)[n] * (x W3)[n], in fp32 (N a multiple of 128).
+ *   a, a_scales  codes and scales of [rows][K], groups by offsets [E+1] (moe_micro_quantize)
+ *   w, w_scales  codes and scales of [E * (N or 2N)][K] in E groups (moe_micro_quantize with offsets NULL)
+ *   a_factor     g_a, one fp32; w_factor g_w [E] fp32; MOE_MICRO_NV only, NULL: 1
+ *   out          [rows][N], pitch ld_out elements (0: N), a multiple of 8
+ *   ws           moe_micro_product_workspace_size() bytes, the device status as for moe_grouped_product
+ * N is a multiple of 8 up to 131072, K of 64, E at most 1023, rows at most 2^26.  Rows from offsets[E] on
+ * are left as they are; rows == 0 is a no-op.  Equal calls give equal bits. */
+#define MOE_MICRO_SWIGLU 0x1u
+typedef struct {
+  int64_t rows;
+  int32_t E, N, K;
+  int32_t format;    /* MOE_MICRO_*           */
+  int32_t out_dtype; /* MOE_BF16 or MOE_F32   */
+  uint32_t flags;    /* MOE_MICRO_SWIGLU      */
+  int64_t ld_out;
+} moe_micro_product_config_t;
+size_t moe_micro_product_workspace_size(const moe_micro_product_config_t* cfg);
+moe_status_t moe_micro_product(const moe_micro_product_config_t* cfg, const int32_t* offsets,
+                               const void* a, const void* a_scales, const float* a_factor,
+                               const void* w, const void* w_scales, const float* w_factor,
+                               void* out, void* ws, size_t ws_bytes, void* stream);
+
 /* Reset the device status word (first 256 bytes of ws) to "no error", enqueued on stream. */
 moe_status_t moe_reset_device_status(void* ws, size_t ws_bytes, void* stream);
 

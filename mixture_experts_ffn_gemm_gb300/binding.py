@@ -1,5 +1,6 @@
-"""ctypes binding of the C ABI in ``include/moe.h`` (argument marshalling; moe_forward_few and
-moe_block_join also refuse operands that are shorter than their configuration).
+"""ctypes binding of the C ABI in ``include/moe.h`` (argument marshalling; moe_forward_few,
+moe_block_join, the products grouped by expert and the microscaled operators also refuse operands whose
+types or sizes are not their configuration's).
 
 Every function has the name of its C entry point and takes torch tensors (device memory) or
 ``None`` for a NULL pointer; the stream defaults to torch's current CUDA stream.  All compute runs
@@ -35,13 +36,21 @@ MOE_FLAG_EXPERT_OUT_F32 = 0x1000
 MOE_FEW_MAX_TOKENS = 16
 MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_ELEMENT = 0, 1, 2, 3
 MOE_JOIN_GATE_SIGMOID = 0x1
+MOE_PRODUCT_FORWARD, MOE_PRODUCT_GRAD_X, MOE_PRODUCT_GRAD_W = 0, 1, 2
+MOE_PRODUCT_ACCUMULATE = 0x1
+MOE_MICRO_MX, MOE_MICRO_NV = 0, 1
+MOE_MICRO_MAX_COPIES = 32
+MOE_MICRO_SWIGLU = 0x1
 
 EXPORTED = ("moe_workspace_size", "moe_router", "moe_permute", "moe_experts", "moe_combine",
             "moe_forward", "moe_forward_host_io", "moe_reset_device_status", "moe_device_status",
             "moe_status_string", "moe_launch_count", "moe_reset_launch_count",
             "moe_profile_enable", "moe_profile_read", "moe_permute_noalloc",
             "moe_last_error_string", "moe_dense_mlp_workspace_size", "moe_dense_mlp",
-            "moe_forward_block", "moe_few_workspace_size", "moe_forward_few", "moe_block_join")
+            "moe_forward_block", "moe_few_workspace_size", "moe_forward_few", "moe_block_join",
+            "moe_product_workspace_size", "moe_grouped_product", "moe_micro_scales_size",
+            "moe_micro_quantize", "moe_micro_dequantize", "moe_micro_product_workspace_size",
+            "moe_micro_product")
 
 
 class MoEError(RuntimeError):
@@ -71,6 +80,24 @@ class moe_join_config_t(ctypes.Structure):
                 ("ld_resid", ctypes.c_int64), ("ld_branch", ctypes.c_int64),
                 ("ld_gate", ctypes.c_int64), ("ld_resid_out", ctypes.c_int64),
                 ("ld_normed", ctypes.c_int64)]
+
+
+class moe_product_config_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("E", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("K", ctypes.c_int32), ("kind", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64)]
+
+
+class moe_micro_config_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("src_rows", ctypes.c_int64), ("K", ctypes.c_int32),
+                ("format", ctypes.c_int32), ("dtype", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("copies", ctypes.c_int32), ("flags", ctypes.c_uint32), ("ld", ctypes.c_int64)]
+
+
+class moe_micro_product_config_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("E", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("K", ctypes.c_int32), ("format", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("ld_out", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -114,6 +141,17 @@ def load_library():
             lib.moe_block_join.restype = S
             lib.moe_block_join.argtypes = [ctypes.POINTER(moe_join_config_t), P, P, P, P, P, P, P,
                                            P]
+            N = ctypes.c_size_t
+            PC, MC, MP = (ctypes.POINTER(t) for t in (moe_product_config_t, moe_micro_config_t,
+                                                      moe_micro_product_config_t))
+            for name, c in (("moe_product_workspace_size", PC), ("moe_micro_scales_size", MC),
+                            ("moe_micro_product_workspace_size", MP)):
+                getattr(lib, name).restype, getattr(lib, name).argtypes = N, [c]
+            for name, args in (("moe_grouped_product", [PC] + [P] * 5 + [N, P]),
+                               ("moe_micro_quantize", [MC] + [P] * 7 + [N, P]),
+                               ("moe_micro_dequantize", [MC] + [P] * 6 + [N, P]),
+                               ("moe_micro_product", [MP] + [P] * 9 + [N, P])):
+                getattr(lib, name).restype, getattr(lib, name).argtypes = S, args
             lib.moe_forward_host_io.restype = S
             lib.moe_forward_host_io.argtypes = lib.moe_forward.argtypes
             lib.moe_reset_device_status.restype = S
@@ -397,6 +435,177 @@ def moe_block_join(cfg: moe_join_config_t, resid, branch, post_w, gate, pre_w, r
         _vector(pre_w, d, act, "pre_w"),
         _pitched(resid_out, T, d, cfg.ld_resid_out, res, "resid_out"),
         _pitched(normed, T, d, cfg.ld_normed, act, "normed"), _stream(stream)), "moe_block_join")
+
+
+_KINDS = {"forward": MOE_PRODUCT_FORWARD, "grad_x": MOE_PRODUCT_GRAD_X,
+          "grad_w": MOE_PRODUCT_GRAD_W}
+_FORMATS = {"mx": MOE_MICRO_MX, "nv": MOE_MICRO_NV}
+
+
+def _one_device(stream, *tensors):
+    """Refuses operands of several devices, or of another than the current one, whose stream is used."""
+    devices = {t.get_device() for t in tensors if t is not None}
+    if len(devices) > 1 or (stream is None and devices != {torch._C._cuda_getDevice()}):
+        raise ValueError(f"operands on the devices {sorted(devices)}: one device, and the current one")
+
+
+def _at_least(t, n: int, dtype, name: str) -> Optional[int]:
+    """Address of at least n consecutive elements of `dtype`."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: {tuple(t.shape)} of {t.dtype} with strides {t.stride()}, the "
+                         f"configuration says {n} consecutive elements of {dtype}")
+    return t.data_ptr()
+
+
+def make_product_config(rows: int, E: int, N: int, K: int, kind: str = "forward",
+                        out_dtype: torch.dtype = torch.bfloat16, accumulate: bool = False,
+                        ld_x: int = 0, ld_y: int = 0) -> moe_product_config_t:
+    """kind: "forward", "grad_x" or "grad_w"; ld_x, ld_y: row pitches in elements of the [rows][K] and
+    [rows][N] buffers, 0 for K and N."""
+    return moe_product_config_t(int(rows), int(E), int(N), int(K), _KINDS[kind], _dt(out_dtype),
+                                MOE_PRODUCT_ACCUMULATE if accumulate else 0, int(ld_x), int(ld_y))
+
+
+def moe_product_workspace_size(cfg: moe_product_config_t) -> int:
+    return int(load_library().moe_product_workspace_size(ctypes.byref(cfg)))
+
+
+def alloc_product_workspace(cfg: moe_product_config_t, device="cuda") -> torch.Tensor:
+    n = moe_product_workspace_size(cfg)
+    if n == 0:
+        raise MoEError(MOE_ERR_INVALID_ARG, "moe_product_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def moe_grouped_product(cfg: moe_product_config_t, offsets, a, b, out, ws, stream=None):
+    """Products grouped by expert: y = x W_e^T (a = x, b = W), dx = dy W_e (a = dy, b = W) or
+    dW_e = dy^T x (a = dy, b = x), rows [offsets[e], offsets[e+1]) of expert e."""
+    R, E, N, K, kind = cfg.rows, cfg.E, cfg.N, cfg.K, cfg.kind
+    bf, odt = torch.bfloat16, _DTYPES.get(cfg.out_dtype)
+    _one_device(stream, offsets, a, b, out, ws)
+    if kind == MOE_PRODUCT_GRAD_W:
+        pa, pb = _pitched(a, R, N, cfg.ld_y, bf, "a"), _pitched(b, R, K, cfg.ld_x, bf, "b")
+        po = _vector(out, E * N * K, odt, "out")
+    elif kind == MOE_PRODUCT_GRAD_X:
+        pa, pb = _pitched(a, R, N, cfg.ld_y, bf, "a"), _vector(b, E * N * K, bf, "b")
+        po = _pitched(out, R, K, cfg.ld_x, odt, "out")
+    else:
+        pa, pb = _pitched(a, R, K, cfg.ld_x, bf, "a"), _vector(b, E * N * K, bf, "b")
+        po = _pitched(out, R, N, cfg.ld_y, odt, "out")
+    _check(load_library().moe_grouped_product(
+        ctypes.byref(cfg), _at_least(offsets, E + 1, torch.int32, "offsets"), pa, pb, po, _dev(ws),
+        ws.numel(), _stream(stream)), "moe_grouped_product")
+
+
+def make_micro_config(rows: int, K: int, format: str = "mx", groups: int = 1,
+                      dtype: torch.dtype = torch.bfloat16, ld: int = 0,
+                      src_rows: Optional[int] = None, copies: int = 1) -> moe_micro_config_t:
+    """format: "mx" (blocks of 32, e8m0 scales) or "nv" (blocks of 16, e4m3 scales, a factor of the
+    tensor); dtype and ld: type and row pitch (0: K) of x or of the values."""
+    return moe_micro_config_t(int(rows), int(rows if src_rows is None else src_rows), int(K),
+                              _FORMATS[format], _dt(dtype), int(groups), int(copies), 0, int(ld))
+
+
+def moe_micro_scales_size(cfg: moe_micro_config_t) -> int:
+    return int(load_library().moe_micro_scales_size(ctypes.byref(cfg)))
+
+
+def alloc_micro(cfg: moe_micro_config_t, device="cuda"):
+    """(codes [rows][K/2], scales): the buffers that moe_micro_quantize fills."""
+    n = moe_micro_scales_size(cfg)
+    if n == 0:
+        raise MoEError(MOE_ERR_INVALID_ARG, "moe_micro_scales_size")
+    return (torch.zeros(cfg.rows, cfg.K // 2, dtype=torch.uint8, device=device),
+            torch.zeros(n, dtype=torch.uint8, device=device))
+
+
+def alloc_micro_workspace(cfg: moe_micro_config_t, device="cuda") -> torch.Tensor:
+    """The status word of moe_micro_quantize and moe_micro_dequantize; any workspace of this library's
+    products serves too."""
+    return torch.zeros(256, dtype=torch.uint8, device=device)
+
+
+def _scale_bytes(rows: int, K: int, groups: int, fmt: int) -> int:
+    """moe_micro_scales_size of a valid configuration."""
+    per = 64 if fmt == MOE_MICRO_NV else 128
+    return (rows // 128 + groups) * ((K + per - 1) // per) * 512
+
+
+def _micro_coded(cfg, codes, scales, offsets, factor):
+    if cfg.format != MOE_MICRO_NV and factor is not None:
+        raise ValueError('factor: the format "mx" has none')
+    n = _scale_bytes(cfg.rows, cfg.K, cfg.groups, cfg.format)
+    return (_vector(codes, cfg.rows * (cfg.K // 2), torch.uint8, "codes"),
+            _at_least(scales, n, torch.uint8, "scales"),
+            _at_least(offsets, cfg.groups + 1, torch.int32, "offsets"),
+            _vector(factor, 1, torch.float32, "factor"))
+
+
+def moe_micro_quantize(cfg: moe_micro_config_t, x, dest, offsets, factor, codes, scales, ws,
+                       stream=None):
+    """Rows of x to codes and scales.  dest: the coded rows that take each row of x ([src_rows][copies],
+    perm_dst of moe_permute), or None; offsets: the experts' rows, or None for `groups` equal groups."""
+    _one_device(stream, x, dest, offsets, factor, codes, scales, ws)
+    pc, ps, po, pf = _micro_coded(cfg, codes, scales, offsets, factor)
+    _check(load_library().moe_micro_quantize(
+        ctypes.byref(cfg),
+        _pitched(x, cfg.src_rows, cfg.K, cfg.ld, _DTYPES.get(cfg.dtype), "x"),
+        _vector(dest, cfg.src_rows * cfg.copies, torch.int32, "dest"), po, pf, pc, ps, _dev(ws),
+        ws.numel(), _stream(stream)), "moe_micro_quantize")
+
+
+def moe_micro_dequantize(cfg: moe_micro_config_t, codes, scales, offsets, factor, out, ws,
+                         stream=None):
+    """The values that codes and scales stand for."""
+    _one_device(stream, codes, scales, offsets, factor, out, ws)
+    pc, ps, po, pf = _micro_coded(cfg, codes, scales, offsets, factor)
+    _check(load_library().moe_micro_dequantize(
+        ctypes.byref(cfg), pc, ps, po, pf,
+        _pitched(out, cfg.rows, cfg.K, cfg.ld, _DTYPES.get(cfg.dtype), "out"), _dev(ws), ws.numel(),
+        _stream(stream)), "moe_micro_dequantize")
+
+
+def make_micro_product_config(rows: int, E: int, N: int, K: int, format: str = "mx",
+                              out_dtype: torch.dtype = torch.bfloat16, swiglu: bool = False,
+                              ld_out: int = 0) -> moe_micro_product_config_t:
+    return moe_micro_product_config_t(int(rows), int(E), int(N), int(K), _FORMATS[format],
+                                      _dt(out_dtype), MOE_MICRO_SWIGLU if swiglu else 0,
+                                      int(ld_out))
+
+
+def moe_micro_product_workspace_size(cfg: moe_micro_product_config_t) -> int:
+    return int(load_library().moe_micro_product_workspace_size(ctypes.byref(cfg)))
+
+
+def alloc_micro_product_workspace(cfg: moe_micro_product_config_t, device="cuda") -> torch.Tensor:
+    n = moe_micro_product_workspace_size(cfg)
+    if n == 0:
+        raise MoEError(MOE_ERR_INVALID_ARG, "moe_micro_product_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def moe_micro_product(cfg: moe_micro_product_config_t, offsets, a, a_scales, a_factor, w, w_scales,
+                      w_factor, out, ws, stream=None):
+    """The experts' product on microscaled operands, plain or with SwiGLU."""
+    R, E, N, K, fmt = cfg.rows, cfg.E, cfg.N, cfg.K, cfg.format
+    if fmt != MOE_MICRO_NV and (a_factor is not None or w_factor is not None):
+        raise ValueError('a_factor, w_factor: the format "mx" has none')
+    per = 2 * N if cfg.flags & MOE_MICRO_SWIGLU else N
+    u8, f32 = torch.uint8, torch.float32
+    _one_device(stream, offsets, a, a_scales, a_factor, w, w_scales, w_factor, out, ws)
+    _check(load_library().moe_micro_product(
+        ctypes.byref(cfg), _at_least(offsets, E + 1, torch.int32, "offsets"),
+        _vector(a, R * (K // 2), u8, "a"),
+        _at_least(a_scales, _scale_bytes(R, K, E, fmt), u8, "a_scales"),
+        _vector(a_factor, 1, f32, "a_factor"), _vector(w, E * per * (K // 2), u8, "w"),
+        _at_least(w_scales, _scale_bytes(E * per, K, E, fmt), u8, "w_scales"),
+        _vector(w_factor, E, f32, "w_factor"),
+        _pitched(out, R, N, cfg.ld_out, _DTYPES.get(cfg.out_dtype), "out"), _dev(ws), ws.numel(),
+        _stream(stream)), "moe_micro_product")
 
 
 def moe_forward_host_io(cfg, x_host, W_r, b, W13, W2, W13_scale, W2_scale, Ws13, Ws2,

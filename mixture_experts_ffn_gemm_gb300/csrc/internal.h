@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -255,6 +256,69 @@ cudaError_t launch_latent_combine(const void* y_perm, const int32_t* perm_dst,
 
 // SMs of the current device (cached per device).
 int num_sms();
+
+// TMA maps over matrices of el-byte elements (2: bf16, 1: bytes) with 128-byte swizzle, elements
+// outside read as zero: [rows][cols] with rows ld elements apart, and [depth][rows][cols] dense.
+// Boxes of box_cols x box_rows (x 1).  False when the driver refuses the map.
+bool make_map_2d(CUtensorMap* m, int el, const void* base, uint64_t cols, uint64_t rows, uint64_t ld,
+                 uint32_t box_cols, uint32_t box_rows);
+bool make_map_3d(CUtensorMap* m, int el, const void* base, uint64_t cols, uint64_t rows,
+                 uint64_t depth, uint32_t box_cols, uint32_t box_rows);
+// Allows `kern` `bytes` of dynamic shared memory on the current device, once a device (`done` holds
+// a bit for each device that has been set; the call is made every time on devices from 64 on).
+cudaError_t set_smem_once(const void* kern, int bytes, std::atomic<uint64_t>* done);
+
+// A product grouped by expert (grouped.cu): operands bf16, a = x or dy, b = W or x.
+struct GroupedProduct {
+  int kind = MOE_PRODUCT_FORWARD;
+  const int32_t* offsets = nullptr;  // device [E + 1]
+  int E = 0, N = 0, K = 0;
+  int64_t rows = 0;
+  const void* a = nullptr;
+  int64_t ld_a = 0;
+  const void* b = nullptr;
+  int64_t ld_b = 0;  // grad_w: x's pitch
+  void* out = nullptr;
+  int64_t ldo = 0;
+  int out_dtype = MOE_BF16;
+  bool accumulate = false;
+  uint32_t* err = nullptr;
+};
+cudaError_t launch_grouped_product(const GroupedProduct& g, int sms, cudaStream_t st);
+
+// Rows to microscaled 4-bit codes and scales, and back (micro_quant.cu).
+struct MicroOp {
+  const void* x = nullptr;  // quantise: [src_rows][ld]; dequantise: the values' buffer [rows][ld]
+  const int32_t* dest = nullptr;
+  const int32_t* offsets = nullptr;
+  const float* factor = nullptr;
+  uint8_t* codes = nullptr;
+  uint8_t* scales = nullptr;
+  uint32_t* err = nullptr;
+  int64_t ld = 0, src_rows = 0, rows = 0;
+  int K = 0, groups = 0, copies = 1, ktiles = 0, format = 0, dtype = MOE_BF16;
+};
+cudaError_t launch_micro_quantize(const MicroOp& m, int sms, cudaStream_t st);
+cudaError_t launch_micro_dequantize(const MicroOp& m, int sms, cudaStream_t st);
+
+// A product grouped by expert of microscaled 4-bit operands (micro_gemm.cu).
+struct MicroProduct {
+  const int32_t* offsets = nullptr;
+  int E = 0, N = 0, K = 0, format = 0;
+  int64_t rows = 0;
+  bool swiglu = false;
+  const uint8_t* a = nullptr;
+  const uint8_t* a_scales = nullptr;
+  const float* a_factor = nullptr;  // [1] or null
+  const uint8_t* w = nullptr;
+  const uint8_t* w_scales = nullptr;
+  const float* w_factor = nullptr;  // [E] or null
+  void* out = nullptr;
+  int64_t ldo = 0;
+  int out_dtype = MOE_BF16;
+  uint32_t* err = nullptr;
+};
+cudaError_t launch_micro_product(const MicroProduct& g, int sms, cudaStream_t st);
 
 // A failed CUDA call as a status: MOE_OK for cudaSuccess, else MOE_ERR_CUDA with the error's name
 // and text kept for moe_last_error_string() (per host thread).
