@@ -264,11 +264,13 @@ bool make_map_2d(CUtensorMap* m, int el, const void* base, uint64_t cols, uint64
                  uint32_t box_cols, uint32_t box_rows);
 bool make_map_3d(CUtensorMap* m, int el, const void* base, uint64_t cols, uint64_t rows,
                  uint64_t depth, uint32_t box_cols, uint32_t box_rows);
+// Over `tiles` dense 512-byte tiles, boxes of box_tiles whole ones at (0, tile), no swizzle.
+bool make_map_tiles(CUtensorMap* m, const void* base, uint64_t tiles, uint32_t box_tiles);
 // Allows `kern` `bytes` of dynamic shared memory on the current device, once a device (`done` holds
 // a bit for each device that has been set; the call is made every time on devices from 64 on).
 cudaError_t set_smem_once(const void* kern, int bytes, std::atomic<uint64_t>* done);
 
-// A product grouped by expert (grouped.cu): operands bf16, a = x or dy, b = W or x.
+// A product grouped by expert (product.cu): operands bf16, a = x or dy, b = W or x.
 struct GroupedProduct {
   int kind = MOE_PRODUCT_FORWARD;
   const int32_t* offsets = nullptr;  // device [E + 1]
@@ -301,7 +303,7 @@ struct MicroOp {
 cudaError_t launch_micro_quantize(const MicroOp& m, int sms, cudaStream_t st);
 cudaError_t launch_micro_dequantize(const MicroOp& m, int sms, cudaStream_t st);
 
-// A product grouped by expert of microscaled 4-bit operands (micro_gemm.cu).
+// A product grouped by expert of microscaled 4-bit operands (product.cu).
 struct MicroProduct {
   const int32_t* offsets = nullptr;
   int E = 0, N = 0, K = 0, format = 0;

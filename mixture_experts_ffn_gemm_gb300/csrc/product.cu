@@ -1,0 +1,594 @@
+// product.cu -- products grouped by expert with ragged sizes, on pairs of SMs (tcgen05 cta_group::2, fp32
+// sums in tensor memory), rows r of expert e from offsets[e] to offsets[e + 1]:
+//
+//   forward  y[r][n]    = sum_k x[r][k] W_e[n][k]        bf16
+//   grad_x   dx[r][k]   = sum_n dy[r][n] W_e[n][k]       bf16
+//   grad_w   dW_e[n][k] = sum_r dy[r][n] x[r][k]         bf16
+//   micro    out[r][n] = g_a g_w[e] sum_blocks S_a S_w sum_{k in block} c_a c_w      4-bit codes and
+//            their scales (MOE_MICRO_MX, MOE_MICRO_NV), plain or with SwiGLU
+//
+// Orientation: the MMA's M side is the weights (256 features a pair, 128 on each SM's lanes), the N side
+// the expert's rows, 32 to 256 of them as the tile has.  Rows are what is ragged: with them on the N side
+// a tile costs its rows rounded up to 32, where rows on the M side would be rounded up to 128 (at 170 rows
+// an expert a quarter of the work), and a decode step's few rows cost an MMA of N = 32.  A pair copies
+// 128 features and half of the tile's rows to each SM for an M = 256 product: two thirds of the bytes a
+// lone SM's 128 x 256 tile takes from L2, whose copies alone ran as long as its MMAs.
+//
+// An operand may lie either way in memory: grad_x sums over W's rows, and grad_w over the rows of x (its M
+// side) and dy (its N side), so those are "MN-major" boxes of 64 outputs (128 bytes) x 64 steps of the sum;
+// the instruction descriptor says which, and nothing is transposed in memory.  A stage holds 64 steps of
+// the sum in bf16, or 256 codes: 128 bytes of each row.
+//
+// Edges: the maps have the operands' true extents and fill with zeros behind them; W has the expert as
+// a third coordinate, so that rows behind W_e are zeros and not the next expert's.  grad_w's last block of
+// a group runs into the next group's rows: each SM's warp 1 overwrites those rows of both operands with
+// zeros in shared memory before the block is issued (zeros on one side alone would leave 0 x inf).
+//
+// Microscaled operands: the MMA takes 64 codes of a row and their scales from tensor memory (two e8m0 or
+// four e4m3 bytes a row) and multiplies each block's sum by both scales in fp32; nothing is decoded.  Scales
+// travel as they lie, in tiles of 128 rows x 4 columns: global to shared memory with the stage,
+// shared to tensor memory by tcgen05.cp ahead of the stage's MMAs, into two sets of columns in turn.
+// Row tiles start at multiples of 64 rows of their expert, so that a tile of at most 192 rows lies in two
+// scale tiles.  Scales of rows outside a group are whatever the buffer holds; they reach only outputs that
+// are not stored.
+//
+// SwiGLU: a W1 and a W3 tile of the same features against the same rows, two sums in tensor memory,
+// g and u of an output in one thread; their 2 x 192 columns leave no room for a second pair of sums, so the
+// epilogue is not hidden behind the next tile there, and its reads free the columns as early as they can.
+//
+// Kernel shape: persistent, warp 0 copies, warp 1 issues (on the pair's even SM), warps 2..9 store: a lane
+// has a feature, so that a warp's store covers 128 (fp32) or 2 x 64 (bf16) consecutive bytes of rows.
+#include <atomic>
+#include <cstring>
+
+#include "internal.h"
+#include "product.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kEpilogueWarps = 8;
+constexpr int kBox = 128 * 128;  // 128 features x 128 bytes
+constexpr int kBox64 = 64 * 128;
+constexpr int kBarBytes = 256;
+constexpr int kTable = (3 * (kProductMaxGroups + 1)) * 4 + kThreads * 4;
+constexpr int kSmemMost = 232448 - 1024 - kBarBytes - kTable;
+
+enum Op { OP_FORWARD, OP_GRAD_X, OP_GRAD_W, OP_MX, OP_NV };
+
+template <int kOp, bool kSwiGLU>
+struct Shape {
+  static constexpr bool kMicro = kOp == OP_MX || kOp == OP_NV;
+  static constexpr int kMaxRows = kMicro ? 192 : 256;      // rows of a tile
+  static constexpr int kBlock = kMicro ? 256 : 64;         // elements of the sum per stage
+  static constexpr int kStep = kMicro ? 64 : 16;           // and per MMA
+  static constexpr int kSums = kSwiGLU ? 2 : 1;            // W1 and W3, or one
+  static constexpr int kTiles = kOp == OP_NV ? 4 : kOp == OP_MX ? 2 : 0;  // scale tiles per 128 rows
+  static constexpr int kOpA = kSums * kBox;
+  static constexpr int kOpB = kMaxRows / 2 * 128;
+  static constexpr int kSfA = kTiles * 512;                // of one sum
+  static constexpr int kSfB = 2 * kTiles * 512;
+  static constexpr int kStage = kOpA + kOpB + kSums * kSfA + kSfB;
+  static constexpr int kFit = kSmemMost / kStage;
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
+  static constexpr int kSmem = 1024 + kStages * kStage + kBarBytes + kTable;
+  static constexpr int kAccs = kSwiGLU ? 1 : 2;            // tiles whose sums are in tensor memory
+  static constexpr int kAccCols = kSums * kMaxRows;
+  static constexpr int kSfCols = (kSums * 4 + 8) * kTiles; // columns of a stage's scales
+  static constexpr int kSfCol0 = kAccs * kAccCols;
+  static_assert(kSfCol0 + 2 * kSfCols <= 512, "tensor memory");
+  static_assert(kStage % 1024 == 0 && kStages >= 3 && (3 * kStages + 5) * 8 + 8 <= kBarBytes, "");
+};
+
+struct ProductParams {
+  CUtensorMap mw;        // weights
+  CUtensorMap mrow[8];   // rows, boxes of 16, 32, .. 128: one copy a stage whatever the tile's rows
+  CUtensorMap msw, msr;  // scale tiles of the weights and of the rows
+  const int32_t* offsets;
+  const float* a_factor;
+  const float* w_factor;
+  int32_t E, rows, F, Kc;  // F: features (outputs of a row), Kc: the sum's length (grad_w: N, its rows)
+  int32_t wrows, ktiles;   // micro: an expert's weight rows, scale tiles along K
+  void* out;
+  int64_t ldo;
+  uint32_t* err;
+};
+
+// Descriptor of an MN-major operand: boxes of 64 outputs (128 bytes) x 64 rows of the sum, 128-byte
+// swizzle; 8-row groups 1024 bytes apart (stride offset), boxes 8192 bytes apart (leading offset).
+__device__ __forceinline__ uint64_t mnmajor_desc(uint32_t smem_addr) {
+  return sw128_kmajor_desc(smem_addr) | (uint64_t)(kBox64 >> 4) << 16;
+}
+
+// Zeros in rows [from, to) of the boxes from `box0` on (each 64 rows of 128 bytes; the swizzle moves
+// 16-byte pieces within a row), for the tensor cores to read.  The whole warp.
+template <int kBoxes>
+__device__ __forceinline__ void clear_rows(uint8_t* box0, int from, int to, int lane) {
+  const int n = (to - from) * 8;
+#pragma unroll
+  for (int b = 0; b < kBoxes; ++b) {
+    uint4* r = reinterpret_cast<uint4*>(box0 + b * kBox64 + from * 128);
+    for (int i = lane; i < n; i += 32) r[i] = make_uint4(0, 0, 0, 0);
+  }
+  fence_async_smem();
+}
+
+// A 512-byte scale tile: 32 rows of 16 bytes without swizzle, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_tile_desc(uint32_t smem_addr) {
+  return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1 << 46;
+}
+// 32 lanes x 4 columns to each of the four lane quarters, in both SMs from their own shared memory.
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+// Block-scaled MMA, e2m1 operands, M = 256: bits [4,6) B's first scale byte, [7,10) and [10,13) formats
+// (1 = e2m1), [17,23) N >> 3, 23 scale type (1 = e8m0, 0 = e4m3), [24,29) M >> 4, [29,31) A's first byte.
+template <bool kNv>
+__device__ __forceinline__ uint32_t idesc_micro(int n, int first) {
+  return ((uint32_t)first << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) |
+         (kNv ? 0u : 1u << 23) | ((256u >> 4) << 24) | ((uint32_t)first << 29);
+}
+template <bool kNv>
+__device__ __forceinline__ void mma_micro_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if constexpr (kNv)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// g / (1 + exp(-g)).  The division is the approximate one (two steps of 2^-23); an exponential that
+// overflows gives 0.  fp32 outputs take the accurate exponential.
+template <bool kAccurate>
+__device__ __forceinline__ float silu(float g) {
+  return __fdividef(g, 1.0f + (kAccurate ? expf(-g) : __expf(-g)));
+}
+
+template <int kOp, bool kSwiGLU, bool kF32, bool kAdd>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ ProductParams p) {
+  using S = Shape<kOp, kSwiGLU>;
+  constexpr bool kMicro = S::kMicro, kNv = kOp == OP_NV, kGradW = kOp == OP_GRAD_W;
+  constexpr bool kAMn = kOp == OP_GRAD_X || kGradW, kBMn = kGradW;
+  constexpr int kStage = S::kStage, kStages = S::kStages, kMaxRows = S::kMaxRows;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int tile0 = (int)(blockIdx.x >> 1), tstep = (int)(gridDim.x >> 1);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStage);
+  uint64_t* empty = full + kStages;
+  uint64_t* cleared = empty + kStages;  // grad_w: the odd SM's rows of a last block are zeros
+  uint64_t* tfull = cleared + kStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  GroupTable tab;
+  tab.tile_start = reinterpret_cast<int*>(smem + kStages * kStage + kBarBytes);
+  tab.row0 = tab.tile_start + kProductMaxGroups + 1;
+  tab.nrows = tab.row0 + kProductMaxGroups + 1;
+  int* scratch = tab.nrows + kProductMaxGroups + 1;
+
+  const int warp = uniform(threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&cleared[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 2 * kEpilogueWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&p.mw);
+    tma_prefetch_map(&p.mrow[kMaxRows / 32 - 1]);
+    if (kMicro) {
+      tma_prefetch_map(&p.msw);
+      tma_prefetch_map(&p.msr);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_holder, 512);
+    tmem_relinquish_pair();
+  }
+  build_group_table<kMaxRows>(tab, scratch, p.offsets, p.E, p.rows,
+                              kGradW ? 0 : (p.F + 255) / 256,
+                              blockIdx.x == 0 ? p.err : nullptr);  // ends with __syncthreads
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both SMs' barriers exist before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  // grad_w: every expert has N in tiles of 256 "rows" and K in tiles of 256 features; its sum runs over the
+  // group's rows
+  const int fts = (p.F + 255) / 256, nts = (p.Kc + kMaxRows - 1) / kMaxRows;
+  const int total = kGradW ? p.E * nts * fts : tab.tile_start[p.E];
+  const auto tile_of = [&](int tile) {
+    if constexpr (!kGradW) return decode_product_tile<kMaxRows>(tile, tab, p.E);
+    ProductTile t;
+    t.g = tile / (nts * fts);
+    const int local = tile - t.g * (nts * fts);
+    t.ft = local / nts;
+    t.lrow0 = (local - t.ft * nts) * kMaxRows;
+    t.row0 = t.g * p.Kc + t.lrow0;
+    t.valid = min(kMaxRows, p.Kc - t.lrow0);
+    return t;
+  };
+  const auto sum_len = [&](const ProductTile& t) { return kGradW ? tab.nrows[t.g] : p.Kc; };
+  // a block of the sum with fewer rows than its last MMA reads is cleared behind them
+  const auto to_clear = [](int left) { return kGradW && left < S::kBlock && left % S::kStep; };
+  // micro: whether the tile's rows lie in two scale tiles
+  const auto two_scale_tiles = [](const ProductTile& t, int n) { return (t.lrow0 & 127) + n > 128; };
+  const auto mma_rows = [](const ProductTile& t) { return (t.valid + 31) & ~31; };
+
+  if (warp == 0) {
+    uint32_t stage = 0, phase = 0;
+    int armed = 0;
+    bool ok = true;
+    for (int tile = tile0; tile < total && ok; tile += tstep) {
+      const ProductTile t = tile_of(tile);
+      const int n = uniform(mma_rows(t)), len = uniform(sum_len(t)), g = uniform(t.g);
+      const int nkb = (len + S::kBlock - 1) / S::kBlock;
+      const int f0 = uniform(t.ft * 256 + (int)rank * 128);      // this SM's first feature
+      const int r0 = uniform(t.row0 + (int)rank * (n / 2));      // and row
+      const bool two = two_scale_tiles(t, n);
+      // bytes of a stage: MN-major rows come in whole boxes
+      const uint32_t bytes =
+          uniform(S::kOpA + (kBMn ? (n / 2 + 63) / 64 * kBox64 : n / 2 * 128) + S::kSums * S::kSfA +
+                  (two ? S::kSfB : S::kSfB / 2));
+      const int w0 = uniform(g * p.wrows);                       // micro: the expert's first weight row
+      const int st_w = uniform(((w0 >> 7) + g + (f0 >> 7)) * p.ktiles);
+      const int st_u = uniform(((w0 >> 7) + g + ((p.F + f0) >> 7)) * p.ktiles);  // its W3
+      const int st_r = uniform(((tab.row0[g] >> 7) + g + (t.lrow0 >> 7)) * p.ktiles);
+      const int gw_n = uniform(t.lrow0 + (int)rank * (n / 2)), gw_r = uniform(tab.row0[g]);
+      const CUtensorMap* mrow = &p.mrow[uniform(n / 32 - 1)];
+      for (int kb = 0; kb < nkb; ++kb) {
+        ok = __all_sync(~0u, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err));
+        if (!ok) break;
+        if (elect_one()) {
+          uint8_t* sa = smem + stage * kStage;
+          uint8_t* sb = sa + S::kOpA;
+          // Both SMs' copies complete on the even SM's barrier; of a block that is cleared, each SM's
+          // on its own, where the warp waits that clears it.
+          const bool own = to_clear(len - kb * S::kBlock);
+          const uint32_t bar = cluster_addr(&full[stage], own ? rank : 0u);
+          if (own || leader) mbar_arrive_expect_tx(&full[stage], own ? bytes : 2 * bytes);
+          const int kx = kb * (kMicro ? 128 : 64);  // bytes or elements: 128 bytes a row
+          if constexpr (kMicro) {
+            tma_load_2d_pair(sa, &p.mw, bar, kx, w0 + f0);
+            if (kSwiGLU) tma_load_2d_pair(sa + kBox, &p.mw, bar, kx, w0 + p.F + f0);
+          } else if constexpr (kGradW) {
+            const int y = gw_r + kx;
+            tma_load_2d_pair(sa, &p.mw, bar, f0, y);
+            tma_load_2d_pair(sa + kBox64, &p.mw, bar, f0 + 64, y);
+            for (int j = 0; j < n / 2; j += 64)
+              tma_load_2d_pair(sb + j * 128, &p.mrow[0], bar, gw_n + j, y);
+          } else if constexpr (kAMn) {
+            tma_load_3d_pair(sa, &p.mw, bar, f0, kx, g);
+            tma_load_3d_pair(sa + kBox64, &p.mw, bar, f0 + 64, kx, g);
+          } else {
+            tma_load_3d_pair(sa, &p.mw, bar, kx, f0, g);
+          }
+          if constexpr (!kBMn) tma_load_2d_pair(sb, mrow, bar, kx, r0);
+          if constexpr (kMicro) {
+            uint8_t* f = sb + S::kOpB;
+            const int kt = kb * S::kTiles;
+            tma_load_2d_pair(f, &p.msw, bar, 0, st_w + kt);
+            if (kSwiGLU) tma_load_2d_pair(f + S::kSfA, &p.msw, bar, 0, st_u + kt);
+            f += S::kSums * S::kSfA;
+            tma_load_2d_pair(f, &p.msr, bar, 0, st_r + kt);
+            if (two) tma_load_2d_pair(f + S::kSfB / 2, &p.msr, bar, 0, st_r + p.ktiles + kt);
+          }
+        }
+        __syncwarp();
+        if (armed < kStages) ++armed;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok && leader) {  // let the copies of the last stage uses land
+      for (int i = 0; i < armed; ++i) {
+        if (stage == 0) {
+          stage = kStages;
+          phase ^= 1u;
+        }
+        --stage;
+        mbar_wait(&full[stage], phase, nullptr, nullptr, kDrainLimitNs);
+      }
+    }
+  } else if (warp == 1 && leader) {
+    // the whole warp follows the stages (grad_w: it clears rows); lane 0 issues
+    uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, buf = 0, cleared_phase = 0;
+    bool ok = true;
+    for (int tile = tile0; tile < total && ok; tile += tstep) {
+      const ProductTile t = tile_of(tile);
+      const int n = uniform(mma_rows(t)), len = uniform(sum_len(t));
+      const int nkb = (len + S::kBlock - 1) / S::kBlock;
+      if (kGradW && nkb == 0) continue;  // a group without rows: the epilogue writes zeros
+      if (!__all_sync(~0u, mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, abort_flag, p.err))) break;
+      tc_fence_after();
+      const bool two = two_scale_tiles(t, n);
+      const uint32_t d = tmem_base + acc * S::kAccCols;
+      const uint32_t b_col = uniform((t.lrow0 & 127) >> 5);  // micro: the tile's first row's scale column
+      const uint32_t idesc = idesc_bf16_f32_pair(n) | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u);
+      for (int kb = 0; kb < nkb; ++kb) {
+        ok = __all_sync(~0u, mbar_wait(&full[stage], phase, abort_flag, p.err));
+        if (!ok) break;
+        const int left = min(S::kBlock, len - kb * S::kBlock);
+        const int steps = (left + S::kStep - 1) / S::kStep;
+        if (to_clear(left)) {
+          clear_rows<4>(smem + stage * kStage, left, steps * S::kStep, lane);
+          // and the odd SM has cleared its part
+          ok = __all_sync(~0u, mbar_wait_cluster(&cleared[stage], cleared_phase >> stage & 1u,
+                                                 abort_flag, p.err));
+          cleared_phase ^= 1u << stage;
+          if (!ok) break;
+          __syncwarp();
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t sa = smem_u32(smem + stage * kStage);
+          const uint32_t sb = sa + S::kOpA;
+          if constexpr (kMicro) {
+            const uint32_t fa = sb + S::kOpB, fb = fa + S::kSums * S::kSfA;
+            const uint32_t ta = tmem_base + S::kSfCol0 + buf * S::kSfCols;
+            const uint32_t tb = ta + S::kSums * 4 * S::kTiles;
+#pragma unroll
+            for (int i = 0; i < S::kTiles; ++i) {
+#pragma unroll
+              for (int m = 0; m < S::kSums; ++m)
+                copy_scales(ta + 4 * (m * S::kTiles + i), scale_tile_desc(fa + m * S::kSfA + i * 512));
+              copy_scales(tb + 8 * i, scale_tile_desc(fb + i * 512));
+              if (two) copy_scales(tb + 8 * i + 4, scale_tile_desc(fb + S::kSfB / 2 + i * 512));
+            }
+            const uint32_t b0 = tb + b_col;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              if (s == steps) break;
+              const int i = kNv ? s : s >> 1;  // scale tile, and first byte in its columns
+              const uint32_t id = idesc_micro<kNv>(n, kNv ? 0 : (s & 1) * 2);
+              const uint64_t bd = sw128_kmajor_desc(sb + s * 32);
+#pragma unroll
+              for (int m = 0; m < S::kSums; ++m)
+                mma_micro_pair<kNv>(d + m * kMaxRows, sw128_kmajor_desc(sa + m * kBox + s * 32), bd, id,
+                                    ta + 4 * (m * S::kTiles + i), b0 + 8 * i, (kb | s) != 0);
+            }
+          } else {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              if (s == steps) break;
+              mma_bf16_pair(d, kAMn ? mnmajor_desc(sa + s * 2048) : sw128_kmajor_desc(sa + s * 32),
+                            kBMn ? mnmajor_desc(sb + s * 2048) : sw128_kmajor_desc(sb + s * 32), idesc,
+                            (kb | s) != 0);
+            }
+          }
+          mma_commit_pair(&empty[stage]);  // frees the stage on both SMs
+        }
+        __syncwarp();
+        buf ^= 1u;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (elect_one()) mma_commit_pair(&tfull[acc]);
+      __syncwarp();
+      if (S::kAccs == 2) acc ^= 1u;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (lane == 0) {
+      mma_commit_pair_own(drain);  // every MMA issued above has completed once this arrives
+      mbar_wait(drain, 0, nullptr, nullptr, kDrainLimitNs);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // the odd SM, grad_w: clear this SM's rows of the blocks that need it
+    if constexpr (kGradW) {
+      uint32_t stage = 0, own_phase = 0;
+      bool ok = true;
+      for (int tile = tile0; tile < total && ok; tile += tstep) {
+        const int len = sum_len(tile_of(tile));
+        for (int at = 0; at < len; at += S::kBlock) {
+          const int left = min(S::kBlock, len - at);
+          if (to_clear(left)) {
+            ok = __all_sync(~0u, mbar_wait(&full[stage], own_phase >> stage & 1u, abort_flag, p.err));
+            own_phase ^= 1u << stage;
+            if (!ok) break;
+            clear_rows<4>(smem + stage * kStage, left, (left + S::kStep - 1) / S::kStep * S::kStep, lane);
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(&cleared[stage], 0));
+          }
+          if (++stage == kStages) stage = 0;
+        }
+      }
+    }
+  } else {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    uint32_t acc = 0, acc_phase = 0;
+    const float ga = kNv && p.a_factor ? __ldg(p.a_factor) : 1.0f;
+    for (int tile = tile0; tile < total; tile += tstep) {
+      const ProductTile t = tile_of(tile);
+      const int n = mma_rows(t);
+      const bool none = kGradW && sum_len(t) == 0;
+      const float alpha = kNv && p.w_factor ? ga * __ldg(p.w_factor + t.g) : ga;
+      if (!none && !__all_sync(~0u, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err))) break;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + acc * S::kAccCols + ((uint32_t)(quarter * 32) << 16);
+      const int feat0 = t.ft * 256 + (int)rank * 128 + quarter * 32;  // this warp's first feature
+      const int end = min(t.valid, half ? n : n / 2);                 // this warp's rows
+      if (feat0 < p.F && !(kAdd && none)) {
+#pragma unroll 1
+        for (int c = half * (n / 2); c < end; c += 16) {
+          uint32_t g[16];
+          float f[16];
+          tmem_ld16(tb + c, g);
+          if constexpr (kSwiGLU) {
+            uint32_t u[16];
+            tmem_ld16(tb + kMaxRows + c, u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              f[i] = silu<kF32>(alpha * __uint_as_float(g[i])) * (alpha * __uint_as_float(u[i]));
+          } else {
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              f[i] = kMicro ? alpha * __uint_as_float(g[i]) : __uint_as_float(g[i]);
+              if (none) f[i] = 0.0f;
+            }
+          }
+          const int64_t row = (int64_t)t.row0 + c;
+          if constexpr (kF32) {
+            float* dst = static_cast<float*>(p.out) + row * p.ldo + feat0 + lane;
+            if (feat0 + lane < p.F) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (c + i < t.valid) dst[i * p.ldo] = kAdd ? dst[i * p.ldo] + f[i] : f[i];
+            }
+          } else {
+            // lanes in twos: the even one takes both features of row i, the odd one those of row i + 1
+            const int odd = lane & 1;
+            __nv_bfloat16* dst =
+                static_cast<__nv_bfloat16*>(p.out) + (row + odd) * p.ldo + feat0 + (lane & ~1);
+            const bool in = feat0 + (lane & ~1) < p.F;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float got = __shfl_xor_sync(~0u, odd ? f[i] : f[i + 1], 1);
+              const uint32_t v = odd ? pack_bf16x2(got, f[i + 1]) : pack_bf16x2(f[i], got);
+              if (in && c + i + odd < t.valid) *reinterpret_cast<uint32_t*>(dst + i * p.ldo) = v;
+            }
+          }
+        }
+      }
+      if (none) continue;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[acc], 0));
+      if (S::kAccs == 2) acc ^= 1u;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no arrival at the peer and no MMA into its tensor memory from here on
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+template <int kOp, bool kSwiGLU, bool kF32, bool kAdd = false>
+cudaError_t launch(const ProductParams& p, int sms, cudaStream_t st, const char* label) {
+  using S = Shape<kOp, kSwiGLU>;
+  auto kern = product_kernel<kOp, kSwiGLU, kF32, kAdd>;
+  static std::atomic<uint64_t> set{0};  // devices whose attribute is set
+  const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), S::kSmem, &set);
+  if (e != cudaSuccess) return e;
+  LaunchScope ls(label, st);
+  return launch_pairs(kern, sms, kThreads, S::kSmem, st, p);
+}
+
+template <int kOp>
+cudaError_t launch_micro(const ProductParams& p, bool swiglu, bool f32, int sms, cudaStream_t st) {
+  if (swiglu)
+    return f32 ? launch<kOp, true, true>(p, sms, st, "micro_product_swiglu")
+               : launch<kOp, true, false>(p, sms, st, "micro_product_swiglu");
+  return f32 ? launch<kOp, false, true>(p, sms, st, "micro_product")
+             : launch<kOp, false, false>(p, sms, st, "micro_product");
+}
+
+}  // namespace
+
+static bool make_row_maps(CUtensorMap* m, int count, int el, const void* base, uint64_t cols,
+                          uint64_t rows, uint64_t ld, uint32_t box_cols) {
+  for (int i = 0; i < count; ++i)
+    if (!make_map_2d(&m[i], el, base, cols, rows, ld, box_cols, 16 * (i + 1))) return false;
+  return true;
+}
+
+cudaError_t launch_grouped_product(const GroupedProduct& g, int sms, cudaStream_t st) {
+  ProductParams p;
+  memset(&p, 0, sizeof p);
+  const bool fwd = g.kind == MOE_PRODUCT_FORWARD, grad_w = g.kind == MOE_PRODUCT_GRAD_W;
+  p.F = fwd ? g.N : g.K;
+  p.Kc = fwd ? g.K : g.N;
+  if (grad_w) {  // x on the feature side, dy on the other
+    if (!make_map_2d(&p.mw, 2, g.b, g.K, g.rows, g.ld_b, 64, 64) ||
+        !make_map_2d(&p.mrow[0], 2, g.a, g.N, g.rows, g.ld_a, 64, 64))
+      return cudaErrorInvalidValue;
+  } else if (!make_map_3d(&p.mw, 2, g.b, g.K, g.N, g.E, 64, fwd ? 128 : 64) ||
+             !make_row_maps(p.mrow, 8, 2, g.a, p.Kc, g.rows, g.ld_a, 64))
+    return cudaErrorInvalidValue;
+  p.offsets = g.offsets;
+  p.E = g.E;
+  p.rows = (int32_t)g.rows;
+  p.out = g.out;
+  p.ldo = g.ldo;
+  p.err = g.err;
+  const bool f32 = g.out_dtype == MOE_F32;
+  if (grad_w) {
+    if (g.accumulate) return launch<OP_GRAD_W, false, true, true>(p, sms, st, "grouped_grad_w");
+    return f32 ? launch<OP_GRAD_W, false, true>(p, sms, st, "grouped_grad_w")
+               : launch<OP_GRAD_W, false, false>(p, sms, st, "grouped_grad_w");
+  }
+  if (fwd)
+    return f32 ? launch<OP_FORWARD, false, true>(p, sms, st, "grouped_forward")
+               : launch<OP_FORWARD, false, false>(p, sms, st, "grouped_forward");
+  return f32 ? launch<OP_GRAD_X, false, true>(p, sms, st, "grouped_grad_x")
+             : launch<OP_GRAD_X, false, false>(p, sms, st, "grouped_grad_x");
+}
+
+cudaError_t launch_micro_product(const MicroProduct& g, int sms, cudaStream_t st) {
+  ProductParams p;
+  memset(&p, 0, sizeof p);
+  const bool nv = g.format == MOE_MICRO_NV;
+  p.wrows = g.swiglu ? 2 * g.N : g.N;
+  const int per = nv ? 64 : 128;  // channels of a scale tile
+  p.ktiles = (g.K + per - 1) / per;
+  const uint64_t half = (uint64_t)g.K / 2, wrows = (uint64_t)g.E * p.wrows;
+  const uint32_t tiles = nv ? Shape<OP_NV, false>::kTiles : Shape<OP_MX, false>::kTiles;
+  if (!make_map_2d(&p.mw, 1, g.w, half, wrows, half, 128, 128) ||
+      !make_row_maps(p.mrow, Shape<OP_MX, false>::kMaxRows / 32, 1, g.a, half, g.rows, half, 128) ||
+      !make_map_tiles(&p.msw, g.w_scales, (wrows / 128 + g.E) * p.ktiles, tiles) ||
+      !make_map_tiles(&p.msr, g.a_scales, ((uint64_t)g.rows / 128 + g.E) * p.ktiles, tiles))
+    return cudaErrorInvalidValue;
+  p.offsets = g.offsets;
+  p.a_factor = g.a_factor;
+  p.w_factor = g.w_factor;
+  p.E = g.E;
+  p.rows = (int32_t)g.rows;
+  p.F = g.N;
+  p.Kc = g.K;
+  p.out = g.out;
+  p.ldo = g.ldo;
+  p.err = g.err;
+  const bool f32 = g.out_dtype == MOE_F32;
+  return nv ? launch_micro<OP_NV>(p, g.swiglu, f32, sms, st)
+            : launch_micro<OP_MX>(p, g.swiglu, f32, sms, st);
+}
+
+}  // namespace moe

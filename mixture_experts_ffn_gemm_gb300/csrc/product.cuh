@@ -1,6 +1,5 @@
-// product.cuh -- device helpers shared by the products grouped by expert (grouped.cu: bf16,
-// micro_gemm.cu: microscaled 4-bit operands): the tile table over ragged groups, copies, and the
-// stores of an output chunk.
+// product.cuh -- helpers of the products grouped by expert (product.cu): the tile table over ragged groups,
+// copies and commits of a pair of SMs, the launch in pairs.
 #pragma once
 
 #include "common.cuh"
@@ -18,9 +17,19 @@ struct GroupTable {
   int* nrows;       // [G]     rows
 };
 
-// Block-wide (blockDim.x threads, scratch of as many ints); ends with __syncthreads().
+// Rows of each of a group's row tiles: as few tiles as hold `rows` in at most kMaxRows each, of about the
+// same size, cut at multiples of 64 rows.
+template <int kMaxRows>
+__device__ __forceinline__ int tile_rows(int rows) {
+  const int n = (rows + kMaxRows - 1) / kMaxRows;
+  return ((rows + n - 1) / n + 63) & ~63;
+}
+
+// Block-wide (blockDim.x threads, scratch of as many ints); ends with __syncthreads().  A group has
+// feat_tiles tiles for each of its row tiles.
+template <int kMaxRows>
 __device__ __forceinline__ void build_group_table(const GroupTable& t, int* scratch,
-                                                  const int32_t* offsets, int G, int rows, int rpt,
+                                                  const int32_t* offsets, int G, int rows,
                                                   int feat_tiles, uint32_t* err) {
   const int nt = blockDim.x;
   const int per = (G + nt - 1) / nt;
@@ -34,7 +43,7 @@ __device__ __forceinline__ void build_group_table(const GroupTable& t, int* scra
     if (a2 != a || z2 != z) raise_flag(err, kErrIndex);
     t.row0[g] = a2;
     t.nrows[g] = z2 - a2;
-    const int n = (z2 - a2 + rpt - 1) / rpt * feat_tiles;
+    const int n = (z2 - a2 + kMaxRows - 1) / kMaxRows * feat_tiles;
     t.tile_start[g] = n;  // count for now
     local += n;
   }
@@ -59,15 +68,15 @@ __device__ __forceinline__ void build_group_table(const GroupTable& t, int* scra
 struct ProductTile {
   int g;      // group
   int row0;   // first row of the tile
-  int valid;  // rows of the tile inside the group, 1..rpt
+  int valid;  // rows of the tile inside the group, 1..kMaxRows
   int ft;     // feature tile
   int lrow0;  // row0 within the group
 };
 
 // A group's tiles are numbered feature tile by feature tile, the row tiles inside: neighbouring CTAs
 // share one weight tile, and the weights stream from memory once.
-__device__ __forceinline__ ProductTile decode_product_tile(int tile, const GroupTable& t, int G,
-                                                           int rpt) {
+template <int kMaxRows>
+__device__ __forceinline__ ProductTile decode_product_tile(int tile, const GroupTable& t, int G) {
   int lo = 0, hi = G - 1;  // largest g with tile_start[g] <= tile (empty groups share starts)
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -77,7 +86,7 @@ __device__ __forceinline__ ProductTile decode_product_tile(int tile, const Group
       hi = mid - 1;
   }
   const int rows = t.nrows[lo];
-  const int nrt = (rows + rpt - 1) / rpt;
+  const int nrt = (rows + kMaxRows - 1) / kMaxRows, rpt = tile_rows<kMaxRows>(rows);
   const int local = tile - t.tile_start[lo];
   ProductTile p;
   p.g = lo;
@@ -88,12 +97,36 @@ __device__ __forceinline__ ProductTile decode_product_tile(int tile, const Group
   return p;
 }
 
-__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
-                                            int32_t x, int32_t y, int32_t z) {
+// One thread of the (converged) warp.  The compiler knows that the branch holds a single thread, and keeps
+// what tcgen05 and TMA instructions take from uniform registers there; after `lane == 0` it moves every
+// operand into them, one by one, for each instruction.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
+
+// The same value in every lane, as the compiler is to see it.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(~0u, v, 0); }
+
+// TMA copy of a 3D box into this CTA's shared memory of a pair, completion counted on the barrier at
+// shared::cluster address `bar_cluster`.
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map,
+                                                 uint32_t bar_cluster, int32_t x, int32_t y,
+                                                 int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Arrive once on this CTA's `bar` alone when every pair MMA this thread issued before has completed.
+__device__ __forceinline__ void mma_commit_pair_own(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
       : "memory");
 }
 
@@ -102,35 +135,23 @@ __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// One epilogue warp writes a chunk of 32 rows x 128 bytes, lane l holding row l's bytes in v: through
-// a 4 KB buffer (16-byte pieces XOR-swizzled by row % 8, no bank conflicts either way), so that a store
-// instruction covers four whole 128-byte rows.  Rows from `rows` on and 16-byte pieces from `pieces`
-// on are not written.  kAdd: fp32 values are added onto what is there.
-template <bool kAdd>
-__device__ __forceinline__ void store_chunk(uint8_t* buf, int lane, const uint4 (&v)[8], uint8_t* row0,
-                                            int64_t pitch, int rows, int pieces) {
-  __syncwarp();  // the previous chunk has been read back
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) = v[j];
-  __syncwarp();
-  const int j = lane & 7;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = i * 4 + (lane >> 3);
-    uint4 w = *reinterpret_cast<const uint4*>(buf + r * 128 + ((j ^ (r & 7)) << 4));
-    if (r < rows && j < pieces) {
-      uint4* dst = reinterpret_cast<uint4*>(row0 + r * pitch + j * 16);
-      if (kAdd) {
-        const uint4 o = *dst;
-        w.x = __float_as_uint(__uint_as_float(w.x) + __uint_as_float(o.x));
-        w.y = __float_as_uint(__uint_as_float(w.y) + __uint_as_float(o.y));
-        w.z = __float_as_uint(__uint_as_float(w.z) + __uint_as_float(o.z));
-        w.w = __float_as_uint(__uint_as_float(w.w) + __uint_as_float(o.w));
-      }
-      *dst = w;
-    }
-  }
+// Launch of a kernel whose CTAs work in pairs (clusters of two), one CTA per SM.
+template <typename Kernel, typename Params>
+inline cudaError_t launch_pairs(Kernel kern, int sms, int threads, int smem, cudaStream_t st,
+                                const Params& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(sms & ~1));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace moe

@@ -1,5 +1,6 @@
 // product_api.cu -- the C ABI of the products grouped by expert and of the microscaled 4-bit operators:
 // host validation, tensor maps, launches.  No allocation and no host synchronisation.
+#include <cstdint>
 #include <mutex>
 
 #include "internal.h"
@@ -94,6 +95,10 @@ moe_status_t validate(const moe_micro_product_config_t* c) {
   if (c->rows > kMaxRows || c->E > kMaxGroups || c->N > kMaxWidth || c->K > kMaxWidth || c->N % 8 ||
       c->K % 64 || ((c->flags & MOE_MICRO_SWIGLU) && c->N % 128))
     return MOE_ERR_UNSUPPORTED;
+  // scale tiles are counted in 31 bits
+  const int64_t kt = (c->K + 63) / 64, per = (int64_t)c->N * (c->flags & MOE_MICRO_SWIGLU ? 2 : 1);
+  if ((c->E * per / 128 + c->E) * kt > INT32_MAX || (c->rows / 128 + c->E) * kt > INT32_MAX)
+    return MOE_ERR_UNSUPPORTED;
   if (pitch(c->ld_out, c->N) < 0) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
@@ -127,6 +132,16 @@ bool make_map_3d(CUtensorMap* m, int el, const void* base, uint64_t cols, uint64
   const cuuint64_t dims[3] = {cols, rows, depth}, strides[2] = {cols * el, cols * rows * el};
   const cuuint32_t box[3] = {box_cols, box_rows, 1};
   return make_map(m, el, base, 3, dims, strides, box);
+}
+
+bool make_map_tiles(CUtensorMap* m, const void* base, uint64_t tiles, uint32_t box_tiles) {
+  EncodeTiled enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {128, tiles}, strides[1] = {512};
+  const cuuint32_t box[2] = {128, box_tiles}, ones[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t set_smem_once(const void* kern, int bytes, std::atomic<uint64_t>* done) {

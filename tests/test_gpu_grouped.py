@@ -95,7 +95,8 @@ def test_ragged_groups(cuda_device, kind, N, K, dtype):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("counts", [[1], [64], [65], [1000], [0, 0, 5], [256] * 3, [3] * 40, [1024, 1500]])
+@pytest.mark.parametrize("counts", [[1], [64], [65], [1000], [0, 0, 5], [256] * 3, [3] * 40, [1024, 1500],
+                                    [0, 300, 1, 1000, 64, 777, 0, 513], [129, 128], [255, 257, 1]])
 def test_group_sizes(cuda_device, kind, counts):
     N, K = 384, 320
     offs, R, a, b = _make(kind, counts, N, K, seed=1)
@@ -115,11 +116,12 @@ def test_rows_inside_wider_buffers(cuda_device, kind, pad):
         assert (whole[:, out.shape[1]:] == 7.0).all()
 
 
+@pytest.mark.parametrize("counts", [[37, 50, 0, 21], [337, 150, 0, 421]])
 @pytest.mark.parametrize("kind", KINDS)
-def test_rows_of_no_expert_and_values_of_others_do_not_reach_a_result(cuda_device, kind):
+def test_rows_of_no_expert_and_values_of_others_do_not_reach_a_result(cuda_device, kind, counts):
     """Rows in front of, between and behind: expert 1's operands and the rows behind the last expert hold
     NaN and infinities; every other expert's results are what they are without."""
-    N, K, counts = 72, 200, [37, 50, 0, 21]
+    N, K = 72, 200
     offs, R, a, b = _make(kind, counts, N, K, behind=70, seed=3)
     parts = _reference(kind, offs, a, b, N, K)
     a, b = a.clone(), b.clone()
@@ -184,10 +186,11 @@ def test_bad_offsets_stay_inside_the_buffers(cuda_device, kind, bad):
     assert B.moe_device_status(ws) == B.MOE_OK
 
 
+@pytest.mark.parametrize("counts", [RAGGED, [0, 300, 1, 1000, 64, 777, 0, 513]])
 @pytest.mark.parametrize("kind", KINDS)
-def test_equal_calls_give_equal_bits_in_a_graph_and_on_another_stream(cuda_device, kind):
+def test_equal_calls_give_equal_bits_in_a_graph_and_on_another_stream(cuda_device, kind, counts):
     N, K = 264, 520
-    offs, R, a, b = _make(kind, RAGGED, N, K, seed=6)
+    offs, R, a, b = _make(kind, counts, N, K, seed=6)
     first = _call(kind, offs, R, a, b, N, K, BF16)
     E = len(offs) - 1
     cfg = _config(kind, R, E, N, K, BF16)
