@@ -14,8 +14,8 @@
 // 128 features and half of the tile's rows to each SM for an M = 256 product: two thirds of the bytes a
 // lone SM's 128 x 256 tile takes from L2, whose copies alone ran as long as its MMAs.
 //
-// An operand may lie either way in memory: grad_x sums over W's rows, and grad_w over the rows of x (its M
-// side) and dy (its N side), so those are "MN-major" boxes of 64 outputs (128 bytes) x 64 steps of the sum;
+// An operand may lie either way in memory: grad_x sums over W's rows, and grad_w over the rows of dy (its M
+// side) and x (its N side), so those are "MN-major" boxes of 64 outputs (128 bytes) x 64 steps of the sum;
 // the instruction descriptor says which, and nothing is transposed in memory.  A stage holds 64 steps of
 // the sum in bf16, or 256 codes: 128 bytes of each row.
 //
@@ -37,7 +37,8 @@
 // epilogue is not hidden behind the next tile there, and its reads free the columns as early as they can.
 //
 // Kernel shape: persistent, warp 0 copies, warp 1 issues (on the pair's even SM), warps 2..9 store: a lane
-// has a feature, so that a warp's store covers 128 (fp32) or 2 x 64 (bf16) consecutive bytes of rows.
+// has a feature, so that a warp's store covers 128 (fp32) or 2 x 64 (bf16) consecutive bytes of rows.  dW
+// leaves through shared memory and TMA (for ACCUMULATE its fp32 addition, one for each element).
 #include <atomic>
 #include <cstring>
 
@@ -71,9 +72,10 @@ struct Shape {
   static constexpr int kSfA = kTiles * 512;                // of one sum
   static constexpr int kSfB = 2 * kTiles * 512;
   static constexpr int kStage = kOpA + kOpB + kSums * kSfA + kSfB;
-  static constexpr int kFit = kSmemMost / kStage;
+  static constexpr int kStaging = kOp == OP_GRAD_W ? kEpilogueWarps * 4096 : 0;
+  static constexpr int kFit = (kSmemMost - kStaging) / kStage;
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
-  static constexpr int kSmem = 1024 + kStages * kStage + kBarBytes + kTable;
+  static constexpr int kSmem = 1024 + kStages * kStage + kStaging + kBarBytes + kTable;
   static constexpr int kAccs = kSwiGLU ? 1 : 2;            // tiles whose sums are in tensor memory
   static constexpr int kAccCols = kSums * kMaxRows;
   static constexpr int kSfCols = (kSums * 4 + 8) * kTiles; // columns of a stage's scales
@@ -86,10 +88,11 @@ struct ProductParams {
   CUtensorMap mw;        // weights
   CUtensorMap mrow[8];   // rows, boxes of 16, 32, .. 128: one copy a stage whatever the tile's rows
   CUtensorMap msw, msr;  // scale tiles of the weights and of the rows
+  CUtensorMap mout;      // grad_w: dW, boxes of 32 rows x 128 bytes
   const int32_t* offsets;
   const float* a_factor;
   const float* w_factor;
-  int32_t E, rows, F, Kc;  // F: features (outputs of a row), Kc: the sum's length (grad_w: N, its rows)
+  int32_t E, rows, F, Kc;  // F: features (outputs of a row), Kc: the sum's length (grad_w: N and K)
   int32_t wrows, ktiles;   // micro: an expert's weight rows, scale tiles along K
   void* out;
   int64_t ldo;
@@ -170,7 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStage);
+  uint8_t* staging = smem + kStages * kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + S::kStaging);
   uint64_t* empty = full + kStages;
   uint64_t* cleared = empty + kStages;  // grad_w: the odd SM's rows of a last block are zeros
   uint64_t* tfull = cleared + kStages;
@@ -179,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   GroupTable tab;
-  tab.tile_start = reinterpret_cast<int*>(smem + kStages * kStage + kBarBytes);
+  tab.tile_start = reinterpret_cast<int*>(staging + S::kStaging + kBarBytes);
   tab.row0 = tab.tile_start + kProductMaxGroups + 1;
   tab.nrows = tab.row0 + kProductMaxGroups + 1;
   int* scratch = tab.nrows + kProductMaxGroups + 1;
@@ -220,8 +224,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();  // both SMs' barriers exist before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  // grad_w: every expert has N in tiles of 256 "rows" and K in tiles of 256 features; its sum runs over the
-  // group's rows
+  // grad_w: the features are dW's rows, and in the place of rows there are its columns, 256 to a tile; the
+  // sum runs over the group's rows
   const int fts = (p.F + 255) / 256, nts = (p.Kc + kMaxRows - 1) / kMaxRows;
   const int total = kGradW ? p.E * nts * fts : tab.tile_start[p.E];
   const auto tile_of = [&](int tile) {
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int local = tile - t.g * (nts * fts);
     t.ft = local / nts;
     t.lrow0 = (local - t.ft * nts) * kMaxRows;
-    t.row0 = t.g * p.Kc + t.lrow0;
+    t.row0 = 0;
     t.valid = min(kMaxRows, p.Kc - t.lrow0);
     return t;
   };
@@ -440,7 +444,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tb = tmem_base + acc * S::kAccCols + ((uint32_t)(quarter * 32) << 16);
       const int feat0 = t.ft * 256 + (int)rank * 128 + quarter * 32;  // this warp's first feature
       const int end = min(t.valid, half ? n : n / 2);                 // this warp's rows
-      if (feat0 < p.F && !(kAdd && none)) {
+      if constexpr (kGradW) {
+        // a lane has a row of dW: chunks of 32 rows x 128 bytes through shared memory (in the 128-byte
+        // swizzle) to TMA, which leaves out what lies behind dW's last row or column
+        constexpr int kCols = kF32 ? 32 : 64;
+        uint8_t* buf = staging + (warp - 2) * 4096;
+        if (feat0 < p.F && !(kAdd && none)) {
+#pragma unroll 1
+          for (int c = half * kCols; c < t.valid; c += 2 * kCols) {
+            uint4 v[8];
+#pragma unroll
+            for (int h = 0; h < kCols / 16; ++h) {
+              uint32_t g[16];
+              tmem_ld16(tb + c + 16 * h, g);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) g[i] = none ? 0u : g[i];
+              if constexpr (kF32) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  v[4 * h + q] = make_uint4(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]);
+              } else {
+                uint32_t k[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  k[i] = pack_bf16x2(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
+                v[2 * h] = make_uint4(k[0], k[1], k[2], k[3]);
+                v[2 * h + 1] = make_uint4(k[4], k[5], k[6], k[7]);
+              }
+            }
+            if (lane == 0) tma_store_wait_read();  // the previous chunk has left the buffer
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) = v[j];
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) tma_store_3d<kAdd>(&p.mout, buf, t.lrow0 + c, feat0, t.g);
+          }
+        }
+      } else if (feat0 < p.F) {
 #pragma unroll 1
         for (int c = half * (n / 2); c < end; c += 16) {
           uint32_t g[16];
@@ -458,7 +501,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               f[i] = kMicro ? alpha * __uint_as_float(g[i]) : __uint_as_float(g[i]);
-              if (none) f[i] = 0.0f;
             }
           }
           const int64_t row = (int64_t)t.row0 + c;
@@ -467,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (feat0 + lane < p.F) {
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                if (c + i < t.valid) dst[i * p.ldo] = kAdd ? dst[i * p.ldo] + f[i] : f[i];
+                if (c + i < t.valid) dst[i * p.ldo] = f[i];
             }
           } else {
             // lanes in twos: the even one takes both features of row i, the odd one those of row i + 1
@@ -491,6 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (S::kAccs == 2) acc ^= 1u;
       if (acc == 0) acc_phase ^= 1u;
     }
+    if (kGradW && lane == 0) tma_store_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -534,11 +577,13 @@ cudaError_t launch_grouped_product(const GroupedProduct& g, int sms, cudaStream_
   ProductParams p;
   memset(&p, 0, sizeof p);
   const bool fwd = g.kind == MOE_PRODUCT_FORWARD, grad_w = g.kind == MOE_PRODUCT_GRAD_W;
-  p.F = fwd ? g.N : g.K;
-  p.Kc = fwd ? g.K : g.N;
-  if (grad_w) {  // x on the feature side, dy on the other
-    if (!make_map_2d(&p.mw, 2, g.b, g.K, g.rows, g.ld_b, 64, 64) ||
-        !make_map_2d(&p.mrow[0], 2, g.a, g.N, g.rows, g.ld_a, 64, 64))
+  p.F = fwd || grad_w ? g.N : g.K;
+  p.Kc = fwd || grad_w ? g.K : g.N;
+  if (grad_w) {  // dy on the feature side, x on the other
+    const int el = g.out_dtype == MOE_F32 ? 4 : 2;
+    if (!make_map_2d(&p.mw, 2, g.a, g.N, g.rows, g.ld_a, 64, 64) ||
+        !make_map_2d(&p.mrow[0], 2, g.b, g.K, g.rows, g.ld_b, 64, 64) ||
+        !make_map_3d(&p.mout, el, g.out, g.K, g.N, g.E, 128 / el, 32))
       return cudaErrorInvalidValue;
   } else if (!make_map_3d(&p.mw, 2, g.b, g.K, g.N, g.E, 64, fwd ? 128 : 64) ||
              !make_row_maps(p.mrow, 8, 2, g.a, p.Kc, g.rows, g.ld_a, 64))

@@ -33,7 +33,10 @@ bool make_map(CUtensorMap* m, int el, const void* base, int rank, const cuuint64
   EncodeTiled enc = encoder();
   if (!enc) return false;
   const cuuint32_t ones[3] = {1, 1, 1};
-  return enc(m, el == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+  return enc(m,
+             el == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+             : el == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                       : CU_TENSOR_MAP_DATA_TYPE_UINT8,
              (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
