@@ -257,8 +257,8 @@ cudaError_t launch_latent_combine(const void* y_perm, const int32_t* perm_dst,
 // SMs of the current device (cached per device).
 int num_sms();
 
-// TMA maps over matrices of el-byte elements (4: fp32, 2: bf16, 1: bytes) with 128-byte swizzle, elements
-// outside read as zero: [rows][cols] with rows ld elements apart, and [depth][rows][cols] dense.
+// TMA maps over matrices of el-byte elements (4: fp32, 2: bf16, 1: bytes), with the swizzle of their boxes'
+// width (128 or 64 bytes), elements outside read as zero: [rows][cols] with rows ld elements apart, and [depth][rows][cols] dense.
 // Boxes of box_cols x box_rows (x 1).  False when the driver refuses the map.
 bool make_map_2d(CUtensorMap* m, int el, const void* base, uint64_t cols, uint64_t rows, uint64_t ld,
                  uint32_t box_cols, uint32_t box_rows);

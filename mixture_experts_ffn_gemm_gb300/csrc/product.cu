@@ -49,12 +49,12 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 320;
 constexpr int kEpilogueWarps = 8;
+constexpr int kMaxThreads = 32 * (2 + kEpilogueWarps + 1);
 constexpr int kBox = 128 * 128;  // 128 features x 128 bytes
 constexpr int kBox64 = 64 * 128;
 constexpr int kBarBytes = 256;
-constexpr int kTable = (3 * (kProductMaxGroups + 1)) * 4 + kThreads * 4;
+constexpr int kTable = (3 * (kProductMaxGroups + 1)) * 4 + kMaxThreads * 4;
 constexpr int kSmemMost = 232448 - 1024 - kBarBytes - kTable;
 
 enum Op { OP_FORWARD, OP_GRAD_X, OP_GRAD_W, OP_MX, OP_NV };
@@ -72,7 +72,8 @@ struct Shape {
   static constexpr int kSfA = kTiles * 512;                // of one sum
   static constexpr int kSfB = 2 * kTiles * 512;
   static constexpr int kStage = kOpA + kOpB + kSums * kSfA + kSfB;
-  static constexpr int kStaging = kOp == OP_GRAD_W ? kEpilogueWarps * 4096 : 0;
+  static constexpr int kThreads = 32 * (2 + kEpilogueWarps + (kOp == OP_GRAD_W ? 1 : 0));
+  static constexpr int kStaging = kOp == OP_GRAD_W ? kEpilogueWarps * 2048 : 0;
   static constexpr int kFit = (kSmemMost - kStaging) / kStage;
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kSmem = 1024 + kStages * kStage + kStaging + kBarBytes + kTable;
@@ -81,14 +82,14 @@ struct Shape {
   static constexpr int kSfCols = (kSums * 4 + 8) * kTiles; // columns of a stage's scales
   static constexpr int kSfCol0 = kAccs * kAccCols;
   static_assert(kSfCol0 + 2 * kSfCols <= 512, "tensor memory");
-  static_assert(kStage % 1024 == 0 && kStages >= 3 && (3 * kStages + 5) * 8 + 8 <= kBarBytes, "");
+  static_assert(kStage % 1024 == 0 && kStages >= 3 && (4 * kStages + 5) * 8 + 8 <= kBarBytes, "");
 };
 
 struct ProductParams {
   CUtensorMap mw;        // weights
   CUtensorMap mrow[8];   // rows, boxes of 16, 32, .. 128: one copy a stage whatever the tile's rows
   CUtensorMap msw, msr;  // scale tiles of the weights and of the rows
-  CUtensorMap mout;      // grad_w: dW, boxes of 32 rows x 128 bytes
+  CUtensorMap mout;      // grad_w: dW, boxes of 32 rows x 64 bytes
   const int32_t* offsets;
   const float* a_factor;
   const float* w_factor;
@@ -161,7 +162,7 @@ __device__ __forceinline__ float silu(float g) {
 }
 
 template <int kOp, bool kSwiGLU, bool kF32, bool kAdd>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<kOp, kSwiGLU>::kThreads, 1)
     product_kernel(const __grid_constant__ ProductParams p) {
   using S = Shape<kOp, kSwiGLU>;
   constexpr bool kMicro = S::kMicro, kNv = kOp == OP_NV, kGradW = kOp == OP_GRAD_W;
@@ -176,7 +177,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* staging = smem + kStages * kStage;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + S::kStaging);
   uint64_t* empty = full + kStages;
-  uint64_t* cleared = empty + kStages;  // grad_w: the odd SM's rows of a last block are zeros
+  // grad_w, blocks that are cleared: this SM's copies have landed; both SMs' rows behind the group are zeros
+  uint64_t* landed = empty + kStages;
+  uint64_t* cleared = landed + kStages;
   uint64_t* tfull = cleared + kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
@@ -194,7 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&cleared[s], 1);
+      mbar_init(&landed[s], 1);
+      mbar_init(&cleared[s], 2);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
@@ -240,14 +244,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     return t;
   };
   const auto sum_len = [&](const ProductTile& t) { return kGradW ? tab.nrows[t.g] : p.Kc; };
-  // a block of the sum with fewer rows than its last MMA reads is cleared behind them
-  const auto to_clear = [](int left) { return kGradW && left < S::kBlock && left % S::kStep; };
+  // grad_w takes the sum's last, shorter block first, so that it is cleared while the MMAs of the tile before
+  // still run.  Steps of the sum in block kb, where it starts, and whether rows behind it are read and so
+  // cleared.
+  const auto block_len = [](int len, int kb) {
+    return kGradW ? (kb ? S::kBlock : len - (len - 1) / S::kBlock * S::kBlock)
+                  : min(S::kBlock, len - kb * S::kBlock);
+  };
+  const auto block_start = [](int len, int kb) {
+    return kGradW ? (kb ? kb - 1 : (len - 1) / S::kBlock) * S::kBlock : kb * S::kBlock;
+  };
+  const auto to_clear = [](int steps) { return kGradW && steps % S::kStep != 0; };
   // micro: whether the tile's rows lie in two scale tiles
   const auto two_scale_tiles = [](const ProductTile& t, int n) { return (t.lrow0 & 127) + n > 128; };
   const auto mma_rows = [](const ProductTile& t) { return (t.valid + 31) & ~31; };
 
   if (warp == 0) {
     uint32_t stage = 0, phase = 0;
+    uint32_t full_uses = 0, landed_uses = 0, in_landed = 0;  // a bit a stage: uses (mod 2), the last one's barrier
     int armed = 0;
     bool ok = true;
     for (int tile = tile0; tile < total && ok; tile += tstep) {
@@ -273,17 +287,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
           uint8_t* sa = smem + stage * kStage;
           uint8_t* sb = sa + S::kOpA;
-          // Both SMs' copies complete on the even SM's barrier; of a block that is cleared, each SM's
-          // on its own, where the warp waits that clears it.
-          const bool own = to_clear(len - kb * S::kBlock);
-          const uint32_t bar = cluster_addr(&full[stage], own ? rank : 0u);
-          if (own || leader) mbar_arrive_expect_tx(&full[stage], own ? bytes : 2 * bytes);
+          // Both SMs' copies complete on the even SM's full[stage]; of a block that is cleared, each
+          // SM's on its own landed[stage], where the warp waits that clears it.
+          const bool own = to_clear(block_len(len, kb));
+          const uint32_t bar = own ? cluster_addr(&landed[stage], rank) : cluster_addr(&full[stage], 0);
+          if (own)
+            mbar_arrive_expect_tx(&landed[stage], bytes);
+          else if (leader)
+            mbar_arrive_expect_tx(&full[stage], 2 * bytes);
           const int kx = kb * (kMicro ? 128 : 64);  // bytes or elements: 128 bytes a row
           if constexpr (kMicro) {
             tma_load_2d_pair(sa, &p.mw, bar, kx, w0 + f0);
             if (kSwiGLU) tma_load_2d_pair(sa + kBox, &p.mw, bar, kx, w0 + p.F + f0);
           } else if constexpr (kGradW) {
-            const int y = gw_r + kx;
+            const int y = gw_r + block_start(len, kb);
             tma_load_2d_pair(sa, &p.mw, bar, f0, y);
             tma_load_2d_pair(sa + kBox64, &p.mw, bar, f0 + 64, y);
             for (int j = 0; j < n / 2; j += 64)
@@ -306,6 +323,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
+        const uint32_t bit = 1u << stage;
+        if (to_clear(block_len(len, kb))) {
+          landed_uses ^= bit;
+          in_landed |= bit;
+        } else {
+          full_uses ^= bit;
+          in_landed &= ~bit;
+        }
         if (armed < kStages) ++armed;
         if (++stage == kStages) {
           stage = 0;
@@ -313,19 +338,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (!ok && leader) {  // let the copies of the last stage uses land
+    if (!ok) {  // let the copies of the last stage uses land (the odd SM's shared ones: the even SM waits)
       for (int i = 0; i < armed; ++i) {
-        if (stage == 0) {
-          stage = kStages;
-          phase ^= 1u;
-        }
-        --stage;
-        mbar_wait(&full[stage], phase, nullptr, nullptr, kDrainLimitNs);
+        stage = stage ? stage - 1 : kStages - 1;
+        const bool own = in_landed >> stage & 1u;
+        if (own || leader)
+          mbar_wait(own ? &landed[stage] : &full[stage],
+                    (own ? landed_uses : full_uses) >> stage & 1u ^ 1u, nullptr, nullptr, kDrainLimitNs);
       }
     }
   } else if (warp == 1 && leader) {
-    // the whole warp follows the stages (grad_w: it clears rows); lane 0 issues
-    uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, buf = 0, cleared_phase = 0;
+    // the whole warp follows the stages, one thread issues; a stage's barrier of each kind has its phase bit
+    uint32_t stage = 0, acc = 0, acc_phase = 0, buf = 0, full_phase = 0, cleared_phase = 0;
     bool ok = true;
     for (int tile = tile0; tile < total && ok; tile += tstep) {
       const ProductTile t = tile_of(tile);
@@ -339,19 +363,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t b_col = uniform((t.lrow0 & 127) >> 5);  // micro: the tile's first row's scale column
       const uint32_t idesc = idesc_bf16_f32_pair(n) | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u);
       for (int kb = 0; kb < nkb; ++kb) {
-        ok = __all_sync(~0u, mbar_wait(&full[stage], phase, abort_flag, p.err));
-        if (!ok) break;
-        const int left = min(S::kBlock, len - kb * S::kBlock);
+        const int left = block_len(len, kb);
         const int steps = (left + S::kStep - 1) / S::kStep;
         if (to_clear(left)) {
-          clear_rows<4>(smem + stage * kStage, left, steps * S::kStep, lane);
-          // and the odd SM has cleared its part
           ok = __all_sync(~0u, mbar_wait_cluster(&cleared[stage], cleared_phase >> stage & 1u,
                                                  abort_flag, p.err));
           cleared_phase ^= 1u << stage;
-          if (!ok) break;
-          __syncwarp();
+        } else {
+          ok = __all_sync(~0u, mbar_wait(&full[stage], full_phase >> stage & 1u, abort_flag, p.err));
+          full_phase ^= 1u << stage;
         }
+        if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
           const uint32_t sa = smem_u32(smem + stage * kStage);
@@ -393,10 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         buf ^= 1u;
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        if (++stage == kStages) stage = 0;
       }
       if (!ok) break;
       if (elect_one()) mma_commit_pair(&tfull[acc]);
@@ -404,33 +423,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (S::kAccs == 2) acc ^= 1u;
       if (acc == 0) acc_phase ^= 1u;
     }
-    if (lane == 0) {
-      mma_commit_pair_own(drain);  // every MMA issued above has completed once this arrives
-      mbar_wait(drain, 0, nullptr, nullptr, kDrainLimitNs);
-    }
+    if (elect_one()) mma_commit_pair_own(drain);  // every MMA issued above has completed once this arrives
     __syncwarp();
-  } else if (warp == 1) {
-    // the odd SM, grad_w: clear this SM's rows of the blocks that need it
-    if constexpr (kGradW) {
-      uint32_t stage = 0, own_phase = 0;
-      bool ok = true;
-      for (int tile = tile0; tile < total && ok; tile += tstep) {
-        const int len = sum_len(tile_of(tile));
-        for (int at = 0; at < len; at += S::kBlock) {
-          const int left = min(S::kBlock, len - at);
-          if (to_clear(left)) {
-            ok = __all_sync(~0u, mbar_wait(&full[stage], own_phase >> stage & 1u, abort_flag, p.err));
-            own_phase ^= 1u << stage;
-            if (!ok) break;
-            clear_rows<4>(smem + stage * kStage, left, (left + S::kStep - 1) / S::kStep * S::kStep, lane);
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(cluster_addr(&cleared[stage], 0));
-          }
-          if (++stage == kStages) stage = 0;
+    mbar_wait(drain, 0, nullptr, nullptr, kDrainLimitNs);
+  } else if (kGradW && warp == 2 + kEpilogueWarps) {
+    // clears this SM's rows behind the group, as soon as a block that has some has landed
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int tile = tile0; tile < total && ok; tile += tstep) {
+      const int len = uniform(sum_len(tile_of(tile)));
+      for (int kb = 0; kb * S::kBlock < len; ++kb) {
+        const int left = block_len(len, kb);
+        if (to_clear(left)) {
+          ok = __all_sync(~0u, mbar_wait(&landed[stage], phase >> stage & 1u, abort_flag, p.err));
+          if (!ok) break;
+          phase ^= 1u << stage;
+          clear_rows<4>(smem + stage * kStage, left, (left + S::kStep - 1) / S::kStep * S::kStep, lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(&cleared[stage], 0));
         }
+        if (++stage == kStages) stage = 0;
       }
     }
-  } else {
+  } else if (warp > 1) {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     uint32_t acc = 0, acc_phase = 0;
     const float ga = kNv && p.a_factor ? __ldg(p.a_factor) : 1.0f;
@@ -445,39 +460,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int feat0 = t.ft * 256 + (int)rank * 128 + quarter * 32;  // this warp's first feature
       const int end = min(t.valid, half ? n : n / 2);                 // this warp's rows
       if constexpr (kGradW) {
-        // a lane has a row of dW: chunks of 32 rows x 128 bytes through shared memory (in the 128-byte
+        // a lane has a row of dW: chunks of 32 rows x 64 bytes through shared memory (in the 64-byte
         // swizzle) to TMA, which leaves out what lies behind dW's last row or column
-        constexpr int kCols = kF32 ? 32 : 64;
-        uint8_t* buf = staging + (warp - 2) * 4096;
+        constexpr int kCols = kF32 ? 16 : 32;
+        uint8_t* buf = staging + (warp - 2) * 2048;
         if (feat0 < p.F && !(kAdd && none)) {
 #pragma unroll 1
           for (int c = half * kCols; c < t.valid; c += 2 * kCols) {
-            uint4 v[8];
+            uint32_t g[kCols];
+            if (none) {
 #pragma unroll
-            for (int h = 0; h < kCols / 16; ++h) {
-              uint32_t g[16];
-              tmem_ld16(tb + c + 16 * h, g);
+              for (int i = 0; i < kCols; ++i) g[i] = 0u;
+            } else {
+#pragma unroll
+              for (int h = 0; h < kCols / 16; ++h)
+                tmem_ld16(tb + c + 16 * h, reinterpret_cast<uint32_t(&)[16]>(g[16 * h]));
               tmem_ld_wait();
+            }
+            if constexpr (!kF32) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) g[i] = none ? 0u : g[i];
-              if constexpr (kF32) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  v[4 * h + q] = make_uint4(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]);
-              } else {
-                uint32_t k[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  k[i] = pack_bf16x2(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
-                v[2 * h] = make_uint4(k[0], k[1], k[2], k[3]);
-                v[2 * h + 1] = make_uint4(k[4], k[5], k[6], k[7]);
-              }
+              for (int i = 0; i < 16; ++i)
+                g[i] = pack_bf16x2(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
             }
             if (lane == 0) tma_store_wait_read();  // the previous chunk has left the buffer
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) = v[j];
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                  make_uint4(g[4 * j], g[4 * j + 1], g[4 * j + 2], g[4 * j + 3]);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) tma_store_3d<kAdd>(&p.mout, buf, t.lrow0 + c, feat0, t.g);
@@ -552,7 +562,7 @@ cudaError_t launch(const ProductParams& p, int sms, cudaStream_t st, const char*
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), S::kSmem, &set);
   if (e != cudaSuccess) return e;
   LaunchScope ls(label, st);
-  return launch_pairs(kern, sms, kThreads, S::kSmem, st, p);
+  return launch_pairs(kern, sms, S::kThreads, S::kSmem, st, p);
 }
 
 template <int kOp>
@@ -583,7 +593,7 @@ cudaError_t launch_grouped_product(const GroupedProduct& g, int sms, cudaStream_
     const int el = g.out_dtype == MOE_F32 ? 4 : 2;
     if (!make_map_2d(&p.mw, 2, g.a, g.N, g.rows, g.ld_a, 64, 64) ||
         !make_map_2d(&p.mrow[0], 2, g.b, g.K, g.rows, g.ld_b, 64, 64) ||
-        !make_map_3d(&p.mout, el, g.out, g.K, g.N, g.E, 128 / el, 32))
+        !make_map_3d(&p.mout, el, g.out, g.K, g.N, g.E, 64 / el, 32))
       return cudaErrorInvalidValue;
   } else if (!make_map_3d(&p.mw, 2, g.b, g.K, g.N, g.E, 64, fwd ? 128 : 64) ||
              !make_row_maps(p.mrow, 8, 2, g.a, p.Kc, g.rows, g.ld_a, 64))
