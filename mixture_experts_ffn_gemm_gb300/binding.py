@@ -442,23 +442,48 @@ _KINDS = {"forward": MOE_PRODUCT_FORWARD, "grad_x": MOE_PRODUCT_GRAD_X,
 _FORMATS = {"mx": MOE_MICRO_MX, "nv": MOE_MICRO_NV}
 
 
-def _one_device(stream, *tensors):
-    """Refuses operands of several devices, or of another than the current one, whose stream is used."""
-    devices = {t.get_device() for t in tensors if t is not None}
-    if len(devices) > 1 or (stream is None and devices != {torch._C._cuda_getDevice()}):
-        raise ValueError(f"operands on the devices {sorted(devices)}: one device, and the current one")
+# What a call checks of an operand: (type, fewest and most elements, name, (rows, width, pitch) or None).
+# Operands without a pitch of their own are that many consecutive elements; for the others no number of
+# elements passes the quick check.
+def _rows(name, dtype, rows, width, ld):
+    if ld and ld != width:
+        return dtype, 1, 0, name, (rows, width, ld)
+    return _dense(name, dtype, rows * width)
 
 
-def _at_least(t, n: int, dtype, name: str) -> Optional[int]:
-    """Address of at least n consecutive elements of `dtype`."""
-    if t is None:
-        return None
+def _dense(name, dtype, n):
+    return dtype, n, n, name, None
+
+
+def _at_least(name, dtype, n):
+    return dtype, n, 1 << 62, name, None
+
+
+def _refuse(t, device, spec):
+    """The address of an operand that is not the plain case, or the reason why it is refused."""
+    dtype, least, most, name, pitched = spec
     if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on device {t.get_device()}, the call runs on device {device}")
+    if pitched is not None:
+        return _pitched(t, *pitched, dtype, name)
+    if t.dtype is not dtype or not t.is_contiguous() or not least <= t.numel() <= most:
         raise ValueError(f"{name}: {tuple(t.shape)} of {t.dtype} with strides {t.stride()}, the "
-                         f"configuration says {n} consecutive elements of {dtype}")
+                         f"configuration says {least} consecutive elements of {dtype}")
     return t.data_ptr()
+
+
+def _addresses(stream, specs, tensors, ws):
+    """Addresses of a call's operands, all of them on the current device (the stream's, when one is given:
+    then on one device, the workspace's)."""
+    device = torch._C._cuda_getDevice() if stream is None else ws.get_device()
+    if device < 0 or ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"ws: on {ws.device}, a contiguous CUDA tensor on the call's device")
+    return [None if t is None else
+            t.data_ptr() if (t.get_device() == device and t.dtype is s[0]
+                             and s[1] <= t.numel() <= s[2] and t.is_contiguous()) else
+            _refuse(t, device, s) for t, s in zip(tensors, specs)]
 
 
 def make_product_config(rows: int, E: int, N: int, K: int, kind: str = "forward",
@@ -484,21 +509,24 @@ def alloc_product_workspace(cfg: moe_product_config_t, device="cuda") -> torch.T
 def moe_grouped_product(cfg: moe_product_config_t, offsets, a, b, out, ws, stream=None):
     """Products grouped by expert: y = x W_e^T (a = x, b = W), dx = dy W_e (a = dy, b = W) or
     dW_e = dy^T x (a = dy, b = x), rows [offsets[e], offsets[e+1]) of expert e."""
-    R, E, N, K, kind = cfg.rows, cfg.E, cfg.N, cfg.K, cfg.kind
-    bf, odt = torch.bfloat16, _DTYPES.get(cfg.out_dtype)
-    _one_device(stream, offsets, a, b, out, ws)
-    if kind == MOE_PRODUCT_GRAD_W:
-        pa, pb = _pitched(a, R, N, cfg.ld_y, bf, "a"), _pitched(b, R, K, cfg.ld_x, bf, "b")
-        po = _vector(out, E * N * K, odt, "out")
-    elif kind == MOE_PRODUCT_GRAD_X:
-        pa, pb = _pitched(a, R, N, cfg.ld_y, bf, "a"), _vector(b, E * N * K, bf, "b")
-        po = _pitched(out, R, K, cfg.ld_x, odt, "out")
-    else:
-        pa, pb = _pitched(a, R, K, cfg.ld_x, bf, "a"), _vector(b, E * N * K, bf, "b")
-        po = _pitched(out, R, N, cfg.ld_y, odt, "out")
-    _check(load_library().moe_grouped_product(
-        ctypes.byref(cfg), _at_least(offsets, E + 1, torch.int32, "offsets"), pa, pb, po, _dev(ws),
-        ws.numel(), _stream(stream)), "moe_grouped_product")
+    o, pa, pb, po = _addresses(stream, _product_specs(bytes(cfg)), (offsets, a, b, out), ws)
+    _check(load_library().moe_grouped_product(ctypes.byref(cfg), o, pa, pb, po, ws.data_ptr(),
+                                              ws.nbytes, _stream(stream)), "moe_grouped_product")
+
+
+@functools.lru_cache(maxsize=64)
+def _product_specs(cfg: bytes) -> tuple:
+    c = moe_product_config_t.from_buffer_copy(cfg)
+    R, E, N, K, bf, odt = c.rows, c.E, c.N, c.K, torch.bfloat16, _DTYPES.get(c.out_dtype)
+    offs = _at_least("offsets", torch.int32, E + 1)
+    if c.kind == MOE_PRODUCT_GRAD_W:
+        return (offs, _rows("a", bf, R, N, c.ld_y), _rows("b", bf, R, K, c.ld_x),
+                _dense("out", odt, E * N * K))
+    if c.kind == MOE_PRODUCT_GRAD_X:
+        return (offs, _rows("a", bf, R, N, c.ld_y), _dense("b", bf, E * N * K),
+                _rows("out", odt, R, K, c.ld_x))
+    return (offs, _rows("a", bf, R, K, c.ld_x), _dense("b", bf, E * N * K),
+            _rows("out", odt, R, N, c.ld_y))
 
 
 def make_micro_config(rows: int, K: int, format: str = "mx", groups: int = 1,
@@ -535,38 +563,47 @@ def _scale_bytes(rows: int, K: int, groups: int, fmt: int) -> int:
     return (rows // 128 + groups) * ((K + per - 1) // per) * 512
 
 
-def _micro_coded(cfg, codes, scales, offsets, factor):
-    if cfg.format != MOE_MICRO_NV and factor is not None:
+@functools.lru_cache(maxsize=64)
+def _micro_specs(cfg: bytes) -> tuple:
+    """Specs of moe_micro_quantize's and of moe_micro_dequantize's operands."""
+    c = moe_micro_config_t.from_buffer_copy(cfg)
+    u8, dt = torch.uint8, _DTYPES.get(c.dtype)
+    offs = _at_least("offsets", torch.int32, c.groups + 1)
+    factor = _dense("factor", torch.float32, 1)
+    codes = _dense("codes", u8, c.rows * (c.K // 2))
+    scales = _at_least("scales", u8, _scale_bytes(c.rows, c.K, c.groups, c.format))
+    return ((_rows("x", dt, c.src_rows, c.K, c.ld),
+             _dense("dest", torch.int32, c.src_rows * c.copies), offs, factor, codes, scales),
+            (codes, scales, offs, factor, _rows("out", dt, c.rows, c.K, c.ld)))
+
+
+def _no_factor(*factors):
+    if any(f is not None for f in factors):
         raise ValueError('factor: the format "mx" has none')
-    n = _scale_bytes(cfg.rows, cfg.K, cfg.groups, cfg.format)
-    return (_vector(codes, cfg.rows * (cfg.K // 2), torch.uint8, "codes"),
-            _at_least(scales, n, torch.uint8, "scales"),
-            _at_least(offsets, cfg.groups + 1, torch.int32, "offsets"),
-            _vector(factor, 1, torch.float32, "factor"))
 
 
 def moe_micro_quantize(cfg: moe_micro_config_t, x, dest, offsets, factor, codes, scales, ws,
                        stream=None):
     """Rows of x to codes and scales.  dest: the coded rows that take each row of x ([src_rows][copies],
     perm_dst of moe_permute), or None; offsets: the experts' rows, or None for `groups` equal groups."""
-    _one_device(stream, x, dest, offsets, factor, codes, scales, ws)
-    pc, ps, po, pf = _micro_coded(cfg, codes, scales, offsets, factor)
-    _check(load_library().moe_micro_quantize(
-        ctypes.byref(cfg),
-        _pitched(x, cfg.src_rows, cfg.K, cfg.ld, _DTYPES.get(cfg.dtype), "x"),
-        _vector(dest, cfg.src_rows * cfg.copies, torch.int32, "dest"), po, pf, pc, ps, _dev(ws),
-        ws.numel(), _stream(stream)), "moe_micro_quantize")
+    if cfg.format != MOE_MICRO_NV:
+        _no_factor(factor)
+    px, pd, po, pf, pc, ps = _addresses(stream, _micro_specs(bytes(cfg))[0],
+                                        (x, dest, offsets, factor, codes, scales), ws)
+    _check(load_library().moe_micro_quantize(ctypes.byref(cfg), px, pd, po, pf, pc, ps,
+                                             ws.data_ptr(), ws.nbytes, _stream(stream)),
+           "moe_micro_quantize")
 
 
 def moe_micro_dequantize(cfg: moe_micro_config_t, codes, scales, offsets, factor, out, ws,
                          stream=None):
     """The values that codes and scales stand for."""
-    _one_device(stream, codes, scales, offsets, factor, out, ws)
-    pc, ps, po, pf = _micro_coded(cfg, codes, scales, offsets, factor)
-    _check(load_library().moe_micro_dequantize(
-        ctypes.byref(cfg), pc, ps, po, pf,
-        _pitched(out, cfg.rows, cfg.K, cfg.ld, _DTYPES.get(cfg.dtype), "out"), _dev(ws), ws.numel(),
-        _stream(stream)), "moe_micro_dequantize")
+    if cfg.format != MOE_MICRO_NV:
+        _no_factor(factor)
+    pc, ps, po, pf, pv = _addresses(stream, _micro_specs(bytes(cfg))[1],
+                                    (codes, scales, offsets, factor, out), ws)
+    _check(load_library().moe_micro_dequantize(ctypes.byref(cfg), pc, ps, po, pf, pv, ws.data_ptr(),
+                                               ws.nbytes, _stream(stream)), "moe_micro_dequantize")
 
 
 def make_micro_product_config(rows: int, E: int, N: int, K: int, format: str = "mx",
@@ -588,24 +625,27 @@ def alloc_micro_product_workspace(cfg: moe_micro_product_config_t, device="cuda"
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
+@functools.lru_cache(maxsize=64)
+def _micro_product_specs(cfg: bytes) -> tuple:
+    c = moe_micro_product_config_t.from_buffer_copy(cfg)
+    R, E, N, K, u8, f32 = c.rows, c.E, c.N, c.K, torch.uint8, torch.float32
+    per = 2 * N if c.flags & MOE_MICRO_SWIGLU else N
+    return (_at_least("offsets", torch.int32, E + 1), _dense("a", u8, R * (K // 2)),
+            _at_least("a_scales", u8, _scale_bytes(R, K, E, c.format)), _dense("a_factor", f32, 1),
+            _dense("w", u8, E * per * (K // 2)),
+            _at_least("w_scales", u8, _scale_bytes(E * per, K, E, c.format)),
+            _dense("w_factor", f32, E), _rows("out", _DTYPES.get(c.out_dtype), R, N, c.ld_out))
+
+
 def moe_micro_product(cfg: moe_micro_product_config_t, offsets, a, a_scales, a_factor, w, w_scales,
                       w_factor, out, ws, stream=None):
     """The experts' product on microscaled operands, plain or with SwiGLU."""
-    R, E, N, K, fmt = cfg.rows, cfg.E, cfg.N, cfg.K, cfg.format
-    if fmt != MOE_MICRO_NV and (a_factor is not None or w_factor is not None):
-        raise ValueError('a_factor, w_factor: the format "mx" has none')
-    per = 2 * N if cfg.flags & MOE_MICRO_SWIGLU else N
-    u8, f32 = torch.uint8, torch.float32
-    _one_device(stream, offsets, a, a_scales, a_factor, w, w_scales, w_factor, out, ws)
-    _check(load_library().moe_micro_product(
-        ctypes.byref(cfg), _at_least(offsets, E + 1, torch.int32, "offsets"),
-        _vector(a, R * (K // 2), u8, "a"),
-        _at_least(a_scales, _scale_bytes(R, K, E, fmt), u8, "a_scales"),
-        _vector(a_factor, 1, f32, "a_factor"), _vector(w, E * per * (K // 2), u8, "w"),
-        _at_least(w_scales, _scale_bytes(E * per, K, E, fmt), u8, "w_scales"),
-        _vector(w_factor, E, f32, "w_factor"),
-        _pitched(out, R, N, cfg.ld_out, _DTYPES.get(cfg.out_dtype), "out"), _dev(ws), ws.numel(),
-        _stream(stream)), "moe_micro_product")
+    if cfg.format != MOE_MICRO_NV:
+        _no_factor(a_factor, w_factor)
+    args = _addresses(stream, _micro_product_specs(bytes(cfg)),
+                      (offsets, a, a_scales, a_factor, w, w_scales, w_factor, out), ws)
+    _check(load_library().moe_micro_product(ctypes.byref(cfg), *args, ws.data_ptr(), ws.nbytes,
+                                            _stream(stream)), "moe_micro_product")
 
 
 def moe_forward_host_io(cfg, x_host, W_r, b, W13, W2, W13_scale, W2_scale, Ws13, Ws2,

@@ -210,7 +210,6 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU>::kThreads, 1)
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_map(&p.mw);
-    tma_prefetch_map(&p.mrow[kMaxRows / 32 - 1]);
     if (kMicro) {
       tma_prefetch_map(&p.msw);
       tma_prefetch_map(&p.msr);
@@ -576,9 +575,10 @@ cudaError_t launch_micro(const ProductParams& p, bool swiglu, bool f32, int sms,
 
 }  // namespace
 
+// Maps of boxes of 16, 32, .. rows, as far as a tile of a group can need them.
 static bool make_row_maps(CUtensorMap* m, int count, int el, const void* base, uint64_t cols,
                           uint64_t rows, uint64_t ld, uint32_t box_cols) {
-  for (int i = 0; i < count; ++i)
+  for (int i = 0; i < count && (uint64_t)i * 32 < rows; ++i)
     if (!make_map_2d(&m[i], el, base, cols, rows, ld, box_cols, 16 * (i + 1))) return false;
   return true;
 }

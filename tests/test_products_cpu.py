@@ -13,8 +13,11 @@ P = 0x10000  # an aligned stand-in address: every call below returns before it i
 
 
 class OnDevice(torch.Tensor):
-    """A CPU tensor that says that it is on the GPU."""
+    """A CPU tensor that says that it is on GPU 0."""
     is_cuda = True
+
+    def get_device(self):
+        return 0
 
 
 class OnAnother(OnDevice):
