@@ -13,8 +13,10 @@
 //
 // Bound by memory: a row is read once and its codes (K / 2 bytes) and scales (K / B) are written to
 // each row that takes it, so the experts' copies of a token are quantised once and written k times.
-// A warp takes a row (or a part of one, when there are few), a lane 16 channels at a time.
+// A warp takes a row (or a part of one, when there are few), a lane 32 channels at a time (16 going back).
 #include <cuda_fp16.h>
+
+#include <cstdint>
 
 #include "common.cuh"
 #include "internal.h"
@@ -39,38 +41,52 @@ struct MicroParams {
   int32_t K, G, group_rows, copies, parts, ktiles;
 };
 
-// Where a row's scales start: its group's first tile is (first row) / 128 + group, the row's place in
-// a tile of 128 rows x 4 columns (r % 32) * 16 + (r / 32) * 4.  The whole warp calls this for one row;
-// -1 (and kErrIndex) for a row outside the groups.  Two rounds of 32 loads find the group.
-__device__ __forceinline__ int64_t scale_base(const MicroParams& p, int64_t row, int lane) {
-  int64_t g, start;
-  if (row < 0 || row >= p.rows) {
-    if (lane == 0) raise_flag(p.err, kErrIndex);
-    return -1;
-  }
+// Where the scales of `n` rows (lane j's `row`, j < n <= kMaxCopies) start, in lane j: a group's first
+// tile is (first row) / 128 + group, a row's place in a tile of 128 rows x 4 columns (r % 32) * 16 + (r / 32) * 4.
+// -1 (and kErrIndex) for a row outside the groups.  The whole warp finds each row's group in two rounds of 32
+// loads, the second round's in flight for kBatch rows at once.
+constexpr int kBatch = 8;
+__device__ __forceinline__ int64_t scale_base(const MicroParams& p, int row, int n, int lane) {
+  int g, start;
+  bool ok = row >= 0 && row < p.rows;
   if (!p.offsets) {
-    g = row / p.group_rows;
+    g = ok ? row / p.group_rows : 0;
     start = g * p.group_rows;
   } else {
     const int stride = (p.G + 31) / 32;
     const int i1 = lane * stride;
-    const bool le = i1 < p.G && __ldg(p.offsets + i1) <= row;
-    const int seg = __popc(__ballot_sync(~0u, le)) - 1;
-    const int i2 = max(seg, 0) * stride + lane;
-    const bool in = lane < stride && i2 < p.G;
-    const int o2 = in ? __ldg(p.offsets + i2) : 0;
-    const int cnt = __popc(__ballot_sync(~0u, in && o2 <= row));
-    start = __shfl_sync(~0u, o2, max(cnt - 1, 0));
-    g = max(seg, 0) * stride + cnt - 1;
-    bool ok = seg >= 0 && cnt > 0 && start >= 0 && start <= row;
-    if (ok && g == p.G - 1) ok = row < __ldg(p.offsets + p.G);
-    if (!ok) {
-      if (lane == 0) raise_flag(p.err, kErrIndex);
-      return -1;
+    const int first = i1 < p.G ? __ldg(p.offsets + i1) : INT32_MAX;
+    const int last = __ldg(p.offsets + p.G);
+    g = -1;
+    start = 0;
+    for (int j0 = 0; j0 < n; j0 += kBatch) {
+      int o2[kBatch], i2[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int r = __shfl_sync(~0u, row, j0 + b);
+        i2[b] = max(__popc(__ballot_sync(~0u, i1 < p.G && first <= r)) - 1, 0) * stride;
+        o2[b] = lane < stride && i2[b] + lane < p.G ? __ldg(p.offsets + i2[b] + lane) : INT32_MAX;
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int r = __shfl_sync(~0u, row, j0 + b);
+        const int cnt = __popc(__ballot_sync(~0u, o2[b] <= r && o2[b] != INT32_MAX));
+        const int o = __shfl_sync(~0u, o2[b], max(cnt - 1, 0));
+        if (lane == j0 + b) {
+          g = cnt > 0 ? i2[b] + cnt - 1 : -1;
+          start = o;
+        }
+      }
     }
+    ok = ok && g >= 0 && start >= 0 && start <= row && row < last;
   }
-  const int64_t lr = row - start;
-  return ((start >> 7) + g + (lr >> 7)) * p.ktiles * 512 + (lr & 31) * 16 + ((lr & 127) >> 5) * 4;
+  if (lane >= n) return -1;
+  if (!ok) {
+    raise_flag(p.err, kErrIndex);
+    return -1;
+  }
+  const int lr = row - start;
+  return (int64_t)((start >> 7) + g + (lr >> 7)) * p.ktiles * 512 + (lr & 31) * 16 + ((lr & 127) >> 5) * 4;
 }
 
 __device__ __forceinline__ uint32_t e2m1x8(const float* v) {
@@ -112,21 +128,104 @@ __device__ __forceinline__ uint32_t nv_scale(float amax, float g) {
   return r > 0.0f || (r == 0.0f && (lo & 1u)) ? hi : lo;
 }
 
+// The magnitude of a code: 0, 0.5, then two to a power of two.
+__device__ __forceinline__ float e2m1_value(uint32_t code) {
+  return code < 2u ? 0.5f * (float)code : __uint_as_float(((code >> 1) + 126u) << 23 | (code & 1u) << 22);
+}
+
 // A magnitude's code between a and a + 1 (which both moved quotients gave), by the exact difference.
 __device__ __forceinline__ uint32_t settle(uint32_t a, uint32_t b, float ax, float s, float g) {
-  const float lut[8] = {0.0f, 0.5f, 1.0f, 1.5f, 2.0f, 3.0f, 4.0f, 6.0f};
-  const float m = 0.5f * (lut[a] + lut[b]);
+  const float m = 0.5f * (e2m1_value(a) + e2m1_value(b));
   const float r = fmaf(-(m * s), g, ax);
   return r > 0.0f || (r == 0.0f && (a & 1u)) ? b : a;
 }
 
+// 16 channels: their magnitude's largest as an integer (NaN and infinities compare above every finite
+// value) and the values.
+template <bool kF32>
+__device__ __forceinline__ uint32_t unpack16(const uint4* raw, float (&v)[16]) {
+  uint32_t top = 0;
+  if constexpr (kF32) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t u[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[4 * q + i] = __uint_as_float(u[i]);
+        top = max(top, u[i] & 0x7fffffffu);
+      }
+    }
+    return top;
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t u[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[8 * q + 2 * i] = __uint_as_float(u[i] << 16);
+      v[8 * q + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      top = __vmaxu2(top, u[i] & 0x7fff7fffu);
+    }
+  }
+  return max(top << 16, top & 0xffff0000u);
+}
+
+__device__ __forceinline__ uint2 codes_mx(float (&v)[16], float inv) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] *= inv;
+  return make_uint2(e2m1x8(v), e2m1x8(v + 8));
+}
+
+// Codes of a block of 16 with the scale s g (s > 0): by both moved quotients, and by the exact difference
+// where they disagree.
+__device__ __forceinline__ uint2 codes_nv(const float (&v)[16], float s, float g) {
+  const float inv = s > 0.0f ? 1.0f / (s * g) : 0.0f;
+  const float il = inv * kLess, ih = inv * kMore;
+  float a[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a[i] = v[i] * il;
+  uint32_t c[2] = {e2m1x8(a), e2m1x8(a + 8)};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a[i] = v[i] * ih;
+  const uint32_t d[2] = {c[0] ^ e2m1x8(a), c[1] ^ e2m1x8(a + 8)};
+  if (d[0] | d[1]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t x = (d[i >> 3] >> (4 * (i & 7))) & 7u;
+      if (x) {
+        const uint32_t lo = (c[i >> 3] >> (4 * (i & 7))) & 7u;
+        c[i >> 3] ^= (settle(lo, lo ^ x, fabsf(v[i]), s, g) ^ lo) << (4 * (i & 7));
+      }
+    }
+  }
+  return make_uint2(c[0], c[1]);
+}
+
+struct CopyTo {  // where a copy of the row starts
+  uint8_t* codes;
+  uint8_t* scales;
+};
+
 template <bool kNv, bool kF32>
-__global__ void __launch_bounds__(kThreads) micro_quantize_kernel(const MicroParams p) {
+__global__ void __launch_bounds__(kThreads, 2) micro_quantize_kernel(const MicroParams p) {
+  __shared__ CopyTo to_all[kThreads / 32][kMaxCopies];
   const int lane = threadIdx.x & 31;
+  CopyTo* to = to_all[threadIdx.x >> 5];
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int64_t t = w / p.parts;
   if (t >= p.src_rows) return;
   const int part = (int)(w - t * p.parts);
+  // a lane has 32 channels: one block of MX, two of NV
+  constexpr int kRaw = kF32 ? 8 : 4;
+  const int chunks = p.K / 32;
+  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) +
+                                                    t * p.ld * (kF32 ? 4 : 2));
+  uint4 raw[kRaw];
+  int c = part * 32 + lane;
+  if (c < chunks) {  // the first loads are under way while the rows' groups are found
+#pragma unroll
+    for (int q = 0; q < kRaw; ++q) raw[q] = __ldg(src + (int64_t)c * kRaw + q);
+  }
   float g = 1.0f;
   bool bad_factor = false;
   if (kNv && p.factor) {
@@ -134,119 +233,68 @@ __global__ void __launch_bounds__(kThreads) micro_quantize_kernel(const MicroPar
     bad_factor = !(g >= 0x1p-100f && g <= 0x1p100f);
     if (bad_factor && lane == 0) raise_flag(p.err, kErrIndex);
   }
-  // lane j: the row that the j-th copy goes to, and where its scales start
-  int64_t my_row = -1, my_scale = -1;
-  for (int j = 0; j < p.copies; ++j) {
-    const int64_t row = p.dest ? (int64_t)__ldg(p.dest + t * p.copies + j) : t;
-    const int64_t sb = scale_base(p, row, lane);
-    if (lane == j) {
-      my_row = sb < 0 ? -1 : row;
-      my_scale = sb;
-    }
+  int copies;
+  {
+    int row = -1;
+    if (lane < p.copies) row = p.dest ? __ldg(p.dest + t * p.copies + lane) : (int)t;
+    const int64_t sb = scale_base(p, row, p.copies, lane);
+    const uint32_t good = __ballot_sync(~0u, sb >= 0);  // the others are skipped
+    if (sb >= 0)
+      to[__popc(good & ((1u << lane) - 1u))] = {p.codes + (int64_t)row * (p.K / 2), p.scales + sb};
+    copies = __popc(good);
+    __syncwarp();
   }
-  const int chunks = p.K / 16;
   for (int c0 = part * 32; c0 < chunks; c0 += p.parts * 32) {
-    const int c = c0 + lane;
     const bool in = c < chunks;
-    float v[16];
-    uint32_t amax = 0;  // as an integer: NaN and infinities compare above every finite value
-    if (in) {
-      if (kF32) {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const float*>(p.x) + t * p.ld) +
-                           (int64_t)c * 4;
+    uint32_t code[4], scale;
+    if (!in) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint4 r = __ldg(src + q);
-          const uint32_t u[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[4 * q + i] = __uint_as_float(u[i]);
-            amax = max(amax, u[i] & 0x7fffffffu);
-          }
-        }
-      } else {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) +
-                                                          t * p.ld) +
-                           (int64_t)c * 2;
-        uint32_t m = 0;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint4 r = __ldg(src + q);
-          const uint32_t u[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[8 * q + 2 * i] = __uint_as_float(u[i] << 16);
-            v[8 * q + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-            m = __vmaxu2(m, u[i] & 0x7fff7fffu);
-          }
-        }
-        amax = max(m << 16, m & 0xffff0000u);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+      for (int q = 0; q < kRaw; ++q) raw[q] = make_uint4(0, 0, 0, 0);
     }
-    uint32_t code0, code1, scale;
-    bool nan;
-    if (!kNv) {
-      amax = max(amax, __shfl_xor_sync(~0u, amax, 1));
-      const uint32_t e = amax >> 23;
-      nan = e == 255u;
-      scale = nan ? 255u : amax == 0 ? 127u : e > 2u ? e - 2u : 0u;
+    float v0[16], v1[16];
+    uint32_t t0 = unpack16<kF32>(raw, v0), t1 = unpack16<kF32>(raw + kRaw / 2, v1);
+    c += p.parts * 32;
+    if (c < chunks) {
+#pragma unroll
+      for (int q = 0; q < kRaw; ++q) raw[q] = __ldg(src + (int64_t)c * kRaw + q);
+    }
+    if constexpr (!kNv) {
+      const uint32_t top = max(t0, t1), e = top >> 23;
+      const bool nan = e == 255u;
+      scale = nan ? 255u : top == 0 ? 127u : e > 2u ? e - 2u : 0u;
       const float inv = __uint_as_float((254u - min(scale, 253u)) << 23);  // 2^(127 - scale)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] *= inv;
-      code0 = e2m1x8(v);
-      code1 = e2m1x8(v + 8);
+      const uint2 a = codes_mx(v0, inv), b = codes_mx(v1, inv);
+      code[0] = nan ? 0u : a.x;
+      code[1] = nan ? 0u : a.y;
+      code[2] = nan ? 0u : b.x;
+      code[3] = nan ? 0u : b.y;
     } else {
-      nan = bad_factor || (amax >> 23) == 255u;
-      scale = nan ? 0x7fu : nv_scale(__uint_as_float(amax), g);
-      const float s = nan ? 0.0f : e4m3_value(scale);
-      const float inv = s > 0.0f ? 1.0f / (s * g) : 0.0f;
-      const float il = inv * kLess, ih = inv * kMore;
-      float a[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) a[i] = v[i] * il;
-      code0 = e2m1x8(a);
-      code1 = e2m1x8(a + 8);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) a[i] = v[i] * ih;
-      const uint32_t d0 = code0 ^ e2m1x8(a), d1 = code1 ^ e2m1x8(a + 8);
-      if (d0 | d1) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          uint32_t& code = i < 8 ? code0 : code1;
-          const uint32_t d = ((i < 8 ? d0 : d1) >> (4 * (i & 7))) & 7u;
-          if (d) {
-            const uint32_t lo = (code >> (4 * (i & 7))) & 7u;
-            const uint32_t pick = settle(lo, lo ^ d, fabsf(v[i]), s, g);
-            code ^= (pick ^ lo) << (4 * (i & 7));
-          }
-        }
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t top = h ? t1 : t0;
+        const bool nan = bad_factor || (top >> 23) == 255u;
+        const uint32_t sc = nan ? 0x7fu : nv_scale(__uint_as_float(top), g);
+        const uint2 a = codes_nv(h ? v1 : v0, nan ? 0.0f : e4m3_value(sc), g);
+        code[2 * h] = nan ? 0u : a.x;
+        code[2 * h + 1] = nan ? 0u : a.y;
+        scale = h ? scale | sc << 8 : sc;
       }
     }
-    if (nan) code0 = code1 = 0;
-    // four (NV) or two (MX) neighbouring scales leave in one store: 64 channels
-    uint32_t packed;
-    if (kNv) {
-      packed = scale | __shfl_down_sync(~0u, scale, 1) << 8;
-      packed |= __shfl_down_sync(~0u, packed, 2) << 16;
-    } else {
-      packed = scale | __shfl_down_sync(~0u, scale, 2) << 8;
-    }
-    const int col = kNv ? c : c >> 1;
-    const int64_t scale_off = (int64_t)(col >> 2) * 512 + (col & 3);
-    for (int j = 0; j < p.copies; ++j) {
-      const int64_t row = __shfl_sync(~0u, my_row, j);
-      const int64_t sb = __shfl_sync(~0u, my_scale, j);
-      if (row < 0 || !in) continue;
-      *reinterpret_cast<uint2*>(p.codes + row * (p.K / 2) + (int64_t)c * 8) =
-          make_uint2(code0, code1);
-      if ((lane & 3) == 0) {
-        if (kNv)
-          *reinterpret_cast<uint32_t*>(p.scales + sb + scale_off) = packed;
-        else
-          *reinterpret_cast<uint16_t*>(p.scales + sb + scale_off) = (uint16_t)packed;
+    // the scales of 64 channels (two lanes) leave in one store
+    const uint32_t packed = scale | __shfl_down_sync(~0u, scale, 1) << (kNv ? 16 : 8);
+    const int at = c - p.parts * 32;           // this chunk
+    const int col = at * (kNv ? 2 : 1);        // and its first scale
+    const int64_t code_off = (int64_t)at * 16, scale_off = (int64_t)(col >> 2) * 512 + (col & 3);
+    if (in) {
+      for (int j = 0; j < copies; ++j) {
+        const CopyTo d = to[j];
+        *reinterpret_cast<uint4*>(d.codes + code_off) = make_uint4(code[0], code[1], code[2], code[3]);
+        if (!(lane & 1)) {
+          if (kNv)
+            *reinterpret_cast<uint32_t*>(d.scales + scale_off) = packed;
+          else
+            *reinterpret_cast<uint16_t*>(d.scales + scale_off) = (uint16_t)packed;
+        }
       }
     }
   }
@@ -261,7 +309,7 @@ __global__ void __launch_bounds__(kThreads) micro_dequantize_kernel(const MicroP
   if (row >= end) return;  // rows behind the last group are left as they are
   const int part = (int)(w - row * p.parts);
   const float g = kNv && p.factor ? __ldg(p.factor) : 1.0f;
-  const int64_t sb = scale_base(p, row, lane);
+  const int64_t sb = __shfl_sync(~0u, scale_base(p, (int)row, 1, lane), 0);
   if (sb < 0) return;
   const int chunks = p.K / 16;
   for (int c = part * 32 + lane; c < chunks; c += p.parts * 32) {
@@ -325,8 +373,8 @@ MicroParams params(const MicroOp& m) {
 }
 
 // Warps for a row: one, or as many as fill the GPU when there are few rows.
-int row_parts(int64_t rows, int K, int sms) {
-  const int64_t most = (K / 16 + 31) / 32;
+int row_parts(int64_t rows, int K, int lane_channels, int sms) {
+  const int64_t most = (K / lane_channels + 31) / 32;
   int64_t n = (int64_t)sms * 16 / (rows > 0 ? rows : 1);
   return (int)(n < 1 ? 1 : n > most ? most : n);
 }
@@ -335,7 +383,7 @@ int row_parts(int64_t rows, int K, int sms) {
 
 cudaError_t launch_micro_quantize(const MicroOp& m, int sms, cudaStream_t st) {
   MicroParams p = params(m);
-  p.parts = row_parts(m.src_rows, m.K, sms);
+  p.parts = row_parts(m.src_rows, m.K, 32, sms);
   const unsigned grid = (unsigned)((m.src_rows * p.parts + kThreads / 32 - 1) / (kThreads / 32));
   LaunchScope ls("micro_quantize", st);
   const bool f32 = m.dtype == MOE_F32;
@@ -355,7 +403,7 @@ cudaError_t launch_micro_quantize(const MicroOp& m, int sms, cudaStream_t st) {
 
 cudaError_t launch_micro_dequantize(const MicroOp& m, int sms, cudaStream_t st) {
   MicroParams p = params(m);
-  p.parts = row_parts(m.rows, m.K, sms);
+  p.parts = row_parts(m.rows, m.K, 16, sms);
   const unsigned grid = (unsigned)((m.rows * p.parts + kThreads / 32 - 1) / (kThreads / 32));
   LaunchScope ls("micro_dequantize", st);
   const bool f32 = m.dtype == MOE_F32;
