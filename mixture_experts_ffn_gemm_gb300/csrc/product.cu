@@ -54,7 +54,7 @@ constexpr int kMaxThreads = 32 * (2 + kEpilogueWarps + 1);
 constexpr int kBox = 128 * 128;  // 128 features x 128 bytes
 constexpr int kBox64 = 64 * 128;
 constexpr int kBarBytes = 256;
-constexpr int kTable = (3 * (kProductMaxGroups + 1)) * 4 + kMaxThreads * 4;
+constexpr int kTable = (4 * (kProductMaxGroups + 1)) * 4 + kMaxThreads * 4;
 constexpr int kSmemMost = 232448 - 1024 - kBarBytes - kTable;
 
 enum Op { OP_FORWARD, OP_GRAD_X, OP_GRAD_W, OP_MX, OP_NV };
@@ -189,7 +189,8 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU>::kThreads, 1)
   tab.tile_start = reinterpret_cast<int*>(staging + S::kStaging + kBarBytes);
   tab.row0 = tab.tile_start + kProductMaxGroups + 1;
   tab.nrows = tab.row0 + kProductMaxGroups + 1;
-  int* scratch = tab.nrows + kProductMaxGroups + 1;
+  tab.cut = tab.nrows + kProductMaxGroups + 1;
+  int* scratch = tab.cut + kProductMaxGroups + 1;
 
   const int warp = uniform(threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -231,18 +232,27 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU>::kThreads, 1)
   // sum runs over the group's rows
   const int fts = (p.F + 255) / 256, nts = (p.Kc + kMaxRows - 1) / kMaxRows;
   const int total = kGradW ? p.E * nts * fts : tab.tile_start[p.E];
+  // The warp's next tile (each call takes one step of tstep).  grad_w: fts x nts tiles a group; ft by the
+  // reciprocal, whose error (512 x 2^-22 at most 512 tiles along K and along N) stays below half a tile's share.
+  TileWalk walk;
+  const float per_nts = 1.0f / (float)nts;
+  int gw_group = 0, gw_local = tile0;
   const auto tile_of = [&](int tile) {
-    if constexpr (!kGradW) return decode_product_tile<kMaxRows>(tile, tab, p.E);
+    if constexpr (!kGradW) return walk.at(tile, tab, p.E, lane);
+    while (gw_local >= nts * fts) {
+      gw_local -= nts * fts;
+      ++gw_group;
+    }
     ProductTile t;
-    t.g = tile / (nts * fts);
-    const int local = tile - t.g * (nts * fts);
-    t.ft = local / nts;
-    t.lrow0 = (local - t.ft * nts) * kMaxRows;
+    t.g = gw_group;
+    t.ft = (int)(((float)gw_local + 0.5f) * per_nts);
+    t.lrow0 = (gw_local - t.ft * nts) * kMaxRows;
     t.row0 = 0;
     t.valid = min(kMaxRows, p.Kc - t.lrow0);
+    gw_local += tstep;
     return t;
   };
-  const auto sum_len = [&](const ProductTile& t) { return kGradW ? tab.nrows[t.g] : p.Kc; };
+  const auto sum_len = [&](const ProductTile& t) { return kGradW ? uniform(tab.nrows[t.g]) : p.Kc; };
   // grad_w takes the sum's last, shorter block first, so that it is cleared while the MMAs of the tile before
   // still run.  Steps of the sum in block kb, where it starts, and whether rows behind it are read and so
   // cleared.
@@ -265,21 +275,21 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU>::kThreads, 1)
     bool ok = true;
     for (int tile = tile0; tile < total && ok; tile += tstep) {
       const ProductTile t = tile_of(tile);
-      const int n = uniform(mma_rows(t)), len = uniform(sum_len(t)), g = uniform(t.g);
+      const int n = mma_rows(t), len = sum_len(t), g = t.g;
       const int nkb = (len + S::kBlock - 1) / S::kBlock;
-      const int f0 = uniform(t.ft * 256 + (int)rank * 128);      // this SM's first feature
-      const int r0 = uniform(t.row0 + (int)rank * (n / 2));      // and row
+      const int f0 = t.ft * 256 + (int)rank * 128;      // this SM's first feature
+      const int r0 = t.row0 + (int)rank * (n / 2);      // and row
       const bool two = two_scale_tiles(t, n);
       // bytes of a stage: MN-major rows come in whole boxes
       const uint32_t bytes =
-          uniform(S::kOpA + (kBMn ? (n / 2 + 63) / 64 * kBox64 : n / 2 * 128) + S::kSums * S::kSfA +
-                  (two ? S::kSfB : S::kSfB / 2));
-      const int w0 = uniform(g * p.wrows);                       // micro: the expert's first weight row
-      const int st_w = uniform(((w0 >> 7) + g + (f0 >> 7)) * p.ktiles);
-      const int st_u = uniform(((w0 >> 7) + g + ((p.F + f0) >> 7)) * p.ktiles);  // its W3
-      const int st_r = uniform(((tab.row0[g] >> 7) + g + (t.lrow0 >> 7)) * p.ktiles);
-      const int gw_n = uniform(t.lrow0 + (int)rank * (n / 2)), gw_r = uniform(tab.row0[g]);
-      const CUtensorMap* mrow = &p.mrow[uniform(n / 32 - 1)];
+          S::kOpA + (kBMn ? (n / 2 + 63) / 64 * kBox64 : n / 2 * 128) + S::kSums * S::kSfA +
+          (two ? S::kSfB : S::kSfB / 2);
+      const int w0 = g * p.wrows;                       // micro: the expert's first weight row
+      const int st_w = ((w0 >> 7) + g + (f0 >> 7)) * p.ktiles;
+      const int st_u = ((w0 >> 7) + g + ((p.F + f0) >> 7)) * p.ktiles;  // its W3
+      const int st_r = (((t.row0 - t.lrow0) >> 7) + g + (t.lrow0 >> 7)) * p.ktiles;
+      const int gw_n = t.lrow0 + (int)rank * (n / 2), gw_r = kGradW ? uniform(tab.row0[g]) : 0;
+      const CUtensorMap* mrow = &p.mrow[n / 32 - 1];
       for (int kb = 0; kb < nkb; ++kb) {
         ok = __all_sync(~0u, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err));
         if (!ok) break;
@@ -352,14 +362,14 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU>::kThreads, 1)
     bool ok = true;
     for (int tile = tile0; tile < total && ok; tile += tstep) {
       const ProductTile t = tile_of(tile);
-      const int n = uniform(mma_rows(t)), len = uniform(sum_len(t));
+      const int n = mma_rows(t), len = sum_len(t);
       const int nkb = (len + S::kBlock - 1) / S::kBlock;
       if (kGradW && nkb == 0) continue;  // a group without rows: the epilogue writes zeros
       if (!__all_sync(~0u, mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, abort_flag, p.err))) break;
       tc_fence_after();
       const bool two = two_scale_tiles(t, n);
       const uint32_t d = tmem_base + acc * S::kAccCols;
-      const uint32_t b_col = uniform((t.lrow0 & 127) >> 5);  // micro: the tile's first row's scale column
+      const uint32_t b_col = (t.lrow0 & 127) >> 5;  // micro: the tile's first row's scale column
       const uint32_t idesc = idesc_bf16_f32_pair(n) | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u);
       for (int kb = 0; kb < nkb; ++kb) {
         const int left = block_len(len, kb);
@@ -430,7 +440,7 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU>::kThreads, 1)
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     for (int tile = tile0; tile < total && ok; tile += tstep) {
-      const int len = uniform(sum_len(tile_of(tile)));
+      const int len = sum_len(tile_of(tile));
       for (int kb = 0; kb * S::kBlock < len; ++kb) {
         const int left = block_len(len, kb);
         if (to_clear(left)) {

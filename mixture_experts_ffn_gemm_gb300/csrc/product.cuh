@@ -15,14 +15,15 @@ struct GroupTable {
   int* tile_start;  // [G + 1] first tile of each group; [G]: all tiles
   int* row0;        // [G]     first row
   int* nrows;       // [G]     rows
+  int* cut;         // [G]     row tiles * 8 + (rows of one) / 64
 };
 
-// Rows of each of a group's row tiles: as few tiles as hold `rows` in at most kMaxRows each, of about the
-// same size, cut at multiples of 64 rows.
+// A group's row tiles: as few as hold `rows` in at most kMaxRows each, of about the same size, cut at
+// multiples of 64 rows.
 template <int kMaxRows>
-__device__ __forceinline__ int tile_rows(int rows) {
+__device__ __forceinline__ int cut_rows(int rows) {
   const int n = (rows + kMaxRows - 1) / kMaxRows;
-  return ((rows + n - 1) / n + 63) & ~63;
+  return n * 8 + (n ? ((rows + n - 1) / n + 63) / 64 : 0);
 }
 
 // Block-wide (blockDim.x threads, scratch of as many ints); ends with __syncthreads().  A group has
@@ -43,7 +44,9 @@ __device__ __forceinline__ void build_group_table(const GroupTable& t, int* scra
     if (a2 != a || z2 != z) raise_flag(err, kErrIndex);
     t.row0[g] = a2;
     t.nrows[g] = z2 - a2;
-    const int n = (z2 - a2 + kMaxRows - 1) / kMaxRows * feat_tiles;
+    const int cut = cut_rows<kMaxRows>(z2 - a2);
+    t.cut[g] = cut;
+    const int n = (cut >> 3) * feat_tiles;
     t.tile_start[g] = n;  // count for now
     local += n;
   }
@@ -73,30 +76,6 @@ struct ProductTile {
   int lrow0;  // row0 within the group
 };
 
-// A group's tiles are numbered feature tile by feature tile, the row tiles inside: neighbouring CTAs
-// share one weight tile, and the weights stream from memory once.
-template <int kMaxRows>
-__device__ __forceinline__ ProductTile decode_product_tile(int tile, const GroupTable& t, int G) {
-  int lo = 0, hi = G - 1;  // largest g with tile_start[g] <= tile (empty groups share starts)
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.tile_start[mid] <= tile)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  const int rows = t.nrows[lo];
-  const int nrt = (rows + kMaxRows - 1) / kMaxRows, rpt = tile_rows<kMaxRows>(rows);
-  const int local = tile - t.tile_start[lo];
-  ProductTile p;
-  p.g = lo;
-  p.ft = local / nrt;
-  p.lrow0 = (local - p.ft * nrt) * rpt;
-  p.row0 = t.row0[lo] + p.lrow0;
-  p.valid = min(rpt, rows - p.lrow0);
-  return p;
-}
-
 // One thread of the (converged) warp.  The compiler knows that the branch holds a single thread, and keeps
 // what tcgen05 and TMA instructions take from uniform registers there; after `lane == 0` it moves every
 // operand into them, one by one, for each instruction.
@@ -110,6 +89,35 @@ __device__ __forceinline__ bool elect_one() {
 
 // The same value in every lane, as the compiler is to see it.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(~0u, v, 0); }
+
+// The tiles of one warp, in increasing order.  A group's tiles are numbered feature tile by feature tile, the
+// row tiles inside: neighbouring SMs share one weight tile, and the weights stream from memory once.
+// A step looks at the starts of the next 32 groups at once (a search from the first group would cost a tile of
+// a short sum as much as its MMAs).  The whole warp takes part, and all of it gets the same values.
+struct TileWalk {
+  int g = 0;
+  __device__ __forceinline__ ProductTile at(int tile, const GroupTable& t, int G, int lane) {
+    for (;;) {  // g: the last group that starts at `tile` or before
+      const int next = g + 1 + lane;
+      const uint32_t past = __ballot_sync(~0u, next < G && t.tile_start[min(next, G)] <= tile);
+      g += __popc(past);
+      if (past != ~0u) break;
+    }
+    ProductTile p;
+    p.g = g;
+    const int cut = uniform(t.cut[g]), local = tile - uniform(t.tile_start[g]);
+    const int rows = uniform(t.nrows[g]), rpt = (cut & 7) * 64, nrt = cut >> 3;
+    p.ft = local;
+    p.lrow0 = 0;
+    if (nrt > 1) {
+      p.ft = local / nrt;
+      p.lrow0 = (local - p.ft * nrt) * rpt;
+    }
+    p.row0 = uniform(t.row0[g]) + p.lrow0;
+    p.valid = min(rpt, rows - p.lrow0);
+    return p;
+  }
+};
 
 // TMA copy of a 3D box into this CTA's shared memory of a pair, completion counted on the barrier at
 // shared::cluster address `bar_cluster`.
