@@ -33,7 +33,9 @@
  *     word of the workspace, read with moe_device_status().
  *   - Layouts are row-major.  Weights are stored [out][in] as on the pages ("The reference module
  *     holds the weight output by input"), i.e. K-contiguous.
- *   - Every pointer must be 16-byte aligned; every row pitch is the row's width (no padding).
+ *   - Every pointer must be 16-byte aligned; every row pitch is the row's width (no padding), but for
+ *     the entry points that take pitches (moe_block_join, the products grouped by expert, the
+ *     microscaled operators).
  *   - Errors are return codes; nothing is launched when host validation fails.
  *   - T == 0 is valid: once the configuration and workspace pass validation every entry point
  *     returns MOE_OK without touching any other pointer (empty tensors may be NULL).
@@ -377,8 +379,8 @@ moe_status_t moe_block_join(const moe_join_config_t* cfg, const void* resid, con
  *           from offsets[E] on belong to no expert: they are not read into any result and their
  *           outputs are left as they are.  An expert without rows has a dW of zeros.
  *   N and K are multiples of 8 up to 131072, E is at most 1023, rows at most 2^26; ld_x and ld_y are the
- *           row pitches in elements of the [rows][K] and [rows][N] buffers (0: K, N), multiples of 8.
- *           Pointers are 16-byte aligned.  W and dW are dense.
+ *           row pitches in elements of the [rows][K] and [rows][N] buffers (0: K, N), multiples of 8
+ *           up to 2^32.  Pointers are 16-byte aligned.  W and dW are dense.
  *   MOE_PRODUCT_ACCUMULATE (GRAD_W with fp32 outputs): dW is added onto what `out` holds.
  *   ws      moe_product_workspace_size() bytes; its first word is the device status.  The call raises
  *           flags there and clears none (moe_reset_device_status does), so one status can watch a run
@@ -436,7 +438,7 @@ typedef struct {
   int32_t groups;   /* 1 .. 1023                                                                   */
   int32_t copies;   /* quantise: coded rows of each row of x, 1 .. MOE_MICRO_MAX_COPIES            */
   uint32_t flags;   /* 0                                                                           */
-  int64_t ld;       /* row pitch of x or the values in elements (0: K), a multiple of 8            */
+  int64_t ld;       /* row pitch of x or the values in elements (0: K), a multiple of 8 up to 2^32 */
 } moe_micro_config_t;
 /* Bytes of the scales (0 for an invalid configuration). */
 size_t moe_micro_scales_size(const moe_micro_config_t* cfg);
@@ -465,7 +467,7 @@ moe_status_t moe_micro_dequantize(const moe_micro_config_t* cfg, const void* cod
  *   a, a_scales  codes and scales of [rows][K], groups by offsets [E+1] (moe_micro_quantize)
  *   w, w_scales  codes and scales of [E * (N or 2N)][K] in E groups (moe_micro_quantize with offsets NULL)
  *   a_factor     g_a, one fp32; w_factor g_w [E] fp32; MOE_MICRO_NV only, NULL: 1
- *   out          [rows][N], pitch ld_out elements (0: N), a multiple of 8
+ *   out          [rows][N], pitch ld_out elements (0: N), a multiple of 8 up to 2^32
  *   ws           moe_micro_product_workspace_size() bytes, the device status as for moe_grouped_product
  * N is a multiple of 8 up to 131072, K of 64, E at most 1023, rows at most 2^26.  Rows from offsets[E] on
  * are left as they are; rows == 0 is a no-op.  Equal calls give equal bits. */

@@ -238,19 +238,22 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU>::kThreads, 1)
   const float per_nts = 1.0f / (float)nts;
   int gw_group = 0, gw_local = tile0;
   const auto tile_of = [&](int tile) {
-    if constexpr (!kGradW) return walk.at(tile, tab, p.E, lane);
-    while (gw_local >= nts * fts) {
-      gw_local -= nts * fts;
-      ++gw_group;
+    if constexpr (kGradW) {
+      while (gw_local >= nts * fts) {
+        gw_local -= nts * fts;
+        ++gw_group;
+      }
+      ProductTile t;
+      t.g = gw_group;
+      t.ft = (int)(((float)gw_local + 0.5f) * per_nts);
+      t.lrow0 = (gw_local - t.ft * nts) * kMaxRows;
+      t.row0 = 0;
+      t.valid = min(kMaxRows, p.Kc - t.lrow0);
+      gw_local += tstep;
+      return t;
+    } else {
+      return walk.at(tile, tab, p.E, lane);
     }
-    ProductTile t;
-    t.g = gw_group;
-    t.ft = (int)(((float)gw_local + 0.5f) * per_nts);
-    t.lrow0 = (gw_local - t.ft * nts) * kMaxRows;
-    t.row0 = 0;
-    t.valid = min(kMaxRows, p.Kc - t.lrow0);
-    gw_local += tstep;
-    return t;
   };
   const auto sum_len = [&](const ProductTile& t) { return kGradW ? uniform(tab.nrows[t.g]) : p.Kc; };
   // grad_w takes the sum's last, shorter block first, so that it is cleared while the MMAs of the tile before

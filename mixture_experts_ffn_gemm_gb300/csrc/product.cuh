@@ -26,7 +26,7 @@ __device__ __forceinline__ int cut_rows(int rows) {
   return n * 8 + (n ? ((rows + n - 1) / n + 63) / 64 : 0);
 }
 
-// Block-wide (blockDim.x threads, scratch of as many ints); ends with __syncthreads().  A group has
+// Block-wide (scratch: an int a warp); ends with __syncthreads().  A group has
 // feat_tiles tiles for each of its row tiles.
 template <int kMaxRows>
 __device__ __forceinline__ void build_group_table(const GroupTable& t, int* scratch,
@@ -50,21 +50,23 @@ __device__ __forceinline__ void build_group_table(const GroupTable& t, int* scra
     t.tile_start[g] = n;  // count for now
     local += n;
   }
-  scratch[threadIdx.x] = local;
-  __syncthreads();
-  for (int off = 1; off < nt; off <<= 1) {  // inclusive scan of the threads' sums
-    const int v = threadIdx.x >= off ? scratch[threadIdx.x - off] : 0;
-    __syncthreads();
-    scratch[threadIdx.x] += v;
-    __syncthreads();
+  // inclusive scan of the threads' sums: within the warps, then over the warps' totals
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int sum = local;
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(~0u, sum, off);
+    if (lane >= off) sum += v;
   }
-  int run = scratch[threadIdx.x] - local;
+  if (lane == 31) scratch[warp] = sum;
+  __syncthreads();
+  int run = sum - local;  // tiles before this thread's first group
+  for (int w = 0; w < warp; ++w) run += scratch[w];
+  if (threadIdx.x == nt - 1) t.tile_start[G] = run + local;
   for (int g = lo; g < hi; ++g) {
     const int n = t.tile_start[g];
     t.tile_start[g] = run;
     run += n;
   }
-  if (threadIdx.x == nt - 1) t.tile_start[G] = scratch[nt - 1];
   __syncthreads();
 }
 

@@ -48,7 +48,7 @@ bool aligned(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u)
 constexpr int64_t kMaxRows = (int64_t)1 << 26;
 constexpr int32_t kMaxWidth = 131072;
 constexpr int32_t kMaxGroups = 1023;
-constexpr int64_t kMaxPitch = (int64_t)1 << 36;
+constexpr int64_t kMaxPitch = (int64_t)1 << 32;  // a buffer's bytes stay within 2^60
 constexpr size_t kStatusBytes = 256;
 
 moe_status_t check_ws(void* ws, size_t ws_bytes, size_t need) {

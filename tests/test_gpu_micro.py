@@ -425,3 +425,73 @@ def test_a_layer_of_microscaled_experts(cuda_device, fmt):
     total = terms.sum(1)
     # k products and k sums in fp32, then half a step
     assert ((out.double() - total).abs() <= 2.0 ** -8 * total.abs() + 2 * k * 2.0 ** -24 * terms.abs().sum(1)).all()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_nan_rows_and_weights_stay_their_own(cuda_device, fmt, swiglu):
+    """A NaN channel makes its row's outputs NaN and no other row's; a NaN weight block its expert's column."""
+    K, N, counts = 256, 128, [40, 70, 9]
+    offs, E = offsets_of(counts), len(counts)
+    g = torch.Generator().manual_seed(4)
+    per = 2 * N if swiglu else N
+    x = torch.randn(offs[-1], K, generator=g).to(BF16)
+    w = (torch.randn(E * per, K, generator=g) / 16).to(BF16)
+
+    def run(x, w):
+        cx = B.make_micro_config(offs[-1], K, fmt, groups=E)
+        cw = B.make_micro_config(E * per, K, fmt, groups=E)
+        bx, bw = B.alloc_micro(cx), B.alloc_micro(cw)
+        ws = B.alloc_micro_workspace(cx)
+        B.moe_micro_quantize(cx, x.cuda(), None, gpu(offs), None, *bx, ws)
+        B.moe_micro_quantize(cw, w.cuda(), None, None, None, *bw, ws)
+        out = torch.zeros(offs[-1], N, device="cuda")
+        cfg = B.make_micro_product_config(offs[-1], E, N, K, fmt, F32, swiglu)
+        B.moe_micro_product(cfg, gpu(offs), *bx, None, *bw, None, out, ws)
+        assert B.moe_device_status(ws) == B.MOE_OK
+        return out.cpu()
+
+    clean = run(x, w)
+    assert torch.isfinite(clean).all()
+    x2, w2 = x.clone(), w.clone()
+    x2[50, 77] = float("nan")
+    x2[0, 3] = float("inf")
+    w2[2 * per + 5, 200] = float("nan")
+    got = run(x2, w2)
+    bad = torch.zeros_like(clean, dtype=torch.bool)
+    bad[50], bad[0] = True, True
+    bad[offs[2]:, 5] = True
+    assert torch.equal(torch.isnan(got), bad)
+    assert torch.equal(got[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_two_streams_at_once(cuda_device, fmt):
+    """Two products and quantisations under way together, each on its own workspace, give what they give
+    alone."""
+    counts = [300, 0, 17, 450]
+    offs, E, N, K = offsets_of(counts), len(counts), 512, 1024
+    g = torch.Generator().manual_seed(6)
+    w, sw, _ = _operand(g, [e * N for e in range(E + 1)], K, fmt)
+    xs = [torch.randn(offs[-1], K, generator=g).to(BF16).cuda() for _ in range(2)]
+    cx = B.make_micro_config(offs[-1], K, fmt, groups=E)
+    cfg = B.make_micro_product_config(offs[-1], E, N, K, fmt)
+    o = gpu(offs)
+
+    def go(x, stream, buf, ws, out):
+        B.moe_micro_quantize(cx, x, None, o, None, *buf, ws, stream=stream)
+        B.moe_micro_product(cfg, o, *buf, None, w, sw, None, out, ws, stream=stream)
+
+    state = [(B.alloc_micro(cx), B.alloc_micro_workspace(cx), torch.zeros(offs[-1], N, dtype=BF16, device="cuda"))
+             for _ in range(4)]
+    for i in range(2):
+        go(xs[i], None, *state[i])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for i in range(2):
+            go(xs[i], streams[i], *state[2 + i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(state[i][2], state[2 + i][2])
+        assert B.moe_device_status(state[2 + i][1]) == B.MOE_OK

@@ -53,7 +53,7 @@ def _product(lib, ptrs=(P,) * 4, ws=P, ws_bytes=256, **kw):
     (dict(rows=-1), B.MOE_ERR_INVALID_ARG), (dict(E=0), B.MOE_ERR_INVALID_ARG),
     (dict(N=0), B.MOE_ERR_INVALID_ARG), (dict(K=-8), B.MOE_ERR_INVALID_ARG),
     (dict(ld_x=120), B.MOE_ERR_INVALID_ARG), (dict(ld_x=132), B.MOE_ERR_INVALID_ARG),
-    (dict(ld_y=60), B.MOE_ERR_INVALID_ARG), (dict(ld_y=2 ** 40), B.MOE_ERR_INVALID_ARG),
+    (dict(ld_y=60), B.MOE_ERR_INVALID_ARG), (dict(ld_y=2 ** 32 + 8), B.MOE_ERR_INVALID_ARG),
     (dict(rows=2 ** 26 + 1), B.MOE_ERR_UNSUPPORTED), (dict(E=1024), B.MOE_ERR_UNSUPPORTED),
     (dict(N=60), B.MOE_ERR_UNSUPPORTED), (dict(K=100), B.MOE_ERR_UNSUPPORTED),
     (dict(K=131080), B.MOE_ERR_UNSUPPORTED), (dict(out_dtype=U8), B.MOE_ERR_INVALID_ARG),
