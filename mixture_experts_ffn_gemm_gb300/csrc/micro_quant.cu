@@ -39,6 +39,7 @@ struct MicroParams {
   int64_t ld;
   int64_t src_rows, rows;
   int32_t K, G, group_rows, copies, parts, ktiles;
+  int32_t wide;              // x or the values: rows at multiples of 32 bytes, which one access takes
 };
 
 // Where the scales of `n` rows (lane j's `row`, j < n <= kMaxCopies) start, in lane j: a group's first
@@ -140,6 +141,27 @@ __device__ __forceinline__ uint32_t settle(uint32_t a, uint32_t b, float ax, flo
   return r > 0.0f || (r == 0.0f && (a & 1u)) ? b : a;
 }
 
+__device__ __forceinline__ void load32(const uint4* p, bool wide, uint4& a, uint4& b) {
+  if (wide) {
+    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+        : "l"(p));
+  } else {
+    a = __ldg(p);
+    b = __ldg(p + 1);
+  }
+}
+__device__ __forceinline__ void store32(void* p, bool wide, const uint32_t (&v)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
 // 16 channels: their magnitude's largest as an integer (NaN and infinities compare above every finite
 // value) and the values.
 template <bool kF32>
@@ -224,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 2) micro_quantize_kernel(const Micro
   int c = part * 32 + lane;
   if (c < chunks) {  // the first loads are under way while the rows' groups are found
 #pragma unroll
-    for (int q = 0; q < kRaw; ++q) raw[q] = __ldg(src + (int64_t)c * kRaw + q);
+    for (int q = 0; q < kRaw; q += 2) load32(src + (int64_t)c * kRaw + q, p.wide, raw[q], raw[q + 1]);
   }
   float g = 1.0f;
   bool bad_factor = false;
@@ -256,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 2) micro_quantize_kernel(const Micro
     c += p.parts * 32;
     if (c < chunks) {
 #pragma unroll
-      for (int q = 0; q < kRaw; ++q) raw[q] = __ldg(src + (int64_t)c * kRaw + q);
+      for (int q = 0; q < kRaw; q += 2) load32(src + (int64_t)c * kRaw + q, p.wide, raw[q], raw[q + 1]);
     }
     if constexpr (!kNv) {
       const uint32_t top = max(t0, t1), e = top >> 23;
@@ -312,10 +334,21 @@ __global__ void __launch_bounds__(kThreads) micro_dequantize_kernel(const MicroP
   const int64_t sb = __shfl_sync(~0u, scale_base(p, (int)row, 1, lane), 0);
   if (sb < 0) return;
   const int chunks = p.K / 16;
-  for (int c = part * 32 + lane; c < chunks; c += p.parts * 32) {
-    const uint2 q = __ldg(reinterpret_cast<const uint2*>(p.codes + row * (p.K / 2)) + c);
+  const auto fetch = [&](int c, uint2& q, uint32_t& sc) {
     const int col = kNv ? c : c >> 1;
-    const uint32_t sc = __ldg(p.scales + sb + (int64_t)(col >> 2) * 512 + (col & 3));
+    q = __ldg(reinterpret_cast<const uint2*>(p.codes + row * (p.K / 2)) + c);
+    sc = __ldg(p.scales + sb + (int64_t)(col >> 2) * 512 + (col & 3));
+  };
+  uint2 next;
+  uint32_t next_sc;
+  int c = part * 32 + lane;
+  if (c < chunks) fetch(c, next, next_sc);
+  while (c < chunks) {
+    const uint2 q = next;
+    const uint32_t sc = next_sc;
+    const int here = c;
+    c += p.parts * 32;
+    if (c < chunks) fetch(c, next, next_sc);
     float s;
     if (kNv)
       s = e4m3_value(sc);
@@ -339,16 +372,18 @@ __global__ void __launch_bounds__(kThreads) micro_dequantize_kernel(const MicroP
         v[2 * b + 1] *= g;
       }
     }
-    if (kF32) {
-      float* dst = static_cast<float*>(const_cast<void*>(p.x)) + row * p.ld + (int64_t)c * 16;
-      store8(dst, reinterpret_cast<const float(&)[8]>(v[0]));
-      store8(dst + 8, reinterpret_cast<const float(&)[8]>(v[8]));
+    uint8_t* dst = static_cast<uint8_t*>(const_cast<void*>(p.x)) +
+                   (row * p.ld + (int64_t)here * 16) * (kF32 ? 4 : 2);
+    uint32_t u[kF32 ? 16 : 8];
+    if constexpr (kF32) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i]);
+      store32(dst + 32, p.wide, reinterpret_cast<const uint32_t(&)[8]>(u[8]));
     } else {
-      __nv_bfloat16* dst =
-          static_cast<__nv_bfloat16*>(const_cast<void*>(p.x)) + row * p.ld + (int64_t)c * 16;
-      store8(dst, reinterpret_cast<const float(&)[8]>(v[0]));
-      store8(dst + 8, reinterpret_cast<const float(&)[8]>(v[8]));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
     }
+    store32(dst, p.wide, reinterpret_cast<const uint32_t(&)[8]>(u[0]));
   }
 }
 
@@ -369,13 +404,15 @@ MicroParams params(const MicroOp& m) {
   p.group_rows = (int32_t)(m.rows / m.groups);
   p.copies = m.copies;
   p.ktiles = m.ktiles;
+  p.wide = ((reinterpret_cast<uintptr_t>(m.x) | (uint64_t)m.ld * (m.dtype == MOE_F32 ? 4 : 2)) & 31) == 0;
   return p;
 }
 
-// Warps for a row: one, or as many as fill the GPU when there are few rows.
+// Warps for a row: as many as give the GPU 64 warps an SM (a few waves of them, whose ends then overlap),
+// at most one for each 32 lanes' channels.
 int row_parts(int64_t rows, int K, int lane_channels, int sms) {
   const int64_t most = (K / lane_channels + 31) / 32;
-  int64_t n = (int64_t)sms * 16 / (rows > 0 ? rows : 1);
+  int64_t n = (int64_t)sms * 64 / (rows > 0 ? rows : 1);
   return (int)(n < 1 ? 1 : n > most ? most : n);
 }
 
