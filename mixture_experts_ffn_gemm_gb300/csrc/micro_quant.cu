@@ -6,10 +6,11 @@
 //   MOE_MICRO_NV  B = 16, S = s g, s = e4m3(amax / (6 g)) rounded to nearest, g a factor of the tensor.
 // c is x / S rounded to nearest, ties to the even code, at most 6.  Both roundings are those of the
 // exact quotient: MX divides by a power of two, which is exact.  NV rounds the quotient's fp32
-// approximation (relative error below 2^-22: S, 1 / S and the product round by 2^-24 each) moved by
-// 2^-21 either way; where both moved values give one code it is the exact quotient's too, and where
-// they do not, the sign of |x| - m s g decides, m the midpoint between the two codes: m s has at most
-// seven bits and is exact, and one fma keeps the sign of the difference.
+// approximation (1 / g rounds by 2^-24, the approximate division by s by at most two steps of 2^-23, the
+// products by 2^-24 each: below 2^-21 together) moved by 2^-20 either way; where both moved values give one
+// code it is the exact quotient's too, and where they do not, the sign of |x| - m s g decides, m the midpoint
+// between the two codes: m s has at most seven bits and is exact, and one fma keeps the sign of the
+// difference.
 //
 // Bound by memory: a row is read once and its codes (K / 2 bytes) and scales (K / B) are written to
 // each row that takes it, so the experts' copies of a token are quantised once and written k times.
@@ -115,12 +116,12 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
   return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
 }
 
-constexpr float kLess = 1.0f - 4.76837158203125e-7f;  // 1 - 2^-21
-constexpr float kMore = 1.0f + 4.76837158203125e-7f;
+constexpr float kLess = 1.0f - 0x1p-20f;
+constexpr float kMore = 1.0f + 0x1p-20f;
 
-// e4m3 code of amax / (6 g), rounded as the exact quotient.
-__device__ __forceinline__ uint32_t nv_scale(float amax, float g) {
-  const float q = amax / (6.0f * g);
+// e4m3 code of amax / (6 g), rounded as the exact quotient; per6g = RN(1 / RN(6 g)).
+__device__ __forceinline__ uint32_t nv_scale(float amax, float g, float per6g) {
+  const float q = amax * per6g;
   const uint32_t pair = e4m3x2(q * kLess, q * kMore);
   const uint32_t lo = pair & 0xffu, hi = pair >> 8;
   if (lo == hi) return lo;
@@ -198,10 +199,10 @@ __device__ __forceinline__ uint2 codes_mx(float (&v)[16], float inv) {
   return make_uint2(e2m1x8(v), e2m1x8(v + 8));
 }
 
-// Codes of a block of 16 with the scale s g (s > 0): by both moved quotients, and by the exact difference
-// where they disagree.
-__device__ __forceinline__ uint2 codes_nv(const float (&v)[16], float s, float g) {
-  const float inv = s > 0.0f ? 1.0f / (s * g) : 0.0f;
+// Codes of a block of 16 with the scale s g (all zero for s = 0): by both moved quotients, and by the exact
+// difference where they disagree.
+__device__ __forceinline__ uint2 codes_nv(const float (&v)[16], float s, float g, float per_g) {
+  const float inv = s > 0.0f ? __fdividef(per_g, s) : 0.0f;
   const float il = inv * kLess, ih = inv * kMore;
   float a[16];
 #pragma unroll
@@ -229,7 +230,7 @@ struct CopyTo {  // where a copy of the row starts
 };
 
 template <bool kNv, bool kF32>
-__global__ void __launch_bounds__(kThreads, 2) micro_quantize_kernel(const MicroParams p) {
+__global__ void __launch_bounds__(kThreads, kF32 ? 2 : 3) micro_quantize_kernel(const MicroParams p) {
   __shared__ CopyTo to_all[kThreads / 32][kMaxCopies];
   const int lane = threadIdx.x & 31;
   CopyTo* to = to_all[threadIdx.x >> 5];
@@ -255,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 2) micro_quantize_kernel(const Micro
     bad_factor = !(g >= 0x1p-100f && g <= 0x1p100f);
     if (bad_factor && lane == 0) raise_flag(p.err, kErrIndex);
   }
+  const float per_g = 1.0f / g, per6g = 1.0f / (6.0f * g);
   int copies;
   {
     int row = -1;
@@ -273,14 +275,17 @@ __global__ void __launch_bounds__(kThreads, 2) micro_quantize_kernel(const Micro
 #pragma unroll
       for (int q = 0; q < kRaw; ++q) raw[q] = make_uint4(0, 0, 0, 0);
     }
-    float v0[16], v1[16];
-    uint32_t t0 = unpack16<kF32>(raw, v0), t1 = unpack16<kF32>(raw + kRaw / 2, v1);
+    uint4 now[kRaw];
+#pragma unroll
+    for (int q = 0; q < kRaw; ++q) now[q] = raw[q];
     c += p.parts * 32;
     if (c < chunks) {
 #pragma unroll
       for (int q = 0; q < kRaw; q += 2) load32(src + (int64_t)c * kRaw + q, p.wide, raw[q], raw[q + 1]);
     }
     if constexpr (!kNv) {
+      float v0[16], v1[16];
+      const uint32_t t0 = unpack16<kF32>(now, v0), t1 = unpack16<kF32>(now + kRaw / 2, v1);
       const uint32_t top = max(t0, t1), e = top >> 23;
       const bool nan = e == 255u;
       scale = nan ? 255u : top == 0 ? 127u : e > 2u ? e - 2u : 0u;
@@ -293,30 +298,27 @@ __global__ void __launch_bounds__(kThreads, 2) micro_quantize_kernel(const Micro
     } else {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t top = h ? t1 : t0;
+        float v[16];
+        const uint32_t top = unpack16<kF32>(now + h * (kRaw / 2), v);
         const bool nan = bad_factor || (top >> 23) == 255u;
-        const uint32_t sc = nan ? 0x7fu : nv_scale(__uint_as_float(top), g);
-        const uint2 a = codes_nv(h ? v1 : v0, nan ? 0.0f : e4m3_value(sc), g);
+        const uint32_t sc = nan ? 0x7fu : nv_scale(__uint_as_float(top), g, per6g);
+        const uint2 a = codes_nv(v, nan ? 0.0f : e4m3_value(sc), g, per_g);
         code[2 * h] = nan ? 0u : a.x;
         code[2 * h + 1] = nan ? 0u : a.y;
         scale = h ? scale | sc << 8 : sc;
       }
     }
-    // the scales of 64 channels (two lanes) leave in one store
-    const uint32_t packed = scale | __shfl_down_sync(~0u, scale, 1) << (kNv ? 16 : 8);
+    // a tile's four columns leave in one store: two lanes' scales (NV), or four lanes' (MX; of the last tile
+    // two may lie behind K)
+    uint32_t packed = scale | __shfl_down_sync(~0u, scale, 1) << (kNv ? 16 : 8);
+    if (!kNv) packed |= __shfl_down_sync(~0u, packed, 2) << 16;
     const int at = c - p.parts * 32;           // this chunk
-    const int col = at * (kNv ? 2 : 1);        // and its first scale
-    const int64_t code_off = (int64_t)at * 16, scale_off = (int64_t)(col >> 2) * 512 + (col & 3);
+    const int64_t code_off = (int64_t)at * 16, scale_off = (int64_t)(at >> (kNv ? 1 : 2)) * 512;
     if (in) {
       for (int j = 0; j < copies; ++j) {
         const CopyTo d = to[j];
         *reinterpret_cast<uint4*>(d.codes + code_off) = make_uint4(code[0], code[1], code[2], code[3]);
-        if (!(lane & 1)) {
-          if (kNv)
-            *reinterpret_cast<uint32_t*>(d.scales + scale_off) = packed;
-          else
-            *reinterpret_cast<uint16_t*>(d.scales + scale_off) = (uint16_t)packed;
-        }
+        if ((lane & (kNv ? 1 : 3)) == 0) *reinterpret_cast<uint32_t*>(d.scales + scale_off) = packed;
       }
     }
   }
