@@ -36,6 +36,11 @@
 // g and u of an output in one thread; their 2 x 192 columns leave no room for a second pair of sums, so the
 // epilogue is not hidden behind the next tile there, and its reads free the columns as early as they can.
 //
+// Sums: the tensor cores cut what falls behind the sum's 24 bits at every MMA, always towards zero, so that
+// a long sum drifts by about 2^-25.5 of itself a step (5 x 10^-6 over 448 steps).  For fp32 outputs a sum stays
+// in tensor memory for 32 steps; the storing warps add such segments up in fp32, rounded to nearest.  A bf16
+// output's rounding is a thousand times that drift.
+//
 // Kernel shape: persistent, warp 0 copies, warp 1 issues (on the pair's even SM), warps 2..9 store: a lane
 // has a feature, so that a warp's store covers 128 (fp32) or 2 x 64 (bf16) consecutive bytes of rows.  dW
 // leaves through shared memory and TMA (for ACCUMULATE its fp32 addition, one for each element).
@@ -59,13 +64,14 @@ constexpr int kSmemMost = 232448 - 1024 - kBarBytes - kTable;
 
 enum Op { OP_FORWARD, OP_GRAD_X, OP_GRAD_W, OP_MX, OP_NV };
 
-template <int kOp, bool kSwiGLU>
+template <int kOp, bool kSwiGLU, bool kF32>
 struct Shape {
   static constexpr bool kMicro = kOp == OP_MX || kOp == OP_NV;
-  static constexpr int kMaxRows = kMicro ? 192 : 256;      // rows of a tile
+  static constexpr int kMaxRows = !kMicro ? 256 : kSwiGLU && kF32 ? 128 : 192;  // rows of a tile
   static constexpr int kBlock = kMicro ? 256 : 64;         // elements of the sum per stage
   static constexpr int kStep = kMicro ? 64 : 16;           // and per MMA
   static constexpr int kSums = kSwiGLU ? 2 : 1;            // W1 and W3, or one
+  static constexpr int kSegment = kF32 ? 8 : 1 << 30;      // blocks summed in tensor memory at a time
   static constexpr int kTiles = kOp == OP_NV ? 4 : kOp == OP_MX ? 2 : 0;  // scale tiles per 128 rows
   static constexpr int kOpA = kSums * kBox;
   static constexpr int kOpB = kMaxRows / 2 * 128;
@@ -154,6 +160,22 @@ __device__ __forceinline__ void mma_micro_pair(uint32_t d, uint64_t a, uint64_t 
         : "memory");
 }
 
+// A chunk of 32 rows of dW x 64 bytes, lane l holding row l's, through 2 KB of shared memory (in the 64-byte
+// swizzle) to TMA, which leaves out what lies behind dW's last row or column.  The whole warp.
+template <bool kAdd>
+__device__ __forceinline__ void store_dw(const CUtensorMap* map, uint8_t* buf, int lane,
+                                         const uint32_t (&v)[16], int x, int y, int z) {
+  if (lane == 0) tma_store_wait_read();  // the previous chunk has left the buffer
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  fence_async_smem();
+  __syncwarp();
+  if (lane == 0) tma_store_3d<kAdd>(map, buf, x, y, z);
+}
+
 // g / (1 + exp(-g)).  The division is the approximate one (two steps of 2^-23); an exponential that
 // overflows gives 0.  fp32 outputs take the accurate exponential.
 template <bool kAccurate>
@@ -162,9 +184,9 @@ __device__ __forceinline__ float silu(float g) {
 }
 
 template <int kOp, bool kSwiGLU, bool kF32, bool kAdd>
-__global__ void __launch_bounds__(Shape<kOp, kSwiGLU>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
     product_kernel(const __grid_constant__ ProductParams p) {
-  using S = Shape<kOp, kSwiGLU>;
+  using S = Shape<kOp, kSwiGLU, kF32>;
   constexpr bool kMicro = S::kMicro, kNv = kOp == OP_NV, kGradW = kOp == OP_GRAD_W;
   constexpr bool kAMn = kOp == OP_GRAD_X || kGradW, kBMn = kGradW;
   constexpr int kStage = S::kStage, kStages = S::kStages, kMaxRows = S::kMaxRows;
@@ -368,13 +390,17 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU>::kThreads, 1)
       const int n = mma_rows(t), len = sum_len(t);
       const int nkb = (len + S::kBlock - 1) / S::kBlock;
       if (kGradW && nkb == 0) continue;  // a group without rows: the epilogue writes zeros
-      if (!__all_sync(~0u, mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, abort_flag, p.err))) break;
-      tc_fence_after();
       const bool two = two_scale_tiles(t, n);
-      const uint32_t d = tmem_base + acc * S::kAccCols;
       const uint32_t b_col = (t.lrow0 & 127) >> 5;  // micro: the tile's first row's scale column
       const uint32_t idesc = idesc_bf16_f32_pair(n) | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u);
       for (int kb = 0; kb < nkb; ++kb) {
+        const bool first = kb % S::kSegment == 0;  // of a segment: into sums that have been read
+        if (first) {
+          ok = __all_sync(~0u, mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, abort_flag, p.err));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t d = tmem_base + acc * S::kAccCols;
         const int left = block_len(len, kb);
         const int steps = (left + S::kStep - 1) / S::kStep;
         if (to_clear(left)) {
@@ -412,7 +438,7 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU>::kThreads, 1)
 #pragma unroll
               for (int m = 0; m < S::kSums; ++m)
                 mma_micro_pair<kNv>(d + m * kMaxRows, sw128_kmajor_desc(sa + m * kBox + s * 32), bd, id,
-                                    ta + 4 * (m * S::kTiles + i), b0 + 8 * i, (kb | s) != 0);
+                                    ta + 4 * (m * S::kTiles + i), b0 + 8 * i, !first || s);
             }
           } else {
 #pragma unroll
@@ -420,7 +446,7 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU>::kThreads, 1)
               if (s == steps) break;
               mma_bf16_pair(d, kAMn ? mnmajor_desc(sa + s * 2048) : sw128_kmajor_desc(sa + s * 32),
                             kBMn ? mnmajor_desc(sb + s * 2048) : sw128_kmajor_desc(sb + s * 32), idesc,
-                            (kb | s) != 0);
+                            !first || s);
             }
           }
           mma_commit_pair(&empty[stage]);  // frees the stage on both SMs
@@ -428,12 +454,13 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU>::kThreads, 1)
         __syncwarp();
         buf ^= 1u;
         if (++stage == kStages) stage = 0;
+        if (kb + 1 == nkb || (kb + 1) % S::kSegment == 0) {
+          if (elect_one()) mma_commit_pair(&tfull[acc]);
+          __syncwarp();
+          if (S::kAccs == 2) acc ^= 1u;
+          if (acc == 0) acc_phase ^= 1u;
+        }
       }
-      if (!ok) break;
-      if (elect_one()) mma_commit_pair(&tfull[acc]);
-      __syncwarp();
-      if (S::kAccs == 2) acc ^= 1u;
-      if (acc == 0) acc_phase ^= 1u;
     }
     if (elect_one()) mma_commit_pair_own(drain);  // every MMA issued above has completed once this arrives
     __syncwarp();
@@ -464,80 +491,115 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU>::kThreads, 1)
     for (int tile = tile0; tile < total; tile += tstep) {
       const ProductTile t = tile_of(tile);
       const int n = mma_rows(t);
-      const bool none = kGradW && sum_len(t) == 0;
+      const int len = sum_len(t);
+      const bool none = kGradW && len == 0;
+      if (kAdd && none) continue;
       const float alpha = kNv && p.w_factor ? ga * __ldg(p.w_factor + t.g) : ga;
+      const int feat0 = t.ft * 256 + (int)rank * 128 + quarter * 32;  // this warp's first feature
+      // this warp's columns: half of the tile's (grad_w: every other chunk)
+      const int end = kGradW ? t.valid : min(t.valid, half ? n : n / 2);
+      uint8_t* buf = staging + (warp - 2) * 2048;                     // grad_w
+      if constexpr (kF32) {
+        // Segments of the sum, added up here in fp32 (rounded to nearest, where the tensor cores cut).
+        constexpr int kChunks = kMaxRows / 32;
+        const auto col = [&](int ch) { return kGradW ? (2 * ch + half) * 16 : half * (n / 2) + 16 * ch; };
+        float sum[S::kSums][kChunks * 16];
+#pragma unroll
+        for (int m = 0; m < S::kSums; ++m)
+#pragma unroll
+          for (int i = 0; i < kChunks * 16; ++i) sum[m][i] = 0.0f;
+        bool ok = true;
+        for (int at = 0; at < len; at += S::kSegment * S::kBlock) {
+          ok = __all_sync(~0u, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t tb = tmem_base + acc * S::kAccCols + ((uint32_t)(quarter * 32) << 16);
+          if (feat0 < p.F) {
+#pragma unroll
+            for (int ch = 0; ch < kChunks; ++ch) {
+              if (col(ch) < end) {
+                uint32_t g[S::kSums][16];
+#pragma unroll
+                for (int m = 0; m < S::kSums; ++m) tmem_ld16(tb + m * kMaxRows + col(ch), g[m]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int m = 0; m < S::kSums; ++m)
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) sum[m][16 * ch + i] += __uint_as_float(g[m][i]);
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[acc], 0));
+          if (S::kAccs == 2) acc ^= 1u;
+          if (acc == 0) acc_phase ^= 1u;
+        }
+        if (!ok) break;
+        if (feat0 >= p.F) continue;
+#pragma unroll
+        for (int ch = 0; ch < kChunks; ++ch) {
+          const int c = col(ch);
+          if (c >= end) continue;
+          if constexpr (kGradW) {
+            uint32_t v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(sum[0][16 * ch + i]);
+            store_dw<kAdd>(&p.mout, buf, lane, v, t.lrow0 + c, feat0, t.g);
+          } else {
+            float* dst = static_cast<float*>(p.out) + ((int64_t)t.row0 + c) * p.ldo + feat0 + lane;
+            if (feat0 + lane < p.F) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float f = sum[0][16 * ch + i];
+                if constexpr (kMicro) f *= alpha;
+                if constexpr (kSwiGLU) f = silu<true>(f) * (alpha * sum[S::kSums - 1][16 * ch + i]);
+                if (c + i < t.valid) dst[i * p.ldo] = f;
+              }
+            }
+          }
+        }
+        continue;
+      }
       if (!none && !__all_sync(~0u, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err))) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + acc * S::kAccCols + ((uint32_t)(quarter * 32) << 16);
-      const int feat0 = t.ft * 256 + (int)rank * 128 + quarter * 32;  // this warp's first feature
-      const int end = min(t.valid, half ? n : n / 2);                 // this warp's rows
-      if constexpr (kGradW) {
-        // a lane has a row of dW: chunks of 32 rows x 64 bytes through shared memory (in the 64-byte
-        // swizzle) to TMA, which leaves out what lies behind dW's last row or column
-        constexpr int kCols = kF32 ? 16 : 32;
-        uint8_t* buf = staging + (warp - 2) * 2048;
-        if (feat0 < p.F && !(kAdd && none)) {
+      if (feat0 < p.F) {
 #pragma unroll 1
-          for (int c = half * kCols; c < t.valid; c += 2 * kCols) {
-            uint32_t g[kCols];
-            if (none) {
-#pragma unroll
-              for (int i = 0; i < kCols; ++i) g[i] = 0u;
-            } else {
-#pragma unroll
-              for (int h = 0; h < kCols / 16; ++h)
-                tmem_ld16(tb + c + 16 * h, reinterpret_cast<uint32_t(&)[16]>(g[16 * h]));
+        for (int c = kGradW ? half * 32 : half * (n / 2); c < end; c += kGradW ? 64 : 16) {
+          if constexpr (kGradW) {
+            // a lane has a row of dW: chunks of 32 rows x 64 bytes
+            uint32_t g[32], v[16];
+            if (!none) {
+              tmem_ld16(tb + c, reinterpret_cast<uint32_t(&)[16]>(g[0]));
+              tmem_ld16(tb + c + 16, reinterpret_cast<uint32_t(&)[16]>(g[16]));
               tmem_ld_wait();
             }
-            if constexpr (!kF32) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                g[i] = pack_bf16x2(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
-            }
-            if (lane == 0) tma_store_wait_read();  // the previous chunk has left the buffer
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-                  make_uint4(g[4 * j], g[4 * j + 1], g[4 * j + 2], g[4 * j + 3]);
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) tma_store_3d<kAdd>(&p.mout, buf, t.lrow0 + c, feat0, t.g);
-          }
-        }
-      } else if (feat0 < p.F) {
-#pragma unroll 1
-        for (int c = half * (n / 2); c < end; c += 16) {
-          uint32_t g[16];
-          float f[16];
-          tmem_ld16(tb + c, g);
-          if constexpr (kSwiGLU) {
-            uint32_t u[16];
-            tmem_ld16(tb + kMaxRows + c, u);
-            tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              f[i] = silu<kF32>(alpha * __uint_as_float(g[i])) * (alpha * __uint_as_float(u[i]));
+              v[i] = none ? 0u : pack_bf16x2(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
+            store_dw<false>(&p.mout, buf, lane, v, t.lrow0 + c, feat0, t.g);
           } else {
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              f[i] = kMicro ? alpha * __uint_as_float(g[i]) : __uint_as_float(g[i]);
-            }
-          }
-          const int64_t row = (int64_t)t.row0 + c;
-          if constexpr (kF32) {
-            float* dst = static_cast<float*>(p.out) + row * p.ldo + feat0 + lane;
-            if (feat0 + lane < p.F) {
+            uint32_t g[16];
+            float f[16];
+            tmem_ld16(tb + c, g);
+            if constexpr (kSwiGLU) {
+              uint32_t u[16];
+              tmem_ld16(tb + kMaxRows + c, u);
+              tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                if (c + i < t.valid) dst[i * p.ldo] = f[i];
+                f[i] = silu<false>(alpha * __uint_as_float(g[i])) * (alpha * __uint_as_float(u[i]));
+            } else {
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                f[i] = kMicro ? alpha * __uint_as_float(g[i]) : __uint_as_float(g[i]);
             }
-          } else {
             // lanes in twos: the even one takes both features of row i, the odd one those of row i + 1
             const int odd = lane & 1;
-            __nv_bfloat16* dst =
-                static_cast<__nv_bfloat16*>(p.out) + (row + odd) * p.ldo + feat0 + (lane & ~1);
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
+                                 ((int64_t)t.row0 + c + odd) * p.ldo + feat0 + (lane & ~1);
             const bool in = feat0 + (lane & ~1) < p.F;
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
@@ -568,7 +630,7 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU>::kThreads, 1)
 
 template <int kOp, bool kSwiGLU, bool kF32, bool kAdd = false>
 cudaError_t launch(const ProductParams& p, int sms, cudaStream_t st, const char* label) {
-  using S = Shape<kOp, kSwiGLU>;
+  using S = Shape<kOp, kSwiGLU, kF32>;
   auto kern = product_kernel<kOp, kSwiGLU, kF32, kAdd>;
   static std::atomic<uint64_t> set{0};  // devices whose attribute is set
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), S::kSmem, &set);
@@ -638,9 +700,9 @@ cudaError_t launch_micro_product(const MicroProduct& g, int sms, cudaStream_t st
   const int per = nv ? 64 : 128;  // channels of a scale tile
   p.ktiles = (g.K + per - 1) / per;
   const uint64_t half = (uint64_t)g.K / 2, wrows = (uint64_t)g.E * p.wrows;
-  const uint32_t tiles = nv ? Shape<OP_NV, false>::kTiles : Shape<OP_MX, false>::kTiles;
+  const uint32_t tiles = nv ? Shape<OP_NV, false, false>::kTiles : Shape<OP_MX, false, false>::kTiles;
   if (!make_map_2d(&p.mw, 1, g.w, half, wrows, half, 128, 128) ||
-      !make_row_maps(p.mrow, Shape<OP_MX, false>::kMaxRows / 32, 1, g.a, half, g.rows, half, 128) ||
+      !make_row_maps(p.mrow, Shape<OP_MX, false, false>::kMaxRows / 32, 1, g.a, half, g.rows, half, 128) ||
       !make_map_tiles(&p.msw, g.w_scales, (wrows / 128 + g.E) * p.ktiles, tiles) ||
       !make_map_tiles(&p.msr, g.a_scales, ((uint64_t)g.rows / 128 + g.E) * p.ktiles, tiles))
     return cudaErrorInvalidValue;
