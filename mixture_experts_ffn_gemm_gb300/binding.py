@@ -11,7 +11,10 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -474,16 +477,62 @@ def _refuse(t, device, spec):
     return t.data_ptr()
 
 
-def _addresses(stream, specs, tensors, ws):
-    """Addresses of a call's operands, all of them on the current device (the stream's, when one is given:
-    then on one device, the workspace's)."""
-    device = torch._C._cuda_getDevice() if stream is None else ws.get_device()
+def _addresses(device, specs, tensors, ws):
+    """Addresses of a call's operands, all of them on `device`."""
     if device < 0 or ws.get_device() != device or not ws.is_contiguous():
         raise ValueError(f"ws: on {ws.device}, a contiguous CUDA tensor on the call's device")
     return [None if t is None else
             t.data_ptr() if (t.get_device() == device and t.dtype is s[0]
                              and s[1] <= t.numel() <= s[2] and t.is_contiguous()) else
             _refuse(t, device, s) for t, s in zip(tensors, specs)]
+
+
+@functools.lru_cache(maxsize=None)
+def _operands_module():
+    """The quick argument check (csrc/operands.cpp)."""
+    path = os.path.join(_HERE, "_build", "_operands.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"the binding's module is not built ({path}); run "
+                           "`python -m mixture_experts_ffn_gemm_gb300.build`")
+    loader = importlib.machinery.ExtensionFileLoader("_operands", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_operands", loader))
+    loader.exec_module(module)
+    return module
+
+
+class _Specs(tuple):
+    """Specs of an entry point's operands, and the same as operands.cpp takes them."""
+
+    @functools.cached_property
+    def packed(self) -> bytes:
+        code = _operands_module().type_code
+        return b"".join(struct.pack("7q", -1 if dt is None else code(dt), least, most, rows is not None,
+                                    *(rows or (0, 0, 0))) for dt, least, most, _, rows in self)
+
+
+def _launch(name, specs_of, cfg, tensors, ws, stream):
+    """The entry point `name` on operands that its specs describe, on the current device and stream, or
+    on a given stream and the workspace's device."""
+    key = bytes(cfg)
+    specs = specs_of(key)
+    lib = load_library()
+    if stream is None:
+        device = torch._C._cuda_getDevice()
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        device = ws.get_device()
+        stream = _stream(stream)
+    if lib is _lib:  # the library itself, not a stand-in
+        status = _operands_module().call(_address(name), key, specs.packed, tensors, ws, device, stream)
+        if status is not None:
+            return _check(status, name)
+    args = _addresses(device, specs, tensors, ws)
+    _check(getattr(lib, name)(ctypes.byref(cfg), *args, ws.data_ptr(), ws.nbytes, stream), name)
+
+
+@functools.lru_cache(maxsize=None)
+def _address(name: str) -> int:
+    return ctypes.cast(getattr(load_library(), name), ctypes.c_void_p).value
 
 
 def make_product_config(rows: int, E: int, N: int, K: int, kind: str = "forward",
@@ -509,9 +558,7 @@ def alloc_product_workspace(cfg: moe_product_config_t, device="cuda") -> torch.T
 def moe_grouped_product(cfg: moe_product_config_t, offsets, a, b, out, ws, stream=None):
     """Products grouped by expert: y = x W_e^T (a = x, b = W), dx = dy W_e (a = dy, b = W) or
     dW_e = dy^T x (a = dy, b = x), rows [offsets[e], offsets[e+1]) of expert e."""
-    o, pa, pb, po = _addresses(stream, _product_specs(bytes(cfg)), (offsets, a, b, out), ws)
-    _check(load_library().moe_grouped_product(ctypes.byref(cfg), o, pa, pb, po, ws.data_ptr(),
-                                              ws.nbytes, _stream(stream)), "moe_grouped_product")
+    _launch("moe_grouped_product", _product_specs, cfg, (offsets, a, b, out), ws, stream)
 
 
 @functools.lru_cache(maxsize=64)
@@ -520,13 +567,13 @@ def _product_specs(cfg: bytes) -> tuple:
     R, E, N, K, bf, odt = c.rows, c.E, c.N, c.K, torch.bfloat16, _DTYPES.get(c.out_dtype)
     offs = _at_least("offsets", torch.int32, E + 1)
     if c.kind == MOE_PRODUCT_GRAD_W:
-        return (offs, _rows("a", bf, R, N, c.ld_y), _rows("b", bf, R, K, c.ld_x),
-                _dense("out", odt, E * N * K))
+        return _Specs((offs, _rows("a", bf, R, N, c.ld_y), _rows("b", bf, R, K, c.ld_x),
+                       _dense("out", odt, E * N * K)))
     if c.kind == MOE_PRODUCT_GRAD_X:
-        return (offs, _rows("a", bf, R, N, c.ld_y), _dense("b", bf, E * N * K),
-                _rows("out", odt, R, K, c.ld_x))
-    return (offs, _rows("a", bf, R, K, c.ld_x), _dense("b", bf, E * N * K),
-            _rows("out", odt, R, N, c.ld_y))
+        return _Specs((offs, _rows("a", bf, R, N, c.ld_y), _dense("b", bf, E * N * K),
+                       _rows("out", odt, R, K, c.ld_x)))
+    return _Specs((offs, _rows("a", bf, R, K, c.ld_x), _dense("b", bf, E * N * K),
+                   _rows("out", odt, R, N, c.ld_y)))
 
 
 def make_micro_config(rows: int, K: int, format: str = "mx", groups: int = 1,
@@ -563,18 +610,27 @@ def _scale_bytes(rows: int, K: int, groups: int, fmt: int) -> int:
     return (rows // 128 + groups) * ((K + per - 1) // per) * 512
 
 
-@functools.lru_cache(maxsize=64)
-def _micro_specs(cfg: bytes) -> tuple:
-    """Specs of moe_micro_quantize's and of moe_micro_dequantize's operands."""
+def _micro_specs(cfg: bytes):
+    """The spec of x or the values by name and rows, and those of the other operands."""
     c = moe_micro_config_t.from_buffer_copy(cfg)
     u8, dt = torch.uint8, _DTYPES.get(c.dtype)
-    offs = _at_least("offsets", torch.int32, c.groups + 1)
-    factor = _dense("factor", torch.float32, 1)
-    codes = _dense("codes", u8, c.rows * (c.K // 2))
-    scales = _at_least("scales", u8, _scale_bytes(c.rows, c.K, c.groups, c.format))
-    return ((_rows("x", dt, c.src_rows, c.K, c.ld),
-             _dense("dest", torch.int32, c.src_rows * c.copies), offs, factor, codes, scales),
-            (codes, scales, offs, factor, _rows("out", dt, c.rows, c.K, c.ld)))
+    return (c, lambda name, rows: _rows(name, dt, rows, c.K, c.ld),
+            _at_least("offsets", torch.int32, c.groups + 1), _dense("factor", torch.float32, 1),
+            _dense("codes", u8, c.rows * (c.K // 2)),
+            _at_least("scales", u8, _scale_bytes(c.rows, c.K, c.groups, c.format)))
+
+
+@functools.lru_cache(maxsize=64)
+def _quantize_specs(cfg: bytes) -> tuple:
+    c, values, offs, factor, codes, scales = _micro_specs(cfg)
+    dest = _dense("dest", torch.int32, c.src_rows * c.copies)
+    return _Specs((values("x", c.src_rows), dest, offs, factor, codes, scales))
+
+
+@functools.lru_cache(maxsize=64)
+def _dequantize_specs(cfg: bytes) -> tuple:
+    c, values, offs, factor, codes, scales = _micro_specs(cfg)
+    return _Specs((codes, scales, offs, factor, values("out", c.rows)))
 
 
 def _no_factor(*factors):
@@ -588,11 +644,8 @@ def moe_micro_quantize(cfg: moe_micro_config_t, x, dest, offsets, factor, codes,
     perm_dst of moe_permute), or None; offsets: the experts' rows, or None for `groups` equal groups."""
     if cfg.format != MOE_MICRO_NV:
         _no_factor(factor)
-    px, pd, po, pf, pc, ps = _addresses(stream, _micro_specs(bytes(cfg))[0],
-                                        (x, dest, offsets, factor, codes, scales), ws)
-    _check(load_library().moe_micro_quantize(ctypes.byref(cfg), px, pd, po, pf, pc, ps,
-                                             ws.data_ptr(), ws.nbytes, _stream(stream)),
-           "moe_micro_quantize")
+    _launch("moe_micro_quantize", _quantize_specs, cfg, (x, dest, offsets, factor, codes, scales), ws,
+            stream)
 
 
 def moe_micro_dequantize(cfg: moe_micro_config_t, codes, scales, offsets, factor, out, ws,
@@ -600,10 +653,8 @@ def moe_micro_dequantize(cfg: moe_micro_config_t, codes, scales, offsets, factor
     """The values that codes and scales stand for."""
     if cfg.format != MOE_MICRO_NV:
         _no_factor(factor)
-    pc, ps, po, pf, pv = _addresses(stream, _micro_specs(bytes(cfg))[1],
-                                    (codes, scales, offsets, factor, out), ws)
-    _check(load_library().moe_micro_dequantize(ctypes.byref(cfg), pc, ps, po, pf, pv, ws.data_ptr(),
-                                               ws.nbytes, _stream(stream)), "moe_micro_dequantize")
+    _launch("moe_micro_dequantize", _dequantize_specs, cfg, (codes, scales, offsets, factor, out), ws,
+            stream)
 
 
 def make_micro_product_config(rows: int, E: int, N: int, K: int, format: str = "mx",
@@ -630,11 +681,12 @@ def _micro_product_specs(cfg: bytes) -> tuple:
     c = moe_micro_product_config_t.from_buffer_copy(cfg)
     R, E, N, K, u8, f32 = c.rows, c.E, c.N, c.K, torch.uint8, torch.float32
     per = 2 * N if c.flags & MOE_MICRO_SWIGLU else N
-    return (_at_least("offsets", torch.int32, E + 1), _dense("a", u8, R * (K // 2)),
-            _at_least("a_scales", u8, _scale_bytes(R, K, E, c.format)), _dense("a_factor", f32, 1),
-            _dense("w", u8, E * per * (K // 2)),
-            _at_least("w_scales", u8, _scale_bytes(E * per, K, E, c.format)),
-            _dense("w_factor", f32, E), _rows("out", _DTYPES.get(c.out_dtype), R, N, c.ld_out))
+    return _Specs((_at_least("offsets", torch.int32, E + 1), _dense("a", u8, R * (K // 2)),
+                   _at_least("a_scales", u8, _scale_bytes(R, K, E, c.format)),
+                   _dense("a_factor", f32, 1), _dense("w", u8, E * per * (K // 2)),
+                   _at_least("w_scales", u8, _scale_bytes(E * per, K, E, c.format)),
+                   _dense("w_factor", f32, E),
+                   _rows("out", _DTYPES.get(c.out_dtype), R, N, c.ld_out)))
 
 
 def moe_micro_product(cfg: moe_micro_product_config_t, offsets, a, a_scales, a_factor, w, w_scales,
@@ -642,10 +694,8 @@ def moe_micro_product(cfg: moe_micro_product_config_t, offsets, a, a_scales, a_f
     """The experts' product on microscaled operands, plain or with SwiGLU."""
     if cfg.format != MOE_MICRO_NV:
         _no_factor(a_factor, w_factor)
-    args = _addresses(stream, _micro_product_specs(bytes(cfg)),
-                      (offsets, a, a_scales, a_factor, w, w_scales, w_factor, out), ws)
-    _check(load_library().moe_micro_product(ctypes.byref(cfg), *args, ws.data_ptr(), ws.nbytes,
-                                            _stream(stream)), "moe_micro_product")
+    _launch("moe_micro_product", _micro_product_specs, cfg,
+            (offsets, a, a_scales, a_factor, w, w_scales, w_factor, out), ws, stream)
 
 
 def moe_forward_host_io(cfg, x_host, W_r, b, W13, W2, W13_scale, W2_scale, Ws13, Ws2,

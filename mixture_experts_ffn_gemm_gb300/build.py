@@ -1,7 +1,8 @@
 """Build the CUDA library ``_build/libmoe_gb300.so`` in-tree with nvcc for sm_103a.
 
 Each ``csrc/*.cu`` compiles to an object in parallel (one ``-gencode``), then nvcc links the shared
-library with the static CUDA runtime.  A rebuild happens only when a source or header is newer than
+library with the static CUDA runtime.  ``csrc/operands.cpp``, the binding's quick argument check, becomes a
+Python module beside it (g++ with torch's headers).  A rebuild happens only when a source or header is newer than
 the library.  Usage: ``python -m mixture_experts_ffn_gemm_gb300.build [--force] [--verbose]``.
 """
 from __future__ import annotations
@@ -13,12 +14,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmoe_gb300.so")
+OPERANDS_SRC = os.path.join(CSRC, "operands.cpp")
+OPERANDS = os.path.join(BUILD, "_operands.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]
@@ -51,17 +55,44 @@ def _compile(nvcc: str, src: str, verbose: bool, extra) -> str:
     return obj
 
 
+def _stale(target: str, deps) -> bool:
+    return not os.path.exists(target) or \
+        os.path.getmtime(target) < max(os.path.getmtime(p) for p in deps)
+
+
+def build_operands(force: bool = False) -> str:
+    """Compile the Python module of the quick argument check; returns its path."""
+    if not force and not _stale(OPERANDS, [OPERANDS_SRC]):
+        return OPERANDS
+    import torch
+    os.makedirs(BUILD, exist_ok=True)
+    home = os.path.dirname(torch.__file__)
+    inc = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"]]
+    tmp = OPERANDS + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{p}" for p in inc], OPERANDS_SRC, "-o", tmp, f"-L{os.path.join(home, 'lib')}",
+           "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for operands.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, OPERANDS)
+    return OPERANDS
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     """Compile and link the library; returns its path."""
     srcs, deps = _inputs()
-    if not force and os.path.exists(LIB):
-        newest = max(os.path.getmtime(p) for p in deps)
-        if os.path.getmtime(LIB) >= newest:
-            return LIB
+    if not force and not _stale(LIB, deps):
+        build_operands()
+        return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        operands = ex.submit(build_operands, force)
         objs = list(ex.map(lambda s: _compile(nvcc, s, verbose, list(extra)), srcs))
+        operands.result()
     tmp = LIB + f".tmp{os.getpid()}"
     # every symbol resolved at link time: a missing definition fails here, not at load time
     r = subprocess.run([nvcc, *ARCH, "-shared", "-Xlinker", "--no-undefined", "-o", tmp, *objs],

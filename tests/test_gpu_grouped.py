@@ -269,3 +269,30 @@ def test_gradients_of_a_loss_by_differences(cuda_device):
                 part = ay[s] @ other if which == 0 else ay[s].t() @ other
                 slack = slack + (part * (v[s] if which == 0 else v[e]).abs()).sum()
             assert (got - want).abs() <= slack + 1e-5 * (grad.double() * v).abs().sum()
+
+
+def test_plain_and_pitched_calls_take_the_quick_check_and_others_are_refused(cuda_device, monkeypatch):
+    """The module beside the library takes every accepted operand; what it leaves is refused with a reason."""
+    N, K, pad = 64, 128, 8
+    offs, R, a, b = _make("forward", [5, 9], N, K, pad, seed=11)
+    want = _call("forward", offs, R, a, b, N, K, F32, pad)
+    slow = B._addresses
+    monkeypatch.setattr(B, "_addresses", None)
+    assert torch.equal(_call("forward", offs, R, a, b, N, K, F32, pad)[:, :], want)
+    assert torch.equal(_call("forward", offs, R, a.contiguous(), b, N, K, F32), want)
+    monkeypatch.setattr(B, "_addresses", slow)
+    o = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    out = _out("forward", R, 2, N, K, F32)
+    cfg = _config("forward", R, 2, N, K, F32)
+    ws = B.alloc_product_workspace(cfg)
+    good = dict(offsets=o, a=a.contiguous(), b=b, out=out)
+    for name, bad in (("offsets", o[:2]), ("offsets", o.long()), ("a", a), ("a", a.float()), ("b", b[:1]),
+                      ("b", b.cpu()), ("out", out.to(BF16)), ("out", out.t())):
+        with pytest.raises(ValueError, match=name):
+            B.moe_grouped_product(cfg, *{**good, name: bad}.values(), ws)
+    with pytest.raises(ValueError, match="ws"):
+        B.moe_grouped_product(cfg, *good.values(), ws.cpu())
+    with pytest.raises(B.MoEError):
+        B.moe_grouped_product(cfg, *good.values(), ws[:128])
+    B.moe_grouped_product(cfg, *good.values(), ws)
+    assert torch.equal(out, want)

@@ -282,3 +282,24 @@ def test_micro_product_refuses_types_and_sizes(calls, swiglu):
     with pytest.raises(ValueError, match="factor"):
         B.moe_micro_product(mx, *op.values(), stream=0)
     assert len(calls) == n
+
+
+def test_the_quick_check_leaves_what_is_not_plain(moelib):
+    """Without a GPU no operand is a plain one: the module calls nothing and says so."""
+    m = B._operands_module()
+    cfg = B.make_product_config(4, 1, 8, 8)
+    specs = B._product_specs(bytes(cfg))
+    t = [torch.zeros(2, dtype=I32), torch.zeros(4, 8, dtype=BF16), torch.zeros(1, 8, 8, dtype=BF16),
+         torch.zeros(4, 8, dtype=BF16)]
+    ws = torch.zeros(256, dtype=U8)
+    assert len(specs.packed) == 4 * 56
+    assert m.call(B._address("moe_grouped_product"), bytes(cfg), specs.packed, tuple(t), ws, 0, None) is None
+    assert m.call(B._address("moe_grouped_product"), bytes(cfg), specs.packed, tuple(t[:3]), ws, 0, None) is None
+    assert m.call(B._address("moe_grouped_product"), bytes(cfg), specs.packed, (1, 2, 3, 4), ws, 0, None) is None
+    for bad in ((), (0, b"", b"", t, ws, 0, None), (0, b"", b"", tuple(t), None, 0, None),
+                ("x", b"", b"", tuple(t), ws, 0, None)):
+        with pytest.raises(TypeError):
+            m.call(*bad)
+    with pytest.raises(TypeError):
+        m.type_code(3)
+    assert len({m.type_code(d) for d in (F32, BF16, U8, I32)}) == 4
