@@ -38,7 +38,8 @@
 //
 // Sums: the tensor cores cut what falls behind the sum's 24 bits at every MMA, always towards zero, so that
 // a long sum drifts by about 2^-25.5 of itself a step (5 x 10^-6 over 448 steps).  For fp32 outputs a sum stays
-// in tensor memory for 32 steps; the storing warps add such segments up in fp32, rounded to nearest.  A bf16
+// in tensor memory for 32 steps (grad_w, whose stores its storing warps barely keep up with, 64: 1024 rows);
+// the storing warps add such segments up in fp32, rounded to nearest.  A bf16
 // output's rounding is a thousand times that drift.
 //
 // Kernel shape: persistent, warp 0 copies, warp 1 issues (on the pair's even SM), warps 2..9 store: a lane
@@ -71,7 +72,8 @@ struct Shape {
   static constexpr int kBlock = kMicro ? 256 : 64;         // elements of the sum per stage
   static constexpr int kStep = kMicro ? 64 : 16;           // and per MMA
   static constexpr int kSums = kSwiGLU ? 2 : 1;            // W1 and W3, or one
-  static constexpr int kSegment = kF32 ? 8 : 1 << 30;      // blocks summed in tensor memory at a time
+  // blocks summed in tensor memory at a time (see above)
+  static constexpr int kSegment = !kF32 ? 1 << 30 : kOp == OP_GRAD_W ? 16 : 8;
   static constexpr int kTiles = kOp == OP_NV ? 4 : kOp == OP_MX ? 2 : 0;  // scale tiles per 128 rows
   static constexpr int kOpA = kSums * kBox;
   static constexpr int kOpB = kMaxRows / 2 * 128;
@@ -385,6 +387,12 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
     // the whole warp follows the stages, one thread issues; a stage's barrier of each kind has its phase bit
     uint32_t stage = 0, acc = 0, acc_phase = 0, buf = 0, full_phase = 0, cleared_phase = 0;
     bool ok = true;
+    // descriptors of stage 0; a stage, a step of the sum and a tile lie at fixed distances (in 16 bytes)
+    const uint32_t s0 = smem_u32(smem);
+    const uint64_t a0 = kAMn ? mnmajor_desc(s0) : sw128_kmajor_desc(s0);
+    const uint64_t b0 = kBMn ? mnmajor_desc(s0 + S::kOpA) : sw128_kmajor_desc(s0 + S::kOpA);
+    const uint64_t f0 = scale_tile_desc(s0 + S::kOpA + S::kOpB);
+    constexpr uint32_t kStepA = (kAMn ? 2048 : 32) >> 4, kStepB = (kBMn ? 2048 : 32) >> 4;
     for (int tile = tile0; tile < total && ok; tile += tstep) {
       const ProductTile t = tile_of(tile);
       const int n = mma_rows(t), len = sum_len(t);
@@ -392,74 +400,71 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
       if (kGradW && nkb == 0) continue;  // a group without rows: the epilogue writes zeros
       const bool two = two_scale_tiles(t, n);
       const uint32_t b_col = (t.lrow0 & 127) >> 5;  // micro: the tile's first row's scale column
-      const uint32_t idesc = idesc_bf16_f32_pair(n) | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u);
-      for (int kb = 0; kb < nkb; ++kb) {
-        const bool first = kb % S::kSegment == 0;  // of a segment: into sums that have been read
-        if (first) {
-          ok = __all_sync(~0u, mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, abort_flag, p.err));
-          if (!ok) break;
-          tc_fence_after();
-        }
-        const uint32_t d = tmem_base + acc * S::kAccCols;
-        const int left = block_len(len, kb);
-        const int steps = (left + S::kStep - 1) / S::kStep;
-        if (to_clear(left)) {
-          ok = __all_sync(~0u, mbar_wait_cluster(&cleared[stage], cleared_phase >> stage & 1u,
-                                                 abort_flag, p.err));
-          cleared_phase ^= 1u << stage;
-        } else {
-          ok = __all_sync(~0u, mbar_wait(&full[stage], full_phase >> stage & 1u, abort_flag, p.err));
-          full_phase ^= 1u << stage;
-        }
+      const uint32_t idesc0 = kMicro ? idesc_micro<kNv>(n, 0)
+                                     : idesc_bf16_f32_pair(n) | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u);
+      const uint32_t idesc_second = idesc_micro<kNv>(0, 2) - idesc_micro<kNv>(0, 0);
+      for (int k0 = 0; k0 < nkb; k0 += S::kSegment) {  // a segment of the sum, into sums that have been read
+        ok = __all_sync(~0u, mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, abort_flag, p.err));
         if (!ok) break;
         tc_fence_after();
-        if (elect_one()) {
-          const uint32_t sa = smem_u32(smem + stage * kStage);
-          const uint32_t sb = sa + S::kOpA;
-          if constexpr (kMicro) {
-            const uint32_t fa = sb + S::kOpB, fb = fa + S::kSums * S::kSfA;
-            const uint32_t ta = tmem_base + S::kSfCol0 + buf * S::kSfCols;
-            const uint32_t tb = ta + S::kSums * 4 * S::kTiles;
-#pragma unroll
-            for (int i = 0; i < S::kTiles; ++i) {
-#pragma unroll
-              for (int m = 0; m < S::kSums; ++m)
-                copy_scales(ta + 4 * (m * S::kTiles + i), scale_tile_desc(fa + m * S::kSfA + i * 512));
-              copy_scales(tb + 8 * i, scale_tile_desc(fb + i * 512));
-              if (two) copy_scales(tb + 8 * i + 4, scale_tile_desc(fb + S::kSfB / 2 + i * 512));
-            }
-            const uint32_t b0 = tb + b_col;
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              if (s == steps) break;
-              const int i = kNv ? s : s >> 1;  // scale tile, and first byte in its columns
-              const uint32_t id = idesc_micro<kNv>(n, kNv ? 0 : (s & 1) * 2);
-              const uint64_t bd = sw128_kmajor_desc(sb + s * 32);
-#pragma unroll
-              for (int m = 0; m < S::kSums; ++m)
-                mma_micro_pair<kNv>(d + m * kMaxRows, sw128_kmajor_desc(sa + m * kBox + s * 32), bd, id,
-                                    ta + 4 * (m * S::kTiles + i), b0 + 8 * i, !first || s);
-            }
+        const uint32_t d = tmem_base + acc * S::kAccCols;
+        const int k1 = nkb - k0 < S::kSegment ? nkb : k0 + S::kSegment;
+        for (int kb = k0; kb < k1; ++kb) {
+          const int left = block_len(len, kb);
+          const int steps = (left + S::kStep - 1) / S::kStep;
+          if (to_clear(left)) {
+            ok = __all_sync(~0u, mbar_wait_cluster(&cleared[stage], cleared_phase >> stage & 1u,
+                                                   abort_flag, p.err));
+            cleared_phase ^= 1u << stage;
           } else {
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              if (s == steps) break;
-              mma_bf16_pair(d, kAMn ? mnmajor_desc(sa + s * 2048) : sw128_kmajor_desc(sa + s * 32),
-                            kBMn ? mnmajor_desc(sb + s * 2048) : sw128_kmajor_desc(sb + s * 32), idesc,
-                            !first || s);
-            }
+            ok = __all_sync(~0u, mbar_wait(&full[stage], full_phase >> stage & 1u, abort_flag, p.err));
+            full_phase ^= 1u << stage;
           }
-          mma_commit_pair(&empty[stage]);  // frees the stage on both SMs
-        }
-        __syncwarp();
-        buf ^= 1u;
-        if (++stage == kStages) stage = 0;
-        if (kb + 1 == nkb || (kb + 1) % S::kSegment == 0) {
-          if (elect_one()) mma_commit_pair(&tfull[acc]);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t at = (uint64_t)(stage * (kStage >> 4));
+            const uint64_t sa = a0 + at, sb = b0 + at;
+            if constexpr (kMicro) {
+              const uint64_t fa = f0 + at, fb = fa + (S::kSums * S::kSfA >> 4);
+              const uint32_t ta = tmem_base + S::kSfCol0 + buf * S::kSfCols;
+              const uint32_t tb = ta + S::kSums * 4 * S::kTiles;
+#pragma unroll
+              for (int i = 0; i < S::kTiles; ++i) {
+#pragma unroll
+                for (int m = 0; m < S::kSums; ++m)
+                  copy_scales(ta + 4 * (m * S::kTiles + i), fa + ((m * S::kSfA + i * 512) >> 4));
+                copy_scales(tb + 8 * i, fb + (i * 512 >> 4));
+                if (two) copy_scales(tb + 8 * i + 4, fb + ((S::kSfB / 2 + i * 512) >> 4));
+              }
+#pragma unroll
+              for (int s = 0; s < 4; ++s) {
+                if (s == steps) break;
+                const int i = kNv ? s : s >> 1;  // scale tile, and first byte in its columns
+                const uint32_t id = kNv ? idesc0 : idesc0 + (s & 1) * idesc_second;
+#pragma unroll
+                for (int m = 0; m < S::kSums; ++m)
+                  mma_micro_pair<kNv>(d + m * kMaxRows, sa + ((m * kBox >> 4) + s * kStepA), sb + s * kStepB, id,
+                                      ta + 4 * (m * S::kTiles + i), tb + b_col + 8 * i, kb != k0 || s);
+              }
+            } else {
+#pragma unroll
+              for (int s = 0; s < 4; ++s) {
+                if (s == steps) break;
+                mma_bf16_pair(d, sa + s * kStepA, sb + s * kStepB, idesc0, kb != k0 || s);
+              }
+            }
+            commit_both(&empty[stage]);  // frees the stage on both SMs
+          }
           __syncwarp();
-          if (S::kAccs == 2) acc ^= 1u;
-          if (acc == 0) acc_phase ^= 1u;
+          buf ^= 1u;
+          if (++stage == kStages) stage = 0;
         }
+        if (!ok) break;
+        if (elect_one()) commit_both(&tfull[acc]);
+        __syncwarp();
+        if (S::kAccs == 2) acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
       }
     }
     if (elect_one()) mma_commit_pair_own(drain);  // every MMA issued above has completed once this arrives
@@ -508,20 +513,31 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
         for (int m = 0; m < S::kSums; ++m)
 #pragma unroll
           for (int i = 0; i < kChunks * 16; ++i) sum[m][i] = 0.0f;
+        const auto release = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[acc], 0));
+          if (S::kAccs == 2) acc ^= 1u;
+          if (acc == 0) acc_phase ^= 1u;
+        };
+        const auto read = [&](int ch, uint32_t (&g)[S::kSums][16]) {
+          const uint32_t tb = tmem_base + acc * S::kAccCols + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll
+          for (int m = 0; m < S::kSums; ++m) tmem_ld16(tb + m * kMaxRows + col(ch), g[m]);
+          tmem_ld_wait();
+        };
         bool ok = true;
-        for (int at = 0; at < len; at += S::kSegment * S::kBlock) {
+        int at = 0;
+        for (; len - at > S::kSegment * S::kBlock; at += S::kSegment * S::kBlock) {  // all but the last
           ok = __all_sync(~0u, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t tb = tmem_base + acc * S::kAccCols + ((uint32_t)(quarter * 32) << 16);
           if (feat0 < p.F) {
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) {
               if (col(ch) < end) {
                 uint32_t g[S::kSums][16];
-#pragma unroll
-                for (int m = 0; m < S::kSums; ++m) tmem_ld16(tb + m * kMaxRows + col(ch), g[m]);
-                tmem_ld_wait();
+                read(ch, g);
 #pragma unroll
                 for (int m = 0; m < S::kSums; ++m)
 #pragma unroll
@@ -529,36 +545,48 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
               }
             }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[acc], 0));
-          if (S::kAccs == 2) acc ^= 1u;
-          if (acc == 0) acc_phase ^= 1u;
+          release();
         }
         if (!ok) break;
-        if (feat0 >= p.F) continue;
+        if (!none) {
+          if (!__all_sync(~0u, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err))) break;
+          tc_fence_after();
+        }
+        if (feat0 < p.F) {
 #pragma unroll
-        for (int ch = 0; ch < kChunks; ++ch) {
-          const int c = col(ch);
-          if (c >= end) continue;
-          if constexpr (kGradW) {
-            uint32_t v[16];
+          for (int ch = 0; ch < kChunks; ++ch) {
+            const int c = col(ch);
+            if (c >= end) continue;
+            uint32_t g[S::kSums][16];
+            if (!none) {
+              read(ch, g);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(sum[0][16 * ch + i]);
-            store_dw<kAdd>(&p.mout, buf, lane, v, t.lrow0 + c, feat0, t.g);
-          } else {
-            float* dst = static_cast<float*>(p.out) + ((int64_t)t.row0 + c) * p.ldo + feat0 + lane;
-            if (feat0 + lane < p.F) {
+              for (int m = 0; m < S::kSums; ++m)
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float f = sum[0][16 * ch + i];
-                if constexpr (kMicro) f *= alpha;
-                if constexpr (kSwiGLU) f = silu<true>(f) * (alpha * sum[S::kSums - 1][16 * ch + i]);
-                if (c + i < t.valid) dst[i * p.ldo] = f;
+                for (int i = 0; i < 16; ++i)
+                  g[m][i] = __float_as_uint(sum[m][16 * ch + i] + __uint_as_float(g[m][i]));
+            }
+            if constexpr (kGradW) {
+              if (none) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) g[0][i] = 0u;
+              }
+              store_dw<kAdd>(&p.mout, buf, lane, g[0], t.lrow0 + c, feat0, t.g);
+            } else {
+              float* dst = static_cast<float*>(p.out) + ((int64_t)t.row0 + c) * p.ldo + feat0 + lane;
+              if (feat0 + lane < p.F) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  float f = __uint_as_float(g[0][i]);
+                  if constexpr (kMicro) f *= alpha;
+                  if constexpr (kSwiGLU) f = silu<true>(f) * (alpha * __uint_as_float(g[S::kSums - 1][i]));
+                  if (c + i < t.valid) dst[i * p.ldo] = f;
+                }
               }
             }
           }
         }
+        if (!none) release();
         continue;
       }
       if (!none && !__all_sync(~0u, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err))) break;

@@ -152,6 +152,16 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
         : "memory");
 }
 
+// Arrive once on the barrier at `bar`'s offset in both CTAs of the pair when every pair MMA and copy into
+// tensor memory that this thread issued before has completed.
+__device__ __forceinline__ void commit_both(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
 // Arrive once on this CTA's `bar` alone when every pair MMA this thread issued before has completed.
 __device__ __forceinline__ void mma_commit_pair_own(uint64_t* bar) {
   asm volatile(
