@@ -99,9 +99,10 @@ moe_status_t validate(const moe_micro_product_config_t* c) {
   if (c->rows > kMaxRows || c->E > kMaxGroups || c->N > kMaxWidth || c->K > kMaxWidth || c->N % 8 ||
       c->K % 64 || ((c->flags & MOE_MICRO_SWIGLU) && c->N % 128))
     return MOE_ERR_UNSUPPORTED;
-  // scale tiles are counted in 31 bits
+  // scale tiles are counted in 31 bits, with room for a row of tiles behind the last
   const int64_t kt = (c->K + 63) / 64, per = (int64_t)c->N * (c->flags & MOE_MICRO_SWIGLU ? 2 : 1);
-  if ((c->E * per / 128 + c->E) * kt > INT32_MAX || (c->rows / 128 + c->E) * kt > INT32_MAX)
+  constexpr int64_t kMost = (int64_t)1 << 30;
+  if ((c->E * per / 128 + c->E) * kt > kMost || (c->rows / 128 + c->E) * kt > kMost)
     return MOE_ERR_UNSUPPORTED;
   if (pitch(c->ld_out, c->N) < 0) return MOE_ERR_INVALID_ARG;
   return MOE_OK;

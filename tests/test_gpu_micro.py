@@ -7,10 +7,14 @@ steps of exact block sums, each step aligned to the largest term and cut no coar
 2^-8 |v| for bf16 and 2^-24 |v| for fp32.  SwiGLU h = g sigma(g) u from such g and u: the derivative of
 SiLU is at most 1.1, its value at most |g|; its exponential is good to 2^-21 (bf16) and 2^-22 (fp32)."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
+from conftest import ROOT
 from mixture_experts_ffn_gemm_gb300 import binding as B
 
 pytestmark = pytest.mark.gpu
@@ -495,3 +499,35 @@ def test_two_streams_at_once(cuda_device, fmt):
     for i in range(2):
         assert torch.equal(state[i][2], state[2 + i][2])
         assert B.moe_device_status(state[2 + i][1]) == B.MOE_OK
+
+
+def test_the_first_call_of_a_process_may_be_captured(cuda_device):
+    """Kernels are loaded and their attributes set by the first call: one under capture, replayed after."""
+    code = """
+import torch
+from mixture_experts_ffn_gemm_gb300 import binding as B
+torch.cuda.init()
+o = torch.tensor([0, 3, 40], dtype=torch.int32, device="cuda")
+x = torch.ones(40, 128, dtype=torch.bfloat16, device="cuda")
+w = torch.ones(2, 64, 128, dtype=torch.bfloat16, device="cuda")
+y = torch.zeros(40, 64, dtype=torch.bfloat16, device="cuda")
+cq, cw = B.make_micro_config(40, 128, groups=2), B.make_micro_config(128, 128, groups=2)
+bq, bw = B.alloc_micro(cq), B.alloc_micro(cw)
+z = torch.zeros(40, 64, device="cuda")
+ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    B.moe_grouped_product(B.make_product_config(40, 2, 64, 128), o, x, w, y, ws)
+    B.moe_micro_quantize(cw, w.view(128, 128), None, None, None, *bw, ws)
+    B.moe_micro_quantize(cq, x, None, o, None, *bq, ws)
+    B.moe_micro_product(B.make_micro_product_config(40, 2, 64, 128, "mx", torch.float32), o, *bq, None,
+                        *bw, None, z, ws)
+assert (y == 0).all() and (z == 0).all()
+g.replay()
+torch.cuda.synchronize()
+assert (y == 128).all() and (z == 128).all() and B.moe_device_status(ws) == B.MOE_OK
+print("replayed")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300,
+                       env=dict(os.environ, PYTHONPATH=ROOT))
+    assert r.returncode == 0 and "replayed" in r.stdout, r.stderr
