@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
     tmem_relinquish_pair();
   }
   wait_for_prior_kernel();
-  build_group_table<kMaxRows>(tab, scratch, p.offsets, p.E, p.rows,
+  build_group_table<kMaxRows, kMicro ? 64 : 32>(tab, scratch, p.offsets, p.E, p.rows,
                               kGradW ? 0 : (p.F + 255) / 256,
                               blockIdx.x == 0 ? p.err : nullptr);  // ends with __syncthreads
   tc_fence_before();

@@ -15,20 +15,20 @@ struct GroupTable {
   int* tile_start;  // [G + 1] first tile of each group; [G]: all tiles
   int* row0;        // [G]     first row
   int* nrows;       // [G]     rows
-  int* cut;         // [G]     row tiles * 8 + (rows of one) / 64
+  int* cut;         // [G]     row tiles * 16 + (rows of one) / 32
 };
 
-// A group's row tiles: as few as hold `rows` in at most kMaxRows each, of about the same size, cut at
-// multiples of 64 rows.
-template <int kMaxRows>
+// A group's row tiles: as few as hold `rows` in at most kMaxRows each, of about the same size (a tile of few
+// rows takes as long as its weights' copies do), cut at multiples of kCut rows.
+template <int kMaxRows, int kCut>
 __device__ __forceinline__ int cut_rows(int rows) {
   const int n = (rows + kMaxRows - 1) / kMaxRows;
-  return n * 8 + (n ? ((rows + n - 1) / n + 63) / 64 : 0);
+  return n * 16 + (n ? ((rows + n - 1) / n + kCut - 1) / kCut * (kCut / 32) : 0);
 }
 
 // Block-wide (scratch: an int a warp); ends with __syncthreads().  A group has
 // feat_tiles tiles for each of its row tiles.
-template <int kMaxRows>
+template <int kMaxRows, int kCut>
 __device__ __forceinline__ void build_group_table(const GroupTable& t, int* scratch,
                                                   const int32_t* offsets, int G, int rows,
                                                   int feat_tiles, uint32_t* err) {
@@ -44,9 +44,9 @@ __device__ __forceinline__ void build_group_table(const GroupTable& t, int* scra
     if (a2 != a || z2 != z) raise_flag(err, kErrIndex);
     t.row0[g] = a2;
     t.nrows[g] = z2 - a2;
-    const int cut = cut_rows<kMaxRows>(z2 - a2);
+    const int cut = cut_rows<kMaxRows, kCut>(z2 - a2);
     t.cut[g] = cut;
-    const int n = (cut >> 3) * feat_tiles;
+    const int n = (cut >> 4) * feat_tiles;
     t.tile_start[g] = n;  // count for now
     local += n;
   }
@@ -108,7 +108,7 @@ struct TileWalk {
     ProductTile p;
     p.g = g;
     const int cut = uniform(t.cut[g]), local = tile - uniform(t.tile_start[g]);
-    const int rows = uniform(t.nrows[g]), rpt = (cut & 7) * 64, nrt = cut >> 3;
+    const int rows = uniform(t.nrows[g]), rpt = (cut & 15) * 32, nrt = cut >> 4;
     p.ft = local;
     p.lrow0 = 0;
     if (nrt > 1) {
