@@ -15,6 +15,10 @@
 // Bound by memory: a row is read once and its codes (K / 2 bytes) and scales (K / B) are written to
 // each row that takes it, so the experts' copies of a token are quantised once and written k times.
 // A warp takes a row (or a part of one, when there are few), a lane 32 channels at a time (16 going back).
+//
+// Measured (GB300, rows of 7168 bf16): 4096 rows to 8 rows each nv 54 us (of 28 for the bytes), mx 42; 32768 rows to
+// one each 135 and 105 us (of 89, 88); back 103 us (of 89).  Copies are bound by their scales, four bytes in each
+// 512-byte tile: without those stores 8192 rows nv take 73 us instead of 112.  One row: 3.5 us.
 #include <cuda_fp16.h>
 
 #include <cstdint>
