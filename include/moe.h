@@ -471,8 +471,8 @@ moe_status_t moe_micro_dequantize(const moe_micro_config_t* cfg, const void* cod
  *   ws           moe_micro_product_workspace_size() bytes, the device status as for moe_grouped_product
  * N is a multiple of 8 up to 131072, K of 64, E at most 1023, rows at most 2^26, and the scale tiles of either
  * operand at most 2^30.  Rows from offsets[E] on are left as they are; rows == 0 is a no-op.  Equal calls
- * give equal bits.  The kernel may start beside a moe_micro_quantize in front of it on the stream, whose
- * results it waits for. */
+ * give equal bits.  (The kernels of this operator, of moe_grouped_product and of the two before may start while
+ * the one in front of them on the stream ends, and touch no memory before its end: programmatic launches.) */
 #define MOE_MICRO_SWIGLU 0x1u
 typedef struct {
   int64_t rows;

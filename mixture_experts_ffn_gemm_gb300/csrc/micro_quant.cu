@@ -237,6 +237,7 @@ template <bool kNv, bool kF32>
 __global__ void __launch_bounds__(kThreads, kF32 ? 2 : 3) micro_quantize_kernel(const MicroParams p) {
   __shared__ CopyTo to_all[kThreads / 32][kMaxCopies];
   allow_next_kernel();
+  wait_for_prior_kernel();
   const int lane = threadIdx.x & 31;
   CopyTo* to = to_all[threadIdx.x >> 5];
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -331,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, kF32 ? 2 : 3) micro_quantize_kernel(
 
 template <bool kNv, bool kF32>
 __global__ void __launch_bounds__(kThreads) micro_dequantize_kernel(const MicroParams p) {
+  wait_for_prior_kernel();
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int64_t row = w / p.parts;
@@ -425,24 +427,32 @@ int row_parts(int64_t rows, int K, int lane_channels, int sms) {
 
 }  // namespace
 
+// Both kernels start as the one before them ends (programmatic launch) and wait for it by themselves.
+template <typename Kernel>
+static cudaError_t launch_rows(Kernel kern, unsigned grid, cudaStream_t st, const MicroParams& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 cudaError_t launch_micro_quantize(const MicroOp& m, int sms, cudaStream_t st) {
   MicroParams p = params(m);
   p.parts = row_parts(m.src_rows, m.K, 32, sms);
   const unsigned grid = (unsigned)((m.src_rows * p.parts + kThreads / 32 - 1) / (kThreads / 32));
   LaunchScope ls("micro_quantize", st);
   const bool f32 = m.dtype == MOE_F32;
-  if (m.format == MOE_MICRO_NV) {
-    if (f32)
-      micro_quantize_kernel<true, true><<<grid, kThreads, 0, st>>>(p);
-    else
-      micro_quantize_kernel<true, false><<<grid, kThreads, 0, st>>>(p);
-  } else {
-    if (f32)
-      micro_quantize_kernel<false, true><<<grid, kThreads, 0, st>>>(p);
-    else
-      micro_quantize_kernel<false, false><<<grid, kThreads, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  if (m.format == MOE_MICRO_NV)
+    return f32 ? launch_rows(micro_quantize_kernel<true, true>, grid, st, p)
+               : launch_rows(micro_quantize_kernel<true, false>, grid, st, p);
+  return f32 ? launch_rows(micro_quantize_kernel<false, true>, grid, st, p)
+             : launch_rows(micro_quantize_kernel<false, false>, grid, st, p);
 }
 
 cudaError_t launch_micro_dequantize(const MicroOp& m, int sms, cudaStream_t st) {
@@ -451,18 +461,11 @@ cudaError_t launch_micro_dequantize(const MicroOp& m, int sms, cudaStream_t st) 
   const unsigned grid = (unsigned)((m.rows * p.parts + kThreads / 32 - 1) / (kThreads / 32));
   LaunchScope ls("micro_dequantize", st);
   const bool f32 = m.dtype == MOE_F32;
-  if (m.format == MOE_MICRO_NV) {
-    if (f32)
-      micro_dequantize_kernel<true, true><<<grid, kThreads, 0, st>>>(p);
-    else
-      micro_dequantize_kernel<true, false><<<grid, kThreads, 0, st>>>(p);
-  } else {
-    if (f32)
-      micro_dequantize_kernel<false, true><<<grid, kThreads, 0, st>>>(p);
-    else
-      micro_dequantize_kernel<false, false><<<grid, kThreads, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  if (m.format == MOE_MICRO_NV)
+    return f32 ? launch_rows(micro_dequantize_kernel<true, true>, grid, st, p)
+               : launch_rows(micro_dequantize_kernel<true, false>, grid, st, p);
+  return f32 ? launch_rows(micro_dequantize_kernel<false, true>, grid, st, p)
+             : launch_rows(micro_dequantize_kernel<false, false>, grid, st, p);
 }
 
 }  // namespace moe

@@ -656,6 +656,7 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
     }
     if (kGradW && lane == 0) tma_store_wait_all();
   }
+  allow_next_kernel();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // no arrival at the peer and no MMA into its tensor memory from here on

@@ -176,7 +176,8 @@ __device__ __forceinline__ void fence_async_smem() {
 
 // Launch of a kernel whose CTAs work in pairs (clusters of two), one CTA per SM.  Its CTAs may start while a
 // kernel before it that allows it (allow_next_kernel) still runs: barriers and tensor memory are set up
-// meanwhile (a quantisation and the product of eight rows: 20.5 -> 18.5 us, replayed from a graph 16.0 -> 15.0).
+// meanwhile (a quantisation and the product of eight rows: 20.5 -> 18.5 us, replayed from a graph 16.0 -> 15.0;
+// with the quantisation launched the same way 15.7 and 14.7).
 template <typename Kernel, typename Params>
 inline cudaError_t launch_pairs(Kernel kern, int sms, int threads, int smem, cudaStream_t st,
                                 const Params& p) {
