@@ -8,6 +8,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+#include <exception>
 
 namespace {
 
@@ -70,12 +71,18 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   if (n > kMaxOperands || PyBytes_GET_SIZE(args[2]) != n * static_cast<Py_ssize_t>(sizeof(Spec)))
     Py_RETURN_NONE;
   const Spec* specs = reinterpret_cast<const Spec*>(PyBytes_AS_STRING(args[2]));
-  U address[kMaxOperands];
-  for (Py_ssize_t i = 0; i < n; ++i)
-    if (!plain(PyTuple_GET_ITEM(args[3], i), specs[i], device, &address[i])) Py_RETURN_NONE;
-  const at::Tensor& ws = THPVariable_Unpack(args[4]);
-  if (!ws.defined() || !ws.is_cuda() || ws.get_device() != device || !ws.is_contiguous()) Py_RETURN_NONE;
-  const U base = reinterpret_cast<U>(ws.data_ptr()), bytes = ws.nbytes();
+  U address[kMaxOperands], base, bytes;
+  try {  // tensors without storage or of irregular sizes throw when asked; binding.py refuses them
+    for (Py_ssize_t i = 0; i < n; ++i)
+      if (!plain(PyTuple_GET_ITEM(args[3], i), specs[i], device, &address[i])) Py_RETURN_NONE;
+    const at::Tensor& ws = THPVariable_Unpack(args[4]);
+    if (!ws.defined() || !ws.is_cuda() || ws.get_device() != device || !ws.is_contiguous()) Py_RETURN_NONE;
+    base = reinterpret_cast<U>(ws.data_ptr());
+    bytes = ws.nbytes();
+  } catch (const std::exception&) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
   const void* cfg = PyBytes_AS_STRING(args[1]);
   int status;
   Py_BEGIN_ALLOW_THREADS

@@ -227,3 +227,23 @@ def test_rows_that_start_at_multiples_of_16_bytes(cuda_device, skip):
     B.moe_micro_dequantize(odd, *one, None, None, v2[:, skip:skip + K], ws)
     assert torch.equal(v1, v2[:, skip:skip + K])
     assert (v2[:, :skip] == 7.0).all() and (v2[:, skip + K:] == 7.0).all()
+
+
+def test_tensors_that_are_no_plain_memory_are_refused(cuda_device):
+    """Tensors that throw when asked for their sizes, strides or address: an error, not the process's end."""
+    N, K, ld = 64, 128, 136
+    offs = torch.tensor([0, 5, 14], dtype=I32, device="cuda")
+    b = _randn(2, N, K)
+    out = torch.empty(14, N, dtype=F32, device="cuda")
+    ragged = torch.nested.nested_tensor([_randn(K), _randn(K - 8)] * 7)
+    sparse = _randn(14, K).to_sparse()
+    fixed = B.make_product_config(rows=14, E=2, N=N, K=K, out_dtype=F32)
+    wide = B.make_product_config(rows=14, E=2, N=N, K=K, out_dtype=F32, ld_x=ld)
+    ws = B.alloc_product_workspace(fixed)
+    for cfg in (fixed, wide):
+        for bad in (ragged, sparse):
+            with pytest.raises((ValueError, RuntimeError)):
+                B.moe_grouped_product(cfg, offs, bad, b, out, ws)
+    with pytest.raises((ValueError, RuntimeError)):
+        B.moe_grouped_product(fixed, offs, _randn(14, K), b, out, torch.zeros(256, dtype=U8, device="cuda").to_sparse())
+    assert B.moe_device_status(ws) == B.MOE_OK
