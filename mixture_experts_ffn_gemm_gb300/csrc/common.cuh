@@ -433,7 +433,8 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
 __device__ __forceinline__ void allow_next_kernel() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
-// Nothing that a kernel before this one wrote, or still reads, may be touched in front of this.
+// Nothing that a kernel before this one wrote, or still reads, may be touched in front of this; __ldg, which
+// takes its data for constant while the kernel runs, may be moved there and does not belong behind it either.
 __device__ __forceinline__ void wait_for_prior_kernel() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -17,7 +17,7 @@
 // A warp takes a row (or a part of one, when there are few), a lane 32 channels at a time (16 going back).
 //
 // Measured (GB300, rows of 7168 bf16): 4096 rows to 8 rows each nv 54 us (of 28 for the bytes), mx 42; 32768 rows to
-// one each 135 and 105 us (of 89, 88); back 103 us (of 89).  Copies are bound by their scales, four bytes in each
+// one each 135 and 105 us (of 89, 88); back 99 us (of 89).  Copies are bound by their scales, four bytes in each
 // 512-byte tile: without those stores 8192 rows nv take 73 us instead of 112.  One row: 3.5 us.
 #include <cuda_fp16.h>
 
@@ -47,6 +47,27 @@ struct MicroParams {
   int32_t wide;              // x or the values: rows at multiples of 32 bytes, which one access takes
 };
 
+// Operands are what a kernel before this one may have written: read by volatile loads, which stay behind the
+// wait for it (__ldg may be moved in front: its data is constant).  Ordinary loads would stay too, but later than
+// need be among the shuffles and stores (one row 3.3 -> 3.7 us; back, 32768 rows nv, 99 -> 103).
+__device__ __forceinline__ int32_t ld_int(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float ld_float(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_16(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // Where the scales of `n` rows (lane j's `row`, j < n <= kMaxCopies) start, in lane j: a group's first
 // tile is (first row) / 128 + group, a row's place in a tile of 128 rows x 4 columns (r % 32) * 16 + (r / 32) * 4.
 // -1 (and kErrIndex) for a row outside the groups.  The whole warp finds each row's group in two rounds of 32
@@ -61,8 +82,8 @@ __device__ __forceinline__ int64_t scale_base(const MicroParams& p, int row, int
   } else {
     const int stride = (p.G + 31) / 32;
     const int i1 = lane * stride;
-    const int first = i1 < p.G ? __ldg(p.offsets + i1) : INT32_MAX;
-    const int last = __ldg(p.offsets + p.G);
+    const int first = i1 < p.G ? ld_int(p.offsets + i1) : INT32_MAX;
+    const int last = ld_int(p.offsets + p.G);
     g = -1;
     start = 0;
     for (int j0 = 0; j0 < n; j0 += kBatch) {
@@ -71,7 +92,7 @@ __device__ __forceinline__ int64_t scale_base(const MicroParams& p, int row, int
       for (int b = 0; b < kBatch; ++b) {
         const int r = __shfl_sync(~0u, row, j0 + b);
         i2[b] = max(__popc(__ballot_sync(~0u, i1 < p.G && first <= r)) - 1, 0) * stride;
-        o2[b] = lane < stride && i2[b] + lane < p.G ? __ldg(p.offsets + i2[b] + lane) : INT32_MAX;
+        o2[b] = lane < stride && i2[b] + lane < p.G ? ld_int(p.offsets + i2[b] + lane) : INT32_MAX;
       }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
@@ -148,12 +169,12 @@ __device__ __forceinline__ uint32_t settle(uint32_t a, uint32_t b, float ax, flo
 
 __device__ __forceinline__ void load32(const uint4* p, bool wide, uint4& a, uint4& b) {
   if (wide) {
-    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-        : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
-        : "l"(p));
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p));
   } else {
-    a = __ldg(p);
-    b = __ldg(p + 1);
+    a = ld_16(p);
+    b = ld_16(p + 1);
   }
 }
 __device__ __forceinline__ void store32(void* p, bool wide, const uint32_t (&v)[8]) {
@@ -258,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, kF32 ? 2 : 3) micro_quantize_kernel(
   float g = 1.0f;
   bool bad_factor = false;
   if (kNv && p.factor) {
-    g = __ldg(p.factor);
+    g = ld_float(p.factor);
     bad_factor = !(g >= 0x1p-100f && g <= 0x1p100f);
     if (bad_factor && lane == 0) raise_flag(p.err, kErrIndex);
   }
@@ -266,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, kF32 ? 2 : 3) micro_quantize_kernel(
   int copies;
   {
     int row = -1;
-    if (lane < p.copies) row = p.dest ? __ldg(p.dest + t * p.copies + lane) : (int)t;
+    if (lane < p.copies) row = p.dest ? ld_int(p.dest + t * p.copies + lane) : (int)t;
     const int64_t sb = scale_base(p, row, p.copies, lane);
     const uint32_t good = __ballot_sync(~0u, sb >= 0);  // the others are skipped
     if (sb >= 0)
@@ -336,17 +357,21 @@ __global__ void __launch_bounds__(kThreads) micro_dequantize_kernel(const MicroP
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int64_t row = w / p.parts;
-  const int64_t end = p.offsets ? min(p.rows, (int64_t)max(__ldg(p.offsets + p.G), 0)) : p.rows;
+  const int64_t end = p.offsets ? min(p.rows, (int64_t)max(ld_int(p.offsets + p.G), 0)) : p.rows;
   if (row >= end) return;  // rows behind the last group are left as they are
   const int part = (int)(w - row * p.parts);
-  const float g = kNv && p.factor ? __ldg(p.factor) : 1.0f;
+  const float g = kNv && p.factor ? ld_float(p.factor) : 1.0f;
   const int64_t sb = __shfl_sync(~0u, scale_base(p, (int)row, 1, lane), 0);
   if (sb < 0) return;
   const int chunks = p.K / 16;
   const auto fetch = [&](int c, uint2& q, uint32_t& sc) {
     const int col = kNv ? c : c >> 1;
-    q = __ldg(reinterpret_cast<const uint2*>(p.codes + row * (p.K / 2)) + c);
-    sc = __ldg(p.scales + sb + (int64_t)(col >> 2) * 512 + (col & 3));
+    asm volatile("ld.global.v2.b32 {%0, %1}, [%2];"
+                 : "=r"(q.x), "=r"(q.y)
+                 : "l"(p.codes + row * (p.K / 2) + (int64_t)c * 8));
+    asm volatile("ld.global.u8 %0, [%1];"
+                 : "=r"(sc)
+                 : "l"(p.scales + sb + (int64_t)(col >> 2) * 512 + (col & 3)));
   };
   uint2 next;
   uint32_t next_sc;

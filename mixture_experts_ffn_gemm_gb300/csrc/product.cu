@@ -501,14 +501,14 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
   } else if (warp > 1) {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     uint32_t acc = 0, acc_phase = 0;
-    const float ga = kNv && p.a_factor ? __ldg(p.a_factor) : 1.0f;
+    const float ga = kNv && p.a_factor ? *p.a_factor : 1.0f;
     for (int tile = tile0; tile < total; tile += tstep) {
       const ProductTile t = tile_of(tile);
       const int n = mma_rows(t);
       const int len = sum_len(t);
       const bool none = kGradW && len == 0;
       if (kAdd && none) continue;
-      const float alpha = kNv && p.w_factor ? ga * __ldg(p.w_factor + t.g) : ga;
+      const float alpha = kNv && p.w_factor ? ga * p.w_factor[t.g] : ga;
       const int feat0 = t.ft * 256 + (int)rank * 128 + quarter * 32;  // this warp's first feature
       // this warp's columns: half of the tile's (grad_w: every other chunk)
       const int end = kGradW ? t.valid : min(t.valid, half ? n : n / 2);

@@ -247,3 +247,65 @@ def test_tensors_that_are_no_plain_memory_are_refused(cuda_device):
     with pytest.raises((ValueError, RuntimeError)):
         B.moe_grouped_product(fixed, offs, _randn(14, K), b, out, torch.zeros(256, dtype=U8, device="cuda").to_sparse())
     assert B.moe_device_status(ws) == B.MOE_OK
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_a_chain_in_which_each_kernel_reads_what_the_one_before_wrote(cuda_device, fmt):
+    """Quantise, multiply, quantise the product in the same buffers, and so on, back to back and captured: the
+    same bits as with a synchronisation behind each call.  Offsets, factors and destinations change too."""
+    R, K, steps = 300, 512, 24
+    w = _randn(2 * K, K, seed=1) * 0.1
+    cw = B.make_micro_config(2 * K, K, fmt, groups=2)
+    bw = B.alloc_micro(cw)
+    cx = B.make_micro_config(R, K, fmt, groups=2)
+    bx = B.alloc_micro(cx)
+    ws = B.alloc_micro_workspace(cx)
+    pc = B.make_micro_product_config(R, 2, K, K, fmt, BF16)
+    B.moe_micro_quantize(cw, w, None, None, None, *bw, ws)
+    first = _randn(R, K, seed=2)
+    x, y = first.clone(), torch.empty_like(first)
+    splits = [[0, (37 * i) % (R + 1), R] for i in range(steps)]
+    all_offs = torch.tensor(splits, dtype=I32, device="cuda")
+    all_dest = torch.stack([torch.randperm(R, generator=torch.Generator().manual_seed(i)) for i in range(steps)])
+    all_dest = all_dest.to(I32).cuda()
+    all_factor = torch.logspace(-3, 3, steps, base=2.0, device="cuda")
+    offs, dest, factor = all_offs[0].clone(), all_dest[0].clone(), all_factor[:1].clone()
+
+    g = factor if fmt == "nv" else None
+
+    def run(sync):
+        wait = torch.cuda.synchronize if sync else (lambda: None)
+        x.copy_(first)
+        for i in range(steps):
+            offs.copy_(all_offs[i])
+            dest.copy_(all_dest[i])
+            factor.copy_(all_factor[i:i + 1])
+            wait()
+            B.moe_micro_quantize(cx, x, dest, offs, g, *bx, ws)
+            wait()
+            B.moe_micro_product(pc, offs, *bx, g, *bw, None, y, ws)
+            wait()
+            B.moe_micro_quantize(cx, y, dest, offs, g, *bx, ws)
+            wait()
+            B.moe_micro_dequantize(cx, *bx, offs, g, x, ws)
+            wait()
+            B.moe_micro_quantize(cx, x, dest, offs, g, *bx, ws)
+            wait()
+            B.moe_micro_product(pc, offs, *bx, g, *bw, None, x, ws)
+            wait()
+        return x.clone(), y.clone(), bx[0].clone(), bx[1].clone()
+
+    want = run(True)
+    assert torch.isfinite(want[0]).all() and (want[0] != 0).any()
+    for _ in range(10):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(False)
+    for _ in range(10):
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    assert B.moe_device_status(ws) == B.MOE_OK
