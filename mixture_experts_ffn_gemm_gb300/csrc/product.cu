@@ -64,6 +64,7 @@ namespace moe {
 namespace {
 
 constexpr int kEpilogueWarps = 8;
+constexpr int kKeep = 3;
 constexpr int kMaxThreads = 32 * (2 + kEpilogueWarps + 1);
 constexpr int kBox = 128 * 128;  // 128 features x 128 bytes
 constexpr int kBox64 = 64 * 128;
@@ -601,6 +602,62 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
       if (!none && !__all_sync(~0u, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err))) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + acc * S::kAccCols + ((uint32_t)(quarter * 32) << 16);
+      // outputs f of 16 rows from column c on, a lane's feature; lanes in twos: the even one stores both features
+      // of row i, the odd one those of row i + 1
+      const auto store_rows = [&](const float (&f)[16], int c) {
+        const int odd = lane & 1;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)t.row0 + c + odd) * p.ldo +
+                             feat0 + (lane & ~1);
+        const bool in = feat0 + (lane & ~1) < p.F;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const float got = __shfl_xor_sync(~0u, odd ? f[i] : f[i + 1], 1);
+          const uint32_t v = odd ? pack_bf16x2(got, f[i + 1]) : pack_bf16x2(f[i], got);
+          if (in && c + i + odd < t.valid) *reinterpret_cast<uint32_t*>(dst + i * p.ldo) = v;
+        }
+      };
+      const auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[acc], 0));
+        if (S::kAccs == 2) acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      };
+      if constexpr (kSwiGLU) {
+        const int c0 = half * (n / 2);
+        const auto finish = [&](const uint32_t (&g)[16], const uint32_t (&u)[16], int c) {
+          float f[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            f[i] = silu<false>(alpha * __uint_as_float(g[i])) * (alpha * __uint_as_float(u[i]));
+          store_rows(f, c);
+        };
+        uint32_t kg[kKeep][16], ku[kKeep][16];
+        if (feat0 < p.F) {
+#pragma unroll
+          for (int k = 0; k < kKeep; ++k)
+            if (c0 + 16 * k < end) {
+              tmem_ld16(tb + c0 + 16 * k, kg[k]);
+              tmem_ld16(tb + kMaxRows + c0 + 16 * k, ku[k]);
+            }
+          tmem_ld_wait();
+#pragma unroll 1
+          for (int c = c0 + 16 * kKeep; c < end; c += 16) {
+            uint32_t g[16], u[16];
+            tmem_ld16(tb + c, g);
+            tmem_ld16(tb + kMaxRows + c, u);
+            tmem_ld_wait();
+            finish(g, u, c);
+          }
+        }
+        release();
+        if (feat0 < p.F) {
+#pragma unroll
+          for (int k = 0; k < kKeep; ++k)
+            if (c0 + 16 * k < end) finish(kg[k], ku[k], c0 + 16 * k);
+        }
+        continue;
+      }
       if (feat0 < p.F) {
 #pragma unroll 1
         for (int c = kGradW ? half * 32 : half * (n / 2); c < end; c += kGradW ? 64 : 16) {
@@ -620,39 +677,15 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
             uint32_t g[16];
             float f[16];
             tmem_ld16(tb + c, g);
-            if constexpr (kSwiGLU) {
-              uint32_t u[16];
-              tmem_ld16(tb + kMaxRows + c, u);
-              tmem_ld_wait();
+            tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                f[i] = silu<false>(alpha * __uint_as_float(g[i])) * (alpha * __uint_as_float(u[i]));
-            } else {
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                f[i] = kMicro ? alpha * __uint_as_float(g[i]) : __uint_as_float(g[i]);
-            }
-            // lanes in twos: the even one takes both features of row i, the odd one those of row i + 1
-            const int odd = lane & 1;
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
-                                 ((int64_t)t.row0 + c + odd) * p.ldo + feat0 + (lane & ~1);
-            const bool in = feat0 + (lane & ~1) < p.F;
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float got = __shfl_xor_sync(~0u, odd ? f[i] : f[i + 1], 1);
-              const uint32_t v = odd ? pack_bf16x2(got, f[i + 1]) : pack_bf16x2(f[i], got);
-              if (in && c + i + odd < t.valid) *reinterpret_cast<uint32_t*>(dst + i * p.ldo) = v;
-            }
+            for (int i = 0; i < 16; ++i)
+              f[i] = kMicro ? alpha * __uint_as_float(g[i]) : __uint_as_float(g[i]);
+            store_rows(f, c);
           }
         }
       }
-      if (none) continue;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[acc], 0));
-      if (S::kAccs == 2) acc ^= 1u;
-      if (acc == 0) acc_phase ^= 1u;
+      if (!none) release();
     }
     if (kGradW && lane == 0) tma_store_wait_all();
   }
