@@ -33,8 +33,10 @@
 // are not stored.
 //
 // SwiGLU: a W1 and a W3 tile of the same features against the same rows, two sums in tensor memory,
-// g and u of an output in one thread; their 2 x 192 columns leave no room for a second pair of sums, so the
-// epilogue is not hidden behind the next tile there, and its reads free the columns as early as they can.
+// g and u of an output in one thread; their 2 x 192 columns leave no room for a second pair of sums.  So that the
+// next tile's MMAs do not wait for the exponentials, three of a storing warp's six chunks are read into
+// registers first and finished after the columns are free (64 experts, 65536 rows, mx: none kept 633 us,
+// three 591, four 625: registers).
 //
 // Sums: the tensor cores cut what falls behind the sum's 24 bits at every MMA, always towards zero, so that
 // a long sum drifts by about 2^-25.5 of itself a step (5 x 10^-6 over 448 steps).  For fp32 outputs a sum stays
@@ -64,12 +66,12 @@ namespace moe {
 namespace {
 
 constexpr int kEpilogueWarps = 8;
-constexpr int kKeep = 3;
-constexpr int kMaxThreads = 32 * (2 + kEpilogueWarps + 1);
+constexpr int kParts = kEpilogueWarps / 4;  // a tile's chunks of rows go to them in turn
+constexpr int kMaxWarps = 2 + kEpilogueWarps + 1;
 constexpr int kBox = 128 * 128;  // 128 features x 128 bytes
 constexpr int kBox64 = 64 * 128;
 constexpr int kBarBytes = 256;
-constexpr int kTable = (4 * (kProductMaxGroups + 1)) * 4 + kMaxThreads * 4;
+constexpr int kTable = (4 * (kProductMaxGroups + 1)) * 4 + kMaxWarps * 4;
 constexpr int kSmemMost = 232448 - 1024 - kBarBytes - kTable;
 
 enum Op { OP_FORWARD, OP_GRAD_X, OP_GRAD_W, OP_MX, OP_NV };
@@ -89,6 +91,7 @@ struct Shape {
   static constexpr int kSfA = kTiles * 512;                // of one sum
   static constexpr int kSfB = 2 * kTiles * 512;
   static constexpr int kStage = kOpA + kOpB + kSums * kSfA + kSfB;
+  static constexpr int kChunks = kMaxRows / 16 / kParts;   // chunks of 16 rows of a storing warp, at most
   static constexpr int kThreads = 32 * (2 + kEpilogueWarps + (kOp == OP_GRAD_W ? 1 : 0));
   static constexpr int kStaging = kOp == OP_GRAD_W ? kEpilogueWarps * 2048 : 0;
   static constexpr int kFit = (kSmemMost - kStaging) / kStage;
@@ -500,24 +503,23 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
       }
     }
   } else if (warp > 1) {
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int quarter = warp & 3, part = (warp - 2) >> 2;
     uint32_t acc = 0, acc_phase = 0;
     const float ga = kNv && p.a_factor ? *p.a_factor : 1.0f;
     for (int tile = tile0; tile < total; tile += tstep) {
       const ProductTile t = tile_of(tile);
-      const int n = mma_rows(t);
       const int len = sum_len(t);
       const bool none = kGradW && len == 0;
       if (kAdd && none) continue;
       const float alpha = kNv && p.w_factor ? ga * p.w_factor[t.g] : ga;
       const int feat0 = t.ft * 256 + (int)rank * 128 + quarter * 32;  // this warp's first feature
-      // this warp's columns: half of the tile's (grad_w: every other chunk)
-      const int end = kGradW ? t.valid : min(t.valid, half ? n : n / 2);
+      // this warp's chunks of 16 columns (of 32: grad_w in bf16)
+      const auto col = [&](int ch) { return (kParts * ch + part) * (kGradW && !kF32 ? 32 : 16); };
+      const int end = t.valid;
       uint8_t* buf = staging + (warp - 2) * 2048;                     // grad_w
       if constexpr (kF32) {
         // Segments of the sum, added up here in fp32 (rounded to nearest, where the tensor cores cut).
-        constexpr int kChunks = kMaxRows / 32;
-        const auto col = [&](int ch) { return kGradW ? (2 * ch + half) * 16 : half * (n / 2) + 16 * ch; };
+        constexpr int kChunks = S::kChunks;
         float sum[S::kSums][kChunks * 16];
 #pragma unroll
         for (int m = 0; m < S::kSums; ++m)
@@ -602,18 +604,30 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
       if (!none && !__all_sync(~0u, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err))) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + acc * S::kAccCols + ((uint32_t)(quarter * 32) << 16);
-      // outputs f of 16 rows from column c on, a lane's feature; lanes in twos: the even one stores both features
-      // of row i, the odd one those of row i + 1
+      // Outputs f of 16 rows from column c on, a lane's feature.  Lanes in twos: of four rows the even one takes both
+      // features of the first two, the odd one those of the others, with one exchange of two rows' bf16 (8192
+      // tokens, W2: 634 us mx; an exchange of fp32 for every row and each store with its condition: 681).
       const auto store_rows = [&](const float (&f)[16], int c) {
         const int odd = lane & 1;
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)t.row0 + c + odd) * p.ldo +
-                             feat0 + (lane & ~1);
-        const bool in = feat0 + (lane & ~1) < p.F;
+        uint32_t v[8];
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float got = __shfl_xor_sync(~0u, odd ? f[i] : f[i + 1], 1);
-          const uint32_t v = odd ? pack_bf16x2(got, f[i + 1]) : pack_bf16x2(f[i], got);
-          if (in && c + i + odd < t.valid) *reinterpret_cast<uint32_t*>(dst + i * p.ldo) = v;
+        for (int k = 0; k < 8; k += 2) {
+          const uint32_t lo = pack_bf16x2(f[2 * k], f[2 * k + 1]), hi = pack_bf16x2(f[2 * k + 2], f[2 * k + 3]);
+          const uint32_t own = odd ? hi : lo, got = __shfl_xor_sync(~0u, odd ? lo : hi, 1);
+          v[k] = __byte_perm(own, got, odd ? 0x1054 : 0x5410);
+          v[k + 1] = __byte_perm(own, got, odd ? 0x3276 : 0x7632);
+        }
+        const int r = c + 2 * odd;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)t.row0 + r) * p.ldo + feat0 + (lane & ~1);
+        const auto row = [](int k) { return 4 * (k / 2) + k % 2; };
+        if (c + 16 <= t.valid && feat0 + 32 <= p.F) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) *reinterpret_cast<uint32_t*>(dst + row(k) * p.ldo) = v[k];
+        } else {
+          const int rows = feat0 + (lane & ~1) < p.F ? t.valid - r : 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (row(k) < rows) *reinterpret_cast<uint32_t*>(dst + row(k) * p.ldo) = v[k];
         }
       };
       const auto release = [&] {
@@ -624,7 +638,7 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
         if (acc == 0) acc_phase ^= 1u;
       };
       if constexpr (kSwiGLU) {
-        const int c0 = half * (n / 2);
+        constexpr int kKeep = 3;
         const auto finish = [&](const uint32_t (&g)[16], const uint32_t (&u)[16], int c) {
           float f[16];
 #pragma unroll
@@ -636,13 +650,13 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
         if (feat0 < p.F) {
 #pragma unroll
           for (int k = 0; k < kKeep; ++k)
-            if (c0 + 16 * k < end) {
-              tmem_ld16(tb + c0 + 16 * k, kg[k]);
-              tmem_ld16(tb + kMaxRows + c0 + 16 * k, ku[k]);
+            if (col(k) < end) {
+              tmem_ld16(tb + col(k), kg[k]);
+              tmem_ld16(tb + kMaxRows + col(k), ku[k]);
             }
           tmem_ld_wait();
 #pragma unroll 1
-          for (int c = c0 + 16 * kKeep; c < end; c += 16) {
+          for (int c = col(kKeep); c < end; c += 16 * kParts) {
             uint32_t g[16], u[16];
             tmem_ld16(tb + c, g);
             tmem_ld16(tb + kMaxRows + c, u);
@@ -654,13 +668,13 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
         if (feat0 < p.F) {
 #pragma unroll
           for (int k = 0; k < kKeep; ++k)
-            if (c0 + 16 * k < end) finish(kg[k], ku[k], c0 + 16 * k);
+            if (col(k) < end) finish(kg[k], ku[k], col(k));
         }
         continue;
       }
       if (feat0 < p.F) {
 #pragma unroll 1
-        for (int c = kGradW ? half * 32 : half * (n / 2); c < end; c += kGradW ? 64 : 16) {
+        for (int c = col(0); c < end; c += kGradW ? 64 : 16 * kParts) {
           if constexpr (kGradW) {
             // a lane has a row of dW: chunks of 32 rows x 64 bytes
             uint32_t g[32], v[16];
