@@ -50,11 +50,12 @@
 // element).
 //
 // Measured (GB300): 8 experts, 32768 rows, 4096 x 7168: 0.98-1.01 ms in bf16 (1.9-1.97 PFLOP/s; the tensor pipe
-// 84% busy), 0.315 ms mx, 0.332 ms nv (6.1, 5.8 PFLOP/s).  384 experts of 2048 x 7168, bf16, 16 tokens:
-// 0.47-0.49 ms, the weights at the memory's rate; SwiGLU nv, 128 tokens: 0.77-0.80 ms, the same.  What bounds it:
-// few rows, the weights' bytes; many, the MMAs (bf16: the clock that their power leaves); between (170 rows an
-// expert), the weights' bytes with 10% for what the epilogue does not hide; grad_w in fp32, operands and dW
-// together between SMs and L2.
+// 89% busy), 0.315 ms mx, 0.332 ms nv (6.1, 5.8 PFLOP/s).  384 experts of 2048 x 7168, bf16, 16 tokens:
+// 0.44-0.48 ms, the weights at the memory's rate; SwiGLU nv, 128 tokens: 0.77 ms, the same; 8192 tokens: SwiGLU mx
+// 0.98-1.0 ms, and 7168 x 2048 0.64 ms.  What bounds it: few rows, the weights' bytes; many, the MMAs (bf16: the
+// clock that their power leaves); between (170 rows an expert), the weights' bytes with what the epilogue does
+// not hide; short sums (2048 and less), the storing warps; grad_w in fp32, operands and dW together between SMs
+// and L2.
 #include <atomic>
 #include <cstring>
 
