@@ -466,7 +466,8 @@ moe_status_t moe_micro_dequantize(const moe_micro_config_t* cfg, const void* cod
  * out[r][n] = SiLU(x W1)[n] * (x W3)[n], in fp32 (N a multiple of 128).
  *   a, a_scales  codes and scales of [rows][K], groups by offsets [E+1] (moe_micro_quantize)
  *   w, w_scales  codes and scales of [E * (N or 2N)][K] in E groups (moe_micro_quantize with offsets NULL)
- *   a_factor     g_a, one fp32; w_factor g_w [E] fp32; MOE_MICRO_NV only, NULL: 1
+ *   a_factor     g_a, one fp32; w_factor g_w [E] fp32; MOE_MICRO_NV only, NULL: 1.  Each in the range of a
+ *                factor; their product need not be an fp32 number
  *   out          [rows][N], pitch ld_out elements (0: N), a multiple of 8 up to 2^32
  *   ws           moe_micro_product_workspace_size() bytes, the device status as for moe_grouped_product
  * N is a multiple of 8 up to 131072, K of 64, E at most 1023, rows at most 2^26, and the scale tiles of either

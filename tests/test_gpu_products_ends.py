@@ -1,0 +1,92 @@
+"""GPU tests of the products grouped by expert and the microscaled operators at the ends that their documents
+allow: factors whose product leaves fp32.
+
+Tolerances as in test_gpu_micro.py: half a step of the output's type, 2^-22 sum |a w| for each MMA step of the
+sum, two roundings of 2^-24 for the factors; below the smallest normal number half a step is 2^-150 in fp32
+(two roundings: 2^-149) and 2^-134 in bf16."""
+import pytest
+import torch
+
+from mixture_experts_ffn_gemm_gb300 import binding as B
+from test_gpu_micro import E4M3, LUT, gpu, offsets_of, pack, scale_index
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16, U8, I32 = torch.float32, torch.bfloat16, torch.uint8, torch.int32
+STEP = {F32: 2.0 ** -24, BF16: 2.0 ** -8}
+TINY = {F32: 2.0 ** -149, BF16: 2.0 ** -134 + 2.0 ** -149}
+MOST = {F32: 2.0 ** 128 * (1 - 2.0 ** -25), BF16: 2.0 ** 128 * (1 - 2.0 ** -9)}  # rounds to infinity from here on
+
+
+def _nv_operand(g, offs, K, low, high, zero_rows=()):
+    """Codes of positive numbers with scale bytes of low..high, zeros in some rows; values in float64."""
+    R = offs[-1]
+    code = torch.randint(0, 8, (R, K), generator=g)
+    byte = torch.randint(low, high + 1, (R, K // 16), generator=g)
+    for r in zero_rows:
+        code[r] = 0
+    val = (LUT[code].view(R, -1, 16) * torch.tensor(E4M3, dtype=torch.float64)[byte][..., None]).view(R, K)
+    scales = torch.full(((R // 128 + len(offs) - 1) * ((K + 63) // 64) * 512,), 255, dtype=U8)
+    scales[scale_index(offs, K, "nv").view(-1)] = byte.to(U8).view(-1)
+    return pack(code).cuda(), scales.cuda(), val.cuda()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("low,high", [(110, 126), (1, 30)])
+@pytest.mark.parametrize("ga,gw", [(4.1e-22, 3.7e-23), (1e-23, 1e-23), (1e22, 1e22), (2.0 ** 100, 2.0 ** -100),
+                                   (2.0 ** -100, 2.0 ** 100), (1e30, 1e-30), (2.0 ** -100, 1.0), (3e-24, 1e18)])
+def test_factors_whose_product_leaves_fp32(cuda_device, ga, gw, low, high, dtype):
+    """Each factor lies in its range, the result in fp32 or not: the value of the formula in either case, and
+    zero for rows of zeros."""
+    K, N, counts = 1024, 136, [5, 0, 140]
+    offs, E = offsets_of(counts), len(counts)
+    g = torch.Generator().manual_seed(1)
+    a, sa, va = _nv_operand(g, offs, K, low, high, zero_rows=(2, 77))
+    w, sw, vw = _nv_operand(g, [e * N for e in range(E + 1)], K, low, high)
+    fa = torch.tensor([ga], device="cuda")
+    fw = torch.tensor([gw, 1.0, gw * 0.75], device="cuda")
+    cfg = B.make_micro_product_config(offs[-1], E, N, K, "nv", dtype)
+    ws = B.alloc_micro_product_workspace(cfg)
+    out = torch.full((offs[-1], N), 7.0, dtype=dtype, device="cuda")
+    B.moe_micro_product(cfg, gpu(offs), a, sa, fa, w, sw, fw, out, ws)
+    assert B.moe_device_status(ws) == B.MOE_OK
+    for e in range(E):
+        s = slice(offs[e], offs[e + 1])
+        f = float(fa.double()) * float(fw[e].double())
+        v = f * (va[s] @ vw[e * N:(e + 1) * N].t())  # all terms are positive: the sum of magnitudes too
+        tol = (STEP[dtype] + (K / 64 + 3) * 2.0 ** -22) * v + TINY[dtype]
+        got = out[s].double()
+        assert (got[v == 0] == 0).all()
+        over, within = v - tol >= MOST[dtype], v + tol < MOST[dtype]
+        assert torch.isinf(got[over]).all()
+        assert ((got - v).abs() <= tol)[within].all(), f"expert {e}"
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("ga,gw", [(1e22, 1e22), (2.0 ** 100, 2.0 ** 100), (2.0 ** 100, 2.0 ** -100),
+                                   (2.0 ** -100, 2.0 ** 100), (1e-23, 1e-23)])
+def test_swiglu_with_factors_whose_product_leaves_fp32(cuda_device, ga, gw, dtype):
+    """Rows of zeros stay zeros; where the factors' product is a plain number, so is every output."""
+    K, N, counts = 256, 128, [5, 0, 140]
+    offs, E = offsets_of(counts), len(counts)
+    g = torch.Generator().manual_seed(2)
+    a, sa, va = _nv_operand(g, offs, K, 30, 60, zero_rows=(2, 77))
+    w, sw, vw = _nv_operand(g, [e * 2 * N for e in range(E + 1)], K, 30, 60)
+    fa, fw = torch.tensor([ga], device="cuda"), torch.full((E,), gw, device="cuda")
+    cfg = B.make_micro_product_config(offs[-1], E, N, K, "nv", dtype, swiglu=True)
+    ws = B.alloc_micro_product_workspace(cfg)
+    out = torch.full((offs[-1], N), 7.0, dtype=dtype, device="cuda")
+    B.moe_micro_product(cfg, gpu(offs), a, sa, fa, w, sw, fw, out, ws)
+    assert B.moe_device_status(ws) == B.MOE_OK
+    assert (out[[2, 77]] == 0).all()
+    if ga * gw == 1.0:
+        for e in range(E):
+            s = slice(offs[e], offs[e + 1])
+            y = va[s] @ vw[e * 2 * N:(e + 1) * 2 * N].t()
+            gate, up = y[:, :N], y[:, N:]
+            v = gate * torch.sigmoid(gate) * up
+            # 1.1 |u| of the gate's error (sigma is at least 1/2 here), |silu| of the other half's, the exponential's
+            tol = (STEP[dtype] + 3.3 * (K / 64 + 3) * 2.0 ** -22 + 2.0 ** -20) * v
+            assert ((out[s].double() - v).abs() <= tol).all(), f"expert {e}"
+    elif ga * gw < 1.0:
+        assert (out == 0).all()  # of the order of 1e-80
