@@ -41,8 +41,9 @@
 // Sums: the tensor cores cut what falls behind the sum's 24 bits at every MMA, always towards zero, so that
 // a long sum drifts by about 2^-25.5 of itself a step (5 x 10^-6 over 448 steps).  For fp32 outputs a sum stays
 // in tensor memory for 32 steps (grad_w, whose stores its storing warps barely keep up with, 64: 1024 rows);
-// the storing warps add such segments up in fp32, rounded to nearest.  A bf16
-// output's rounding is a thousand times that drift.
+// the storing warps add such segments up in fp32, rounded to nearest.  A bf16 output's half step, 2^-9 to 2^-8 of
+// it, is twelve times the drift of the 8192 steps that the widest forward and grad_x have, and that a group of
+// kLongRows rows has; weight gradients over more rows than that are summed in segments of 1024 steps.
 //
 // Kernel shape: persistent, warp 0 copies, warp 1 issues (on the pair's even SM), warps 2..9 store, grad_w's
 // warp 10 clears: a lane has a feature, so that a warp's store covers 128 (fp32) or 2 x 64 (bf16) consecutive
@@ -75,9 +76,15 @@ constexpr int kBarBytes = 256;
 constexpr int kTable = (4 * (kProductMaxGroups + 1)) * 4 + kMaxWarps * 4;
 constexpr int kSmemMost = 232448 - 1024 - kBarBytes - kTable;
 
+// Rows of a call above which a bf16 weight gradient, whose groups' sizes the host does not know, is summed in
+// segments (see above).  8192 rows of 64 experts, 4096 x 7168: 899 us without them, 989 with them (the storing warps
+// hold a tile's sums in registers until the last segment); 133120 rows, 2048 x 2048, 8 and 64 experts: 596 and 651
+// without, 598 and 657 with them; 2^23 rows of one expert: 5% too small without.
+constexpr int64_t kLongRows = 1 << 17;
+
 enum Op { OP_FORWARD, OP_GRAD_X, OP_GRAD_W, OP_MX, OP_NV };
 
-template <int kOp, bool kSwiGLU, bool kF32>
+template <int kOp, bool kSwiGLU, bool kF32, bool kLong = false>
 struct Shape {
   static constexpr bool kMicro = kOp == OP_MX || kOp == OP_NV;
   static constexpr int kMaxRows = !kMicro ? 256 : kSwiGLU && kF32 ? 128 : 192;  // rows of a tile
@@ -85,7 +92,8 @@ struct Shape {
   static constexpr int kStep = kMicro ? 64 : 16;           // and per MMA
   static constexpr int kSums = kSwiGLU ? 2 : 1;            // W1 and W3, or one
   // blocks summed in tensor memory at a time (see above)
-  static constexpr int kSegment = !kF32 ? 1 << 30 : kOp == OP_GRAD_W ? 16 : 8;
+  static constexpr bool kSegmented = kF32 || kLong;
+  static constexpr int kSegment = !kSegmented ? 1 << 30 : !kF32 ? 256 : kOp == OP_GRAD_W ? 16 : 8;
   static constexpr int kTiles = kOp == OP_NV ? 4 : kOp == OP_MX ? 2 : 0;  // scale tiles per 128 rows
   static constexpr int kOpA = kSums * kBox;
   static constexpr int kOpB = kMaxRows / 2 * 128;
@@ -198,10 +206,10 @@ __device__ __forceinline__ float silu(float g) {
   return __fdividef(g, 1.0f + (kAccurate ? expf(-g) : __expf(-g)));
 }
 
-template <int kOp, bool kSwiGLU, bool kF32, bool kAdd>
-__global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
+template <int kOp, bool kSwiGLU, bool kF32, bool kAdd, bool kLong>
+__global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
     product_kernel(const __grid_constant__ ProductParams p) {
-  using S = Shape<kOp, kSwiGLU, kF32>;
+  using S = Shape<kOp, kSwiGLU, kF32, kLong>;
   constexpr bool kMicro = S::kMicro, kNv = kOp == OP_NV, kGradW = kOp == OP_GRAD_W;
   constexpr bool kAMn = kOp == OP_GRAD_X || kGradW, kBMn = kGradW;
   constexpr int kStage = S::kStage, kStages = S::kStages, kMaxRows = S::kMaxRows;
@@ -540,14 +548,15 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
       const auto col = [&](int ch) { return (kParts * ch + part) * (kGradW && !kF32 ? 32 : 16); };
       const int end = t.valid;
       uint8_t* buf = staging + (warp - 2) * 2048;                     // grad_w
-      if constexpr (kF32) {
+      if constexpr (S::kSegmented) {
         // Segments of the sum, added up here in fp32 (rounded to nearest, where the tensor cores cut).
-        constexpr int kChunks = S::kChunks;
-        float sum[S::kSums][kChunks * 16];
+        constexpr int kPieces = kGradW && !kF32 ? 2 : 1;  // of 16 columns, in a chunk
+        constexpr int kChunks = S::kChunks / kPieces;
+        float sum[S::kSums][S::kChunks * 16];
 #pragma unroll
         for (int m = 0; m < S::kSums; ++m)
 #pragma unroll
-          for (int i = 0; i < kChunks * 16; ++i) sum[m][i] = 0.0f;
+          for (int i = 0; i < S::kChunks * 16; ++i) sum[m][i] = 0.0f;
         const auto release = [&] {
           tc_fence_before();
           __syncwarp();
@@ -555,10 +564,10 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
           if (S::kAccs == 2) acc ^= 1u;
           if (acc == 0) acc_phase ^= 1u;
         };
-        const auto read = [&](int ch, uint32_t (&g)[S::kSums][16]) {
+        const auto read = [&](int c, uint32_t (&g)[S::kSums][16]) {
           const uint32_t tb = tmem_base + acc * S::kAccCols + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll
-          for (int m = 0; m < S::kSums; ++m) tmem_ld16(tb + m * kMaxRows + col(ch), g[m]);
+          for (int m = 0; m < S::kSums; ++m) tmem_ld16(tb + m * kMaxRows + c, g[m]);
           tmem_ld_wait();
         };
         bool ok = true;
@@ -571,12 +580,16 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) {
               if (col(ch) < end) {
-                uint32_t g[S::kSums][16];
-                read(ch, g);
 #pragma unroll
-                for (int m = 0; m < S::kSums; ++m)
+                for (int h = 0; h < kPieces; ++h) {
+                  uint32_t g[S::kSums][16];
+                  read(col(ch) + 16 * h, g);
 #pragma unroll
-                  for (int i = 0; i < 16; ++i) sum[m][16 * ch + i] += __uint_as_float(g[m][i]);
+                  for (int m = 0; m < S::kSums; ++m)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                      sum[m][16 * (kPieces * ch + h) + i] += __uint_as_float(g[m][i]);
+                }
               }
             }
           }
@@ -594,8 +607,24 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
             const int c = col(ch);
             if (c >= end) continue;
             uint32_t g[S::kSums][16];
+            if constexpr (kPieces == 2) {
+              uint32_t v[16];
+#pragma unroll
+              for (int h = 0; h < kPieces; ++h) {
+                float* part_sum = &sum[0][16 * (kPieces * ch + h)];
+                if (!none) {
+                  read(c + 16 * h, g);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) part_sum[i] += __uint_as_float(g[0][i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[8 * h + i] = pack_bf16x2(part_sum[2 * i], part_sum[2 * i + 1]);
+              }
+              store_dw<false>(&p.mout, buf, lane, v, t.lrow0 + c, feat0, t.g);
+              continue;
+            }
             if (!none) {
-              read(ch, g);
+              read(c, g);
 #pragma unroll
               for (int m = 0; m < S::kSums; ++m)
 #pragma unroll
@@ -742,10 +771,10 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32>::kThreads, 1)
   }
 }
 
-template <int kOp, bool kSwiGLU, bool kF32, bool kAdd = false>
+template <int kOp, bool kSwiGLU, bool kF32, bool kAdd = false, bool kLong = false>
 cudaError_t launch(const ProductParams& p, int sms, cudaStream_t st, const char* label) {
-  using S = Shape<kOp, kSwiGLU, kF32>;
-  auto kern = product_kernel<kOp, kSwiGLU, kF32, kAdd>;
+  using S = Shape<kOp, kSwiGLU, kF32, kLong>;
+  auto kern = product_kernel<kOp, kSwiGLU, kF32, kAdd, kLong>;
   static std::atomic<uint64_t> set{0};  // devices whose attribute is set
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), S::kSmem, &set);
   if (e != cudaSuccess) return e;
@@ -796,8 +825,9 @@ cudaError_t launch_grouped_product(const GroupedProduct& g, int sms, cudaStream_
   const bool f32 = g.out_dtype == MOE_F32;
   if (grad_w) {
     if (g.accumulate) return launch<OP_GRAD_W, false, true, true>(p, sms, st, "grouped_grad_w");
-    return f32 ? launch<OP_GRAD_W, false, true>(p, sms, st, "grouped_grad_w")
-               : launch<OP_GRAD_W, false, false>(p, sms, st, "grouped_grad_w");
+    if (f32) return launch<OP_GRAD_W, false, true>(p, sms, st, "grouped_grad_w");
+    return g.rows > kLongRows ? launch<OP_GRAD_W, false, false, false, true>(p, sms, st, "grouped_grad_w")
+                              : launch<OP_GRAD_W, false, false>(p, sms, st, "grouped_grad_w");
   }
   if (fwd)
     return f32 ? launch<OP_FORWARD, false, true>(p, sms, st, "grouped_forward")

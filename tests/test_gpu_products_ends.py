@@ -1,5 +1,5 @@
 """GPU tests of the products grouped by expert and the microscaled operators at the ends that their documents
-allow: factors whose product leaves fp32.
+allow: factors whose product leaves fp32, weight gradients over millions of rows.
 
 Tolerances as in test_gpu_micro.py: half a step of the output's type, 2^-22 sum |a w| for each MMA step of the
 sum, two roundings of 2^-24 for the factors; below the smallest normal number half a step is 2^-150 in fp32
@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from mixture_experts_ffn_gemm_gb300 import binding as B
+import test_gpu_grouped as grouped
 from test_gpu_micro import E4M3, LUT, gpu, offsets_of, pack, scale_index
 
 pytestmark = pytest.mark.gpu
@@ -90,3 +91,38 @@ def test_swiglu_with_factors_whose_product_leaves_fp32(cuda_device, ga, gw, dtyp
             assert ((out[s].double() - v).abs() <= tol).all(), f"expert {e}"
     elif ga * gw < 1.0:
         assert (out == 0).all()  # of the order of 1e-80
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows", [1 << 21, (1 << 23) - 5])
+def test_weight_gradients_of_long_groups_do_not_drift(cuda_device, rows, dtype):
+    """Positive terms.  A step cuts the sum by at most 2^-23 of it, always downwards, and a bf16 output's sum is
+    cut at most 1024 times (an fp32 one's 64 times) before it is added to the others in fp32: 2^-13 (2^-17) of the
+    sum.  rows / 16384 (rows / 1024) such additions round by 2^-24 of it each."""
+    N, K, counts = 24, 40, [rows, 100, 0, 37]
+    offs, R, a, b = grouped._make("grad_w", counts, N, K, seed=20)
+    a.abs_(), b.abs_()
+    out = grouped._call("grad_w", offs, R, a, b, N, K, dtype)
+    steps = 1024 if dtype is BF16 else 64
+    for e in range(len(counts)):
+        v = torch.zeros(N, K, dtype=torch.float64, device="cuda")
+        for lo in range(offs[e], offs[e + 1], 1 << 20):
+            s = slice(lo, min(lo + (1 << 20), offs[e + 1]))
+            v += a[s].double().t() @ b[s].double()
+        tol = STEP[dtype] + steps * 2.0 ** -23 + (counts[e] / (16 * steps) + 2) * 2.0 ** -24
+        assert ((out[e].double() - v).abs() <= tol * v).all(), f"expert {e}"
+
+
+@pytest.mark.parametrize("counts", [[0, 1, 127, 128, 129, 0, 300, 16, 33, 0], [16384, 16385, 0, 16383, 32768 + 17, 5],
+                                    [70000, 3, 64, 0, 60000]])
+@pytest.mark.parametrize("N,K", [(264, 72), (200, 520), (8, 8), (736, 1000)])
+def test_weight_gradients_of_calls_with_many_rows(cuda_device, counts, N, K):
+    """Ragged groups in a call of more than 2^17 rows, most of them of no expert in the first case."""
+    behind = (1 << 17) + 8 - sum(counts) if sum(counts) <= 1 << 17 else 0
+    offs, R, a, b = grouped._make("grad_w", counts, N, K, behind=behind, seed=21)
+    assert R > 1 << 17
+    a[offs[-1]:], b[offs[-1]:] = float("nan"), float("inf")
+    out = grouped._call("grad_w", offs, R, a, b, N, K, BF16)
+    grouped._check("grad_w", out, offs, grouped._reference("grad_w", offs, a, b, N, K))
+    again = grouped._call("grad_w", offs, R, a, b, N, K, BF16)
+    assert torch.equal(out, again)
