@@ -445,9 +445,10 @@ size_t moe_micro_scales_size(const moe_micro_config_t* cfg);
 /* Rows of x to codes and scales.
  *   x      [src_rows][K] dtype;  dest [src_rows][copies] int32: the coded rows that take source row t
  *          (perm_dst of moe_permute with copies = k: the experts' rows, each token quantised once), or
- *          NULL with copies == 1 and src_rows == rows: row t.  Coded rows that no entry names are left
- *          as they are; an entry outside the groups' rows is skipped and raises MOE_ERR_DEVICE_CHECK.
- *          Two entries may not name one row.
+ *          NULL with copies == 1 and src_rows == rows: row t, for t < offsets[groups].  Coded rows that
+ *          no entry names and, without dest, rows from offsets[groups] on are left as they are; an entry
+ *          outside the groups' rows is skipped and raises MOE_ERR_DEVICE_CHECK.  Two entries may not name
+ *          one row.
  *   factor g, one fp32 on the device (MOE_MICRO_NV; NULL: 1).  Ignored for MOE_MICRO_MX.
  *   ws     at least 256 bytes, the device status as for moe_grouped_product. */
 moe_status_t moe_micro_quantize(const moe_micro_config_t* cfg, const void* x, const int32_t* dest,

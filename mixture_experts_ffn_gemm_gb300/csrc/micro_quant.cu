@@ -254,6 +254,11 @@ struct CopyTo {  // where a copy of the row starts
   uint8_t* scales;
 };
 
+// Where the rows of the last group end: rows behind are left as they are.
+__device__ __forceinline__ int64_t rows_end(const MicroParams& p) {
+  return p.offsets ? min(p.rows, (int64_t)max(ld_int(p.offsets + p.G), 0)) : p.rows;
+}
+
 template <bool kNv, bool kF32>
 __global__ void __launch_bounds__(kThreads, kF32 ? 2 : 3) micro_quantize_kernel(const MicroParams p) {
   __shared__ CopyTo to_all[kThreads / 32][kMaxCopies];
@@ -263,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, kF32 ? 2 : 3) micro_quantize_kernel(
   CopyTo* to = to_all[threadIdx.x >> 5];
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int64_t t = w / p.parts;
-  if (t >= p.src_rows) return;
+  if (t >= p.src_rows || (!p.dest && t >= rows_end(p))) return;
   const int part = (int)(w - t * p.parts);
   // a lane has 32 channels: one block of MX, two of NV
   constexpr int kRaw = kF32 ? 8 : 4;
@@ -357,8 +362,7 @@ __global__ void __launch_bounds__(kThreads) micro_dequantize_kernel(const MicroP
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int64_t row = w / p.parts;
-  const int64_t end = p.offsets ? min(p.rows, (int64_t)max(ld_int(p.offsets + p.G), 0)) : p.rows;
-  if (row >= end) return;  // rows behind the last group are left as they are
+  if (row >= rows_end(p)) return;
   const int part = (int)(w - row * p.parts);
   const float g = kNv && p.factor ? ld_float(p.factor) : 1.0f;
   const int64_t sb = __shfl_sync(~0u, scale_base(p, (int)row, 1, lane), 0);

@@ -1,5 +1,5 @@
 """GPU tests of the products grouped by expert and the microscaled operators at the ends that their documents
-allow: factors whose product leaves fp32, weight gradients over millions of rows.
+allow: factors whose product leaves fp32, weight gradients over millions of rows, rows behind the last expert.
 
 Tolerances as in test_gpu_micro.py: half a step of the output's type, 2^-22 sum |a w| for each MMA step of the
 sum, two roundings of 2^-24 for the factors; below the smallest normal number half a step is 2^-150 in fp32
@@ -9,7 +9,7 @@ import torch
 
 from mixture_experts_ffn_gemm_gb300 import binding as B
 import test_gpu_grouped as grouped
-from test_gpu_micro import E4M3, LUT, gpu, offsets_of, pack, scale_index
+from test_gpu_micro import E4M3, LUT, gpu, offsets_of, pack, quantize64, scale_index, unpack
 
 pytestmark = pytest.mark.gpu
 
@@ -126,3 +126,64 @@ def test_weight_gradients_of_calls_with_many_rows(cuda_device, counts, N, K):
     grouped._check("grad_w", out, offs, grouped._reference("grad_w", offs, a, b, N, K))
     again = grouped._call("grad_w", offs, R, a, b, N, K, BF16)
     assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("counts,behind", [([3, 0, 140], 200), ([1], 1), ([0, 0], 5), ([128, 128], 7), ([2, 700], 3000)])
+def test_rows_behind_the_last_expert_are_not_quantised(cuda_device, fmt, dtype, counts, behind):
+    """A padded buffer without destinations: the groups' rows as ever; the others' codes and scales stay, and the
+    status too."""
+    K, offs = 320, offsets_of(counts)
+    R, E = offs[-1], len(counts)
+    x = torch.randn(R + behind, K, generator=torch.Generator().manual_seed(30)).to(dtype)
+    x[R:] = float("nan")
+    cfg = B.make_micro_config(R + behind, K, fmt, groups=E, dtype=dtype)
+    codes, scales = B.alloc_micro(cfg)
+    codes.fill_(0xEE)
+    scales.fill_(0xEE)
+    ws = B.alloc_micro_workspace(cfg)
+    B.moe_micro_quantize(cfg, x.cuda(), None, gpu(offs), None, codes, scales, ws)
+    assert B.moe_device_status(ws) == B.MOE_OK
+    code, byte = quantize64(x[:R], fmt)
+    assert torch.equal(unpack(codes)[:R], code) and (codes[R:] == 0xEE).all()
+    got = scales.cpu()
+    idx = scale_index(offs, K, fmt)
+    assert torch.equal(got[idx.view(-1)].long(), byte.view(-1))
+    # columns behind K in a row's last tile (of 64 channels with nv, which K fills, of 128 with mx) are free;
+    # everything else is as it was
+    written = torch.zeros_like(got, dtype=torch.bool)
+    tile = 64 if fmt == "nv" else 128
+    whole = scale_index(offs, (K + tile - 1) // tile * tile, fmt)
+    written[whole.view(-1)] = True
+    assert (got[~written] == 0xEE).all()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_a_padded_chain_of_products_raises_nothing(cuda_device, fmt):
+    """Product, quantisation, product, back in a buffer with room for more rows than the experts have: the status
+    stays clear, rows behind keep what they held, and the others are what they are without the room."""
+    counts, N, K = [70, 0, 33], 128, 192
+    offs, E = offsets_of(counts), len(counts)
+    w1, w2 = (torch.randn(E, N, k, generator=torch.Generator().manual_seed(31)).to(BF16).cuda() for k in (K, N))
+    x = torch.randn(offs[-1], K, generator=torch.Generator().manual_seed(32)).to(BF16).cuda()
+    results = []
+    for room in (0, 77):
+        R = offs[-1] + room
+        xp = torch.full((R, K), float("nan"), dtype=BF16, device="cuda")
+        xp[:offs[-1]] = x
+        h, y, back = (torch.full((R, N), 7.0, dtype=t, device="cuda") for t in (BF16, F32, F32))
+        cfg = B.make_micro_config(R, N, fmt, groups=E)
+        cw = B.make_micro_config(E * N, N, fmt, groups=E)
+        ws = B.alloc_micro_workspace(cfg)
+        hq, wq = B.alloc_micro(cfg), B.alloc_micro(cw)
+        B.moe_micro_quantize(cw, w2.view(E * N, N), None, None, None, *wq, ws)
+        B.moe_grouped_product(B.make_product_config(R, E, N, K), gpu(offs), xp, w1, h, ws)
+        B.moe_micro_quantize(cfg, h, None, gpu(offs), None, *hq, ws)
+        B.moe_micro_product(B.make_micro_product_config(R, E, N, N, fmt, F32), gpu(offs), *hq, None, *wq, None, y, ws)
+        B.moe_micro_dequantize(B.make_micro_config(R, N, fmt, groups=E, dtype=F32), *hq, gpu(offs), None, back, ws)
+        assert B.moe_device_status(ws) == B.MOE_OK
+        assert all((t[offs[-1]:] == 7.0).all() for t in (h, y, back))
+        results.append([t[:offs[-1]].clone() for t in (h, y, back)])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
