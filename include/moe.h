@@ -394,12 +394,17 @@ typedef enum {
   MOE_PRODUCT_GRAD_W = 2
 } moe_product_t;
 #define MOE_PRODUCT_ACCUMULATE 0x1u
+/* Test hook for the failure path: the second SM of each pair stops copying after three blocks, so that the
+ * waits for its operands (shortened to 20 ms under this flag) expire; the kernel flags MOE_ERR_TIMEOUT in the
+ * device status, lets its copies land, frees its tensor memory and returns, and the output is incomplete.
+ * Never set in normal use. */
+#define MOE_PRODUCT_TEST_STALL 0x100u
 typedef struct {
   int64_t rows;      /* rows of the row buffers, >= 0         */
   int32_t E, N, K;   /* experts, W's rows and columns         */
   int32_t kind;      /* MOE_PRODUCT_*                         */
   int32_t out_dtype; /* MOE_BF16 or MOE_F32                   */
-  uint32_t flags;    /* MOE_PRODUCT_ACCUMULATE                */
+  uint32_t flags;    /* MOE_PRODUCT_ACCUMULATE (or _TEST_*)   */
   int64_t ld_x, ld_y;
 } moe_product_config_t;
 size_t moe_product_workspace_size(const moe_product_config_t* cfg);

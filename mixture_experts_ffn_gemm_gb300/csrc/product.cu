@@ -127,6 +127,8 @@ struct ProductParams {
   void* out;
   int64_t ldo;
   uint32_t* err;
+  uint64_t wait_ns;        // the bounded waits' limit
+  int32_t stall;           // test hook: blocks after which a pair's odd SM copies nothing more (0: none)
 };
 
 // Descriptor of an MN-major operand: boxes of 64 outputs (128 bytes) x 64 rows of the sum, 128-byte
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
   if (warp == 0) {
     uint32_t stage = 0, phase = 0;
     uint32_t full_uses = 0, landed_uses = 0, in_landed = 0;  // a bit a stage: uses (mod 2), the last one's barrier
-    int armed = 0;
+    int armed = 0, blocks = 0;
     bool ok = true;
     for (int tile = tile0; tile < total && ok; tile += tstep) {
       const ProductTile t = tile_of(tile);
@@ -340,9 +342,10 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
       const int gw_n = t.lrow0 + (int)rank * (n / 2), gw_r = kGradW ? uniform(tab.row0[g]) : 0;
       const CUtensorMap* mrow = &p.mrow[n / 32 - 1];
       for (int kb = 0; kb < nkb; ++kb) {
-        ok = __all_sync(~0u, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err));
+        ok = __all_sync(~0u, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err, p.wait_ns));
         if (!ok) break;
-        if (elect_one()) {
+        const bool mute = p.stall && !leader && blocks++ >= p.stall;
+        if (!mute && elect_one()) {
           uint8_t* sa = smem + stage * kStage;
           uint8_t* sb = sa + S::kOpA;
           // Both SMs' copies complete on the even SM's full[stage]; of a block that is cleared, each
@@ -396,13 +399,22 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
         }
       }
     }
-    if (!ok) {  // let the copies of the last stage uses land (the odd SM's shared ones: the even SM waits)
+    if (!ok) {  // let the copies of the last stage uses land
+      bool counted_there = false;
       for (int i = 0; i < armed; ++i) {
         stage = stage ? stage - 1 : kStages - 1;
         const bool own = in_landed >> stage & 1u;
         if (own || leader)
           mbar_wait(own ? &landed[stage] : &full[stage],
                     (own ? landed_uses : full_uses) >> stage & 1u ^ 1u, nullptr, nullptr, kDrainLimitNs);
+        else
+          counted_there = true;
+      }
+      // Copies of the odd SM that count on the even SM's barriers: only that SM can ask those, and it may have
+      // stopped before it expected the last of them.  They get the limit itself; both SMs stay until it is over.
+      if (counted_there) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 <= kDrainLimitNs) __nanosleep(1000);
       }
     }
   } else if (warp == 1 && leader) {
@@ -426,7 +438,7 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
                                      : idesc_bf16_f32_pair(n) | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u);
       const uint32_t idesc_second = idesc_micro<kNv>(0, 2) - idesc_micro<kNv>(0, 0);
       for (int k0 = 0; k0 < nkb; k0 += S::kSegment) {  // a segment of the sum, into sums that have been read
-        ok = __all_sync(~0u, mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, abort_flag, p.err));
+        ok = __all_sync(~0u, mbar_wait_cluster(&tempty[acc], acc_phase ^ 1u, abort_flag, p.err, p.wait_ns));
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem_base + acc * S::kAccCols;
@@ -436,10 +448,10 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
           const int steps = (left + S::kStep - 1) / S::kStep;
           if (to_clear(left)) {
             ok = __all_sync(~0u, mbar_wait_cluster(&cleared[stage], cleared_phase >> stage & 1u,
-                                                   abort_flag, p.err));
+                                                   abort_flag, p.err, p.wait_ns));
             cleared_phase ^= 1u << stage;
           } else {
-            ok = __all_sync(~0u, mbar_wait(&full[stage], full_phase >> stage & 1u, abort_flag, p.err));
+            ok = __all_sync(~0u, mbar_wait(&full[stage], full_phase >> stage & 1u, abort_flag, p.err, p.wait_ns));
             full_phase ^= 1u << stage;
           }
           if (!ok) break;
@@ -501,7 +513,7 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
       for (int kb = 0; kb * S::kBlock < len; ++kb) {
         const int left = block_len(len, kb);
         if (to_clear(left)) {
-          ok = __all_sync(~0u, mbar_wait(&landed[stage], phase >> stage & 1u, abort_flag, p.err));
+          ok = __all_sync(~0u, mbar_wait(&landed[stage], phase >> stage & 1u, abort_flag, p.err, p.wait_ns));
           if (!ok) break;
           phase ^= 1u << stage;
           clear_rows<4>(smem + stage * kStage, left, (left + S::kStep - 1) / S::kStep * S::kStep, lane);
@@ -573,7 +585,7 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
         bool ok = true;
         int at = 0;
         for (; len - at > S::kSegment * S::kBlock; at += S::kSegment * S::kBlock) {  // all but the last
-          ok = __all_sync(~0u, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err));
+          ok = __all_sync(~0u, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err, p.wait_ns));
           if (!ok) break;
           tc_fence_after();
           if (feat0 < p.F) {
@@ -597,7 +609,7 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
         }
         if (!ok) break;
         if (!none) {
-          if (!__all_sync(~0u, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err))) break;
+          if (!__all_sync(~0u, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err, p.wait_ns))) break;
           tc_fence_after();
         }
         if (feat0 < p.F) {
@@ -656,7 +668,7 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
         continue;
       }
       read_factors();
-      if (!none && !__all_sync(~0u, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err))) break;
+      if (!none && !__all_sync(~0u, mbar_wait(&tfull[acc], acc_phase, abort_flag, p.err, p.wait_ns))) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + acc * S::kAccCols + ((uint32_t)(quarter * 32) << 16);
       // Outputs f of 16 rows from column c on, a lane's feature.  Lanes in twos: of four rows the even one takes both
@@ -822,6 +834,8 @@ cudaError_t launch_grouped_product(const GroupedProduct& g, int sms, cudaStream_
   p.out = g.out;
   p.ldo = g.ldo;
   p.err = g.err;
+  p.wait_ns = g.test_stall ? 20000000ull : kWaitLimitNs;
+  p.stall = g.test_stall ? 3 : 0;
   const bool f32 = g.out_dtype == MOE_F32;
   if (grad_w) {
     if (g.accumulate) return launch<OP_GRAD_W, false, true, true>(p, sms, st, "grouped_grad_w");
@@ -860,6 +874,7 @@ cudaError_t launch_micro_product(const MicroProduct& g, int sms, cudaStream_t st
   p.out = g.out;
   p.ldo = g.ldo;
   p.err = g.err;
+  p.wait_ns = kWaitLimitNs;
   const bool f32 = g.out_dtype == MOE_F32;
   return nv ? launch_micro<OP_NV>(p, g.swiglu, f32, sms, st)
             : launch_micro<OP_MX>(p, g.swiglu, f32, sms, st);

@@ -1,5 +1,6 @@
 """GPU tests of the products grouped by expert and the microscaled operators at the ends that their documents
-allow: factors whose product leaves fp32, weight gradients over millions of rows, rows behind the last expert.
+allow: factors whose product leaves fp32, weight gradients over millions of rows, rows behind the last expert; and waits that
+run out.
 
 Tolerances as in test_gpu_micro.py: half a step of the output's type, 2^-22 sum |a w| for each MMA step of the
 sum, two roundings of 2^-24 for the factors; below the smallest normal number half a step is 2^-150 in fp32
@@ -187,3 +188,20 @@ def test_a_padded_chain_of_products_raises_nothing(cuda_device, fmt):
         results.append([t[:offs[-1]].clone() for t in (h, y, back)])
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind", grouped.KINDS)
+def test_an_expired_wait_is_reported_and_the_next_call_is_right(cuda_device, kind, dtype):
+    """The failure path without a GPU fault: the test flag withholds copies, the waits for them (20 ms) run out,
+    the kernel returns with MOE_ERR_TIMEOUT in the status and the context stays usable."""
+    N, K, counts = 264, 520, [0, 1, 127, 128, 129, 0, 300, 16, 33, 0]
+    offs, R, a, b = grouped._make(kind, counts, N, K, seed=40)
+    cfg = grouped._config(kind, R, len(counts), N, K, dtype)
+    cfg.flags |= B.MOE_PRODUCT_TEST_STALL
+    ws = B.alloc_product_workspace(cfg)
+    out = grouped._out(kind, R, len(counts), N, K, dtype)
+    B.moe_grouped_product(cfg, gpu(offs), a, b, out, ws)
+    assert B.moe_device_status(ws) == B.MOE_ERR_TIMEOUT
+    out = grouped._call(kind, offs, R, a, b, N, K, dtype)
+    grouped._check(kind, out, offs, grouped._reference(kind, offs, a, b, N, K))
