@@ -394,11 +394,12 @@ typedef enum {
   MOE_PRODUCT_GRAD_W = 2
 } moe_product_t;
 #define MOE_PRODUCT_ACCUMULATE 0x1u
-/* Test hook for the failure path: the second SM of each pair stops copying after three blocks, so that the
+/* Test hooks, never set in normal use.  SHORT_WAITS: bounded waits give up after 10 ms in place of 2 s; a run of
+ * any length passes, as each wait is for the tile at hand.  STALL, for the failure path: the second SM of each pair stops copying after three blocks, so that the
  * waits for its operands (shortened to 20 ms under this flag) expire; the kernel flags MOE_ERR_TIMEOUT in the
- * device status, lets its copies land, frees its tensor memory and returns, and the output is incomplete.
- * Never set in normal use. */
+ * device status, lets its copies land, frees its tensor memory and returns, and the output is incomplete. */
 #define MOE_PRODUCT_TEST_STALL 0x100u
+#define MOE_PRODUCT_TEST_SHORT_WAITS 0x200u
 typedef struct {
   int64_t rows;      /* rows of the row buffers, >= 0         */
   int32_t E, N, K;   /* experts, W's rows and columns         */

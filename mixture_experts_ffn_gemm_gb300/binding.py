@@ -41,7 +41,7 @@ MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_ELEMENT = 0, 1, 2, 3
 MOE_JOIN_GATE_SIGMOID = 0x1
 MOE_PRODUCT_FORWARD, MOE_PRODUCT_GRAD_X, MOE_PRODUCT_GRAD_W = 0, 1, 2
 MOE_PRODUCT_ACCUMULATE = 0x1
-MOE_PRODUCT_TEST_STALL = 0x100
+MOE_PRODUCT_TEST_STALL, MOE_PRODUCT_TEST_SHORT_WAITS = 0x100, 0x200
 MOE_MICRO_MX, MOE_MICRO_NV = 0, 1
 MOE_MICRO_MAX_COPIES = 32
 MOE_MICRO_SWIGLU = 0x1

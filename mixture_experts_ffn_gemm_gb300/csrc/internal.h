@@ -284,7 +284,7 @@ struct GroupedProduct {
   int64_t ldo = 0;
   int out_dtype = MOE_BF16;
   bool accumulate = false;
-  bool test_stall = false;  // test hook (MOE_PRODUCT_TEST_STALL): see moe.h
+  bool test_stall = false, test_short_waits = false;  // test hooks (MOE_PRODUCT_TEST_*): see moe.h
   uint32_t* err = nullptr;
 };
 cudaError_t launch_grouped_product(const GroupedProduct& g, int sms, cudaStream_t st);

@@ -111,7 +111,7 @@ struct Shape {
   static constexpr int kSfCols = (kSums * 4 + 8) * kTiles; // columns of a stage's scales
   static constexpr int kSfCol0 = kAccs * kAccCols;
   static_assert(kSfCol0 + 2 * kSfCols <= 512, "tensor memory");
-  static_assert(kStage % 1024 == 0 && kStages >= 3 && (4 * kStages + 5) * 8 + 8 <= kBarBytes, "");
+  static_assert(kStage % 1024 == 0 && kStages >= 3 && (4 * kStages + 5) * 8 + 12 <= kBarBytes, "");
 };
 
 struct ProductParams {
@@ -148,6 +148,29 @@ __device__ __forceinline__ void clear_rows(uint8_t* box0, int from, int to, int 
     for (int i = lane; i < n; i += 32) r[i] = make_uint4(0, 0, 0, 0);
   }
   fence_async_smem();
+}
+
+// mbar_wait for a warp that may be any number of blocks ahead of the copies that it waits for: it gives up after
+// a limit's time in which no block was copied.
+__device__ __forceinline__ bool wait_behind(uint64_t* bar, uint32_t parity, volatile const int* copied,
+                                            volatile int* abort, uint32_t* err, uint64_t limit_ns) {
+  if (mbar_test(bar, parity)) return true;
+  int seen = *copied;
+  uint64_t t0 = globaltimer_ns();
+  while (!mbar_test(bar, parity)) {
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      const int now = *copied;
+      if (now == seen) {
+        *abort = 1;
+        raise_flag(err, kErrTimeout);
+        return false;
+      }
+      seen = now;
+      t0 = globaltimer_ns();
+    }
+  }
+  return true;
 }
 
 // A 512-byte scale tile: 32 rows of 16 bytes without swizzle, 8-row groups 128 bytes apart.
@@ -232,6 +255,7 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  volatile int* blocks_copied = abort_flag + 1;  // grad_w: this SM's copying warp counts them
   GroupTable tab;
   tab.tile_start = reinterpret_cast<int*>(staging + S::kStaging + kBarBytes);
   tab.row0 = tab.tile_start + kProductMaxGroups + 1;
@@ -254,6 +278,7 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
+    *blocks_copied = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -322,7 +347,8 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
   if (warp == 0) {
     uint32_t stage = 0, phase = 0;
     uint32_t full_uses = 0, landed_uses = 0, in_landed = 0;  // a bit a stage: uses (mod 2), the last one's barrier
-    int armed = 0, blocks = 0;
+    int armed = 0;
+    uint32_t blocks = 0;
     bool ok = true;
     for (int tile = tile0; tile < total && ok; tile += tstep) {
       const ProductTile t = tile_of(tile);
@@ -344,7 +370,7 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
       for (int kb = 0; kb < nkb; ++kb) {
         ok = __all_sync(~0u, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err, p.wait_ns));
         if (!ok) break;
-        const bool mute = p.stall && !leader && blocks++ >= p.stall;
+        const bool mute = p.stall && !leader && blocks >= (uint32_t)p.stall;
         if (!mute && elect_one()) {
           uint8_t* sa = smem + stage * kStage;
           uint8_t* sb = sa + S::kOpA;
@@ -383,6 +409,8 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
             if (two) tma_load_2d_pair(f + S::kSfB / 2, &p.msr, bar, 0, st_r + p.ktiles + kt);
           }
         }
+        ++blocks;
+        if (kGradW && lane == 0) *blocks_copied = (int)blocks;
         __syncwarp();
         const uint32_t bit = 1u << stage;
         if (to_clear(block_len(len, kb))) {
@@ -505,7 +533,8 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
     __syncwarp();
     mbar_wait(drain, 0, nullptr, nullptr, kDrainLimitNs);
   } else if (kGradW && warp == 2 + kEpilogueWarps) {
-    // clears this SM's rows behind the group, as soon as a block that has some has landed
+    // clears this SM's rows behind the group, as soon as a block that has some has landed; it does not wait
+    // for the others, of which there may be a whole group's
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     for (int tile = tile0; tile < total && ok; tile += tstep) {
@@ -513,7 +542,8 @@ __global__ void __launch_bounds__(Shape<kOp, kSwiGLU, kF32, kLong>::kThreads, 1)
       for (int kb = 0; kb * S::kBlock < len; ++kb) {
         const int left = block_len(len, kb);
         if (to_clear(left)) {
-          ok = __all_sync(~0u, mbar_wait(&landed[stage], phase >> stage & 1u, abort_flag, p.err, p.wait_ns));
+          ok = __all_sync(~0u, wait_behind(&landed[stage], phase >> stage & 1u, blocks_copied, abort_flag, p.err,
+                                           p.wait_ns));
           if (!ok) break;
           phase ^= 1u << stage;
           clear_rows<4>(smem + stage * kStage, left, (left + S::kStep - 1) / S::kStep * S::kStep, lane);
@@ -834,7 +864,7 @@ cudaError_t launch_grouped_product(const GroupedProduct& g, int sms, cudaStream_
   p.out = g.out;
   p.ldo = g.ldo;
   p.err = g.err;
-  p.wait_ns = g.test_stall ? 20000000ull : kWaitLimitNs;
+  p.wait_ns = g.test_stall ? 20000000ull : g.test_short_waits ? 10000000ull : kWaitLimitNs;
   p.stall = g.test_stall ? 3 : 0;
   const bool f32 = g.out_dtype == MOE_F32;
   if (grad_w) {

@@ -66,7 +66,8 @@ moe_status_t validate(const moe_product_config_t* c) {
   if (!c || c->rows < 0 || c->E < 1 || c->N < 1 || c->K < 1) return MOE_ERR_INVALID_ARG;
   if (c->kind < MOE_PRODUCT_FORWARD || c->kind > MOE_PRODUCT_GRAD_W) return MOE_ERR_INVALID_ARG;
   if (c->out_dtype != MOE_BF16 && c->out_dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
-  if (c->flags & ~(MOE_PRODUCT_ACCUMULATE | MOE_PRODUCT_TEST_STALL)) return MOE_ERR_INVALID_ARG;
+  if (c->flags & ~(MOE_PRODUCT_ACCUMULATE | MOE_PRODUCT_TEST_STALL | MOE_PRODUCT_TEST_SHORT_WAITS))
+    return MOE_ERR_INVALID_ARG;
   if ((c->flags & MOE_PRODUCT_ACCUMULATE) &&
       (c->kind != MOE_PRODUCT_GRAD_W || c->out_dtype != MOE_F32))
     return MOE_ERR_UNSUPPORTED;
@@ -202,6 +203,7 @@ moe_status_t moe_grouped_product(const moe_product_config_t* cfg, const int32_t*
   g.out_dtype = cfg->out_dtype;
   g.accumulate = (cfg->flags & MOE_PRODUCT_ACCUMULATE) != 0;
   g.test_stall = (cfg->flags & MOE_PRODUCT_TEST_STALL) != 0;
+  g.test_short_waits = (cfg->flags & MOE_PRODUCT_TEST_SHORT_WAITS) != 0;
   g.err = static_cast<uint32_t*>(ws);
   const int sms = num_sms();
   (void)cudaGetLastError();

@@ -205,3 +205,31 @@ def test_an_expired_wait_is_reported_and_the_next_call_is_right(cuda_device, kin
     assert B.moe_device_status(ws) == B.MOE_ERR_TIMEOUT
     out = grouped._call(kind, offs, R, a, b, N, K, dtype)
     grouped._check(kind, out, offs, grouped._reference(kind, offs, a, b, N, K))
+
+
+@pytest.mark.parametrize("width,rows,dtype", [(8192, 393216, BF16), (8192, 393216, F32), (16384, 129024, BF16)])
+def test_a_run_longer_than_the_waits_limit_passes(cuda_device, width, rows, dtype):
+    """A group whose blocks are all whole, several times the limit long (10 ms under this flag), and behind it
+    one whose last block is cleared: the warp that clears it waits from the start, and no wait runs out."""
+    counts = [rows, 7]
+    offs, R = offsets_of(counts), sum(counts)
+    g = torch.Generator(device="cuda").manual_seed(41)
+    a, b = (torch.empty(R, width, dtype=BF16, device="cuda").normal_(generator=g) for _ in range(2))
+    cfg = grouped._config("grad_w", R, 2, width, width, dtype)
+    cfg.flags |= B.MOE_PRODUCT_TEST_SHORT_WAITS
+    ws = B.alloc_product_workspace(cfg)
+    out = torch.empty(2, width, width, dtype=dtype, device="cuda")
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    B.moe_grouped_product(cfg, gpu(offs), a, b, out, ws)
+    end.record()
+    assert B.moe_device_status(ws) == B.MOE_OK
+    assert start.elapsed_time(end) > 20.0  # else it shows nothing
+    for e, n in enumerate(counts):
+        v, mag = (torch.zeros(64, 64, dtype=torch.float64, device="cuda") for _ in range(2))
+        for lo in range(offs[e], offs[e + 1], 1 << 16):
+            p, q = (t[lo:min(lo + (1 << 16), offs[e + 1]), -64:].double() for t in (a, b))
+            v += p.t() @ q
+            mag += p.abs().t() @ q.abs()
+        tol = STEP[dtype] * v.abs() + (n / 16 + 2) * 2.0 ** -22 * mag
+        assert ((out[e, -64:, -64:].double() - v).abs() <= tol).all()
