@@ -511,9 +511,20 @@ class _Specs(tuple):
                                     *(rows or (0, 0, 0))) for dt, least, most, _, rows in self)
 
 
+def _refuse_devices(device, stream):
+    """The library launches on the current device: a stream or operands of another one are refused.  (A handle of 0
+    is every device's default stream, so that such a call would run here, on the other device's addresses.)"""
+    current = torch._C._cuda_getDevice()
+    of_stream = getattr(stream, "device", None)
+    if of_stream is not None and of_stream.index != current:
+        raise ValueError(f"stream: of device {of_stream.index}, the current device is {current}")
+    if device >= 0 and device != current:
+        raise ValueError(f"ws: on device {device}, the current device is {current}")
+
+
 def _launch(name, specs_of, cfg, tensors, ws, stream):
-    """The entry point `name` on operands that its specs describe, on the current device and stream, or
-    on a given stream and the workspace's device."""
+    """The entry point `name` on operands that its specs describe, on the current device and its current
+    stream or the given one."""
     key = bytes(cfg)
     specs = specs_of(key)
     lib = load_library()
@@ -522,6 +533,8 @@ def _launch(name, specs_of, cfg, tensors, ws, stream):
         stream = torch._C._cuda_getCurrentRawStream(device)
     else:
         device = ws.get_device()
+        if lib is _lib:
+            _refuse_devices(device, stream)
         stream = _stream(stream)
     if lib is _lib:  # the library itself, not a stand-in
         status = _operands_module().call(_address(name), key, specs.packed, tensors, ws, device, stream)
