@@ -25,6 +25,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "launch_order.cuh"
 
 namespace moe {
 
