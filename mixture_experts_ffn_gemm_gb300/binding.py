@@ -491,7 +491,8 @@ def _addresses(device, specs, tensors, ws):
 @functools.lru_cache(maxsize=None)
 def _operands_module():
     """The quick argument check (csrc/operands.cpp)."""
-    path = os.path.join(_HERE, "_build", "_operands.so")
+    from .build import operands_path
+    path = operands_path()
     if not os.path.exists(path):
         raise RuntimeError(f"the binding's module is not built ({path}); run "
                            "`python -m mixture_experts_ffn_gemm_gb300.build`")

@@ -22,7 +22,6 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmoe_gb300.so")
 OPERANDS_SRC = os.path.join(CSRC, "operands.cpp")
-OPERANDS = os.path.join(BUILD, "_operands.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]
@@ -60,16 +59,24 @@ def _stale(target: str, deps) -> bool:
         os.path.getmtime(target) < max(os.path.getmtime(p) for p in deps)
 
 
+def operands_path() -> str:
+    """The module of the quick argument check.  It reads tensors by the layout of the torch and the Python that it
+    was compiled with, so its name holds both: another version has a module of its own."""
+    import torch
+    return os.path.join(BUILD, f"_operands.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}.so")
+
+
 def build_operands(force: bool = False) -> str:
     """Compile the Python module of the quick argument check; returns its path."""
-    if not force and not _stale(OPERANDS, [OPERANDS_SRC]):
-        return OPERANDS
+    target = operands_path()
+    if not force and not _stale(target, [OPERANDS_SRC]):
+        return target
     import torch
     os.makedirs(BUILD, exist_ok=True)
     home = os.path.dirname(torch.__file__)
     inc = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"]]
-    tmp = OPERANDS + f".tmp{os.getpid()}"
+    tmp = target + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[f"-I{p}" for p in inc], OPERANDS_SRC, "-o", tmp, f"-L{os.path.join(home, 'lib')}",
@@ -77,8 +84,8 @@ def build_operands(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for operands.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, OPERANDS)
-    return OPERANDS
+    os.replace(tmp, target)
+    return target
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
