@@ -490,12 +490,11 @@ def _addresses(device, specs, tensors, ws):
 
 @functools.lru_cache(maxsize=None)
 def _operands_module():
-    """The quick argument check (csrc/operands.cpp)."""
+    """The quick argument check (csrc/operands.cpp), or None where it could not be built."""
     from .build import operands_path
     path = operands_path()
     if not os.path.exists(path):
-        raise RuntimeError(f"the binding's module is not built ({path}); run "
-                           "`python -m mixture_experts_ffn_gemm_gb300.build`")
+        return None
     loader = importlib.machinery.ExtensionFileLoader("_operands", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_operands", loader))
     loader.exec_module(module)
@@ -537,8 +536,9 @@ def _launch(name, specs_of, cfg, tensors, ws, stream):
         if lib is _lib:
             _refuse_devices(device, stream)
         stream = _stream(stream)
-    if lib is _lib:  # the library itself, not a stand-in
-        status = _operands_module().call(_address(name), key, specs.packed, tensors, ws, device, stream)
+    quick = _operands_module() if lib is _lib else None  # the library itself, not a stand-in
+    if quick is not None:
+        status = quick.call(_address(name), key, specs.packed, tensors, ws, device, stream)
         if status is not None:
             return _check(status, name)
     args = _addresses(device, specs, tensors, ws)

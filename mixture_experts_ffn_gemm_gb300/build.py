@@ -2,7 +2,7 @@
 
 Each ``csrc/*.cu`` compiles to an object in parallel (one ``-gencode``), then nvcc links the shared
 library with the static CUDA runtime.  ``csrc/operands.cpp``, the binding's quick argument check, becomes a
-Python module beside it (g++ with torch's headers).  A rebuild happens only when a source or header is newer than
+Python module beside it (g++ with torch's headers; the library does not need it).  A rebuild happens only when a source or header is newer than
 the library.  Usage: ``python -m mixture_experts_ffn_gemm_gb300.build [--force] [--verbose]``.
 """
 from __future__ import annotations
@@ -15,6 +15,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -88,16 +89,29 @@ def build_operands(force: bool = False) -> str:
     return target
 
 
+def _try_operands(force: bool = False) -> None:
+    """build_operands where there are a C++ compiler and torch's and Python's headers; without them the binding
+    makes the same checks in Python."""
+    try:
+        build_operands(force)
+    except (RuntimeError, OSError) as e:
+        target = operands_path()
+        if os.path.exists(target):  # of older sources
+            os.remove(target)
+        warnings.warn(f"the quick argument check is not built, calls of the products and microscaled operators "
+                      f"check their operands in Python (some 5 us a call more): {e}", RuntimeWarning)
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     """Compile and link the library; returns its path."""
     srcs, deps = _inputs()
     if not force and not _stale(LIB, deps):
-        build_operands()
+        _try_operands()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        operands = ex.submit(build_operands, force)
+        operands = ex.submit(_try_operands, force)
         objs = list(ex.map(lambda s: _compile(nvcc, s, verbose, list(extra)), srcs))
         operands.result()
     tmp = LIB + f".tmp{os.getpid()}"

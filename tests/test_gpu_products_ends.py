@@ -233,3 +233,30 @@ def test_a_run_longer_than_the_waits_limit_passes(cuda_device, width, rows, dtyp
             mag += p.abs().t() @ q.abs()
         tol = STEP[dtype] * v.abs() + (n / 16 + 2) * 2.0 ** -22 * mag
         assert ((out[e, -64:, -64:].double() - v).abs() <= tol).all()
+
+
+def test_calls_without_the_quick_check_give_the_same(cuda_device, monkeypatch):
+    """Where the module of the quick check could not be built, the binding checks and calls by itself."""
+    N, K, counts, pad = 72, 192, [5, 0, 140], 8
+    offs, E = offsets_of(counts), len(counts)
+    offs, R, a, b = grouped._make("forward", counts, N, K, pad, seed=50)
+
+    def run():
+        y = grouped._call("forward", offs, R, a, b, N, K, F32, pad)
+        cfg = B.make_micro_config(R, K, "nv", groups=E, ld=K + pad)
+        cw = B.make_micro_config(E * N, K, "nv", groups=E)
+        q, w, ws = B.alloc_micro(cfg), B.alloc_micro(cw), B.alloc_micro_workspace(cfg)
+        f = torch.tensor([0.01], device="cuda")
+        out, back = (torch.zeros(R, n, device="cuda") for n in (N, K))
+        B.moe_micro_quantize(cfg, a, None, gpu(offs), f, *q, ws)
+        B.moe_micro_quantize(cw, b.view(E * N, K), None, None, f, *w, ws)
+        B.moe_micro_product(B.make_micro_product_config(R, E, N, K, "nv", F32), gpu(offs), *q, f, *w, f.expand(E)
+                            .contiguous(), out, ws)
+        B.moe_micro_dequantize(B.make_micro_config(R, K, "nv", groups=E, dtype=F32), *q, gpu(offs), f, back, ws)
+        assert B.moe_device_status(ws) == B.MOE_OK
+        return y, *q, out, back
+
+    want = run()
+    monkeypatch.setattr(B, "_operands_module", lambda: None)
+    for one, other in zip(want, run()):
+        assert torch.equal(one, other)
