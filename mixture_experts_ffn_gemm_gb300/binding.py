@@ -446,6 +446,11 @@ _KINDS = {"forward": MOE_PRODUCT_FORWARD, "grad_x": MOE_PRODUCT_GRAD_X,
 _FORMATS = {"mx": MOE_MICRO_MX, "nv": MOE_MICRO_NV}
 
 
+# Configurations whose specs are kept, an entry point (about 2 KB each): a server's row counts come back in any
+# order, and specs made anew cost a call 11 us more (a small one takes 5).
+_CONFIGURATIONS = 4096
+
+
 # What a call checks of an operand: (type, fewest and most elements, name, (rows, width, pitch) or None).
 # Operands without a pitch of their own are that many consecutive elements; for the others no number of
 # elements passes the quick check.
@@ -576,7 +581,7 @@ def moe_grouped_product(cfg: moe_product_config_t, offsets, a, b, out, ws, strea
     _launch("moe_grouped_product", _product_specs, cfg, (offsets, a, b, out), ws, stream)
 
 
-@functools.lru_cache(maxsize=64)
+@functools.lru_cache(maxsize=_CONFIGURATIONS)
 def _product_specs(cfg: bytes) -> tuple:
     c = moe_product_config_t.from_buffer_copy(cfg)
     R, E, N, K, bf, odt = c.rows, c.E, c.N, c.K, torch.bfloat16, _DTYPES.get(c.out_dtype)
@@ -635,14 +640,14 @@ def _micro_specs(cfg: bytes):
             _at_least("scales", u8, _scale_bytes(c.rows, c.K, c.groups, c.format)))
 
 
-@functools.lru_cache(maxsize=64)
+@functools.lru_cache(maxsize=_CONFIGURATIONS)
 def _quantize_specs(cfg: bytes) -> tuple:
     c, values, offs, factor, codes, scales = _micro_specs(cfg)
     dest = _dense("dest", torch.int32, c.src_rows * c.copies)
     return _Specs((values("x", c.src_rows), dest, offs, factor, codes, scales))
 
 
-@functools.lru_cache(maxsize=64)
+@functools.lru_cache(maxsize=_CONFIGURATIONS)
 def _dequantize_specs(cfg: bytes) -> tuple:
     c, values, offs, factor, codes, scales = _micro_specs(cfg)
     return _Specs((codes, scales, offs, factor, values("out", c.rows)))
@@ -691,7 +696,7 @@ def alloc_micro_product_workspace(cfg: moe_micro_product_config_t, device="cuda"
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-@functools.lru_cache(maxsize=64)
+@functools.lru_cache(maxsize=_CONFIGURATIONS)
 def _micro_product_specs(cfg: bytes) -> tuple:
     c = moe_micro_product_config_t.from_buffer_copy(cfg)
     R, E, N, K, u8, f32 = c.rows, c.E, c.N, c.K, torch.uint8, torch.float32
