@@ -385,7 +385,8 @@ moe_status_t moe_block_join(const moe_join_config_t* cfg, const void* resid, con
  *   ws      moe_product_workspace_size() bytes; its first word is the device status.  The call raises
  *           flags there and clears none (moe_reset_device_status does), so one status can watch a run
  *           of calls: MOE_ERR_TIMEOUT (a bounded wait expired, the output is incomplete),
- *           MOE_ERR_DEVICE_CHECK (an offset outside its range, taken as the nearest allowed one).
+ *           MOE_ERR_DEVICE_CHECK (an offset outside its range: an expert's first row is taken into
+ *           [0, rows] and its end from there to rows, so that nothing outside the buffers is touched).
  * `out` may not overlap an operand.  rows == 0 is a no-op, but for GRAD_W without ACCUMULATE, which
  * writes zeros.  Equal calls give equal bits. */
 typedef enum {
