@@ -374,7 +374,9 @@ moe_status_t moe_block_join(const moe_join_config_t* cfg, const void* resid, con
  *                        a = dy [rows][N], b = W [E][N][K]
  *   MOE_PRODUCT_GRAD_W   out = dW [E][N][K]:  dW_e[n][k] = sum_r a[r][n] b[r][k]
  *                        a = dy [rows][N], b = x [rows][K]
- * Each output is rounded once, from its fp32 sum, to out_dtype (MOE_BF16 or MOE_F32).
+ * Each output is rounded once, from its fp32 sum, to out_dtype (MOE_BF16 or MOE_F32).  A step of the tensor cores
+ * (16 terms) cuts the sum by at most 2^-23 of it, towards zero; fp32 outputs are cut at most 64 times and bf16
+ * ones at most 8192 times before what has been summed is added up in fp32.
  *   offsets [E+1] int32, as moe_permute gives them: not decreasing, from 0 on, at most `rows`.  Rows
  *           from offsets[E] on belong to no expert: they are not read into any result and their
  *           outputs are left as they are.  An expert without rows has a dW of zeros.
@@ -422,7 +424,7 @@ moe_status_t moe_grouped_product(const moe_product_config_t* cfg, const int32_t*
  *   MOE_MICRO_NV  B = 16, S = s g: s an e4m3 byte (at most 448; 127: NaN), s = amax / (6 g) rounded to
  *                 nearest (ties to even), g a factor of the whole tensor in [2^-100, 2^100]
  * with amax the block's largest magnitude.  c is x / S rounded to nearest, ties to the even code, at
- * most 6; where s is zero all codes are.  The roundings are those of the exact quotients.  A block that
+ * most 6; where s is zero all codes are zeros, with x's signs.  The roundings are those of the exact quotients.  A block that
  * holds a NaN or an infinity has the scale NaN and codes 0: every value of it reads as NaN.  A factor
  * outside its range makes every block NaN (and raises MOE_ERR_DEVICE_CHECK).
  *   codes   [rows][K/2] bytes, channel 2i in the low half of byte i

@@ -447,7 +447,7 @@ _FORMATS = {"mx": MOE_MICRO_MX, "nv": MOE_MICRO_NV}
 
 
 # Configurations whose specs are kept, an entry point (about 2 KB each): a server's row counts come back in any
-# order, and specs made anew cost a call 11 us more (a small one takes 5).
+# order, and specs made anew cost a call 11 us more.
 _CONFIGURATIONS = 4096
 
 
