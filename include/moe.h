@@ -397,10 +397,11 @@ typedef enum {
   MOE_PRODUCT_GRAD_W = 2
 } moe_product_t;
 #define MOE_PRODUCT_ACCUMULATE 0x1u
-/* Test hooks, never set in normal use.  SHORT_WAITS: bounded waits give up after 10 ms in place of 2 s; a run of
- * any length passes, as each wait is for the tile at hand.  STALL, for the failure path: the second SM of each pair stops copying after three blocks, so that the
- * waits for its operands (shortened to 20 ms under this flag) expire; the kernel flags MOE_ERR_TIMEOUT in the
- * device status, lets its copies land, frees its tensor memory and returns, and the output is incomplete. */
+/* Test hooks, never set in normal use.  SHORT_WAITS: bounded waits give up after 10 ms in place of 2 s; a run
+ * of any length passes, as each wait is for the tile at hand.  STALL, for the failure path: the second SM of each
+ * pair stops copying after three blocks, so that the waits for its operands (shortened to 20 ms under this flag)
+ * expire; the kernel flags MOE_ERR_TIMEOUT in the device status, lets its copies land, frees its tensor memory
+ * and returns, and the output is incomplete. */
 #define MOE_PRODUCT_TEST_STALL 0x100u
 #define MOE_PRODUCT_TEST_SHORT_WAITS 0x200u
 typedef struct {
@@ -424,9 +425,9 @@ moe_status_t moe_grouped_product(const moe_product_config_t* cfg, const int32_t*
  *   MOE_MICRO_NV  B = 16, S = s g: s an e4m3 byte (at most 448; 127: NaN), s = amax / (6 g) rounded to
  *                 nearest (ties to even), g a factor of the whole tensor in [2^-100, 2^100]
  * with amax the block's largest magnitude.  c is x / S rounded to nearest, ties to the even code, at
- * most 6; where s is zero all codes are zeros, with x's signs.  The roundings are those of the exact quotients.  A block that
- * holds a NaN or an infinity has the scale NaN and codes 0: every value of it reads as NaN.  A factor
- * outside its range makes every block NaN (and raises MOE_ERR_DEVICE_CHECK).
+ * most 6; where s is zero all codes are zeros, with x's signs.  The roundings are those of the exact
+ * quotients.  A block that holds a NaN or an infinity has the scale NaN and codes 0: every value of it
+ * reads as NaN.  A factor outside its range makes every block NaN (and raises MOE_ERR_DEVICE_CHECK).
  *   codes   [rows][K/2] bytes, channel 2i in the low half of byte i
  *   scales  bytes in tiles of 128 rows x 4 scale columns (512 bytes), in which the tensor cores take
  *           them: the scale of row r of a group and column c (channels cB .. cB+B-1) is byte

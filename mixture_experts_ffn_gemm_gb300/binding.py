@@ -519,11 +519,13 @@ class _Specs(tuple):
 def _refuse_devices(device, stream):
     """The library launches on the current device: a stream or operands of another one are refused.  (A handle of 0
     is every device's default stream, so that such a call would run here, on the other device's addresses.)"""
+    if device < 0:  # not on a GPU at all: refused with the other operands
+        return
     current = torch._C._cuda_getDevice()
     of_stream = getattr(stream, "device", None)
     if of_stream is not None and of_stream.index != current:
         raise ValueError(f"stream: of device {of_stream.index}, the current device is {current}")
-    if device >= 0 and device != current:
+    if device != current:
         raise ValueError(f"ws: on device {device}, the current device is {current}")
 
 
