@@ -10,7 +10,7 @@ import torch
 
 from mixture_experts_ffn_gemm_gb300 import binding as B
 import test_gpu_grouped as grouped
-from test_gpu_micro import E4M3, LUT, gpu, offsets_of, pack, quantize64, scale_index, unpack
+from test_gpu_micro import E4M3, LUT, _operand, gpu, offsets_of, pack, quantize64, scale_index, unpack
 
 pytestmark = pytest.mark.gpu
 
@@ -260,3 +260,34 @@ def test_calls_without_the_quick_check_give_the_same(cuda_device, monkeypatch):
     monkeypatch.setattr(B, "_operands_module", lambda: None)
     for one, other in zip(want, run()):
         assert torch.equal(one, other)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale", [0.02, 1.0, 1e4, 1e12])
+def test_swiglu_of_large_gates_of_either_sign(cuda_device, scale, dtype):
+    """Gates from a hundredth to far beyond the exponential's range, both signs: SiLU is the gate, or zero."""
+    K, N, counts = 256, 128, [5, 0, 140]
+    offs, E = offsets_of(counts), len(counts)
+    g = torch.Generator().manual_seed(60)
+    a, sa, va = _operand(g, offs, K, "nv")
+    w, sw, vw = _operand(g, [e * 2 * N for e in range(E + 1)], K, "nv")
+    fa, fw = torch.tensor([scale], device="cuda"), torch.full((E,), 2.0 ** -10, device="cuda")
+    cfg = B.make_micro_product_config(offs[-1], E, N, K, "nv", dtype, swiglu=True)
+    ws = B.alloc_micro_product_workspace(cfg)
+    out = torch.full((offs[-1], N), 7.0, dtype=dtype, device="cuda")
+    B.moe_micro_product(cfg, gpu(offs), a, sa, fa, w, sw, fw, out, ws)
+    assert B.moe_device_status(ws) == B.MOE_OK
+    f = float(fa.double()) * 2.0 ** -10
+    for e in range(E):
+        s = slice(offs[e], offs[e + 1])
+        we = vw[e * 2 * N:(e + 1) * 2 * N]
+        y = f * (va[s] @ we.t())
+        err = ((K / 64 + 3) * 2.0 ** -22) * f * (va[s].abs() @ we.abs().t())
+        gate, up, eg, eu = y[:, :N], y[:, N:], err[:, :N], err[:, N:]
+        act = gate * torch.sigmoid(gate)
+        # SiLU moves by at most 1.1 times its argument's error, and hardly where it is zero (x exp(x) of the end
+        # nearer to it).  The approximate division is zero where 1 + exp(-x) passes 2^126: there |SiLU| is below
+        # 89 * 2^-126, which is 1.05e-36
+        slope = torch.where(gate < -20, (1 - gate) * torch.exp(gate + eg), torch.full_like(gate, 1.1))
+        tol = slope * eg * (up.abs() + eu) + act.abs() * eu + (STEP[dtype] + 2.0 ** -20) * (act * up).abs() + 1.1e-36 * up.abs()
+        assert ((out[s].double() - act * up).abs() <= tol + TINY[dtype]).all(), f"expert {e}"
