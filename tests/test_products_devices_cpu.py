@@ -79,3 +79,14 @@ def test_another_current_device(calls, monkeypatch):
     for call in _calls_of(OnDevice, 0):
         with pytest.raises(ValueError, match="current device is 1"):
             call()
+
+
+def test_operands_outside_any_gpu_are_refused_before_a_device_is_asked_for(calls, monkeypatch):
+    def none():
+        raise RuntimeError("no driver")
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", none)
+    for call in _calls_of(torch.Tensor, 0):
+        with pytest.raises(ValueError, match="ws"):
+            call()
+    assert calls == []
